@@ -53,7 +53,7 @@ MFMA_INT8_PEAK_TOPS = 5000.0   # MI355X dense int8 matrix peak (5.0 POPS)
 NOMINAL_SCLK_MHZ = 2400.0      # the clock that peak is quoted at
 HBM_PEAK_GBS = 8000.0          # MI355X HBM3E
 PROFILE_TRAFFIC = os.path.join(ROOT, "profiles", "gemm_traffic.json")
-GEMM_SOURCE = os.path.join(ROOT, "w8a8_int8_quantized_token_amd", "csrc", "gemm_i8.hip")
+GEMM_SOURCE = os.path.join(ROOT, "w8a8_int8_quantized_token_amd", "csrc", "gemm_kernel.h")
 
 
 def parse():

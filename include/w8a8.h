@@ -277,6 +277,131 @@ w8a8_status w8a8_linear_splitk_noalloc(const int8_t *xq, const float *x_scale, c
 w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int64_t N, int64_t K,
                               int64_t iters, int64_t *sink, hipStream_t stream);
 
+/*
+ * The linear from bf16 activations: w8a8_quantize_act and w8a8_linear (or
+ * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  For
+ * at most 32 tokens whose codes fit a compute unit's LDS it is one launch that
+ * reads the weight once and needs no workspace; otherwise the codes are made
+ * in the workspace first (then the few-token kernel, the K-split or the tiled
+ * kernel, by shape).
+ *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;
+ *   y bf16 [M,N] (16-byte aligned where w8a8_linear_splitk asks for it:
+ *   W8A8_ERR_ALIGN otherwise); workspace of at least
+ *   w8a8_linear_dynamic_workspace(M, N, K) bytes, 16-byte aligned (may be
+ *   NULL where that is 0).  The workspace belongs to the call until its work
+ *   on the stream is done: calls that may overlap need one each.
+ */
+size_t w8a8_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K);
+w8a8_status w8a8_linear_dynamic(const uint16_t *x, const int8_t *wq, const float *w_scale,
+                                const uint16_t *bias, uint16_t *y, int64_t M, int64_t N,
+                                int64_t K, int gelu, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/*
+ * Gated product, the first half of a gated feed-forward block: both
+ * projections, the activation and the product in one kernel.  wq [2N,K] holds
+ * the gate's N rows and below them the up projection's; w_scale and bias [2N]
+ * likewise (bias may be NULL).
+ *   g[m,n] = w8a8_linear's fp32 value for row n, u[m,n] for row N + n,
+ *   y[m,n] = bf16_rne( act(g[m,n]) * u[m,n] ),
+ *   act 0: SiLU, v / (1 + exp(-v)); act 1: GELU (exact erf definition); both
+ *   in fp32 with a relative error below 3e-5.
+ * Contracts as for w8a8_linear with 2N in the place of N; `tile` as for
+ * w8a8_linear_tile (every tile gives the same bits).  The dynamic form takes
+ * bf16 activations as w8a8_linear_dynamic does, with the same bits as
+ * w8a8_quantize_act and w8a8_gated_linear.
+ */
+#define W8A8_ACT_SILU 0
+#define W8A8_ACT_GELU 1
+w8a8_status w8a8_gated_linear(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                              const float *w_scale, const uint16_t *bias, uint16_t *y,
+                              int64_t M, int64_t N, int64_t K, int act, hipStream_t stream);
+w8a8_status w8a8_gated_linear_tile(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                                   const float *w_scale, const uint16_t *bias, uint16_t *y,
+                                   int64_t M, int64_t N, int64_t K, int act, int tile,
+                                   hipStream_t stream);
+size_t w8a8_gated_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K);
+w8a8_status w8a8_gated_linear_dynamic(const uint16_t *x, const int8_t *wq, const float *w_scale,
+                                      const uint16_t *bias, uint16_t *y, int64_t M, int64_t N,
+                                      int64_t K, int act, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of w8a8_linear for dy bf16 [M,N], the rounding to codes passed
+ * straight through:
+ *   dx[m,k]  = bf16( sum_n dy[m,n] * w[n,k] ),  w = wq * w_scale,
+ *   dw[n,k]  = bf16( sum_m dy[m,n] * x[m,k] ),  x = xq * x_scale,
+ *   dbias[n] = bf16( sum_m dy[m,n] ).
+ * Each output is bf16 and is left out where its pointer is NULL; dx needs wq
+ * and w_scale, dw needs xq and x_scale.  Sums are fp32 (bf16 matrix cores);
+ * the values w and x are rounded to bf16 once before their products.  Results
+ * do not depend on timing (no atomics).
+ * The gated form has wq [2N,K], w_scale, bias and dbias [2N] and dw [2N,K] as
+ * w8a8_gated_linear; it needs all of xq, x_scale, wq, w_scale and the
+ * forward's bias, forms g and u again from them, and
+ *   dg = dy * u * act'(g),  du = dy * act(g)   (fp32; for the products rounded
+ *   to bf16 once, with the scale of the other operand, whose codes are exact).
+ * Without tokens (M = 0) dw and dbias are set to zeros.
+ * Limits: N (gated: 2N, each half rounded up to 8) at most 2^21 for dx, M at
+ * most 2^21 for dw (W8A8_ERR_SHAPE).  dy, bias and outputs 2-byte aligned
+ * (16-byte aligned dy with N % 8 == 0 avoids a copy).  The workspace as above.
+ */
+size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias);
+w8a8_status w8a8_linear_backward(const uint16_t *dy, const int8_t *xq, const float *x_scale,
+                                 const int8_t *wq, const float *w_scale, uint16_t *dx,
+                                 uint16_t *dw, uint16_t *dbias, int64_t M, int64_t N, int64_t K,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t w8a8_gated_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw,
+                                            int dbias);
+w8a8_status w8a8_gated_linear_backward(const uint16_t *dy, const int8_t *xq,
+                                       const float *x_scale, const int8_t *wq,
+                                       const float *w_scale, const uint16_t *bias, uint16_t *dx,
+                                       uint16_t *dw, uint16_t *dbias, int64_t M, int64_t N,
+                                       int64_t K, int act, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * RMS norm of each head of the queries and keys and the position rotation, in
+ * one pass over the output of a QKV linear.  q is [M,Hq,D], k [M,Hk,D] (bf16;
+ * element (m,h,d) at m * row + h * head + d, so both may lie in one packed
+ * QKV matrix).  For each head vector x:
+ *   n = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: ones)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for the pairs of the first `rot`
+ *   values: (n[i], n[i + rot/2]) or, `interleaved` non-zero, (n[2i], n[2i+1]),
+ *   with cos, sin fp32 [P, rot/2] of the row's position (positions int32 [M],
+ *   or NULL: m mod P, one sequence of P tokens after another).
+ * Arithmetic in fp32, rounded to bf16 once.  A row whose position is outside
+ * [0, P) (padding) gets zeros in every head, and in the gradients, and adds
+ * nothing to the weights' gradients.  q_out and k_out may be q and k (same
+ * strides); Hq or Hk may be 0 (its pointers are then not looked at).
+ * The gradient takes the outputs' gradients dq, dk and the inputs q, k, and
+ * writes dq_in, dk_in (bf16; they may be dq, dk or q, k with the same strides)
+ * and, where not NULL, dq_weight, dk_weight (fp32 [D], summed over rows and
+ * heads in a fixed order; they need the workspace).
+ * Contract: 16 <= D <= 1024, D and rot multiples of 16, 0 <= rot <= D,
+ * M * (Hq + Hk) * (D/16 rounded up to a power of two) <= 2^31, P < 2^31,
+ * eps >= 0; all bf16 and table pointers 16-byte aligned, strides multiples of
+ * 8, weight gradients and positions 4-byte aligned.
+ */
+w8a8_status w8a8_qk_norm_rope(const uint16_t *q, int64_t q_row, int64_t q_head,
+                              const uint16_t *k, int64_t k_row, int64_t k_head,
+                              const uint16_t *q_weight, const uint16_t *k_weight,
+                              const float *cos, const float *sin, const int32_t *positions,
+                              uint16_t *q_out, int64_t q_out_row, int64_t q_out_head,
+                              uint16_t *k_out, int64_t k_out_row, int64_t k_out_head,
+                              int64_t M, int64_t P, int64_t Hq, int64_t Hk, int64_t D,
+                              int64_t rot, float eps, int interleaved, hipStream_t stream);
+size_t w8a8_qk_norm_rope_backward_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D);
+w8a8_status w8a8_qk_norm_rope_backward(
+    const uint16_t *dq, int64_t dq_row, int64_t dq_head, const uint16_t *dk, int64_t dk_row,
+    int64_t dk_head, const uint16_t *q, int64_t q_row, int64_t q_head, const uint16_t *k,
+    int64_t k_row, int64_t k_head, const uint16_t *q_weight, const uint16_t *k_weight,
+    const float *cos, const float *sin, const int32_t *positions, uint16_t *dq_in,
+    int64_t dq_in_row, int64_t dq_in_head, uint16_t *dk_in, int64_t dk_in_row,
+    int64_t dk_in_head, float *dq_weight, float *dk_weight, int64_t M, int64_t P, int64_t Hq,
+    int64_t Hk, int64_t D, int64_t rot, float eps, int interleaved, void *workspace,
+    size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

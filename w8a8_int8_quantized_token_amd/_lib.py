@@ -27,6 +27,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is not built; run `python w8a8_int8_quantized_token_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     p, i64, i32, st = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int
+    sz, view = ctypes.c_size_t, (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64)
     sig = {
         "w8a8_status_str": (ctypes.c_char_p, [st]),
         "w8a8_quantize_weight": (st, [p, i64, i64, p, p, p]),
@@ -52,6 +53,21 @@ def _load() -> ctypes.CDLL:
         "w8a8_linear_splitk_workspace": (ctypes.c_size_t, [i64, i64, i32]),
         "w8a8_linear_splitk": (st, [p, p, p, p, p, p, i64, i64, i64, i32, i32, i32, p, ctypes.c_size_t, p]),
         "w8a8_linear_splitk_noalloc": (st, [p, p, p, p, p, p, i64, i64, i64, i32, i32, i32, p]),
+        "w8a8_linear_dynamic_workspace": (sz, [i64, i64, i64]),
+        "w8a8_linear_dynamic": (st, [p, p, p, p, p, i64, i64, i64, i32, p, sz, p]),
+        "w8a8_gated_linear": (st, [p, p, p, p, p, p, i64, i64, i64, i32, p]),
+        "w8a8_gated_linear_tile": (st, [p, p, p, p, p, p, i64, i64, i64, i32, i32, p]),
+        "w8a8_gated_linear_dynamic_workspace": (sz, [i64, i64, i64]),
+        "w8a8_gated_linear_dynamic": (st, [p, p, p, p, p, i64, i64, i64, i32, p, sz, p]),
+        "w8a8_linear_backward_workspace": (sz, [i64, i64, i64, i32, i32, i32]),
+        "w8a8_linear_backward": (st, [p, p, p, p, p, p, p, p, i64, i64, i64, p, sz, p]),
+        "w8a8_gated_linear_backward_workspace": (sz, [i64, i64, i64, i32, i32, i32]),
+        "w8a8_gated_linear_backward": (st, [p, p, p, p, p, p, p, p, p, i64, i64, i64, i32, p, sz, p]),
+        "w8a8_qk_norm_rope": (st, [*view, *view, p, p, p, p, p, *view, *view, i64, i64, i64, i64, i64, i64,
+                                   ctypes.c_float, i32, p]),
+        "w8a8_qk_norm_rope_backward_workspace": (sz, [i64, i64, i64, i64]),
+        "w8a8_qk_norm_rope_backward": (st, [*view, *view, *view, *view, p, p, p, p, p, *view, *view, p, p, i64,
+                                            i64, i64, i64, i64, i64, ctypes.c_float, i32, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -1,0 +1,376 @@
+// C ABI of the operators around the linear (few-token forms, gated product,
+// backward passes, norm and rotation of queries and keys): argument checks,
+// workspace layout and launches.  Semantics are documented in include/w8a8.h;
+// checks always complete before anything is launched.
+#include "../../include/w8a8.h"
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace {
+
+using w8a8::GateAct;
+
+constexpr int64_t kMaxRows = int64_t(1) << 26;
+// Longest summed index of a backward product: a tile's 256 rows of bf16 stay
+// within the 31-bit offsets of its buffer ranges.
+constexpr int64_t kMaxSummed = int64_t(1) << 21;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+w8a8_status launched(hipError_t e) { return e == hipSuccess ? W8A8_OK : W8A8_ERR_LAUNCH; }
+
+// N output channels from `per` weight rows each.
+bool shape_ok(int64_t M, int64_t N, int64_t K, int per) {
+  return M >= 0 && M <= kMaxRows && N >= 1 && N <= kMaxRows / per && K >= 16 && K % 16 == 0 && K <= W8A8_MAX_K;
+}
+
+// Consecutive 256-byte aligned pieces of a workspace.
+struct Pieces {
+  int64_t bytes = 0;
+  int64_t add(int64_t n) {
+    const int64_t at = bytes;
+    bytes += (n + 255) / 256 * 256;
+    return at;
+  }
+};
+template <class T>
+T* at(void* ws, int64_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+
+// ---- few tokens / quantize on the way ----
+
+struct DynamicPlan {
+  bool few, codes;     // one of the few-token launches; codes made beforehand
+  int splits, tile;    // otherwise the linear's plan (gated: tile -1, no split)
+  int64_t xq, xs, slices;
+  int64_t bytes;
+};
+DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated) {
+  DynamicPlan p{};
+  p.few = M <= w8a8::kFewTokens;
+  p.codes = !p.few || !w8a8::few_tokens_in_lds(M, K, gated);
+  p.splits = 1;
+  p.tile = -1;
+  Pieces w;
+  if (p.codes) {
+    p.xq = w.add(M * K);
+    p.xs = w.add(4 * M);
+  }
+  if (!p.few && !gated) {
+    p.splits = w8a8::select_splitk(M, N, K, &p.tile);
+    if (p.splits > 1) p.slices = w.add((int64_t)w8a8_linear_splitk_workspace(M, N, p.splits));
+  }
+  p.bytes = w.bytes;
+  return p;
+}
+
+w8a8_status dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, const uint16_t* bias, uint16_t* y,
+                    int64_t M, int64_t N, int64_t K, int act, bool gated, void* ws, size_t ws_bytes,
+                    hipStream_t stream) {
+  if (!shape_ok(M, N, K, gated ? 2 : 1)) return W8A8_ERR_SHAPE;
+  if (act < 0 || act > 1) return W8A8_ERR_ARG;
+  if (M == 0) return W8A8_OK;
+  const DynamicPlan p = dynamic_plan(M, N, K, gated);
+  if (!x || !wq || !w_scale || !y || (p.bytes && !ws)) return W8A8_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(w_scale, 4) || !aligned(y, 2) || (bias && !aligned(bias, 2)) ||
+      (p.bytes && !aligned(ws, 16)) || (p.splits > 1 && !aligned(y, 16)))
+    return W8A8_ERR_ALIGN;
+  if (ws_bytes < (size_t)p.bytes) return W8A8_ERR_ARG;
+  int8_t* xq = nullptr;
+  float* xs = nullptr;
+  if (p.codes) {
+    xq = at<int8_t>(ws, p.xq);
+    xs = at<float>(ws, p.xs);
+    if (w8a8::launch_quantize_rows(x, xq, xs, M, K, stream) != hipSuccess) return W8A8_ERR_LAUNCH;
+  }
+  if (p.few)
+    return launched(w8a8::launch_few_tokens(x, xq, xs, wq, w_scale, bias, y, M, N, K, act, gated, stream));
+  if (gated)
+    return launched(w8a8::launch_gated(-1, static_cast<GateAct>(act), xq, xs, wq, w_scale, bias, y, M, N, K, stream));
+  if (p.splits > 1)
+    return w8a8_linear_splitk(xq, xs, wq, w_scale, bias, y, M, N, K, p.splits, p.tile, act, at<void>(ws, p.slices),
+                              (size_t)(p.bytes - p.slices), stream);
+  return act ? w8a8_linear_gelu(xq, xs, wq, w_scale, bias, y, M, N, K, stream)
+             : w8a8_linear(xq, xs, wq, w_scale, bias, y, M, N, K, stream);
+}
+
+// ---- backward products ----
+
+// Pieces of the input's gradient (first operand where it is not dy itself,
+// weight turned) and of the weight's (both operands) and the bias's sums.
+// The first two are used one after the other and share their space.
+struct BackPlan {
+  int64_t ld, mp;             // summed lengths, rounded up to 8 (gated: both halves)
+  int64_t first, wt;          // input's gradient
+  int64_t second, xt;         // weight's gradient
+  int64_t sums, sum_rows;
+  int64_t bytes;
+};
+BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy) {
+  BackPlan p{};
+  p.ld = (gated ? 2 : 1) * up8(N);
+  p.mp = up8(M);
+  const int64_t cols = (gated ? 2 : 1) * N;
+  Pieces w;
+  if (db) {
+    p.sum_rows = gated ? w8a8::gated_grad_sum_rows(M, N, K)
+                       : (M + w8a8::transpose_sum_span(M, N) - 1) / w8a8::transpose_sum_span(M, N);
+    p.sums = w.add(4 * p.sum_rows * cols);
+  }
+  // a gated gradient's first operands come out of one launch together
+  Pieces a = w, b = w;
+  if (dx) {
+    if (gated || copy_dy) p.first = a.add(2 * M * p.ld);
+    if (gated) b = a;
+    p.wt = a.add(2 * K * p.ld);
+  }
+  if (dw) {
+    p.second = b.add(2 * cols * p.mp);
+    if (gated && dx) p.wt = b.bytes;
+    p.xt = b.add(2 * K * p.mp);
+    if (gated && dx) a.bytes = p.wt + (2 * K * p.ld + 255) / 256 * 256;
+  }
+  p.bytes = std::max(a.bytes, b.bytes);
+  return p;
+}
+
+// dw and dbias of no tokens are zeros.
+w8a8_status no_tokens(uint16_t* dw, uint16_t* dbias, int64_t cols, int64_t K, hipStream_t stream) {
+  if (dw && w8a8::launch_zero(dw, cols * K, stream) != hipSuccess) return W8A8_ERR_LAUNCH;
+  if (dbias && w8a8::launch_zero(dbias, cols, stream) != hipSuccess) return W8A8_ERR_LAUNCH;
+  return W8A8_OK;
+}
+
+w8a8_status check_back(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
+                       const float* w_scale, const uint16_t* bias, const uint16_t* dx, const uint16_t* dw,
+                       const uint16_t* dbias, int64_t M, int64_t N, int64_t K, bool gated) {
+  if (!shape_ok(M, N, K, gated ? 2 : 1)) return W8A8_ERR_SHAPE;
+  if ((dx && up8(N) * (gated ? 2 : 1) > kMaxSummed) || (dw && up8(M) > kMaxSummed)) return W8A8_ERR_SHAPE;
+  const bool codes = dw || (gated && (dx || dbias)), weight = dx || (gated && (dw || dbias));
+  if (M > 0) {
+    if ((dx || dw || dbias) && !dy) return W8A8_ERR_NULL;
+    if ((codes && (!xq || !x_scale)) || (weight && (!wq || !w_scale))) return W8A8_ERR_NULL;
+  }
+  if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(dw, 2) || !aligned(dbias, 2) || !aligned(bias, 2))
+    return W8A8_ERR_ALIGN;
+  if (M > 0 && ((codes && (!aligned(xq, 16) || !aligned(x_scale, 4))) ||
+                (weight && (!aligned(wq, 16) || !aligned(w_scale, 4)))))
+    return W8A8_ERR_ALIGN;
+  return W8A8_OK;
+}
+
+w8a8_status check_workspace(const void* ws, size_t have, int64_t need) {
+  if (need == 0) return W8A8_OK;
+  if (!ws) return W8A8_ERR_NULL;
+  if (!aligned(ws, 16)) return W8A8_ERR_ALIGN;
+  return have < (size_t)need ? W8A8_ERR_ARG : W8A8_OK;
+}
+
+#define TRY(call) \
+  if ((call) != hipSuccess) return W8A8_ERR_LAUNCH
+
+// ---- norm and rotation ----
+
+w8a8_status check_rope(const w8a8::RopeArgs& a, int64_t Hq, int64_t Hk, int64_t D, int64_t rot) {
+  if (a.M < 0 || a.M > kMaxRows || Hq < 0 || Hk < 0 || Hq + Hk < 1 || Hq + Hk > 65536 || D < 16 || D > 1024 ||
+      D % 16 != 0 || rot < 0 || rot > D || rot % 16 != 0 || (rot > 0 && (a.P < 1 || a.P > INT32_MAX)))
+    return W8A8_ERR_SHAPE;
+  int64_t lanes = 1;
+  while (lanes * 16 < D) lanes *= 2;
+  if (a.M * (Hq + Hk) * lanes > (int64_t(1) << 31)) return W8A8_ERR_SHAPE;
+  if (!(a.eps >= 0.0f)) return W8A8_ERR_ARG;
+  return W8A8_OK;
+}
+w8a8_status check_view(const w8a8::RopeView& v, int64_t heads) {
+  if (heads == 0) return W8A8_OK;
+  if (!v.p) return W8A8_ERR_NULL;
+  return !aligned(v.p, 16) || v.row % 8 != 0 || v.head % 8 != 0 ? W8A8_ERR_ALIGN : W8A8_OK;
+}
+w8a8_status check_rope_ptrs(const w8a8::RopeArgs& a) {
+  for (const auto& c : {check_view(a.q, a.Hq), check_view(a.k, a.Hk), check_view(a.qo, a.Hq), check_view(a.ko, a.Hk)})
+    if (c != W8A8_OK) return c;
+  if (a.rot > 0 && (!a.cos || !a.sin)) return W8A8_ERR_NULL;
+  if (!aligned(a.cos, 16) || !aligned(a.sin, 16) || !aligned(a.qw, 16) || !aligned(a.kw, 16) ||
+      !aligned(a.positions, 4))
+    return W8A8_ERR_ALIGN;
+  return W8A8_OK;
+}
+
+w8a8::RopeView view(const uint16_t* p, int64_t row, int64_t head) { return {const_cast<uint16_t*>(p), row, head}; }
+
+}  // namespace
+
+extern "C" {
+
+size_t w8a8_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K) {
+  return shape_ok(M, N, K, 1) ? (size_t)dynamic_plan(M, N, K, false).bytes : 0;
+}
+
+w8a8_status w8a8_linear_dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, const uint16_t* bias,
+                                uint16_t* y, int64_t M, int64_t N, int64_t K, int gelu, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  return dynamic(x, wq, w_scale, bias, y, M, N, K, gelu ? 1 : 0, false, workspace, workspace_bytes, stream);
+}
+
+w8a8_status w8a8_gated_linear_tile(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                                   const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int act,
+                                   int tile, hipStream_t stream) {
+  if (!shape_ok(M, N, K, 2)) return W8A8_ERR_SHAPE;
+  if (act < 0 || act > 1 || tile >= w8a8::num_tiles()) return W8A8_ERR_ARG;
+  if (M == 0) return W8A8_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !y) return W8A8_ERR_NULL;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, 2) ||
+      !aligned(bias, 2))
+    return W8A8_ERR_ALIGN;
+  return launched(w8a8::launch_gated(tile, static_cast<GateAct>(act), xq, x_scale, wq, w_scale, bias, y, M, N, K,
+                                     stream));
+}
+
+w8a8_status w8a8_gated_linear(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                              const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int act,
+                              hipStream_t stream) {
+  return w8a8_gated_linear_tile(xq, x_scale, wq, w_scale, bias, y, M, N, K, act, -1, stream);
+}
+
+size_t w8a8_gated_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K) {
+  return shape_ok(M, N, K, 2) ? (size_t)dynamic_plan(M, N, K, true).bytes : 0;
+}
+
+w8a8_status w8a8_gated_linear_dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale,
+                                      const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, int act,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return dynamic(x, wq, w_scale, bias, y, M, N, K, act, true, workspace, workspace_bytes, stream);
+}
+
+// Both sizes allow for the copy of dy that an odd N or address needs.
+size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
+  if (!shape_ok(M, N, K, 1) || M == 0) return 0;
+  return (size_t)back_plan(M, N, K, false, dx, dw, dbias, true).bytes;
+}
+
+w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
+                                 const float* w_scale, uint16_t* dx, uint16_t* dw, uint16_t* dbias, int64_t M,
+                                 int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  w8a8_status st = check_back(dy, xq, x_scale, wq, w_scale, nullptr, dx, dw, dbias, M, N, K, false);
+  if (st != W8A8_OK) return st;
+  if (M == 0) return no_tokens(dw, dbias, N, K, stream);
+  const bool copy = N % 8 != 0 || !aligned(dy, 16);
+  const BackPlan p = back_plan(M, N, K, false, dx, dw, dbias, copy);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != W8A8_OK) return st;
+  if (dx) {
+    uint16_t* wt = at<uint16_t>(workspace, p.wt);
+    const uint16_t* first = dy;
+    if (copy) {
+      uint16_t* padded = at<uint16_t>(workspace, p.first);
+      TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ld, stream));
+      first = padded;
+    }
+    TRY(w8a8::launch_transpose_codes(wq, w_scale, wt, N, K, p.ld, 0, p.ld, stream));
+    TRY(w8a8::launch_gemm_bf16(first, wt, dx, M, K, p.ld, stream));
+  }
+  if (dw || dbias) {
+    uint16_t* dyt = dw ? at<uint16_t>(workspace, p.second) : nullptr;
+    float* sums = dbias ? at<float>(workspace, p.sums) : nullptr;
+    TRY(w8a8::launch_transpose_bf16(dy, dyt, sums, M, N, p.mp, p.mp, stream));
+    if (dw) {
+      uint16_t* xt = at<uint16_t>(workspace, p.xt);
+      TRY(w8a8::launch_transpose_codes(xq, x_scale, xt, M, K, p.mp, 0, p.mp, stream));
+      TRY(w8a8::launch_gemm_bf16(dyt, xt, dw, N, K, p.mp, stream));
+    }
+    if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, N, stream));
+  }
+  return W8A8_OK;
+}
+
+size_t w8a8_gated_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
+  if (!shape_ok(M, N, K, 2) || M == 0) return 0;
+  return (size_t)back_plan(M, N, K, true, dx, dw, dbias, true).bytes;
+}
+
+w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
+                                       const float* w_scale, const uint16_t* bias, uint16_t* dx, uint16_t* dw,
+                                       uint16_t* dbias, int64_t M, int64_t N, int64_t K, int act, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  w8a8_status st = check_back(dy, xq, x_scale, wq, w_scale, bias, dx, dw, dbias, M, N, K, true);
+  if (st != W8A8_OK) return st;
+  if (act < 0 || act > 1) return W8A8_ERR_ARG;
+  if (M == 0) return no_tokens(dw, dbias, 2 * N, K, stream);
+  if (!dx && !dw && !dbias) return W8A8_OK;
+  const BackPlan p = back_plan(M, N, K, true, dx, dw, dbias, true);
+  st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != W8A8_OK) return st;
+  uint16_t* first = dx ? at<uint16_t>(workspace, p.first) : nullptr;
+  uint16_t* second = dw ? at<uint16_t>(workspace, p.second) : nullptr;
+  float* sums = dbias ? at<float>(workspace, p.sums) : nullptr;
+  TRY(w8a8::launch_gated_grad(static_cast<GateAct>(act), dy, xq, x_scale, wq, w_scale, bias, first, p.ld, second,
+                              p.mp, sums, M, N, K, stream));
+  if (dx) {
+    uint16_t* wt = at<uint16_t>(workspace, p.wt);
+    TRY(w8a8::launch_transpose_codes(wq, nullptr, wt, N, K, p.ld, 0, p.ld / 2, stream));
+    TRY(w8a8::launch_transpose_codes(wq + N * K, nullptr, wt, N, K, p.ld, p.ld / 2, p.ld / 2, stream));
+    TRY(w8a8::launch_gemm_bf16(first, wt, dx, M, K, p.ld, stream));
+  }
+  if (dw) {
+    uint16_t* xt = at<uint16_t>(workspace, p.xt);
+    TRY(w8a8::launch_transpose_codes(xq, nullptr, xt, M, K, p.mp, 0, p.mp, stream));
+    TRY(w8a8::launch_gemm_bf16(second, xt, dw, 2 * N, K, p.mp, stream));
+  }
+  if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, 2 * N, stream));
+  return W8A8_OK;
+}
+
+w8a8_status w8a8_qk_norm_rope(const uint16_t* q, int64_t q_row, int64_t q_head, const uint16_t* k, int64_t k_row,
+                              int64_t k_head, const uint16_t* q_weight, const uint16_t* k_weight, const float* cos,
+                              const float* sin, const int32_t* positions, uint16_t* q_out, int64_t q_out_row,
+                              int64_t q_out_head, uint16_t* k_out, int64_t k_out_row, int64_t k_out_head, int64_t M,
+                              int64_t P, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, float eps, int interleaved,
+                              hipStream_t stream) {
+  w8a8::RopeArgs a{view(q, q_row, q_head), view(k, k_row, k_head), view(q_out, q_out_row, q_out_head),
+                   view(k_out, k_out_row, k_out_head), q_weight, k_weight, cos, sin, rot > 0 ? positions : nullptr,
+                   M, rot > 0 ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
+  w8a8_status st = check_rope(a, Hq, Hk, D, rot);
+  if (st != W8A8_OK || M == 0) return st;
+  st = check_rope_ptrs(a);
+  if (st != W8A8_OK) return st;
+  return launched(w8a8::launch_norm_rope(a, interleaved != 0, stream));
+}
+
+size_t w8a8_qk_norm_rope_backward_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D) {
+  if (M < 1 || Hq < 0 || Hk < 0 || D < 16 || D > 1024 || M > kMaxRows || Hq + Hk < 1 || Hq + Hk > 65536) return 0;
+  return (size_t)(w8a8::norm_rope_grad_rows(M, Hq, Hk, (int)D) * D * 4);
+}
+
+w8a8_status w8a8_qk_norm_rope_backward(
+    const uint16_t* dq, int64_t dq_row, int64_t dq_head, const uint16_t* dk, int64_t dk_row, int64_t dk_head,
+    const uint16_t* q, int64_t q_row, int64_t q_head, const uint16_t* k, int64_t k_row, int64_t k_head,
+    const uint16_t* q_weight, const uint16_t* k_weight, const float* cos, const float* sin, const int32_t* positions,
+    uint16_t* dq_in, int64_t dq_in_row, int64_t dq_in_head, uint16_t* dk_in, int64_t dk_in_row, int64_t dk_in_head,
+    float* dq_weight, float* dk_weight, int64_t M, int64_t P, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
+    float eps, int interleaved, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  w8a8::RopeArgs a{view(q, q_row, q_head), view(k, k_row, k_head), view(dq, dq_row, dq_head),
+                   view(dk, dk_row, dk_head), q_weight, k_weight, cos, sin, rot > 0 ? positions : nullptr,
+                   M, rot > 0 ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
+  w8a8_status st = check_rope(a, Hq, Hk, D, rot);
+  if (st != W8A8_OK) return st;
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return W8A8_ERR_ALIGN;
+  if (M == 0) {
+    if (dq_weight) TRY(w8a8::launch_zero(dq_weight, 2 * D, stream));
+    if (dk_weight) TRY(w8a8::launch_zero(dk_weight, 2 * D, stream));
+    return W8A8_OK;
+  }
+  const w8a8::RopeView oq = view(dq_in, dq_in_row, dq_in_head), ok = view(dk_in, dk_in_row, dk_in_head);
+  st = check_rope_ptrs(a);
+  if (st == W8A8_OK) st = check_view(oq, Hq);
+  if (st == W8A8_OK) st = check_view(ok, Hk);
+  if (st != W8A8_OK) return st;
+  const bool sums = dq_weight || dk_weight;
+  if (sums) {
+    st = check_workspace(workspace, workspace_bytes, (int64_t)w8a8_qk_norm_rope_backward_workspace(M, Hq, Hk, D));
+    if (st != W8A8_OK) return st;
+  }
+  return launched(w8a8::launch_norm_rope_grad(a, oq, ok, interleaved != 0, sums ? static_cast<float*>(workspace) : nullptr,
+                                              dq_weight, dk_weight, stream));
+}
+
+}  // extern "C"

@@ -39,4 +39,34 @@ __device__ __forceinline__ float gelu(float v) {
   return fmaxf(v, 0.0f) - fabsf(v * h);
 }
 
+// The same evaluation with the slope: a = gelu(v),
+// slope = gelu'(v) = Phi(v) + v phi(v), phi(v) = exp(-v^2/2) / sqrt(2 pi).
+__device__ __forceinline__ void gelu_slope(float v, float& a, float& slope) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35355339059327373f, 1.0f));
+  float q = 0.33010232f;
+  q = fmaf(q, t, -1.0232229f);
+  q = fmaf(q, t, 0.6846277f);
+  q = fmaf(q, t, 0.3670476f);
+  q = fmaf(q, t, 1.4686903f);
+  q = fmaf(q, t, -2.827234f);
+  const float x = v * -0.72134752044448170f;   // x * v = -log2(e) v^2 / 2
+  const float h = t * __builtin_amdgcn_exp2f(fmaf(x, v, q));
+  a = fmaxf(v, 0.0f) - fabsf(v * h);
+  slope = fmaf(v * 0.39894228040143268f, __builtin_amdgcn_exp2f(x * v), v < 0.0f ? h : 1.0f - h);
+}
+
+// SiLU, v * sigmoid(v), by the hardware's exp2 and reciprocal (1 ulp each).
+// Where 2^x overflows (v below about -88) the reciprocal is 0 and so is the
+// result (the exact one is below 1e-36).
+__device__ __forceinline__ float silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+}
+
+// a = silu(v), slope = silu'(v) = s (1 + v (1 - s)), s = sigmoid(v).
+__device__ __forceinline__ void silu_slope(float v, float& a, float& slope) {
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+  a = v * s;
+  slope = s * fmaf(v, 1.0f - s, 1.0f);
+}
+
 }  // namespace w8a8

@@ -36,8 +36,14 @@ int select_tile(int64_t M, int64_t N, int64_t K);
 int select_splitk(int64_t M, int64_t N, int64_t K, int* tile);
 
 // kBf16ScaleBias: y = bf16(((acc*sx)*sw)+b); kBf16GeluScaleBias: the same
-// value through GELU before the bf16 rounding; kRawI32: the accumulators.
-enum class Epilogue { kBf16ScaleBias, kBf16GeluScaleBias, kRawI32 };
+// value through GELU before the bf16 rounding; kRawI32: the accumulators;
+// kBf16Plain: the accumulators rounded to bf16.
+// Gated (two products, gate and up, with values g and u as above):
+// k*Gate: y = bf16(act(g) * u); k*GateGrad: the gradients of g and u.
+enum class Epilogue {
+  kBf16ScaleBias, kBf16GeluScaleBias, kRawI32, kBf16Plain,
+  kSiluGate, kGeluGate, kSiluGateGrad, kGeluGateGrad
+};
 
 // int8 GEMM acc[m,n] = sum_k xq[m,k] * wq[n,k] with the chosen epilogue.
 // For the bf16 epilogues `out` is bf16 [M,N] and sx/sw/bias are used (bias
@@ -74,5 +80,74 @@ hipError_t launch_gemm_fp8(int tile, Epilogue epi, const uint8_t* xq, const uint
 constexpr int kCeilingWorkgroups = 256;
 hipError_t launch_mfma_ceiling(const int8_t* xq, const int8_t* wq, int64_t M, int64_t N, int64_t K,
                                int64_t iters, int64_t* sink, hipStream_t stream);
+
+// Activation of a gated product's gate.
+enum class GateAct { kSilu = 0, kGelu = 1 };
+
+// The gated int8 product: wq [2N,K] holds the gate's rows and below them the
+// up projection's, sw and bias [2N] likewise; y bf16 [M,N] = act(g) * u.
+// tile < 0 chooses.
+hipError_t launch_gated(int tile, GateAct act, const int8_t* xq, const float* sx, const int8_t* wq,
+                        const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
+                        int64_t K, hipStream_t stream);
+
+// Gradients dg, du of the gated product's two values for dy bf16 [M,N], each
+// output as far as not null: p bf16 [M,ldp] (dg * sw_gate in columns 0..N-1,
+// du * sw_up from column ldp/2, zeros between; ldp = 2 * (N rounded up to 8)),
+// qt bf16 [2N,ldq] ((dg * sx)^T over (du * sx)^T, zeros past column M;
+// ldq = M rounded up to 8), sums fp32 [gated_grad_sum_rows(), 2N] (column
+// sums over blocks of rows).
+int64_t gated_grad_sum_rows(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, const int8_t* xq, const float* sx,
+                             const int8_t* wq, const float* sw, const uint16_t* bias, uint16_t* p,
+                             int64_t ldp, uint16_t* qt, int64_t ldq, float* sums, int64_t M,
+                             int64_t N, int64_t K, hipStream_t stream);
+
+// out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; Kpad a
+// multiple of 8, rows 16-byte aligned.
+hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, int64_t M,
+                            int64_t N, int64_t Kpad, hipStream_t stream);
+
+// Operand layout of the backward products (see transpose.hip).
+hipError_t launch_transpose_codes(const int8_t* q, const float* scale, uint16_t* out, int64_t R,
+                                  int64_t C, int64_t ld, int64_t col0, int64_t Rpad,
+                                  hipStream_t stream);
+int64_t transpose_sum_span(int64_t R, int64_t C);   // rows of one block of sums
+hipError_t launch_transpose_bf16(const uint16_t* x, uint16_t* out, float* sums, int64_t R, int64_t C,
+                                 int64_t ld, int64_t Rpad, hipStream_t stream);
+hipError_t launch_pad_rows(const uint16_t* x, uint16_t* out, int64_t R, int64_t C, int64_t ld,
+                           hipStream_t stream);
+hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream);   // 16-bit zeros
+hipError_t launch_sum_rows(const float* part, uint16_t* out, int64_t P, int64_t C, hipStream_t stream);
+
+// The linear (act: 0 none, 1 GELU) or gated pair (act: a GateAct) for at most
+// kFewTokens tokens, from bf16 x, or from codes and scales where those are
+// given (xq not null; needed where few_tokens_in_lds() says no).
+constexpr int64_t kFewTokens = 32;
+bool few_tokens_in_lds(int64_t M, int64_t K, bool gated);
+hipError_t launch_few_tokens(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq,
+                             const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
+                             int64_t K, int act, bool gated, hipStream_t stream);
+
+// Queries or keys [M, heads, D]: element (m, h, d) at p[m * row + h * head + d].
+struct RopeView {
+  uint16_t* p;
+  int64_t row, head;
+};
+struct RopeArgs {
+  RopeView q, k;     // inputs
+  RopeView qo, ko;   // forward: outputs; gradient: the outputs' gradients
+  const uint16_t *qw, *kw;      // norm weights bf16 [D], or null
+  const float *cos, *sin;       // [P, rot / 2]
+  const int32_t* positions;     // [M], or null: row m has position m % P
+  int64_t M, P;
+  int Hq, Hk, D, rot;
+  float eps;
+};
+hipError_t launch_norm_rope(const RopeArgs& a, bool interleaved, hipStream_t stream);
+// part fp32 [norm_rope_grad_rows(), D] (null: no weight gradients).
+int64_t norm_rope_grad_rows(int64_t M, int64_t Hq, int64_t Hk, int D);
+hipError_t launch_norm_rope_grad(const RopeArgs& a, const RopeView& dq, const RopeView& dk, bool interleaved,
+                                 float* part, float* dqw, float* dkw, hipStream_t stream);
 
 }  // namespace w8a8

@@ -23,7 +23,7 @@ import json
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-GEMM_SOURCE = os.path.join(HERE, "csrc", "gemm_i8.hip")
+GEMM_SOURCE = os.path.join(HERE, "csrc", "gemm_kernel.h")
 COPY_BYTES = 1 << 30
 GEMM_KERNEL = "gemm_i8_kernel"
 CALIB_KERNEL = "bitwise_not"

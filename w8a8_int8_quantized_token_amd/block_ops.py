@@ -16,42 +16,86 @@ from ._lib import check, lib
 ACTS = {"silu": 0, "gelu": 1}
 
 
-def _on(t, dtype, shape, name, device=None):
-    """t's address, checked: a contiguous device tensor of that type and shape
-    (None in a shape: any size), on `device` where given."""
+def _on(t, dtype, shape, name, device):
+    """t's address, checked: a contiguous tensor of that type and shape on
+    the CUDA device of that index (one expression where all is well: these
+    checks are most of a small call's host time)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(got)})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, other tensors on device {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _matrix(t, dtype, name):
+    """(address, rows, columns, device index) of the matrix that the call's
+    other tensors go by."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D (got shape {tuple(shape)})")
+    device = t.get_device()
+    return _on(t, dtype, shape, name, device), shape[0], shape[1], device
+
+
+def _rows(t, name):
+    """Rows and columns of a weight, whose type and place are checked later."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (got shape {tuple(t.shape)})")
+    return t.shape
 
 
 def _call(device, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
-    if device.index != torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(device)   # current_stream(device).cuda_stream
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = fn(*args, stream)
     else:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    check(status, fn.__name__)
+        status = fn(*args, stream)
+    if status:
+        check(status, fn.__name__)
+
+
+def _empty(shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
+
+
+class _Devices(dict):
+    """torch.device objects by index, made once."""
+
+    def __missing__(self, index):
+        self[index] = torch.device("cuda", index)
+        return self[index]
+
+
+_DEVICES = _Devices()
 
 
 def _workspace(given, need, device):
-    """(address, bytes) of the call's workspace and the tensor that holds it."""
+    """(address, bytes, tensor that holds them) of the call's workspace."""
     if given is None:
         if need == 0:
             return None, 0, None
-        given = torch.empty((need,), dtype=torch.uint8, device=device)
-    return _on(given, torch.uint8, (None,), "workspace", device), given.numel(), given
+        given = _empty((need,), torch.uint8, device)
+        return given.data_ptr(), need, given
+    if not isinstance(given, torch.Tensor) or given.dim() != 1:
+        raise ValueError("workspace must be a 1-D uint8 device tensor")
+    return _on(given, torch.uint8, given.shape, "workspace", device), given.numel(), given
 
 
 def _act(act):
@@ -60,20 +104,24 @@ def _act(act):
     return ACTS[act]
 
 
+def _out(y, shape, device):
+    """The given output's address, checked, or a new one."""
+    if y is None:
+        y = _empty(shape, torch.bfloat16, device)
+        return y, y.data_ptr()
+    return y, _on(y, torch.bfloat16, shape, "y", device)
+
+
 def _dynamic(fn, workspace_fn, x, wq, w_scale, bias, y, per, act, workspace):
-    px = _on(x, torch.bfloat16, (None, None), "x")
-    M, K = x.shape
-    dev = x.device
-    pw = _on(wq, torch.int8, (None, K), "wq", dev)
-    rows = wq.shape[0]
+    px, M, K, dev = _matrix(x, torch.bfloat16, "x")
+    rows = _rows(wq, "wq")[0]
+    pw = _on(wq, torch.int8, (rows, K), "wq", dev)
     if rows % per:
         raise ValueError("wq must hold as many gate rows as up rows")
     N = rows // per
     ps = _on(w_scale, torch.float32, (rows,), "w_scale", dev)
     pb = None if bias is None else _on(bias, torch.bfloat16, (rows,), "bias", dev)
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    py = _on(y, torch.bfloat16, (M, N), "y", dev)
+    y, py = _out(y, (M, N), dev)
     pws, nws, workspace = _workspace(workspace, workspace_fn(M, N, K), dev)
     _call(dev, fn, px, pw, ps, pb, py, M, N, K, act, pws, nws)
     return y
@@ -97,28 +145,23 @@ def gated_linear(xq, x_scale, wq, w_scale, bias=None, y=None, act: str = "silu",
     """Gated product: bf16 y [M,N] = act(gate) * up, gate and up being
     ``linear``'s values for the first and the last N rows of wq [2N,K]."""
     a = _act(act)
-    px = _on(xq, torch.int8, (None, None), "xq")
-    M, K = xq.shape
-    dev = xq.device
-    pw = _on(wq, torch.int8, (None, K), "wq", dev)
-    rows = wq.shape[0]
+    px, M, K, dev = _matrix(xq, torch.int8, "xq")
+    rows = _rows(wq, "wq")[0]
+    pw = _on(wq, torch.int8, (rows, K), "wq", dev)
     if rows % 2:
         raise ValueError("wq must hold as many gate rows as up rows")
     pxs = _on(x_scale, torch.float32, (M,), "x_scale", dev)
     ps = _on(w_scale, torch.float32, (rows,), "w_scale", dev)
     pb = None if bias is None else _on(bias, torch.bfloat16, (rows,), "bias", dev)
-    if y is None:
-        y = torch.empty((M, rows // 2), dtype=torch.bfloat16, device=dev)
-    py = _on(y, torch.bfloat16, (M, rows // 2), "y", dev)
+    y, py = _out(y, (M, rows // 2), dev)
     _call(dev, lib.w8a8_gated_linear_tile, px, pxs, pw, ps, pb, py, M, rows // 2, K, a, tile)
     return y
 
 
 def _grads(dev, M, rows, K, dx, dw, dbias):
     bf = torch.bfloat16
-    return (torch.empty((M, K), dtype=bf, device=dev) if dx else None,
-            torch.empty((rows, K), dtype=bf, device=dev) if dw else None,
-            torch.empty((rows,), dtype=bf, device=dev) if dbias else None)
+    return (_empty((M, K), bf, dev) if dx else None, _empty((rows, K), bf, dev) if dw else None,
+            _empty((rows,), bf, dev) if dbias else None)
 
 
 def _ptr(t):
@@ -130,11 +173,9 @@ def linear_backward(dy, xq, x_scale, wq, w_scale, dx: bool = True, dw: bool = Tr
     """Gradients of ``linear`` (without GELU) for dy bf16 [M,N], the rounding
     to codes passed straight through: (dx bf16 [M,K], dw bf16 [N,K], dbias bf16
     [N]), None where not asked for.  xq and x_scale may be None without dw."""
-    pdy = _on(dy, torch.bfloat16, (None, None), "dy")
-    M, N = dy.shape
-    dev = dy.device
-    pw = _on(wq, torch.int8, (N, None), "wq", dev)
-    K = wq.shape[1]
+    pdy, M, N, dev = _matrix(dy, torch.bfloat16, "dy")
+    K = _rows(wq, "wq")[1]
+    pw = _on(wq, torch.int8, (N, K), "wq", dev)
     ps = _on(w_scale, torch.float32, (N,), "w_scale", dev)
     if xq is None and x_scale is None and not dw:
         pxq = pxs = None
@@ -154,11 +195,9 @@ def gated_linear_backward(dy, xq, x_scale, wq, w_scale, bias=None, act: str = "s
     passed straight through: (dx bf16 [M,K], dw bf16 [2N,K], dbias bf16 [2N]),
     None where not asked for."""
     a = _act(act)
-    pdy = _on(dy, torch.bfloat16, (None, None), "dy")
-    M, N = dy.shape
-    dev = dy.device
-    pw = _on(wq, torch.int8, (2 * N, None), "wq", dev)
-    K = wq.shape[1]
+    pdy, M, N, dev = _matrix(dy, torch.bfloat16, "dy")
+    K = _rows(wq, "wq")[1]
+    pw = _on(wq, torch.int8, (2 * N, K), "wq", dev)
     pxq = _on(xq, torch.int8, (M, K), "xq", dev)
     pxs = _on(x_scale, torch.float32, (M,), "x_scale", dev)
     ps = _on(w_scale, torch.float32, (2 * N,), "w_scale", dev)
@@ -171,46 +210,58 @@ def gated_linear_backward(dy, xq, x_scale, wq, w_scale, bias=None, act: str = "s
     return gx, gw, gb
 
 
-def _heads(t, name, M=None, D=None, device=None, heads=None):
-    """(address, row stride, head stride) of bf16 [M, heads, D], last dimension dense."""
+def _heads(t, shape, name, device):
+    """Address, row stride and head stride of bf16 [M, heads, D], dense along D."""
+    try:
+        row, head, last = t.stride()
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device >= 0 and last == 1:
+            # the stride of a dimension of one element is never used
+            return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bf16 (got {t.dtype})")
-    s = t.shape
-    if len(s) != 3 or (M is not None and (s[0] != M or s[2] != D)) or (heads is not None and s[1] != heads):
-        raise ValueError(f"{name} must be [rows, heads, head size] like its partners (got {tuple(s)})")
-    if not t.is_cuda or (device is not None and t.device != device):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} must be on the device of the other tensors (got {t.device})")
-    row, head, last = t.stride()
-    if last != 1 and s[2] > 1:
-        raise ValueError(f"{name} must be dense along the head")
-    # the stride of a dimension of one element is never used
-    return t.data_ptr(), row if s[0] > 1 else 0, head if s[1] > 1 else 0
+    raise ValueError(f"{name} must be dense along the head")
 
 
-def _out_heads(t, name, like, D, device):
-    """An output's view: no two of its elements may share an address."""
-    v = _heads(t, name, like.shape[0], D, device, like.shape[1])
-    (M, H, _), (row, head) = t.shape, v[1:]
-    if H > 1 and abs(head) < D or M > 1 and abs(row) < D or \
-            (M > 1 and H > 1 and not (abs(row) >= (H - 1) * abs(head) + D or abs(head) >= (M - 1) * abs(row) + D)):
+def _out_heads(t, shape, name, device):
+    """An output and its view, new where not given; no two elements of a
+    given one may share an address."""
+    M, H, D = shape
+    if t is None:
+        t = _empty(shape, torch.bfloat16, device)
+        return t, (t.data_ptr(), H * D, D)
+    v = _heads(t, shape, name, device)
+    row, head = v[1:]
+    if (H > 1 and head < D) or (M > 1 and row < D) or \
+            (M > 1 and H > 1 and row < (H - 1) * head + D and head < (M - 1) * row + D):
         raise ValueError(f"{name} must not overlap itself")
-    return v
+    return t, v
 
 
 def _rope_args(q, k, q_weight, k_weight, cos, sin, positions):
-    vq = _heads(q, "q")
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
+        raise TypeError("q and k must be torch.Tensors")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head size]")
+    dev = q.get_device()
     M, Hq, D = q.shape
-    dev = q.device
-    vk = _heads(k, "k", M, D, dev)
+    Hk = k.shape[1]
+    vq, vk = _heads(q, q.shape, "q", dev), _heads(k, (M, Hk, D), "k", dev)
     pqw = None if q_weight is None else _on(q_weight, torch.bfloat16, (D,), "q_weight", dev)
     pkw = None if k_weight is None else _on(k_weight, torch.bfloat16, (D,), "k_weight", dev)
-    pc = _on(cos, torch.float32, (None, None), "cos", dev)
-    P, half = cos.shape
+    pc, P, half, _ = _matrix(cos, torch.float32, "cos")
     ps = _on(sin, torch.float32, (P, half), "sin", dev)
+    if cos.get_device() != dev:
+        raise ValueError(f"cos is on {cos.device}, other tensors on device {dev}")
     pp = None if positions is None else _on(positions, torch.int32, (M,), "positions", dev)
-    return vq, vk, (pqw, pkw, pc, ps, pp), (M, P, Hq, k.shape[1], D, 2 * half), dev
+    return vq, vk, (pqw, pkw, pc, ps, pp), (M, P, Hq, Hk, D, 2 * half), dev
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6,
@@ -222,12 +273,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float 
     None.  Returns (q_out, k_out), new dense tensors unless given; they may be
     q and k themselves.  Rows at a position outside [0, P) become zeros."""
     vq, vk, ptrs, sizes, dev = _rope_args(q, k, q_weight, k_weight, cos, sin, positions)
-    D = sizes[4]
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-    vqo, vko = _out_heads(q_out, "q_out", q, D, dev), _out_heads(k_out, "k_out", k, D, dev)
+    q_out, vqo = _out_heads(q_out, q.shape, "q_out", dev)
+    k_out, vko = _out_heads(k_out, k.shape, "k_out", dev)
     _call(dev, lib.w8a8_qk_norm_rope, *vq, *vk, *ptrs, *vqo, *vko, *sizes, eps, int(bool(interleaved)))
     return q_out, k_out
 
@@ -239,16 +286,15 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions=
     bf16; of q_weight, of k_weight, fp32 [D], None without ``weights``)."""
     vq, vk, ptrs, sizes, dev = _rope_args(q, k, q_weight, k_weight, cos, sin, positions)
     M, _, Hq, Hk, D, _ = sizes
-    vdq, vdk = _heads(dq, "dq", M, D, dev, Hq), _heads(dk, "dk", M, D, dev, Hk)
-    gq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    gk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    vdq, vdk = _heads(dq, q.shape, "dq", dev), _heads(dk, k.shape, "dk", dev)
+    gq, vgq = _out_heads(None, q.shape, "", dev)
+    gk, vgk = _out_heads(None, k.shape, "", dev)
     gqw = gkw = None
     need = 0
     if weights:
-        gqw = torch.empty((D,), dtype=torch.float32, device=dev)
-        gkw = torch.empty((D,), dtype=torch.float32, device=dev)
+        gqw, gkw = _empty((2, D), torch.float32, dev)
         need = lib.w8a8_qk_norm_rope_backward_workspace(M, Hq, Hk, D)
     pws, nws, workspace = _workspace(workspace, need, dev)
-    _call(dev, lib.w8a8_qk_norm_rope_backward, *vdq, *vdk, *vq, *vk, *ptrs, gq.data_ptr(), Hq * D, D, gk.data_ptr(),
-          Hk * D, D, _ptr(gqw), _ptr(gkw), *sizes, eps, int(bool(interleaved)), pws, nws)
+    _call(dev, lib.w8a8_qk_norm_rope_backward, *vdq, *vdk, *vq, *vk, *ptrs, *vgq, *vgk, _ptr(gqw),
+          _ptr(gkw), *sizes, eps, int(bool(interleaved)), pws, nws)
     return gq, gk, gqw, gkw

@@ -17,7 +17,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 26;
 constexpr int64_t kMaxSummed = int64_t(1) << 21;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 w8a8_status launched(hipError_t e) { return e == hipSuccess ? W8A8_OK : W8A8_ERR_LAUNCH; }
 
 // N output channels from `per` weight rows each.
@@ -96,39 +96,41 @@ w8a8_status dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, c
 
 // ---- backward products ----
 
-// Pieces of the input's gradient (first operand where it is not dy itself,
-// weight turned) and of the weight's (both operands) and the bias's sums.
-// The first two are used one after the other and share their space.
+// Workspace of a backward pass: the padded copy of dy where it is needed, the
+// sums for the bias, a gated gradient's first operands (made in one launch),
+// and then what the input's gradient and the weight's need, which are made
+// one after the other in the same space.
 struct BackPlan {
-  int64_t ld, mp;             // summed lengths, rounded up to 8 (gated: both halves)
-  int64_t first, wt;          // input's gradient
-  int64_t second, xt;         // weight's gradient
+  int64_t ldy;                // row length of the copy of dy
+  int64_t ld, mp;             // summed lengths of the two products, padded
+  int64_t copy, first, second, wt, xt, slices_x, slices_w;
   int64_t sums, sum_rows;
   int64_t bytes;
 };
 BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy) {
   BackPlan p{};
-  p.ld = (gated ? 2 : 1) * up8(N);
-  p.mp = up8(M);
   const int64_t cols = (gated ? 2 : 1) * N;
+  p.ldy = up(N, 8);
+  p.ld = gated ? 2 * up(N, 16) : p.ldy;
+  p.mp = up(M, 8);
   Pieces w;
   if (db) {
     p.sum_rows = gated ? w8a8::gated_grad_sum_rows(M, N, K)
                        : (M + w8a8::transpose_sum_span(M, N) - 1) / w8a8::transpose_sum_span(M, N);
     p.sums = w.add(4 * p.sum_rows * cols);
   }
-  // a gated gradient's first operands come out of one launch together
+  if (copy_dy && (gated || dx)) p.copy = w.add(2 * M * p.ldy);
+  if (gated && dx) p.first = w.add(2 * M * p.ld);
+  if (gated && dw) p.second = w.add(2 * cols * p.mp);
   Pieces a = w, b = w;
   if (dx) {
-    if (gated || copy_dy) p.first = a.add(2 * M * p.ld);
-    if (gated) b = a;
     p.wt = a.add(2 * K * p.ld);
+    p.slices_x = a.add(w8a8::gemm_bf16_slices(M, K, p.ld));
   }
   if (dw) {
-    p.second = b.add(2 * cols * p.mp);
-    if (gated && dx) p.wt = b.bytes;
+    if (!gated) p.second = b.add(2 * cols * p.mp);
     p.xt = b.add(2 * K * p.mp);
-    if (gated && dx) a.bytes = p.wt + (2 * K * p.ld + 255) / 256 * 256;
+    p.slices_w = b.add(w8a8::gemm_bf16_slices(cols, K, p.mp));
   }
   p.bytes = std::max(a.bytes, b.bytes);
   return p;
@@ -145,7 +147,9 @@ w8a8_status check_back(const uint16_t* dy, const int8_t* xq, const float* x_scal
                        const float* w_scale, const uint16_t* bias, const uint16_t* dx, const uint16_t* dw,
                        const uint16_t* dbias, int64_t M, int64_t N, int64_t K, bool gated) {
   if (!shape_ok(M, N, K, gated ? 2 : 1)) return W8A8_ERR_SHAPE;
-  if ((dx && up8(N) * (gated ? 2 : 1) > kMaxSummed) || (dw && up8(M) > kMaxSummed)) return W8A8_ERR_SHAPE;
+  // (a gated gradient's epilogue addresses a tile's rows of dy the same way)
+  if (((dx || gated) && (gated ? 2 * up(N, 16) : up(N, 8)) > kMaxSummed) || (dw && up(M, 8) > kMaxSummed))
+    return W8A8_ERR_SHAPE;
   const bool codes = dw || (gated && (dx || dbias)), weight = dx || (gated && (dw || dbias));
   if (M > 0) {
     if ((dx || dw || dbias) && !dy) return W8A8_ERR_NULL;
@@ -262,12 +266,12 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
     uint16_t* wt = at<uint16_t>(workspace, p.wt);
     const uint16_t* first = dy;
     if (copy) {
-      uint16_t* padded = at<uint16_t>(workspace, p.first);
-      TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ld, stream));
+      uint16_t* padded = at<uint16_t>(workspace, p.copy);
+      TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ldy, stream));
       first = padded;
     }
-    TRY(w8a8::launch_transpose_codes(wq, w_scale, wt, N, K, p.ld, 0, p.ld, stream));
-    TRY(w8a8::launch_gemm_bf16(first, wt, dx, M, K, p.ld, stream));
+    TRY(w8a8::launch_transpose_codes(wq, w_scale, wt, N, K, p.ld, false, stream));
+    TRY(w8a8::launch_gemm_bf16(first, wt, dx, at<float>(workspace, p.slices_x), M, K, p.ld, stream));
   }
   if (dw || dbias) {
     uint16_t* dyt = dw ? at<uint16_t>(workspace, p.second) : nullptr;
@@ -275,8 +279,8 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
     TRY(w8a8::launch_transpose_bf16(dy, dyt, sums, M, N, p.mp, p.mp, stream));
     if (dw) {
       uint16_t* xt = at<uint16_t>(workspace, p.xt);
-      TRY(w8a8::launch_transpose_codes(xq, x_scale, xt, M, K, p.mp, 0, p.mp, stream));
-      TRY(w8a8::launch_gemm_bf16(dyt, xt, dw, N, K, p.mp, stream));
+      TRY(w8a8::launch_transpose_codes(xq, x_scale, xt, M, K, p.mp, false, stream));
+      TRY(w8a8::launch_gemm_bf16(dyt, xt, dw, at<float>(workspace, p.slices_w), N, K, p.mp, stream));
     }
     if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, N, stream));
   }
@@ -297,24 +301,29 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, con
   if (act < 0 || act > 1) return W8A8_ERR_ARG;
   if (M == 0) return no_tokens(dw, dbias, 2 * N, K, stream);
   if (!dx && !dw && !dbias) return W8A8_OK;
-  const BackPlan p = back_plan(M, N, K, true, dx, dw, dbias, true);
+  const bool copy = N % 8 != 0 || !aligned(dy, 16);
+  const BackPlan p = back_plan(M, N, K, true, dx, dw, dbias, copy);
   st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;
   uint16_t* first = dx ? at<uint16_t>(workspace, p.first) : nullptr;
   uint16_t* second = dw ? at<uint16_t>(workspace, p.second) : nullptr;
   float* sums = dbias ? at<float>(workspace, p.sums) : nullptr;
-  TRY(w8a8::launch_gated_grad(static_cast<GateAct>(act), dy, xq, x_scale, wq, w_scale, bias, first, p.ld, second,
-                              p.mp, sums, M, N, K, stream));
+  if (copy) {
+    uint16_t* padded = at<uint16_t>(workspace, p.copy);
+    TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ldy, stream));
+    dy = padded;
+  }
+  TRY(w8a8::launch_gated_grad(static_cast<GateAct>(act), dy, p.ldy, xq, x_scale, wq, w_scale, bias, first, p.ld,
+                              second, p.mp, sums, M, N, K, stream));
   if (dx) {
     uint16_t* wt = at<uint16_t>(workspace, p.wt);
-    TRY(w8a8::launch_transpose_codes(wq, nullptr, wt, N, K, p.ld, 0, p.ld / 2, stream));
-    TRY(w8a8::launch_transpose_codes(wq + N * K, nullptr, wt, N, K, p.ld, p.ld / 2, p.ld / 2, stream));
-    TRY(w8a8::launch_gemm_bf16(first, wt, dx, M, K, p.ld, stream));
+    TRY(w8a8::launch_transpose_codes(wq, nullptr, wt, 2 * N, K, p.ld, true, stream));
+    TRY(w8a8::launch_gemm_bf16(first, wt, dx, at<float>(workspace, p.slices_x), M, K, p.ld, stream));
   }
   if (dw) {
     uint16_t* xt = at<uint16_t>(workspace, p.xt);
-    TRY(w8a8::launch_transpose_codes(xq, nullptr, xt, M, K, p.mp, 0, p.mp, stream));
-    TRY(w8a8::launch_gemm_bf16(second, xt, dw, 2 * N, K, p.mp, stream));
+    TRY(w8a8::launch_transpose_codes(xq, nullptr, xt, M, K, p.mp, false, stream));
+    TRY(w8a8::launch_gemm_bf16(second, xt, dw, at<float>(workspace, p.slices_w), 2 * N, K, p.mp, stream));
   }
   if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, 2 * N, stream));
   return W8A8_OK;

@@ -58,6 +58,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
+typedef uint32_t __attribute__((may_alias)) lds_word;
 
 constexpr int kWave = 64;
 constexpr int kNumXcd = 8;
@@ -161,6 +162,57 @@ __device__ __forceinline__ void split_halves(v4i v, u32x2& a, u32x2& b) {
   b = u32x2{r0[1], r1[1]};
 }
 
+// Exchanges lanes 16..31 and 48..63 of a with lanes 0..15 and 32..47 of b
+// (v_permlane16_swap_b32).
+__device__ __forceinline__ void swap_rows16(v4i& a, v4i& b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto r = __builtin_amdgcn_permlane16_swap((uint32_t)a[e], (uint32_t)b[e], false, false);
+    a[e] = (int)r[0];
+    b[e] = (int)r[1];
+  }
+}
+// v of each lane plus that of the lane 16 away in the same wavefront half.
+__device__ __forceinline__ float add_rows16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The value of the lane whose number differs in bit 0, 1, 2 or 3 (DPP).
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t lane_xor1(uint32_t v) { return dpp<0xB1>(v); }   // quad_perm [1,0,3,2]
+__device__ __forceinline__ uint32_t lane_xor2(uint32_t v) { return dpp<0x4E>(v); }   // quad_perm [2,3,0,1]
+__device__ __forceinline__ uint32_t lane_ror8(uint32_t v) { return dpp<0x128>(v); }  // row_ror:8
+__device__ __forceinline__ uint32_t lane_xor4(uint32_t v) {
+  // row_shl:4 into the even banks of four lanes, row_shr:4 into the odd ones
+  const int even = __builtin_amdgcn_update_dpp(0, (int)v, 0x104, 0xf, 0x5, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(even, (int)v, 0x114, 0xf, 0xa, false);
+}
+// One step of a reduction that halves the values per lane: the lanes of `hi`
+// keep b, the others a, each with the partner's share added.
+template <class F>
+__device__ __forceinline__ float keep_half(float a, float b, int hi, F partner) {
+  const float send = hi ? a : b, keep = hi ? b : a;
+  return keep + __uint_as_float(partner(__float_as_uint(send)));
+}
+
+// Buffer accesses (kept out of the kernel's lambdas like dma16): a range of
+// `n` bf16 values, 16-byte loads and stores at byte offsets in it; loads past
+// its end give zeros, stores past it are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_range(const uint16_t* p, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), (short)0, n * 2, kRsrcWord3);
+}
+__device__ __forceinline__ v4i buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t o) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+}
+__device__ __forceinline__ void buffer_store16(v4i v, __amdgpu_buffer_rsrc_t r, uint32_t o) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 0);
+}
+
 // s_waitcnt vmcnt(n) leaving the other counters alone (gfx9 encoding).
 template <int n>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -191,6 +243,11 @@ struct OpI8 {
   static constexpr int kStepK = 32;   // K bytes per MFMA
   typedef v4i Frag;
   typedef v16i Acc;
+};
+// int8 with the outputs a gradient epilogue is to make.
+template <int kWant_>
+struct OpI8Want : OpI8 {
+  static constexpr int kWant = kWant_;
 };
 struct OpF8 {
   static constexpr bool kF8 = true;
@@ -239,10 +296,10 @@ __device__ __forceinline__ void tile_origin(int t, int tiles_m, int tiles_n, int
 }
 
 // K split of a launch: the reduction of each output tile is cut into `chunks`
-// equal ranges of K bytes, each its own work item, whose raw int32 sums go to
-// their own output slice (`out_stride` elements apart); the kernel's K is then
-// the length of one range and `ldk` the row length of X and W.  No split:
-// chunks = 1, ldk = K.
+// equal ranges of K bytes (bf16: the last may be shorter), each its own work
+// item, whose raw sums go to their own output slice (`out_stride` elements
+// apart); the kernel's K is then the length of one range and `ldk` the row
+// length of X and W.  No split: chunks = 1, ldk = K.
 struct KSplit {
   int ldk;
   int chunks;
@@ -273,21 +330,22 @@ struct UpArgs {
     if (bias) bias += n;
   }
 };
-// Gradient of the gated product (plans of one launch only).  For the
-// gradients dg, du of the two products' values, as far as wanted:
-//   p    bf16 [M, ldp]: dg * sw_gate in columns 0 .. N-1, du * sw_up in
-//        columns p_up .. p_up+N-1 (p_up = N rounded up to 8, zeros between):
-//        the first operand of the input's gradient, whose other operand is
-//        then the codes themselves;
+// Gradient of the gated product.  For the gradients dg, du of the two
+// products' values, as far as wanted (OpI8Want):
+//   p    bf16 [M, ldp], ldp = 2 * (N rounded up to 16): dg * sw_gate of 16
+//        channels, then du * sw_up of the same 16, and so on (zeros for
+//        channels past N): the first operand of the input's gradient, whose
+//        other operand is then the codes themselves, in the same order;
 //   qt   bf16 [2N, ldq]: (dg * sx)^T and below it (du * sx)^T, zeros past
 //        column M: the first operand of the weight's gradient;
 //   dbp  fp32 [ceil(M / BM) * WM, 2N]: sums of dg, du over each wavefront's
 //        rows.
+constexpr int kWantP = 1, kWantQ = 2, kWantSums = 4;
 struct GradArgs : UpArgs {
-  const uint16_t* dy;   // [M, N]
-  int dy_vec;           // rows of dy are 16-byte aligned
+  const uint16_t* dy;   // [M, ld_dy], 16-byte aligned rows, zeros or nothing past column N
+  int ld_dy;
   uint16_t* p;
-  int ldp, p_up;
+  int ldp;
   uint16_t* qt;
   int ldq;
   float* dbp;
@@ -300,13 +358,19 @@ using EpiArgs = std::conditional_t<kGateGrad<EPI>, GradArgs,
 template <Epilogue EPI>
 constexpr int out_columns(int bn) { return kGated<EPI> ? bn / 2 : bn; }
 
-// Persistent kernel: gridDim.x workgroups (at most one per CU) walk the work
+// Workgroups per compute unit.  The tiles whose ring leaves room for several
+// have them for the gated and bf16 products, so that one workgroup's epilogue
+// and stage waits run under another's MFMAs.
+template <class T, Epilogue EPI, class Op>
+constexpr int kResident = (!kGated<EPI> && !Op::kBf16) ? 1 : T::kLdsBytes <= 40 * 1024 ? 3 : T::kLdsBytes <= 80 * 1024 ? 2 : 1;
+
+// Persistent kernel: gridDim.x workgroups (at most kResident per CU) walk the work
 // items t = blockIdx.x, blockIdx.x + gridDim.x, ... (output tile t mod
 // tiles, K range t / tiles).  With the split ring, the first two requests of
 // a workgroup's next item are issued before the epilogue of the current one,
 // so the epilogue hides their latency.
 template <class T, Epilogue EPI, class Op>
-__global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
+__global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_kernel(
     const int8_t* __restrict__ X, const int8_t* __restrict__ W, const float* __restrict__ sx,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, void* __restrict__ out,
     int M, int N, int K, int ldy, int tiles_m, int tiles_n, int vec_store, KSplit ks,
@@ -396,21 +460,23 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
   // each resource ends with the last valid row's last byte of the range
   // (rows past M or N read as zeros; bytes of a row past the range are never
   // requested: the K loop stops at the range's end).
+  // bf16: the last range of a split may be shorter than the others.
   struct TileAddr {
     int m0, n0, c;
     __amdgpu_buffer_rsrc_t rx, rw;
   };
+  auto range_len = [&](int c) { return Op::kBf16 ? min(K, ks.ldk - c * K) : K; };
   auto setup = [&](int t, TileAddr& a) {
     a.c = t / ntiles;
     tile_origin(t - a.c * ntiles, tiles_m, tiles_n, T::BM, kCols, a.m0, a.n0);
     const int rows_x = min(T::BM, M - a.m0), rows_w = min(kCols, N - a.n0);
     const int64_t k0 = (int64_t)a.c * K;
     a.rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(X + (int64_t)a.m0 * ks.ldk + k0), (short)0,
-                                             (rows_x - 1) * ks.ldk + K, kRsrcWord3);
+                                             (rows_x - 1) * ks.ldk + range_len(a.c), kRsrcWord3);
     const int8_t* w = W;
     if constexpr (kGated<EPI>) w = w_up_half ? extra.w : W;
     a.rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(w + (int64_t)a.n0 * ks.ldk + k0), (short)0,
-                                             (rows_w - 1) * ks.ldk + K, kRsrcWord3);
+                                             (rows_w - 1) * ks.ldk + range_len(a.c), kRsrcWord3);
   };
   // Request the X (W) part of stage kt of tile `a` into `buf`; chunks at or
   // past K read as zeros.
@@ -423,7 +489,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
   // of off0 (one add, plus a select past K): hoisted out of the loops they
   // would hold 2 x DX + DW registers through the whole kernel.
   // `gated_w`: the rows are those of a gated W (their offsets are off0_w's).
-  auto issue_rows = [&](__amdgpu_buffer_rsrc_t r, int n, int8_t* buf, int kt, auto interior, auto gated_w) {
+  auto issue_rows = [&](__amdgpu_buffer_rsrc_t r, int n, int8_t* buf, int kt, int klen, auto interior, auto gated_w) {
     constexpr bool kGw = decltype(gated_w)::value;
     const int kb = kt * T::BK;
     uint32_t o = kGw ? off0_w : off0;
@@ -433,7 +499,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
       for (int i = 0; i < n; ++i)
         dma16(r, buf + (wave + i * kDmaWaves) * kDmaBytes, o + (uint32_t)(i * (kGw ? blk_stride_w : blk_stride)), kb);
     } else {
-      const bool in_k = kb + col < K;
+      const bool in_k = kb + col < klen;
 #pragma unroll
       for (int i = 0; i < n; ++i)
         dma16(r, buf + (wave + i * kDmaWaves) * kDmaBytes,
@@ -441,10 +507,10 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
     }
   };
   auto issue_x = [&](const TileAddr& a, int8_t* buf, int kt, auto interior) {
-    issue_rows(a.rx, DXk, buf, kt, interior, std::false_type{});
+    issue_rows(a.rx, DXk, buf, kt, range_len(a.c), interior, std::false_type{});
   };
   auto issue_w = [&](const TileAddr& a, int8_t* buf, int kt, auto interior) {
-    issue_rows(a.rw, DWk, buf, kt, interior, std::integral_constant<bool, kGated<EPI>>{});
+    issue_rows(a.rw, DWk, buf, kt, range_len(a.c), interior, std::integral_constant<bool, kGated<EPI>>{});
   };
   // split ring: A = the operand with three slots, B = the one with two
   auto issue_a = [&](const TileAddr& a, int8_t* buf, int kt, auto interior) {
@@ -792,7 +858,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
         constexpr std::false_type not_last{};
         int kt = 0;
         if constexpr (kSplitK)
-          for (; kt < KT6 && (kt + 9) * T::BK <= K; kt += 6) six(kt, kInterior, std::false_type{}, not_last);
+          for (; kt < KT6 && (kt + 9) * T::BK <= range_len(cur.c); kt += 6) six(kt, kInterior, std::false_type{}, not_last);
         if constexpr (kEpiOwn) {
           for (; kt < KT6 - 6; kt += 6) six(kt, kChecked, std::false_type{}, not_last);
           if constexpr (decltype(role)::value) {
@@ -801,6 +867,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
               setup(t + (int)gridDim.x, pre);
             } else {
               pre.m0 = pre.n0 = 0;
+              if constexpr (Op::kBf16) pre.c = 0;
               pre.rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(X), (short)0, 0, kRsrcWord3);
               pre.rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(W), (short)0, 0, kRsrcWord3);
             }
@@ -844,7 +911,7 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
       };
       int kt = 0;
       if constexpr (kSplitK)
-        for (; kt < KTr && (kt + 2 * T::S) * T::BK <= K; kt += T::S) round(kt, kInterior);
+        for (; kt < KTr && (kt + 2 * T::S) * T::BK <= range_len(cur.c); kt += T::S) round(kt, kInterior);
       for (; kt < KTr; kt += T::S) round(kt, kChecked);
     }
     if constexpr (!kEpiOwn) {
@@ -989,101 +1056,121 @@ __global__ __launch_bounds__(T::kThreads, 1) void gemm_i8_kernel(
           }
         }
       } else if constexpr (kGateGrad<EPI>) {
+        // Tile b's dy is requested before tile b - 1 is worked on and before
+        // its stores, so neither its latency nor theirs is waited for; loads
+        // and stores are branch-free (rows past M and columns past N fall
+        // outside the buffer ranges), which keeps the counts exact.
+        constexpr int kWant = Op::kWant, NB = T::FM * T::FN;
+        const int rows = min(T::BM, M - m0), chans = min(kCols, N - n0);
+        const __amdgpu_buffer_rsrc_t dy_rsrc = buffer_range(extra.dy + (int64_t)m0 * extra.ld_dy, rows * extra.ld_dy);
+        [[maybe_unused]] __amdgpu_buffer_rsrc_t p_rsrc, qg_rsrc, qu_rsrc;
+        if constexpr (kWant & kWantP) p_rsrc = buffer_range(extra.p + (int64_t)m0 * extra.ldp, rows * extra.ldp);
+        if constexpr (kWant & kWantQ) {
+          qg_rsrc = buffer_range(extra.qt + (int64_t)n0 * extra.ldq, chans * extra.ldq);
+          qu_rsrc = buffer_range(extra.qt + (int64_t)(N + n0) * extra.ldq, chans * extra.ldq);
+        }
+        // first channel of column tile j, first row of row tile i, in the block
+        auto chan0 = [&](int j) { return (wn * T::TN + j * 32) / 2; };
+        auto row0 = [&](int i) { return wm * T::TM + i * 32; };
+        auto load_dy = [&](int b) {
+          const int n = n0 + chan0(b / T::FM) + 8 * e_kh;
+          const uint32_t o = (uint32_t)((row0(b % T::FM) + e_row) * extra.ld_dy + n) * 2u;
+          return buffer_load16(dy_rsrc, n < N ? o : kOOB);
+        };
+        float sum[16];
+        v4i d_next = load_dy(0);
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j) {
-          load_sb(j);
-          const int nb = n0 + (wn * T::TN + j * 32) / 2;
-          const int n = nb + 8 * e_kh;   // this lane's 8 channels in memory
-          float sum[16];
+        for (int b = 0; b < NB; ++b) {
+          const int j = b / T::FM, i = b % T::FM, nb = n0 + chan0(j);
+          u32x2 dh[2];
+          split_halves(d_next, dh[0], dh[1]);
+          if (b + 1 < NB) d_next = load_dy(b + 1);
+          if (i == 0) {
+            load_sb(j);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) sum[r] = 0.0f;
+          }
+          const typename Op::Acc& c = acc[i][j];
+          float dg[8], du[8];   // gradients of this lane's 8 gate and up values
 #pragma unroll
-          for (int i = 0; i < T::FM; ++i) {
-            const typename Op::Acc& c = acc[i][j];
-            const int mt = m0 + wm * T::TM + i * 32, m = mt + e_row;
-            v4i d4 = v4i{0, 0, 0, 0};
-            if (m < M) {
-              const uint16_t* drow = extra.dy + (int64_t)m * N;
-              if (extra.dy_vec) {
-                if (n < N) d4 = *reinterpret_cast<const v4i*>(drow + n);
-              } else {
+          for (int g = 0; g < 2; ++g)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (n + e < N) d4[e / 2] |= (int)((uint32_t)drow[n + e] << (16 * (e % 2)));
-              }
-            }
-            u32x2 dh[2];
-            split_halves(d4, dh[0], dh[1]);
-            float dg[8], du[8];   // gradients of this lane's 8 gate and up values
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float gate = dequant((float)c[4 * g + e], sa[i], sv[g][e], bv[g][e]);
-                const float up = dequant((float)c[8 + 4 * g + e], sa[i], sv[g + 2][e], bv[g + 2][e]);
-                const uint32_t dw = dh[g][e / 2];
-                const float d = __uint_as_float(e % 2 ? dw & 0xffff0000u : dw << 16);
-                float a, slope;
-                if constexpr (EPI == Epilogue::kGeluGateGrad) gelu_slope(gate, a, slope);
-                else silu_slope(gate, a, slope);
-                dg[4 * g + e] = d * up * slope;
-                du[4 * g + e] = d * a;
+            for (int e = 0; e < 4; ++e) {
+              const float gate = dequant((float)c[4 * g + e], sa[i], sv[g][e], bv[g][e]);
+              const float up = dequant((float)c[8 + 4 * g + e], sa[i], sv[g + 2][e], bv[g + 2][e]);
+              const uint32_t dw = dh[g][e / 2];
+              const float d = __uint_as_float(e % 2 ? dw & 0xffff0000u : dw << 16);
+              float a, slope;
+              if constexpr (EPI == Epilogue::kGeluGateGrad) gelu_slope(gate, a, slope);
+              else silu_slope(gate, a, slope);
+              dg[4 * g + e] = d * up * slope;
+              du[4 * g + e] = d * a;
+              if constexpr (kWant & kWantSums) {
                 sum[4 * g + e] += dg[4 * g + e];
                 sum[8 + 4 * g + e] += du[4 * g + e];
               }
-            if (extra.p != nullptr) {
-              float pg[8], pu[8];
-#pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                pg[r] = dg[r] * sv[r / 4][r % 4];
-                pu[r] = du[r] * sv[2 + r / 4][r % 4];
-              }
-              const v4i vg = join_halves(pack4_bf16(pg), pack4_bf16(pg + 4));
-              const v4i vu = join_halves(pack4_bf16(pu), pack4_bf16(pu + 4));
-              if (m < M && n < extra.p_up) {
-                uint16_t* prow = extra.p + (int64_t)m * extra.ldp;
-                *reinterpret_cast<v4i*>(prow + n) = vg;
-                *reinterpret_cast<v4i*>(prow + extra.p_up + n) = vu;
-              }
             }
-            if (extra.qt != nullptr) {
-              // turned around in the wavefront's LDS region: 32 rows (16 gate
-              // and 16 up channels) of 32 tokens
-              uint16_t* reg = reinterpret_cast<uint16_t*>(reg_a + wave * kRegion);
+          if constexpr (kWant & kWantP) {
+            float pg[8], pu[8];
 #pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                const int row = (r / 4) * 8 + e_kh * 4 + r % 4;
-                reg[row * 32 + e_row] = to_bf16(dg[r] * sa[i]);
-                reg[(16 + row) * 32 + e_row] = to_bf16(du[r] * sa[i]);
+            for (int r = 0; r < 8; ++r) {
+              pg[r] = dg[r] * sv[r / 4][r % 4];
+              pu[r] = du[r] * sv[2 + r / 4][r % 4];
+            }
+            // 16 gate and 16 up columns of a token are 64 consecutive bytes:
+            // after the exchange the first vector holds tokens 0..15 of the
+            // tile, four lanes (pieces) each, the second 16..31
+            v4i v0 = join_halves(pack4_bf16(pg), pack4_bf16(pg + 4));
+            v4i v1 = join_halves(pack4_bf16(pu), pack4_bf16(pu + 4));
+            swap_rows16(v0, v1);
+            const int piece = e_kh + 2 * ((e_lane >> 4) & 1);
+            const uint32_t o = (uint32_t)((row0(i) + (e_lane & 15)) * extra.ldp + 2 * nb + piece * 8) * 2u;
+            buffer_store16(v0, p_rsrc, nb < N ? o : kOOB);
+            buffer_store16(v1, p_rsrc, nb < N ? o + 32u * (uint32_t)extra.ldp : kOOB);
+          }
+          if constexpr (kWant & kWantQ) {
+            // turned around in the wavefront's LDS region: 32 rows (16 gate
+            // and 16 up channels) of 32 tokens; neighbouring lanes exchange
+            // halves of a packed channel pair, so a write has two tokens
+            int8_t* const reg = reg_a + wave * kRegion;
+            const uint32_t sel = e_lane & 1 ? 0x07060302u : 0x01000504u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int r = 0; r < 8; r += 2) {
+                const float* v = h ? du : dg;
+                const uint32_t own = __builtin_bit_cast(
+                    uint32_t, __builtin_convertvector((f32x2{v[r] * sa[i], v[r + 1] * sa[i]}), bf16x2));
+                // even lanes: channel r of both tokens, odd lanes: channel r + 1
+                const uint32_t two = __builtin_amdgcn_perm(own, lane_xor1(own), sel);
+                const int row = h * 16 + (r / 4) * 8 + e_kh * 4 + r % 4 + (e_lane & 1);
+                *reinterpret_cast<lds_word*>(reg + row * 64 + (e_row >> 1) * 4) = two;
               }
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int ch = nb + e_lane / 4, mc = mt + (e_lane % 4) * 8;
-                const v4i v = *reinterpret_cast<const v4i*>(reg + (h * 16 + e_lane / 4) * 32 + (e_lane % 4) * 8);
-                if (ch < N && mc < extra.ldq)
-                  *reinterpret_cast<v4i*>(extra.qt + (int64_t)(h * N + ch) * extra.ldq + mc) = v;
-              }
+            for (int h = 0; h < 2; ++h) {
+              const v4i v = *reinterpret_cast<const v4i*>(reg + (h * 16 + e_lane / 4) * 64 + (e_lane % 4) * 16);
+              const int m = m0 + row0(i) + (e_lane % 4) * 8;
+              const uint32_t o = (uint32_t)((chan0(j) + e_lane / 4) * extra.ldq + m) * 2u;
+              buffer_store16(v, h ? qu_rsrc : qg_rsrc, m < extra.ldq ? o : kOOB);
             }
           }
-          if (extra.dbp != nullptr) {
-            // sums over the 32 tokens of each wavefront half: half of the
-            // values change lanes at every step
+          if constexpr (kWant & kWantSums) {
+            if (i == T::FM - 1) {
+              // over the 32 tokens of each wavefront half: every step halves
+              // the values a lane keeps
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int off = 16 >> s;
-              const bool hi = e_lane & off;
+              for (int q = 0; q < 8; ++q) sum[q] = keep_half(sum[q], sum[q + 8], e_lane & 8, lane_ror8);
 #pragma unroll
-              for (int q = 0; q < (8 >> s); ++q) {
-                const float send = hi ? sum[q] : sum[q + (8 >> s)];
-                const float keep = hi ? sum[q + (8 >> s)] : sum[q];
-                sum[q] = keep + __shfl_xor(send, off, kWave);
-              }
+              for (int q = 0; q < 4; ++q) sum[q] = keep_half(sum[q], sum[q + 4], e_lane & 4, lane_xor4);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) sum[q] = keep_half(sum[q], sum[q + 2], e_lane & 2, lane_xor2);
+              float s = keep_half(sum[0], sum[1], e_lane & 1, lane_xor1);
+              s = add_rows16(s);
+              // value index of this lane: bits 3, 2, 1, 0 of its number
+              const int r = e_lane & 15, ch = nb + ((r >> 2) & 1) * 8 + e_kh * 4 + (r & 3);
+              if (!(e_lane & 16) && ch < N)
+                extra.dbp[(int64_t)((m0 + wm * T::TM) / T::TM) * 2 * N + (r >> 3) * N + ch] = s;
             }
-            sum[0] += __shfl_xor(sum[0], 1, kWave);
-            const int r = ((e_lane >> 4) & 1) * 8 + ((e_lane >> 3) & 1) * 4 + ((e_lane >> 2) & 1) * 2 + ((e_lane >> 1) & 1);
-            const int ch = nb + ((r / 4) % 2) * 8 + e_kh * 4 + r % 4;
-            if (!(e_lane & 1) && ch < N)
-              extra.dbp[(int64_t)((m0 + wm * T::TM) / T::TM) * 2 * N + (r / 8) * N + ch] = sum[0];
           }
         }
       } else if (vec_store) {
@@ -1282,9 +1369,9 @@ hipError_t launch_t(const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, int
   constexpr int kCols = out_columns<EPI>(T::BN);
   const int tiles_m = (int)((M + T::BM - 1) / T::BM);
   const int tiles_n = (int)((N + kCols - 1) / kCols);
-  // at most one workgroup per CU (the tiles occupy a whole CU); a multiple
+  // at most kResident workgroups per CU (the large tiles occupy a whole CU); a multiple
   // of the 8 XCDs so that each workgroup stays on its XCD's tile range
-  const dim3 grid((unsigned)std::min<int64_t>((int64_t)tiles_m * tiles_n * ks.chunks, num_cus()));
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)tiles_m * tiles_n * ks.chunks, num_cus() * kResident<T, EPI, Op>));
   const dim3 block(T::kThreads);
   const uintptr_t a = reinterpret_cast<uintptr_t>(o.out);
   // 16-byte stores; the split ring's buffer stores take 32-bit offsets

@@ -91,27 +91,29 @@ hipError_t launch_gated(int tile, GateAct act, const int8_t* xq, const float* sx
                         const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                         int64_t K, hipStream_t stream);
 
-// Gradients dg, du of the gated product's two values for dy bf16 [M,N], each
-// output as far as not null: p bf16 [M,ldp] (dg * sw_gate in columns 0..N-1,
-// du * sw_up from column ldp/2, zeros between; ldp = 2 * (N rounded up to 8)),
-// qt bf16 [2N,ldq] ((dg * sx)^T over (du * sx)^T, zeros past column M;
-// ldq = M rounded up to 8), sums fp32 [gated_grad_sum_rows(), 2N] (column
-// sums over blocks of rows).
+// Gradients dg, du of the gated product's two values for dy bf16 [M,ld_dy]
+// (rows 16-byte aligned; columns past N zeros or, N % 8 == 0, none), each
+// output as far as not null: p bf16 [M,ldp] (columns in blocks of 32: dg *
+// sw_gate of 16 channels, du * sw_up of the same, zeros past channel N; ldp =
+// 2 * (N rounded up to 16)), qt bf16 [2N,ldq] ((dg * sx)^T over (du * sx)^T,
+// zeros past column M; ldq = M rounded up to 8), sums fp32
+// [gated_grad_sum_rows(), 2N] (column sums over blocks of rows).
 int64_t gated_grad_sum_rows(int64_t M, int64_t N, int64_t K);
-hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, const int8_t* xq, const float* sx,
+hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, int64_t ld_dy, const int8_t* xq, const float* sx,
                              const int8_t* wq, const float* sw, const uint16_t* bias, uint16_t* p,
                              int64_t ldp, uint16_t* qt, int64_t ldq, float* sums, int64_t M,
                              int64_t N, int64_t K, hipStream_t stream);
 
-// out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; Kpad a
-// multiple of 8, rows 16-byte aligned.
-hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, int64_t M,
+// out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; N and Kpad
+// multiples of 8, rows 16-byte aligned; slices: gemm_bf16_slices() bytes of
+// workspace, 16-byte aligned.
+int64_t gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad);
+hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, float* slices, int64_t M,
                             int64_t N, int64_t Kpad, hipStream_t stream);
 
 // Operand layout of the backward products (see transpose.hip).
 hipError_t launch_transpose_codes(const int8_t* q, const float* scale, uint16_t* out, int64_t R,
-                                  int64_t C, int64_t ld, int64_t col0, int64_t Rpad,
-                                  hipStream_t stream);
+                                  int64_t C, int64_t ld, bool paired, hipStream_t stream);
 int64_t transpose_sum_span(int64_t R, int64_t C);   // rows of one block of sums
 hipError_t launch_transpose_bf16(const uint16_t* x, uint16_t* out, float* sums, int64_t R, int64_t C,
                                  int64_t ld, int64_t Rpad, hipStream_t stream);

@@ -2,8 +2,10 @@
 // operands contiguous along the summed index, but the input's gradient sums
 // over output channels (rows of the weight) and the weight's gradient over
 // tokens (rows of the activations), so
-//   transpose_codes: int8 [R,C] (times scale[r]) -> bf16 [C, ld], columns
-//     col0 .. col0+R-1, zeros up to col0+Rpad-1;
+//   transpose_codes: int8 [R,C] (times scale[r]) -> bf16 [C, ld], zeros past
+//     column R; or, `paired`, the R = 2N rows of a stacked [gate; up] weight
+//     with 16 gate columns, the 16 up columns of the same channels, and so on
+//     (the order of the gated gradient's columns; zeros for channels past N);
 //   transpose_bf16:  bf16 [R,C] -> bf16 [C, ld] the same way, and the fp32
 //     sums of each column over blocks of rows;
 //   pad_rows:        bf16 [R,C] -> bf16 [R, ld], zeros past column C;
@@ -33,34 +35,46 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float bf(uint32_t half) { return __uint_as_float(half << 16); }
 
-// grid (ceil(C/64), ceil(Rpad/64)); C % 16 == 0, Rpad % 8 == 0.
+// Source row of output column v (-1: none, a zero).
+__device__ __forceinline__ int64_t source_row(int64_t v, int64_t R, bool paired) {
+  if (!paired) return v < R ? v : -1;
+  const int64_t ch = (v >> 5) * 16 + (v & 15), n = R / 2;
+  return ch < n ? ((v >> 4) & 1) * n + ch : -1;
+}
+
+// grid (ceil(C/64), ceil(ld/64)); C % 16 == 0, ld % 8 == 0.
+template <bool kPaired>
 __global__ __launch_bounds__(kThreads) void transpose_codes_kernel(
     const int8_t* __restrict__ q, const float* __restrict__ scale, uint16_t* __restrict__ out,
-    int64_t R, int64_t C, int64_t ld, int64_t col0, int64_t Rpad) {
+    int64_t R, int64_t C, int64_t ld) {
   __shared__ __attribute__((aligned(16))) int8_t tile[kT][kT + 4];
   __shared__ float s_lds[kT];
   const int tid = threadIdx.x;
   const int64_t c0 = (int64_t)blockIdx.x * kT;
-  for (int64_t r0 = (int64_t)blockIdx.y * kT; r0 < Rpad; r0 += (int64_t)gridDim.y * kT) {
+  for (int64_t r0 = (int64_t)blockIdx.y * kT; r0 < ld; r0 += (int64_t)gridDim.y * kT) {
     {
       const int r = tid / 4, c = (tid % 4) * 16;
+      const int64_t from = source_row(r0 + r, R, kPaired);
       u32x4 v = u32x4{0, 0, 0, 0};
-      if (r0 + r < R && c0 + c < C) v = *reinterpret_cast<const u32x4*>(q + (r0 + r) * C + c0 + c);
+      if (from >= 0 && c0 + c < C) v = *reinterpret_cast<const u32x4*>(q + from * C + c0 + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(&tile[r][c + 4 * e]) = v[e];
-      if (tid < kT) s_lds[tid] = scale == nullptr ? 1.0f : r0 + tid < R ? scale[r0 + tid] : 0.0f;
+      if (tid < kT) {
+        const int64_t at = source_row(r0 + tid, R, kPaired);
+        s_lds[tid] = scale == nullptr ? 1.0f : at >= 0 ? scale[at] : 0.0f;
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int it = 0; it < kT * kT / 8 / kThreads; ++it) {
       const int id = it * kThreads + tid, c = id / 8, r = (id % 8) * 8;
-      if (c0 + c < C && r0 + r < Rpad) {
+      if (c0 + c < C && r0 + r < ld) {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           w[e] = pack2((float)tile[r + 2 * e][c] * s_lds[r + 2 * e],
                        (float)tile[r + 2 * e + 1][c] * s_lds[r + 2 * e + 1]);
-        *reinterpret_cast<u32x4*>(out + (c0 + c) * ld + col0 + r0 + r) = w;
+        *reinterpret_cast<u32x4*>(out + (c0 + c) * ld + r0 + r) = w;
       }
     }
     __syncthreads();
@@ -175,11 +189,12 @@ hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream) {
 }
 
 hipError_t launch_transpose_codes(const int8_t* q, const float* scale, uint16_t* out, int64_t R,
-                                  int64_t C, int64_t ld, int64_t col0, int64_t Rpad,
-                                  hipStream_t stream) {
-  const dim3 grid((unsigned)((C + kT - 1) / kT), (unsigned)std::min<int64_t>((Rpad + kT - 1) / kT, 65535));
-  hipLaunchKernelGGL(transpose_codes_kernel, grid, dim3(kThreads), 0, stream, q, scale, out, R, C, ld,
-                     col0, Rpad);
+                                  int64_t C, int64_t ld, bool paired, hipStream_t stream) {
+  const dim3 grid((unsigned)((C + kT - 1) / kT), (unsigned)std::min<int64_t>((ld + kT - 1) / kT, 65535));
+  if (paired)
+    hipLaunchKernelGGL((transpose_codes_kernel<true>), grid, dim3(kThreads), 0, stream, q, scale, out, R, C, ld);
+  else
+    hipLaunchKernelGGL((transpose_codes_kernel<false>), grid, dim3(kThreads), 0, stream, q, scale, out, R, C, ld);
   return hipGetLastError();
 }
 

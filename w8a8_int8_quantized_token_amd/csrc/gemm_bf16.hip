@@ -30,21 +30,23 @@ __global__ __launch_bounds__(256) void join_slices_kernel(const f32x4* __restric
   }
 }
 
-// Tile and number of K ranges, by a model of the time in us (measured on
-// MI355X over 16 shapes from 16 x 1024 x 2048 to 8192 x 4096 x 24576, every
-// tile and 1 to 8 ranges; the choice was within 7% of the best at each):
-//   launch + rounds * (tile overhead + stages * max(stage, power)) + join,
+// Tile and number of K ranges, by a model of the time in us, fitted to
+// measurements on MI355X of every tile with 1 to 8 ranges at 22 shapes from
+// 16 x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was the fastest, or
+// within 12% of it, at each; 2% in the mean):
+//   4 + rounds * (tile + stages * max(stage, power)) + join,
 // stage the time of 128 K bytes of a tile alone on its compute unit, power
-// the same with all units busy, when the chip's power limit holds the whole
-// launch to about 1250 TFLOP/s.  Ranges pay where tiles leave units idle:
-// 1037 x 2064 x 10944: 106 us whole, 72 in three; 777 x 1168 x 4608: 32 us
-// whole, 25 in three; 4096 x 4096 x 4096: 110 us whole, 162 in two.
+// the same when `rate` TFLOP/s is what the whole chip's power limit allows.
+// Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 106 us whole,
+// 70 in ranges; 777 x 1168 x 4608: 32 us whole, 25 in three; but 4096 x 4096
+// x 4096: 110 us whole, 162 in two.
 struct Cost {
-  double tile_us, stage_us;
+  double tile_us, stage_us, rate;
   int ring;
 };
-constexpr Cost kCost[kNumCfg] = {{6.0, 0.97, 6}, {6.0, 1.04, 2}, {5.0, 0.72, 6}, {4.0, 0.56, 3},
-                                 {4.0, 0.70, 3}, {1.2, 0.52, 4}, {0.7, 0.38, 3}};
+constexpr Cost kCost[kNumCfg] = {{2.0, 1.12, 1330, 6}, {2.2, 1.28, 1425, 2}, {2.6, 0.88, 1570, 6},
+                                 {3.4, 0.56, 1250, 3}, {2.4, 0.79, 1140, 3}, {0.3, 0.45, 800, 4},
+                                 {0.2, 0.24, 450, 3}};
 constexpr int64_t kMaxSlices = int64_t(1) << 29;   // bytes of workspace a split may take
 
 struct Choice {
@@ -53,19 +55,21 @@ struct Choice {
 
 double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   const TileDesc& d = kCfgs[cfg];
-  const int64_t tiles = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * chunks;
-  // 64-byte-stage tiles run several workgroups per unit; a round is still
-  // counted as one tile per unit
-  const int64_t rounds = (tiles + kCUs - 1) / kCUs;
+  const Cost& c = kCost[cfg];
+  const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * chunks;
+  const double tiles = (double)items;
+  const int resident = cfg == k64 ? 3 : cfg == k128 ? 2 : 1;   // as kResident
+  // tiles that share a compute unit overlap by about a quarter
+  const double rounds = resident == 1 ? (double)((items + kCUs - 1) / kCUs)
+                        : items <= kCUs ? 1.0
+                        : items <= kCUs * resident ? 1.0 + (tiles / kCUs - 1.0) * 0.75
+                                                   : tiles / kCUs;
   const int64_t range = (kb + 128 * chunks - 1) / (128 * chunks) * 128;
-  const int64_t per = d.block_k, ring = kCost[cfg].ring;
-  const int64_t stages = ((range + per - 1) / per + ring - 1) / ring * ring;
-  const double active = (double)std::min<int64_t>(tiles, kCUs);
-  const double power = active * (double)(d.block_m * d.block_n) * 128.0 / 1250e6;   // 2 * 64 operations a byte pair
-  const double stage = std::max(kCost[cfg].stage_us, power) * (double)per / 128.0;
-  double us = 4.0 + (double)rounds * (kCost[cfg].tile_us + (double)stages * stage);
-  if (chunks > 1) us += 3.0 + (double)chunks * (double)(M * N) * 8.0 / 4.5e6;
-  return us;
+  const int64_t stages = ((range + d.block_k - 1) / d.block_k + c.ring - 1) / c.ring * c.ring;
+  // 128 operations per output and 128 bytes of K
+  const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
+  const double us = 4.0 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power) * d.block_k / 128.0);
+  return chunks > 1 ? us + 1.8 + (double)chunks * (double)M * (double)N * 1.6e-6 : us;
 }
 
 Choice choose(int64_t M, int64_t N, int64_t kb) {

@@ -35,6 +35,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float bf(uint32_t half) { return __uint_as_float(half << 16); }
 
+// Eight values of a row of C from column c on, zeros past its end, from any
+// 2-byte address (an unaligned 16-byte load where all eight are there).
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t c, int64_t C) {
+  u32x4 v = u32x4{0, 0, 0, 0};
+  if (c + 8 <= C) {
+    __builtin_memcpy(&v, row + c, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < C) v[e / 2] |= (uint32_t)row[c + e] << (16 * (e % 2));
+  }
+  return v;
+}
+
 // Source row of output column v (-1: none, a zero).
 __device__ __forceinline__ int64_t source_row(int64_t v, int64_t R, bool paired) {
   if (!paired) return v < R ? v : -1;
@@ -42,39 +56,54 @@ __device__ __forceinline__ int64_t source_row(int64_t v, int64_t R, bool paired)
   return ch < n ? ((v >> 4) & 1) * n + ch : -1;
 }
 
-// grid (ceil(C/64), ceil(ld/64)); C % 16 == 0, ld % 8 == 0.
+// grid (ceil(C/128), ceil(ld/64)); C % 16 == 0, ld % 8 == 0.  64 rows by 128
+// columns; a thread turns 8 rows of 4 columns, read as 8 words (LDS rows of 33
+// words: the 64 lanes' words lie in 64 banks) and written as four 16-byte
+// pieces of 128-byte runs.  33.5 MB of codes to 67 MB: see the figures at
+// launch_transpose_codes.
+constexpr int kCodeRows = 64, kCodeCols = 128;
 template <bool kPaired>
 __global__ __launch_bounds__(kThreads) void transpose_codes_kernel(
     const int8_t* __restrict__ q, const float* __restrict__ scale, uint16_t* __restrict__ out,
     int64_t R, int64_t C, int64_t ld) {
-  __shared__ __attribute__((aligned(16))) int8_t tile[kT][kT + 4];
-  __shared__ float s_lds[kT];
+  __shared__ uint32_t tile[kCodeRows][kCodeCols / 4 + 1];
+  __shared__ __attribute__((aligned(16))) float s_lds[kCodeRows];
   const int tid = threadIdx.x;
-  const int64_t c0 = (int64_t)blockIdx.x * kT;
-  for (int64_t r0 = (int64_t)blockIdx.y * kT; r0 < ld; r0 += (int64_t)gridDim.y * kT) {
-    {
-      const int r = tid / 4, c = (tid % 4) * 16;
-      const int64_t from = source_row(r0 + r, R, kPaired);
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (from >= 0 && c0 + c < C) v = *reinterpret_cast<const u32x4*>(q + from * C + c0 + c);
+  const int64_t c0 = (int64_t)blockIdx.x * kCodeCols;
+  const int tr = (tid % 8) * 8, tc = tid / 8;   // this thread's rows and word column when writing
+  for (int64_t r0 = (int64_t)blockIdx.y * kCodeRows; r0 < ld; r0 += (int64_t)gridDim.y * kCodeRows) {
+    const int r = tid / 8, c = (tid % 8) * 16;
+    u32x4 v[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(&tile[r][c + 4 * e]) = v[e];
-      if (tid < kT) {
-        const int64_t at = source_row(r0 + tid, R, kPaired);
-        s_lds[tid] = scale == nullptr ? 1.0f : at >= 0 ? scale[at] : 0.0f;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const int64_t from = source_row(r0 + i * 32 + r, R, kPaired);
+      v[i] = from >= 0 && c0 + c < C ? *reinterpret_cast<const u32x4*>(q + from * C + c0 + c) : u32x4{0, 0, 0, 0};
     }
-    __syncthreads();
+    if (scale != nullptr && tid < kCodeRows) {
+      const int64_t at = source_row(r0 + tid, R, kPaired);
+      s_lds[tid] = at >= 0 ? scale[at] : 0.0f;
+    }
 #pragma unroll
-    for (int it = 0; it < kT * kT / 8 / kThreads; ++it) {
-      const int id = it * kThreads + tid, c = id / 8, r = (id % 8) * 8;
-      if (c0 + c < C && r0 + r < ld) {
-        u32x4 w;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[i * 32 + r][c / 4 + e] = v[i][e];
+    __syncthreads();
+    if (c0 + tc * 4 < C && r0 + tr < ld) {
+      uint32_t w[8];
+      float s[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[k] = tile[tr + k][tc];
+        s[k] = scale != nullptr ? s_lds[tr + k] : 1.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          w[e] = pack2((float)tile[r + 2 * e][c] * s_lds[r + 2 * e],
-                       (float)tile[r + 2 * e + 1][c] * s_lds[r + 2 * e + 1]);
-        *reinterpret_cast<u32x4*>(out + (c0 + c) * ld + r0 + r) = w;
+          o[e] = pack2((float)(int8_t)(w[2 * e] >> (8 * j)) * s[2 * e],
+                       (float)(int8_t)(w[2 * e + 1] >> (8 * j)) * s[2 * e + 1]);
+        *reinterpret_cast<u32x4*>(out + (c0 + tc * 4 + j) * ld + r0 + tr) = o;
       }
     }
     __syncthreads();
@@ -82,11 +111,10 @@ __global__ __launch_bounds__(kThreads) void transpose_codes_kernel(
 }
 
 // One workgroup: 64 columns, `span` rows (a multiple of 64).  out may be
-// null (sums only), sums may be null.  C may be any size: `vec` says that
-// rows are 16-byte aligned.
+// null (sums only), sums may be null.
 __global__ __launch_bounds__(kThreads) void transpose_bf16_kernel(
     const uint16_t* __restrict__ x, uint16_t* __restrict__ out, float* __restrict__ sums, int64_t R,
-    int64_t C, int64_t ld, int64_t Rpad, int span, int vec) {
+    int64_t C, int64_t ld, int64_t Rpad, int span) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[kT][kT + 2];
   __shared__ float part[kThreads / 8][kT];   // 32 row groups of each column
   const int tid = threadIdx.x;
@@ -100,16 +128,7 @@ __global__ __launch_bounds__(kThreads) void transpose_bf16_kernel(
     for (int it = 0; it < 2; ++it) {
       const int r = it * 32 + tid / 8, c = (tid % 8) * 8;
       u32x4 v = u32x4{0, 0, 0, 0};
-      if (r0 + r < R) {
-        const uint16_t* row = x + (r0 + r) * C + c0 + c;
-        if (vec) {
-          if (c0 + c < C) v = *reinterpret_cast<const u32x4*>(row);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c0 + c + e < C) v[e / 2] |= (uint32_t)row[e] << (16 * (e % 2));
-        }
-      }
+      if (r0 + r < R) v = load8(x + (r0 + r) * C, c0 + c, C);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         acc[2 * e] += bf(v[e] & 0xffffu);
@@ -151,28 +170,36 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t* __re
   const int64_t per_row = ld / 8, n = R * per_row;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
     const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-    u32x4 v = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < C) v[e / 2] |= (uint32_t)x[r * C + c + e] << (16 * (e % 2));
-    *reinterpret_cast<u32x4*>(out + r * ld + c) = v;
+    *reinterpret_cast<u32x4*>(out + r * ld + c) = load8(x + r * C, c, C);
   }
 }
 
-// 64 columns per workgroup, 4 groups of rows, joined in a fixed order.
-__global__ __launch_bounds__(kThreads) void sum_rows_kernel(const float* __restrict__ part,
-                                                            uint16_t* __restrict__ out, int64_t P,
-                                                            int64_t C) {
-  __shared__ float s_lds[4][64];
-  const int g = threadIdx.x / 64, l = threadIdx.x % 64;
-  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+// 32 columns per workgroup, 32 groups of rows with eight loads in flight
+// each, joined in a fixed order.
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void sum_rows_kernel(const float* __restrict__ part,
+                                                               uint16_t* __restrict__ out, int64_t P,
+                                                               int64_t C) {
+  constexpr int kGroups = kSumThreads / 32;
+  __shared__ float s_lds[kGroups][33];
+  const int g = threadIdx.x / 32, l = threadIdx.x % 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + l;
   float s = 0.0f;
   if (c < C)
-    for (int64_t p = g; p < P; p += 4) s += part[p * C + c];
+    for (int64_t p = g; p < P; p += 8 * kGroups) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p + i * kGroups < P ? part[(p + i * kGroups) * C + c] : 0.0f;
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
   s_lds[g][l] = s;
   __syncthreads();
-  if (g == 0 && c < C)
-    out[c] = __builtin_bit_cast(uint16_t, (__bf16)((s_lds[0][l] + s_lds[1][l]) + (s_lds[2][l] + s_lds[3][l])));
+  if (g == 0 && c < C) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) t += s_lds[i][l];
+    out[c] = __builtin_bit_cast(uint16_t, (__bf16)t);
+  }
 }
 
 // A fill kernel rather than a memset, which a captured graph would record.
@@ -190,7 +217,8 @@ hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream) {
 
 hipError_t launch_transpose_codes(const int8_t* q, const float* scale, uint16_t* out, int64_t R,
                                   int64_t C, int64_t ld, bool paired, hipStream_t stream) {
-  const dim3 grid((unsigned)((C + kT - 1) / kT), (unsigned)std::min<int64_t>((ld + kT - 1) / kT, 65535));
+  const dim3 grid((unsigned)((C + kCodeCols - 1) / kCodeCols),
+                  (unsigned)std::min<int64_t>((ld + kCodeRows - 1) / kCodeRows, 65535));
   if (paired)
     hipLaunchKernelGGL((transpose_codes_kernel<true>), grid, dim3(kThreads), 0, stream, q, scale, out, R, C, ld);
   else
@@ -212,9 +240,8 @@ hipError_t launch_transpose_bf16(const uint16_t* x, uint16_t* out, float* sums, 
                                  int64_t ld, int64_t Rpad, hipStream_t stream) {
   const int64_t span = transpose_sum_span(R, C);
   const dim3 grid((unsigned)((C + kT - 1) / kT), (unsigned)((R + span - 1) / span));
-  const int vec = C % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   hipLaunchKernelGGL(transpose_bf16_kernel, grid, dim3(kThreads), 0, stream, x, out, sums, R, C, ld, Rpad,
-                     (int)span, vec);
+                     (int)span);
   return hipGetLastError();
 }
 
@@ -227,7 +254,7 @@ hipError_t launch_pad_rows(const uint16_t* x, uint16_t* out, int64_t R, int64_t 
 }
 
 hipError_t launch_sum_rows(const float* part, uint16_t* out, int64_t P, int64_t C, hipStream_t stream) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((C + 63) / 64)), dim3(kThreads), 0, stream, part, out,
+  hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((C + 31) / 32)), dim3(kSumThreads), 0, stream, part, out,
                      P, C);
   return hipGetLastError();
 }

@@ -48,7 +48,7 @@ struct DynamicPlan {
 DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated) {
   DynamicPlan p{};
   p.few = M <= w8a8::kFewTokens;
-  p.codes = !p.few || !w8a8::few_tokens_in_lds(M, K, gated);
+  p.codes = !p.few || !w8a8::few_tokens_in_lds(M, K);
   p.splits = 1;
   p.tile = -1;
   Pieces w;

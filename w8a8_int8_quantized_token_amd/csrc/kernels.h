@@ -126,7 +126,7 @@ hipError_t launch_sum_rows(const float* part, uint16_t* out, int64_t P, int64_t 
 // kFewTokens tokens, from bf16 x, or from codes and scales where those are
 // given (xq not null; needed where few_tokens_in_lds() says no).
 constexpr int64_t kFewTokens = 32;
-bool few_tokens_in_lds(int64_t M, int64_t K, bool gated);
+bool few_tokens_in_lds(int64_t M, int64_t K);
 hipError_t launch_few_tokens(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq,
                              const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                              int64_t K, int act, bool gated, hipStream_t stream);

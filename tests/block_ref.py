@@ -102,3 +102,12 @@ def check(got, ref, slack, what, rms_steps=1.0):
     over = (err - bound).max() if err.numel() else torch.tensor(0.0)
     assert float(over) <= 0, (what, float(over), float(err.max()))
     assert rms(err) <= rms_steps * BF16_HALF_STEP * rms(ref) + 1e-30, (what, rms(err), rms(ref))
+
+
+def norm_rope_any(x, w, cos, sin, eps):
+    """norm_rope with halves paired, written with differentiable operations."""
+    rot = 2 * cos.shape[1]
+    n = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w.to(F64)
+    c, s = cos.to(F64)[:, None], sin.to(F64)[:, None]
+    a, b = n[..., :rot // 2], n[..., rot // 2:rot]
+    return torch.cat([a * c - b * s, b * c + a * s, n[..., rot:]], -1)

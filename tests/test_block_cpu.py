@@ -186,3 +186,19 @@ def test_norm_rope_gradient_formula(interleaved):
     dx, dw, _ = ref.norm_rope_grad(dy, x, w, a.cos(), a.sin(), 1e-3, interleaved)
     assert torch.allclose(differences(loss, x), dx, rtol=1e-6, atol=1e-8)
     assert torch.allclose(differences(loss, w), dw, rtol=1e-6, atol=1e-8)
+
+
+def test_module_construction_checks(w8):
+    lin = w8.W8A8Linear(torch.zeros(96, 32, dtype=torch.int8), torch.zeros(96), None)
+    with pytest.raises(ValueError):
+        w8.W8A8QKV(lin, 5, 3)                                    # 96 rows are not 11 heads
+    assert w8.W8A8QKV(lin, 2, 2).heads == (2, 2, 16)
+    with pytest.raises(ValueError):
+        w8.W8A8GatedMLP(torch.zeros(64, 32, dtype=torch.int8), torch.zeros(64), None, lin, "silu")
+    down = w8.W8A8Linear(torch.zeros(32, 48, dtype=torch.int8), torch.zeros(32), None)
+    with pytest.raises(ValueError):
+        w8.W8A8GatedMLP(lin.wq, lin.w_scale, None, down, "tanh")
+    m = w8.W8A8GatedMLP(lin.wq, lin.w_scale, None, down)
+    with pytest.raises(TypeError):
+        m(torch.zeros(2, 32))                                    # bf16 activations only
+    assert set(m.state_dict()) == {"wq", "w_scale", "down.wq", "down.w_scale"}

@@ -280,15 +280,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float 
 
 
 def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6,
-                          interleaved: bool = False, weights: bool = True, workspace=None):
+                          interleaved: bool = False, weights: bool = True, workspace=None, q_grad=None, k_grad=None):
     """Gradients of ``qk_norm_rope`` for the outputs' gradients dq [M,Hq,D],
     dk [M,Hk,D] (bf16, any row and head strides): (gradient of q, of k,
-    bf16; of q_weight, of k_weight, fp32 [D], None without ``weights``)."""
+    bf16, new tensors unless given as q_grad, k_grad; of q_weight, of k_weight,
+    fp32 [D], None without ``weights``)."""
     vq, vk, ptrs, sizes, dev = _rope_args(q, k, q_weight, k_weight, cos, sin, positions)
     M, _, Hq, Hk, D, _ = sizes
     vdq, vdk = _heads(dq, q.shape, "dq", dev), _heads(dk, k.shape, "dk", dev)
-    gq, vgq = _out_heads(None, q.shape, "", dev)
-    gk, vgk = _out_heads(None, k.shape, "", dev)
+    gq, vgq = _out_heads(q_grad, q.shape, "q_grad", dev)
+    gk, vgk = _out_heads(k_grad, k.shape, "k_grad", dev)
     gqw = gkw = None
     need = 0
     if weights:

@@ -280,10 +280,10 @@ w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int
 /*
  * The linear from bf16 activations: w8a8_quantize_act and w8a8_linear (or
  * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  For
- * at most 32 tokens whose codes fit a compute unit's LDS it is one launch that
- * reads the weight once and needs no workspace; otherwise the codes are made
- * in the workspace first (then the few-token kernel, the K-split or the tiled
- * kernel, by shape).
+ * at most 16 tokens whose codes take at most 22 KB (one token of K = 22272,
+ * five of 4096) it is one launch that reads the weight once and needs no
+ * workspace; otherwise the codes are made in the workspace first (then the
+ * few-token kernel up to 32 tokens, the K-split or the tiled kernel, by shape).
  *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;
  *   y bf16 [M,N] (16-byte aligned where w8a8_linear_splitk asks for it:
  *   W8A8_ERR_ALIGN otherwise); workspace of at least

@@ -203,3 +203,16 @@ def test_module_construction_checks(w8):
     with pytest.raises(TypeError):
         m(torch.zeros(2, 32))                                    # bf16 activations only
     assert set(m.state_dict()) == {"wq", "w_scale", "down.wq", "down.w_scale"}
+
+
+def test_native_calls_leave_everything_unusual_to_the_checks(w8):
+    from w8a8_int8_quantized_token_amd import _calls
+    x, wq, ws = torch.zeros(2, 32, dtype=BF), torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8)
+    q = torch.zeros(2, 2, 16, dtype=BF)
+    for args in ((x, wq, ws, None, 0, 1), (None, wq, ws, None, 0, 1), (x, wq, ws, None, 0), (x, wq, ws, None, "a", 1),
+                 (x, wq, ws, None, 2 ** 40, 1), (x[0], wq, ws, None, 0, 1), ()):
+        assert _calls.dynamic(*args) is None
+    assert _calls.backward(x, wq, ws, wq, ws, None, -1, True, True, True) is None
+    assert _calls.backward(x, wq, ws, wq, ws, None, -1, 1, True, True) is None
+    assert _calls.qk_norm_rope(q, q, None, None, ws, ws, None, "eps", False) is None
+    assert _calls.qk_norm_rope_backward(q, q, None, None, x, x, None, 1e-6, False, q, q, True) is None

@@ -393,3 +393,43 @@ def test_rope_beyond_4_gib(w8):
     assert same(back[0][rows], want_b[0]) and same(back[1][rows], want_b[1])
     w8.qk_norm_rope(q, k, None, None, a.cos(), a.sin(), q_out=q, k_out=k)
     assert same(q[rows], want[0]) and same(k[rows], want[1])
+
+
+def test_native_and_checked_calls_agree(w8):
+    """A plain call is one native step; with an output or workspace given the
+    same call goes through the binding's checks."""
+    from w8a8_int8_quantized_token_amd import _calls
+    g = torch.Generator().manual_seed(9)
+    M, N, K = 21, 40, 64
+    wq, ws = [t.to(DEV) for t in ref.codes_of(torch.randn(2 * N, K, generator=g).to(BF))]
+    xq, xs = [t.to(DEV) for t in ref.codes_of(torch.randn(M, K, generator=g).to(BF))]
+    x, dy = torch.randn(M, K, generator=g).to(BF).to(DEV), torch.randn(M, N, generator=g).to(BF).to(DEV)
+    b = torch.randn(2 * N, generator=g).to(BF).to(DEV)
+    room = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    for act in ("silu", "gelu"):
+        assert _calls.dynamic(x, wq, ws, b, {"silu": 0, "gelu": 1}[act], 2) is not None
+        assert same(w8.gated_linear_dynamic(x, wq, ws, b, act=act),
+                    w8.gated_linear_dynamic(x, wq, ws, b, act=act, workspace=room))
+        assert equal_all(w8.gated_linear_backward(dy, xq, xs, wq, ws, b, act=act),
+                         w8.gated_linear_backward(dy, xq, xs, wq, ws, b, act=act, workspace=room))
+    for gelu in (False, True):
+        assert same(w8.linear_dynamic(x, wq, ws, b, gelu=gelu), w8.linear_dynamic(x, wq, ws, b, gelu=gelu, workspace=room))
+    dy2 = torch.cat([dy, dy], 1)
+    assert _calls.backward(dy2, xq, xs, wq, ws, None, -1, True, True, True) is not None
+    assert equal_all(w8.linear_backward(dy2, xq, xs, wq, ws), w8.linear_backward(dy2, xq, xs, wq, ws, workspace=room))
+    q, k = torch.randn(M, 4, 32, generator=g).to(BF).to(DEV), torch.randn(M, 2, 32, generator=g).to(BF).to(DEV)
+    a = torch.rand(M, 16, generator=g).to(DEV)
+    w = torch.ones(32, dtype=BF, device=DEV)
+    for inter in (False, True):
+        args = (q, k, w, None, a.cos(), a.sin(), None, 1e-6, inter)
+        assert _calls.qk_norm_rope(*args) is not None
+        assert equal_all(w8.qk_norm_rope(*args), w8.qk_norm_rope(*args, q_out=torch.empty_like(q)))
+        assert equal_all(w8.qk_norm_rope_backward(q, k, *args), w8.qk_norm_rope_backward(q, k, *args, workspace=room))
+    # refused alike
+    for bad in (lambda **o: w8.linear_dynamic(x, wq, ws[1:], None, **o), lambda **o: w8.linear_dynamic(x[:, :24], wq, ws, **o),
+                lambda **o: w8.linear_backward(dy2, xq, xs[1:], wq, ws, **o)):
+        for o in ({}, {"workspace": room}):
+            with pytest.raises(ValueError):
+                bad(**o)
+    with pytest.raises(w8.W8A8Error):
+        w8.linear_dynamic(x[:, :24].contiguous(), wq[:, :24].contiguous(), ws)      # K not a multiple of 16

@@ -6,11 +6,17 @@ As in ``ops``: argument checks, output allocation with torch and the call on
 the current stream of the tensors' device.  Tensors of one call are on one
 device (it need not be the current one).  Workspaces are allocated per call
 from torch's caching allocator, on the call's stream, unless given.
+
+A plain call (no output or workspace given, every argument as it should be, the
+tensors on the current device) is made in one native step by ``_calls``, which
+gives None, with nothing launched, where it is not one; the code here then
+makes the call or names what is wrong.
 """
 from __future__ import annotations
 
 import torch
 
+from . import _calls
 from ._lib import check, lib
 
 ACTS = {"silu": 0, "gelu": 1}
@@ -130,6 +136,10 @@ def _dynamic(fn, workspace_fn, x, wq, w_scale, bias, y, per, act, workspace):
 def linear_dynamic(x, wq, w_scale, bias=None, y=None, gelu: bool = False, workspace=None):
     """bf16 x [M,K] -> bf16 y [M,N]: ``quantize_act`` and ``linear`` in one
     call, the same bits; one launch for a few tokens."""
+    if y is None and workspace is None:
+        out = _calls.dynamic(x, wq, w_scale, bias, 1 if gelu else 0, 1)
+        if out is not None:
+            return out
     return _dynamic(lib.w8a8_linear_dynamic, lib.w8a8_linear_dynamic_workspace, x, wq, w_scale, bias, y, 1,
                     int(bool(gelu)), workspace)
 
@@ -137,6 +147,10 @@ def linear_dynamic(x, wq, w_scale, bias=None, y=None, gelu: bool = False, worksp
 def gated_linear_dynamic(x, wq, w_scale, bias=None, y=None, act: str = "silu", workspace=None):
     """bf16 x [M,K] -> bf16 y [M,N]: ``quantize_act`` and ``gated_linear`` in
     one call, the same bits; one launch for a few tokens."""
+    if y is None and workspace is None:
+        out = _calls.dynamic(x, wq, w_scale, bias, _act(act), 2)
+        if out is not None:
+            return out
     return _dynamic(lib.w8a8_gated_linear_dynamic, lib.w8a8_gated_linear_dynamic_workspace, x, wq, w_scale, bias,
                     y, 2, _act(act), workspace)
 
@@ -173,6 +187,10 @@ def linear_backward(dy, xq, x_scale, wq, w_scale, dx: bool = True, dw: bool = Tr
     """Gradients of ``linear`` (without GELU) for dy bf16 [M,N], the rounding
     to codes passed straight through: (dx bf16 [M,K], dw bf16 [N,K], dbias bf16
     [N]), None where not asked for.  xq and x_scale may be None without dw."""
+    if workspace is None:
+        grads = _calls.backward(dy, xq, x_scale, wq, w_scale, None, -1, dx, dw, dbias)
+        if grads is not None:
+            return grads
     pdy, M, N, dev = _matrix(dy, torch.bfloat16, "dy")
     K = _rows(wq, "wq")[1]
     pw = _on(wq, torch.int8, (N, K), "wq", dev)
@@ -195,6 +213,10 @@ def gated_linear_backward(dy, xq, x_scale, wq, w_scale, bias=None, act: str = "s
     passed straight through: (dx bf16 [M,K], dw bf16 [2N,K], dbias bf16 [2N]),
     None where not asked for."""
     a = _act(act)
+    if workspace is None:
+        grads = _calls.backward(dy, xq, x_scale, wq, w_scale, bias, a, dx, dw, dbias)
+        if grads is not None:
+            return grads
     pdy, M, N, dev = _matrix(dy, torch.bfloat16, "dy")
     K = _rows(wq, "wq")[1]
     pw = _on(wq, torch.int8, (2 * N, K), "wq", dev)
@@ -272,6 +294,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float 
     position (int32 [M]; None: row mod P).  q_weight, k_weight: bf16 [D] or
     None.  Returns (q_out, k_out), new dense tensors unless given; they may be
     q and k themselves.  Rows at a position outside [0, P) become zeros."""
+    if q_out is None and k_out is None:
+        out = _calls.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        if out is not None:
+            return out
     vq, vk, ptrs, sizes, dev = _rope_args(q, k, q_weight, k_weight, cos, sin, positions)
     q_out, vqo = _out_heads(q_out, q.shape, "q_out", dev)
     k_out, vko = _out_heads(k_out, k.shape, "k_out", dev)
@@ -285,6 +311,11 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, cos, sin, positions=
     dk [M,Hk,D] (bf16, any row and head strides): (gradient of q, of k,
     bf16, new tensors unless given as q_grad, k_grad; of q_weight, of k_weight,
     fp32 [D], None without ``weights``)."""
+    if workspace is None and q_grad is None and k_grad is None:
+        grads = _calls.qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, dq, dk,
+                                             weights)
+        if grads is not None:
+            return grads
     vq, vk, ptrs, sizes, dev = _rope_args(q, k, q_weight, k_weight, cos, sin, positions)
     M, _, Hq, Hk, D, _ = sizes
     vdq, vdk = _heads(dq, q.shape, "dq", dev), _heads(dk, k.shape, "dk", dev)

@@ -1,4 +1,5 @@
-"""Build libw8a8.so (HIP, gfx950) in-tree with hipcc.
+"""Build libw8a8.so (HIP, gfx950) and _calls.so (the binding's native calls,
+host code against torch's headers) in-tree with hipcc and g++.
 
 Usage: python w8a8_int8_quantized_token_amd/build.py
 """
@@ -8,12 +9,14 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw8a8.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["quantize_rows.hip", "dequantize_rows.hip", "gemm_i8.hip", "splitk_reduce.hip",
            "mfma_ceiling.hip", "w8a8_api.hip", "gemm_gated.hip", "gemm_gated_grad.hip", "gemm_bf16.hip",
            "transpose.hip", "few_tokens.hip", "qk_norm_rope.hip", "block_api.hip"]
@@ -40,16 +43,46 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(OBJ, exist_ok=True)
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
+def _run(cmd: list[str], what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+
+def _calls_object() -> str:
+    """The native calls, compiled (they need only torch's headers)."""
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(OBJ, "torch_calls.o")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-I{p}" for p in cpp_extension.include_paths()], f"-I{sysconfig.get_paths()['include']}",
+          f"-I{rocm}/include", "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj], "g++ for torch_calls.cpp")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    libs = [p for p in cpp_extension.library_paths() if os.path.basename(p) == "lib"]
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    _run(["g++", "-shared", "-o", tmp, obj, *[f"-L{p}" for p in libs], f"-L{PKG}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+          "-ltorch_hip", "-ltorch_python", "-l:libw8a8.so", "-Wl,-rpath,$ORIGIN"], "link of _calls.so")
+    os.replace(tmp, CALLS)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(OBJ, exist_ok=True)
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(_calls_object)
+        objs = list(ex.map(_compile, SOURCES))
+    tmp = LIB + ".tmp%d" % os.getpid()
+    # (the soname is what _calls.so looks for beside itself)
+    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libw8a8.so", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB)
+    _link_calls(calls.result())
     if verbose:
         print(LIB)
     return LIB

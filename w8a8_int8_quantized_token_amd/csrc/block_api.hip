@@ -97,14 +97,16 @@ w8a8_status dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, c
 // ---- backward products ----
 
 // Workspace of a backward pass: the padded copy of dy where it is needed, the
-// sums for the bias, a gated gradient's first operands (made in one launch),
-// and then what the input's gradient and the weight's need, which are made
-// one after the other in the same space.
+// sums for the bias, and for the input's and the weight's gradient their first
+// operands (where not dy itself), their second ones, and the slices of a
+// product that is split along its sum.
 struct BackPlan {
   int64_t ldy;                // row length of the copy of dy
   int64_t ld, mp;             // summed lengths of the two products, padded
-  int64_t copy, first, second, wt, xt, slices_x, slices_w;
-  int64_t sums, sum_rows;
+  int64_t copy, sums, sum_rows;
+  int64_t first, wt, slices_x;
+  int64_t second, xt, slices_w;
+  int ranges_x, ranges_w;
   int64_t bytes;
 };
 BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy) {
@@ -120,20 +122,43 @@ BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw
     p.sums = w.add(4 * p.sum_rows * cols);
   }
   if (copy_dy && (gated || dx)) p.copy = w.add(2 * M * p.ldy);
-  if (gated && dx) p.first = w.add(2 * M * p.ld);
-  if (gated && dw) p.second = w.add(2 * cols * p.mp);
-  Pieces a = w, b = w;
   if (dx) {
-    p.wt = a.add(2 * K * p.ld);
-    p.slices_x = a.add(w8a8::gemm_bf16_slices(M, K, p.ld));
+    if (gated) p.first = w.add(2 * M * p.ld);
+    p.wt = w.add(2 * K * p.ld);
+    p.ranges_x = w8a8::gemm_bf16_slices(M, K, p.ld);
+    if (p.ranges_x > 1) p.slices_x = w.add(4 * M * K * p.ranges_x);
   }
   if (dw) {
-    if (!gated) p.second = b.add(2 * cols * p.mp);
-    p.xt = b.add(2 * K * p.mp);
-    p.slices_w = b.add(w8a8::gemm_bf16_slices(cols, K, p.mp));
+    p.second = w.add(2 * cols * p.mp);
+    p.xt = w.add(2 * K * p.mp);
+    p.ranges_w = w8a8::gemm_bf16_slices(cols, K, p.mp);
+    if (p.ranges_w > 1) p.slices_w = w.add(4 * cols * K * p.ranges_w);
   }
-  p.bytes = std::max(a.bytes, b.bytes);
+  p.bytes = w.bytes;
   return p;
+}
+
+// The products of a backward pass and what comes after them: dx [M,K] from
+// first [M,ld] and wt [K,ld], dw [cols,K] from second [cols,mp] and xt [K,mp],
+// dbias [cols] from the sums.
+hipError_t products(const BackPlan& p, void* ws, const uint16_t* first, uint16_t* dx, uint16_t* dw, uint16_t* dbias,
+                    int64_t M, int64_t cols, int64_t K, hipStream_t stream) {
+  w8a8::JoinJob jobs[w8a8::kMaxJobs];
+  int n = 0;
+  hipError_t e = hipSuccess;
+  if (dx) {
+    // the join writes 16 bytes at a time
+    float* slices = p.ranges_x > 1 && aligned(dx, 16) ? at<float>(ws, p.slices_x) : nullptr;
+    e = w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.wt), dx, slices, M, K, p.ld, stream);
+    if (slices) jobs[n++] = {slices, dx, p.ranges_x, M * K, true, 0};
+  }
+  if (dw && e == hipSuccess) {
+    float* slices = p.ranges_w > 1 && aligned(dw, 16) ? at<float>(ws, p.slices_w) : nullptr;
+    e = w8a8::launch_gemm_bf16(at<uint16_t>(ws, p.second), at<uint16_t>(ws, p.xt), dw, slices, cols, K, p.mp, stream);
+    if (slices) jobs[n++] = {slices, dw, p.ranges_w, cols * K, true, 0};
+  }
+  if (dbias) jobs[n++] = {at<float>(ws, p.sums), dbias, p.sum_rows, cols, false, 0};
+  return e == hipSuccess && n > 0 ? w8a8::launch_finish(jobs, n, stream) : e;
 }
 
 // dw and dbias of no tokens are zeros.
@@ -262,29 +287,24 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
   const BackPlan p = back_plan(M, N, K, false, dx, dw, dbias, copy);
   st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;
+  if (!dx && !dw && !dbias) return W8A8_OK;
+  using Job = w8a8::LayoutJob;
+  Job jobs[w8a8::kMaxJobs];
+  int n = 0;
+  const uint16_t* first = dy;
   if (dx) {
-    uint16_t* wt = at<uint16_t>(workspace, p.wt);
-    const uint16_t* first = dy;
     if (copy) {
-      uint16_t* padded = at<uint16_t>(workspace, p.copy);
-      TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ldy, stream));
-      first = padded;
+      jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(workspace, p.copy), nullptr, M, N, p.ldy, 0};
+      first = at<uint16_t>(workspace, p.copy);
     }
-    TRY(w8a8::launch_transpose_codes(wq, w_scale, wt, N, K, p.ld, false, stream));
-    TRY(w8a8::launch_gemm_bf16(first, wt, dx, at<float>(workspace, p.slices_x), M, K, p.ld, stream));
+    jobs[n++] = {Job::kTurnCodes, wq, w_scale, at<uint16_t>(workspace, p.wt), nullptr, N, K, p.ld, 0};
   }
-  if (dw || dbias) {
-    uint16_t* dyt = dw ? at<uint16_t>(workspace, p.second) : nullptr;
-    float* sums = dbias ? at<float>(workspace, p.sums) : nullptr;
-    TRY(w8a8::launch_transpose_bf16(dy, dyt, sums, M, N, p.mp, p.mp, stream));
-    if (dw) {
-      uint16_t* xt = at<uint16_t>(workspace, p.xt);
-      TRY(w8a8::launch_transpose_codes(xq, x_scale, xt, M, K, p.mp, false, stream));
-      TRY(w8a8::launch_gemm_bf16(dyt, xt, dw, at<float>(workspace, p.slices_w), N, K, p.mp, stream));
-    }
-    if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, N, stream));
-  }
-  return W8A8_OK;
+  if (dw || dbias)
+    jobs[n++] = {Job::kTurnValues, dy, nullptr, dw ? at<uint16_t>(workspace, p.second) : nullptr,
+                 dbias ? at<float>(workspace, p.sums) : nullptr, M, N, p.mp, w8a8::transpose_sum_span(M, N)};
+  if (dw) jobs[n++] = {Job::kTurnCodes, xq, x_scale, at<uint16_t>(workspace, p.xt), nullptr, M, K, p.mp, 0};
+  TRY(w8a8::launch_prepare(jobs, n, stream));
+  return launched(products(p, workspace, first, dx, dw, dbias, M, N, K, stream));
 }
 
 size_t w8a8_gated_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
@@ -308,25 +328,19 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, con
   uint16_t* first = dx ? at<uint16_t>(workspace, p.first) : nullptr;
   uint16_t* second = dw ? at<uint16_t>(workspace, p.second) : nullptr;
   float* sums = dbias ? at<float>(workspace, p.sums) : nullptr;
+  using Job = w8a8::LayoutJob;
+  Job jobs[w8a8::kMaxJobs];
+  int n = 0;
   if (copy) {
-    uint16_t* padded = at<uint16_t>(workspace, p.copy);
-    TRY(w8a8::launch_pad_rows(dy, padded, M, N, p.ldy, stream));
-    dy = padded;
+    jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(workspace, p.copy), nullptr, M, N, p.ldy, 0};
+    dy = at<uint16_t>(workspace, p.copy);
   }
+  if (dx) jobs[n++] = {Job::kTurnPaired, wq, nullptr, at<uint16_t>(workspace, p.wt), nullptr, 2 * N, K, p.ld, 0};
+  if (dw) jobs[n++] = {Job::kTurnCodes, xq, nullptr, at<uint16_t>(workspace, p.xt), nullptr, M, K, p.mp, 0};
+  if (n > 0) TRY(w8a8::launch_prepare(jobs, n, stream));
   TRY(w8a8::launch_gated_grad(static_cast<GateAct>(act), dy, p.ldy, xq, x_scale, wq, w_scale, bias, first, p.ld,
                               second, p.mp, sums, M, N, K, stream));
-  if (dx) {
-    uint16_t* wt = at<uint16_t>(workspace, p.wt);
-    TRY(w8a8::launch_transpose_codes(wq, nullptr, wt, 2 * N, K, p.ld, true, stream));
-    TRY(w8a8::launch_gemm_bf16(first, wt, dx, at<float>(workspace, p.slices_x), M, K, p.ld, stream));
-  }
-  if (dw) {
-    uint16_t* xt = at<uint16_t>(workspace, p.xt);
-    TRY(w8a8::launch_transpose_codes(xq, nullptr, xt, M, K, p.mp, false, stream));
-    TRY(w8a8::launch_gemm_bf16(second, xt, dw, at<float>(workspace, p.slices_w), 2 * N, K, p.mp, stream));
-  }
-  if (dbias) TRY(w8a8::launch_sum_rows(sums, dbias, p.sum_rows, 2 * N, stream));
-  return W8A8_OK;
+  return launched(products(p, workspace, first, dx, dw, dbias, M, 2 * N, K, stream));
 }
 
 w8a8_status w8a8_qk_norm_rope(const uint16_t* q, int64_t q_row, int64_t q_head, const uint16_t* k, int64_t k_row,

@@ -6,29 +6,11 @@
 //
 // Few output tiles and a long sum (an input's gradient over few tokens) leave
 // compute units idle, so K is then cut into ranges whose fp32 sums go to
-// slices of a workspace and are joined, in order, by a second kernel.
+// slices of a workspace and are joined, in order, by a later launch.
 #include "gemm_kernel.h"
 
 namespace w8a8 {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// Eight outputs of a row per thread; N % 8 == 0.
-__global__ __launch_bounds__(256) void join_slices_kernel(const f32x4* __restrict__ part, int chunks, int64_t slice,
-                                                          u32x4* __restrict__ out, int64_t groups) {
-  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < groups; g += (int64_t)gridDim.x * 256) {
-    f32x4 lo = f32x4{0, 0, 0, 0}, hi = lo;
-    for (int c = 0; c < chunks; ++c) {
-      const f32x4* p = part + (c * slice + g * 8) / 4;
-      lo += __builtin_nontemporal_load(p);
-      hi += __builtin_nontemporal_load(p + 1);
-    }
-    const float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    const u32x2 a = pack4_bf16(f), b = pack4_bf16(f + 4);
-    out[g] = u32x4{a[0], a[1], b[0], b[1]};
-  }
-}
 
 // Tile and number of K ranges, by a model of the time in us, fitted to
 // measurements on MI355X of every tile with 1 to 8 ranges at 22 shapes from
@@ -53,6 +35,9 @@ struct Choice {
   int cfg, chunks;
 };
 
+// Bytes of a range: whole 128-byte stages (chunks ranges, or one fewer).
+int64_t range_bytes(int64_t kb, int chunks) { return (kb + 128 * chunks - 1) / (128 * chunks) * 128; }
+
 double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   const TileDesc& d = kCfgs[cfg];
   const Cost& c = kCost[cfg];
@@ -64,7 +49,7 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
                         : items <= kCUs ? 1.0
                         : items <= kCUs * resident ? 1.0 + (tiles / kCUs - 1.0) * 0.75
                                                    : tiles / kCUs;
-  const int64_t range = (kb + 128 * chunks - 1) / (128 * chunks) * 128;
+  const int64_t range = range_bytes(kb, chunks);
   const int64_t stages = ((range + d.block_k - 1) / d.block_k + c.ring - 1) / c.ring * c.ring;
   // 128 operations per output and 128 bytes of K
   const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
@@ -72,7 +57,7 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   return chunks > 1 ? us + 1.8 + (double)chunks * (double)M * (double)N * 1.6e-6 : us;
 }
 
-Choice choose(int64_t M, int64_t N, int64_t kb) {
+Choice cheapest(int64_t M, int64_t N, int64_t kb) {
   Choice best{kWhole256, 1};
   double us = cost_us(best.cfg, 1, M, N, kb);
   for (int cfg = 0; cfg < kNumCfg; ++cfg)
@@ -84,40 +69,46 @@ Choice choose(int64_t M, int64_t N, int64_t kb) {
   return best;
 }
 
-}  // namespace
-
-hipError_t launch_gemm_bf16_cfg(int cfg, int chunks, const uint16_t* a, const uint16_t* b, uint16_t* out,
-                                float* part, int64_t M, int64_t N, int64_t Kpad, hipStream_t stream) {
-  const int64_t kb = 2 * Kpad;   // bytes per row
-  const int8_t *pa = reinterpret_cast<const int8_t*>(a), *pb = reinterpret_cast<const int8_t*>(b);
-  if (chunks <= 1) {
-    const KSplit whole{(int)kb, 1, 0};
-    return launch_cfg<OpB16, Epilogue::kBf16Plain>(cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, N,
-                                                   stream, whole);
-  }
-  // ranges of whole stages
-  const int64_t range = (kb + 128 * chunks - 1) / (128 * chunks) * 128;
-  const KSplit ks{(int)kb, (int)((kb + range - 1) / range), M * N};
-  const hipError_t e = launch_cfg<OpB16, Epilogue::kRawI32>(cfg, {pa, pb, nullptr, nullptr, nullptr, part, {}}, M, N,
-                                                            range, N, stream, ks);
-  if (e != hipSuccess) return e;
-  const int64_t groups = M * N / 8;
-  hipLaunchKernelGGL(join_slices_kernel, dim3((unsigned)std::min<int64_t>((groups + 255) / 256, 256 * 16)), dim3(256),
-                     0, stream, reinterpret_cast<const f32x4*>(part), ks.chunks, M * N,
-                     reinterpret_cast<u32x4*>(out), groups);
-  return hipGetLastError();
+// The model takes about a microsecond, and a backward pass asks three times
+// for each of its products (workspace size, layout, launch): the last shapes'
+// choices are kept per thread.
+Choice choose(int64_t M, int64_t N, int64_t kb) {
+  struct Entry {
+    int64_t M, N, kb;
+    Choice c;
+  };
+  thread_local Entry last[4] = {};
+  thread_local unsigned next = 0;
+  for (const Entry& e : last)
+    if (e.M == M && e.N == N && e.kb == kb) return e.c;
+  Entry& e = last[next++ % 4];
+  e = {M, N, kb, cheapest(M, N, kb)};
+  return e.c;
 }
 
-int64_t gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad) {
-  const Choice c = choose(M, N, 2 * Kpad);
-  return c.chunks > 1 ? 4 * M * N * c.chunks : 0;
+}  // namespace
+
+int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad) {
+  const int64_t kb = 2 * Kpad;
+  const int64_t range = range_bytes(kb, choose(M, N, kb).chunks);
+  return (int)((kb + range - 1) / range);
 }
 
 hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, float* slices, int64_t M,
                             int64_t N, int64_t Kpad, hipStream_t stream) {
-  Choice c = choose(M, N, 2 * Kpad);
-  if (reinterpret_cast<uintptr_t>(out) % 16 != 0) c.chunks = 1;   // the join writes 16 bytes at a time
-  return launch_gemm_bf16_cfg(c.cfg, c.chunks, a, b, out, slices, M, N, Kpad, stream);
+  const int64_t kb = 2 * Kpad;   // bytes per row
+  const int8_t *pa = reinterpret_cast<const int8_t*>(a), *pb = reinterpret_cast<const int8_t*>(b);
+  const Choice c = choose(M, N, kb);
+  const int64_t range = range_bytes(kb, c.chunks);
+  const int ranges = (int)((kb + range - 1) / range);
+  if (ranges == 1 || slices == nullptr) {
+    const KSplit whole{(int)kb, 1, 0};
+    return launch_cfg<OpB16, Epilogue::kBf16Plain>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, N,
+                                                   stream, whole);
+  }
+  const KSplit ks{(int)kb, ranges, M * N};
+  return launch_cfg<OpB16, Epilogue::kRawI32>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, slices, {}}, M, N, range, N,
+                                              stream, ks);
 }
 
 }  // namespace w8a8

@@ -105,22 +105,36 @@ hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, int64_t ld_dy, con
                              int64_t N, int64_t K, hipStream_t stream);
 
 // out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; N and Kpad
-// multiples of 8, rows 16-byte aligned; slices: gemm_bf16_slices() bytes of
-// workspace, 16-byte aligned.
-int64_t gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad);
+// multiples of 8, rows 16-byte aligned.  The sum is cut into gemm_bf16_slices()
+// ranges; where they are more than one, their fp32 sums go to slices [ranges,
+// M, N] for a JoinJob (out must then be 16-byte aligned) and out is not
+// written; with slices null the product is made whole.
+int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad);
 hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, float* slices, int64_t M,
                             int64_t N, int64_t Kpad, hipStream_t stream);
 
-// Operand layout of the backward products (see transpose.hip).
-hipError_t launch_transpose_codes(const int8_t* q, const float* scale, uint16_t* out, int64_t R,
-                                  int64_t C, int64_t ld, bool paired, hipStream_t stream);
-int64_t transpose_sum_span(int64_t R, int64_t C);   // rows of one block of sums
-hipError_t launch_transpose_bf16(const uint16_t* x, uint16_t* out, float* sums, int64_t R, int64_t C,
-                                 int64_t ld, int64_t Rpad, hipStream_t stream);
-hipError_t launch_pad_rows(const uint16_t* x, uint16_t* out, int64_t R, int64_t C, int64_t ld,
-                           hipStream_t stream);
+// Operand layout of the backward products and the joins after them (see
+// backward_layout.hip): one launch each for up to kMaxJobs jobs.
+constexpr int kMaxJobs = 4;
+struct LayoutJob {
+  enum Kind { kTurnCodes, kTurnPaired, kTurnValues, kPadRows } kind;
+  const void* in;        // [R,C]: int8 codes or bf16 values
+  const float* scale;    // codes: [R] or null
+  uint16_t* out;         // [C,ld] (kPadRows: [R,ld])
+  float* sums;           // kTurnValues: [ceil(R / span), C] or null
+  int64_t R, C, ld, span;
+};
+struct JoinJob {
+  const float* part;     // [P, n]
+  uint16_t* out;         // [n]
+  int64_t P, n;
+  bool slices;           // few long rows (a product's slices, n % 8 == 0), or many short ones
+  int64_t blocks;        // set by the launch
+};
+int64_t transpose_sum_span(int64_t R, int64_t C);   // kTurnValues' rows of one block of sums
+hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream);
+hipError_t launch_finish(const JoinJob* jobs, int n, hipStream_t stream);
 hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream);   // 16-bit zeros
-hipError_t launch_sum_rows(const float* part, uint16_t* out, int64_t P, int64_t C, hipStream_t stream);
 
 // The linear (act: 0 none, 1 GELU) or gated pair (act: a GateAct) for at most
 // kFewTokens tokens, from bf16 x, or from codes and scales where those are

@@ -285,8 +285,7 @@ w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int
  * workspace; otherwise the codes are made in the workspace first (then the
  * few-token kernel up to 32 tokens, the K-split or the tiled kernel, by shape).
  *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;
- *   y bf16 [M,N] (16-byte aligned where w8a8_linear_splitk asks for it:
- *   W8A8_ERR_ALIGN otherwise); workspace of at least
+ *   y bf16 [M,N] 2-byte aligned; workspace of at least
  *   w8a8_linear_dynamic_workspace(M, N, K) bytes, 16-byte aligned (may be
  *   NULL where that is 0).  The workspace belongs to the call until its work
  *   on the stream is done: calls that may overlap need one each.
@@ -342,8 +341,8 @@ w8a8_status w8a8_gated_linear_dynamic(const uint16_t *x, const int8_t *wq, const
  *   dg = dy * u * act'(g),  du = dy * act(g)   (fp32; for the products rounded
  *   to bf16 once, with the scale of the other operand, whose codes are exact).
  * Without tokens (M = 0) dw and dbias are set to zeros.
- * Limits: N (gated: 2N, each half rounded up to 8) at most 2^21 for dx, M at
- * most 2^21 for dw (W8A8_ERR_SHAPE).  dy, bias and outputs 2-byte aligned
+ * Limits (W8A8_ERR_SHAPE): N at most 2^21 for dx, gated N at most 2^20 for any
+ * output, M at most 2^21 for dw.  dy, bias and outputs 2-byte aligned
  * (16-byte aligned dy with N % 8 == 0 avoids a copy).  The workspace as above.
  */
 size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias);

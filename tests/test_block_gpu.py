@@ -321,3 +321,28 @@ def test_rope_of_zero_rows_and_zero_vectors(w8):
     assert e[0].shape == (0, 2, 64)
     b = w8.qk_norm_rope_backward(e[0], e[1], q[:0], k[:0], qw, kw, cos, sin)
     assert not b[2].any() and not b[3].any()
+
+
+def test_rope_of_queries_or_keys_alone(w8):
+    q, k, (qw, kw), cos, sin, _ = rope_inputs(9, 9, 4, 2, 64, 64, 6)
+    none = q[:, :0]
+    both = w8.qk_norm_rope(q, k, qw, kw, cos, sin)
+    one = w8.qk_norm_rope(q, none, qw, None, cos, sin)
+    other = w8.qk_norm_rope(none, k, None, kw, cos, sin)
+    assert torch.equal(bits(one[0]), bits(both[0])) and one[1].shape == (9, 0, 64)
+    assert torch.equal(bits(other[1]), bits(both[1]))
+    g = w8.qk_norm_rope_backward(q, k, q, k, qw, kw, cos, sin)
+    g1 = w8.qk_norm_rope_backward(q, none, q, none, qw, None, cos, sin)
+    g2 = w8.qk_norm_rope_backward(none, k, none, k, None, kw, cos, sin)
+    assert torch.equal(bits(g1[0]), bits(g[0])) and torch.equal(bits(g2[1]), bits(g[1]))
+    assert not g1[3].any() and not g2[2].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 256, 4096), (40, 64, 128), (300, 136, 64), (5, 24, 64)])
+def test_outputs_at_odd_addresses(w8, M, N, K):
+    g = gen(M)
+    wq, ws, b = dev(*weights(2 * N, K, g, True))
+    x = torch.randn(M, K, generator=g).to(BF).to(DEV)
+    for f, n in ((w8.linear_dynamic, 2 * N), (w8.gated_linear_dynamic, N)):
+        room = torch.empty(M * n + 1, dtype=BF, device=DEV)
+        assert torch.equal(bits(f(x, wq, ws, b, y=room[1:].view(M, n))), bits(f(x, wq, ws, b)))

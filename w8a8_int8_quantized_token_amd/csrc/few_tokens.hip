@@ -7,12 +7,12 @@
 // Bound by reading the weight once (N*K bytes; the activations come from L2),
 // below about 20 MB by the launch and the way through one group.  A workgroup
 // of eight wavefronts takes 16 output channels (gated: 16 gate and the 16 up
-// rows) at a time, each wavefront every eighth 256-byte piece of K.  A piece
+// rows) at a time, each wavefront every eighth 128-byte piece of K.  A piece
 // of 16 rows goes straight to the wavefront's own LDS ring (buffer_load ...
-// lds, one to three pieces ahead, no barriers): a request then reads 256-byte
-// runs of four rows, and the workgroup 2 KB runs, where loads straight into
+// lds, one to five pieces ahead, no barriers): a request then reads 128-byte
+// runs of eight rows, and the workgroup 1 KB runs, where loads straight into
 // the MFMA's register layout read 64-byte runs of sixteen rows (a plain read
-// of 96 MB: 5.8 TB/s against 4.9).  16-byte chunks are XOR swizzled by row on
+// of 96 MB: 5.4 TB/s against 4.9).  16-byte chunks are XOR swizzled by row on
 // the way in, so the fragment reads do not conflict.  The product is
 // v_mfma_i32_16x16x64_i8 with weight rows as the first operand and the tokens'
 // codes as the second; the partial sums of the wavefronts are exact int32 and
@@ -44,7 +44,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kWave = 64;
 constexpr int kRows = 16;            // output channels of a group
-constexpr int kPiece = 256;          // bytes of K of a piece
+constexpr int kPiece = 128;          // bytes of K of a piece
 constexpr int kPieceBytes = kRows * kPiece;
 constexpr int kCodeBytes = 22 * 1024;
 constexpr uint32_t kOOB = 0x80000000u;    // buffer offset past any range: reads as zeros
@@ -62,13 +62,13 @@ struct Few {
   static constexpr int NW = kGate ? 2 : 1;                 // weight rows per channel
   static constexpr int NV = NW * MT;                       // accumulators
   static constexpr int kTiles = NW + (kCodes ? MT : 0);    // 16-row tiles of a piece
-  static constexpr int kDma = 4 * kTiles;                  // requests per piece
-  // Eight wavefronts where LDS allows (their pieces make 2 KB runs of a row: a
-  // plain read of 96 MB in that order 5.8 TB/s, with four wavefronts 5.1).
-  static constexpr int kWaves = kTiles <= 2 ? 8 : 4;
+  static constexpr int kDma = kPieceBytes / 1024 * kTiles; // requests per piece
+  // (their pieces make 1 KB runs of a row: a plain read of 96 MB in that order
+  // 5.4 TB/s, with four wavefronts 4.8)
+  static constexpr int kWaves = 8;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kSlotBytes = kWaves * kTiles * kPieceBytes;
-  static constexpr int kSlots = kTiles == 1 ? 4 : kTiles == 3 ? 3 : 2;
+  static constexpr int kSlots = kTiles == 1 ? 6 : kTiles == 2 ? 4 : kTiles == 3 ? 3 : 2;   // as LDS allows
   static constexpr int kAhead = kThreads / (kRows * NW);   // groups whose scales are in LDS
   static constexpr int kLds = kSlots * kSlotBytes + (kCodes ? 0 : kCodeBytes) + 12 * kThreads + 64;
   static_assert(kCodes || MT == 1, "codes in LDS are one tile of tokens");
@@ -118,7 +118,13 @@ __device__ __forceinline__ v4i lds_read16(uint32_t a) {
   asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(r) : "v"(a) : "memory");
   return r;
 }
-// 16 bytes at each of four addresses
+// 16 bytes at each of two and of four addresses
+__device__ __forceinline__ void lds_read16x2(uint32_t a0, uint32_t a1, v4i* r) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(r[0]), "=&v"(r[1])
+               : "v"(a0), "v"(a1)
+               : "memory");
+}
 __device__ __forceinline__ void lds_read16x4(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, v4i* r) {
   asm volatile(
       "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
@@ -128,15 +134,19 @@ __device__ __forceinline__ void lds_read16x4(uint32_t a0, uint32_t a1, uint32_t 
       : "memory");
 }
 
-// Sixteen rows of a piece at K byte k0 into LDS: request i brings rows 4i ..
-// 4i+3.  Lane p = 16 h + l16 fills chunk l16 of row 4i + h with that row's
-// chunk l16 ^ (4i + h); chunks at or past K and rows past the range are zeros.
+// Where 16-byte chunk c of row r of a piece lies in LDS: rows of 128 bytes,
+// so that reads of one chunk of 16 rows fill all 256 bytes of banks.
+__device__ __forceinline__ int swizzled(int r, int c) { return c ^ ((r >> 1) & 7); }
+
+// Sixteen rows of a piece at K byte k0 into LDS: request i brings rows 8i ..
+// 8i+7.  Lane p fills chunk p % 8 of row 8i + p / 8 with the chunk of that row
+// that belongs there; chunks at or past K and rows past the range are zeros.
 // kAux 2: non-temporal (the weight is read once).
 template <int kAux>
-__device__ __forceinline__ void request_tile(__amdgpu_buffer_rsrc_t r, int8_t* lds, int k0, int K, int l16, int h) {
+__device__ __forceinline__ void request_tile(__amdgpu_buffer_rsrc_t r, int8_t* lds, int k0, int K, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * i + h, k = k0 + (l16 ^ row) * 16;
+  for (int i = 0; i < kPieceBytes / 1024; ++i) {
+    const int row = 8 * i + lane / 8, k = k0 + swizzled(row, lane % 8) * 16;
     const uint32_t o = k < K ? (uint32_t)(row * K + k) : kOOB;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + i * 1024), 16, (int)o, 0, 0, kAux);
   }
@@ -144,6 +154,23 @@ __device__ __forceinline__ void request_tile(__amdgpu_buffer_rsrc_t r, int8_t* l
 
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t o) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+}
+
+// Maximum over the wavefront by DPP exchanges (a tenth of the latency of six
+// trips through LDS): within fours, eights, sixteens, then across rows.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t wave_max_dpp(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
+  v = max(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
+  v = max(v, dpp<0x141>(v));   // row_half_mirror
+  v = max(v, dpp<0x140>(v));   // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
 // kCodes: the codes and scales come from memory (xq, sx); otherwise from x.
@@ -158,7 +185,7 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
   __shared__ __attribute__((aligned(16))) int8_t codes[kCodes ? 16 : kCodeBytes];
   __shared__ float sx_lds[kThreads];
   __shared__ __attribute__((aligned(16))) float s_lds[kThreads], b_lds[kThreads];
-  __shared__ uint32_t amax_lds[kWaves];
+  __shared__ __attribute__((aligned(16))) uint32_t amax_lds[8];
 
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -168,25 +195,36 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
   const int mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // groups of this workgroup
   const int items = mine * per;
 
-  // Requests of item t: piece wave + 4 * (t mod per) of group t / per.
+  // Requests of the next item into a slot: the wavefront's pieces of each of
+  // the workgroup's groups in turn, then nothing (zeros).
+  int r_left = per, r_piece = wave;
+  int64_t r_n0 = (int64_t)blockIdx.x * kRows;
+  int r_items = items;
   int8_t* const my_ring = ring + wave * (F::kTiles * kPieceBytes);
-  auto request = [&](int t, int slot) {
-    const int gi = t / per, piece = wave + kWaves * (t - gi * per);
-    const int64_t n0 = ((int64_t)blockIdx.x + (int64_t)gi * gridDim.x) * kRows;
-    const bool there = t < items;
+  auto request = [&](int slot) {
+    const bool there = r_items > 0;
+    const int64_t n0 = r_n0;
+    const int piece = r_piece;
     const int rows = there ? (int)min((int64_t)kRows, N - n0) : 0;
+    --r_items;
+    r_piece += kWaves;
+    if (--r_left == 0) {
+      r_left = per;
+      r_piece = wave;
+      r_n0 += (int64_t)gridDim.x * kRows;
+    }
     int8_t* dst = my_ring + slot * F::kSlotBytes;
     auto range = [&](const int8_t* from, int bytes) {
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(from), (short)0, bytes, kRsrcWord3);
     };
 #pragma unroll
     for (int i = 0; i < NW; ++i)
-      request_tile<2>(range(W + (there ? (n0 + i * N) * K : 0), rows * K), dst + i * kPieceBytes, piece * kPiece, K, l16, h);
+      request_tile<2>(range(W + (there ? (n0 + i * N) * K : 0), rows * K), dst + i * kPieceBytes, piece * kPiece, K, lane);
     if constexpr (kCodes) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         request_tile<0>(range(xq + (int64_t)m * 16 * K, there ? min(16, M - m * 16) * K : 0),
-                        dst + (NW + m) * kPieceBytes, piece * kPiece, K, l16, h);
+                        dst + (NW + m) * kPieceBytes, piece * kPiece, K, lane);
     }
   };
   // Channel scales and biases of kAhead groups from gi on, into LDS: a load at
@@ -224,7 +262,7 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
   const uint32_t first_bias = bias_or[n_first];
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int s = 0; s + 1 < S; ++s) request(s, s);
+  for (int s = 0; s + 1 < S; ++s) request(s);
   __builtin_amdgcn_sched_barrier(0);
   lds_write(lds_address(s_lds + tid), __float_as_uint(first_scale));
   lds_write(lds_address(b_lds + tid), bias != nullptr ? first_bias << 16 : 0u);
@@ -246,13 +284,17 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx = absmax_bits(mx, z[e]);
       }
-      mx = wave_max(max(mx & 0xffffu, mx >> 16));
+      mx = wave_max_dpp(max(mx & 0xffffu, mx >> 16));
       if (P > 1) {
         // every wavefront comes here exactly once (those of a fourth token
         // slot with three tokens below)
         if (lane == 0) lds_write(lds_address(amax_lds + wave), mx);
         barrier();
-        for (int q = 0; q < P; ++q) mx = max(mx, lds_read_word(lds_address(amax_lds + wave / P * P + q)));
+        v4i all[2];
+        lds_read16x2(lds_address(amax_lds), lds_address(amax_lds + 4), all);
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q)
+          if (q / P == wave / P) mx = max(mx, (uint32_t)all[q / 4][q % 4]);
       }
       const RowScale rs = row_scale<false>(mx);
       const uint32_t row = lds_address(codes) + (uint32_t)(m * row_bytes);
@@ -350,20 +392,20 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
 
   int left = per;      // pieces of the current group still to come
   int gi = 0, slot = 0;
-  uint32_t chunk[4];   // this lane's four fragments of a 16-row tile
+  uint32_t chunk[2];   // this lane's fragments of a 16-row tile
 #pragma unroll
-  for (int k = 0; k < 4; ++k) chunk[k] = lds_address(my_ring) + (uint32_t)(l16 * kPiece + ((4 * k + h) ^ l16) * 16);
+  for (int k = 0; k < 2; ++k) chunk[k] = lds_address(my_ring) + (uint32_t)(l16 * kPiece + swizzled(l16, 4 * k + h) * 16);
   for (int t = 0; t < items; ++t) {
     // the slot read one item ago takes the piece S - 1 items ahead (past the
     // end: zeros, which keeps the count below)
-    request(t + S - 1, slot == 0 ? S - 1 : slot - 1);
+    request(slot == 0 ? S - 1 : slot - 1);
     wait_vmcnt<(S - 1) * F::kDma>();   // item t has landed
     const uint32_t base = (uint32_t)(slot * F::kSlotBytes);
     auto read = [&](int tile, v4i* f) {
       const uint32_t o = base + (uint32_t)(tile * kPieceBytes);
-      lds_read16x4(chunk[0] + o, chunk[1] + o, chunk[2] + o, chunk[3] + o, f);
+      lds_read16x2(chunk[0] + o, chunk[1] + o, f);
     };
-    v4i w[NW][4], c[MT][4];
+    v4i w[NW][2], c[MT][2];
 #pragma unroll
     for (int i = 0; i < NW; ++i) read(i, w[i]);
     if constexpr (kCodes) {
@@ -372,10 +414,10 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
     } else {
       const int at = min(wave + kWaves * (per - left), pieces - 1) * kPiece;
       const uint32_t a = lds_address(codes) + (uint32_t)(min(l16, M - 1) * (int)code_row(K) + at + h * 16);
-      lds_read16x4(a, a + 64, a + 128, a + 192, c[0]);
+      lds_read16x2(a, a + 64, c[0]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll

@@ -12,23 +12,52 @@
 namespace w8a8 {
 namespace {
 
+// Tiles: the int8 product's large ones, and small ones with 128-byte stages
+// (64 values; the int8 ones have 64-byte stages, whose barrier every 256
+// cycles of MFMAs cost these a third: 777 x 1168 x 4608 on 64x64 tiles 31 us
+// with 64-byte stages, 20 with 128).
+using Cfg128s2 = Tile<128, 128, 128, 2, 2, 2>;
+using Cfg128s4 = Tile<128, 128, 128, 2, 2, 4>;
+using Cfg64s3 = Tile<64, 64, 128, 2, 2, 3>;
+using Cfg64x128 = Tile<64, 128, 128, 2, 2, 3>;
+using Cfg128x64 = Tile<128, 64, 128, 2, 2, 3>;
+enum BfCfg { kBf256, kBfWhole256, kBf192, kBf128x256, kBf128s2, kBf128s4, kBf64, kBf64x128, kBf128x64, kNumBf };
+const TileDesc kBfTiles[kNumBf] = {desc<CfgSplit>(), desc<CfgWhole>(), desc<Cfg192>(), desc<CfgTail>(), desc<Cfg128s2>(),
+                                   desc<Cfg128s4>(), desc<Cfg64s3>(), desc<Cfg64x128>(), desc<Cfg128x64>()};
+
+template <Epilogue EPI>
+hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, hipStream_t s, KSplit ks) {
+  switch (cfg) {
+    case kBf256: return launch_t<CfgSplit, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBfWhole256: return launch_t<CfgWhole, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf192: return launch_t<Cfg192, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf128x256: return launch_t<CfgTail, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf128s2: return launch_t<Cfg128s2, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf128s4: return launch_t<Cfg128s4, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf64: return launch_t<Cfg64s3, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf64x128: return launch_t<Cfg64x128, OpB16, EPI>(o, M, N, K, N, s, ks);
+    default: return launch_t<Cfg128x64, OpB16, EPI>(o, M, N, K, N, s, ks);
+  }
+}
+
 // Tile and number of K ranges, by a model of the time in us, fitted to
-// measurements on MI355X of every tile with 1 to 8 ranges at 22 shapes from
-// 16 x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was the fastest, or
-// within 12% of it, at each; 2% in the mean):
-//   4 + rounds * (tile + stages * max(stage, power)) + join,
+// measurements on MI355X of every tile with 1 to 8 ranges at 35 shapes from 16
+// x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 8% of the
+// fastest at each, 1% in the mean):
+//   3.6 + rounds * (tile + stages * max(stage, power)) + join,
 // stage the time of 128 K bytes of a tile alone on its compute unit, power
 // the same when `rate` TFLOP/s is what the whole chip's power limit allows.
-// Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 106 us whole,
-// 70 in ranges; 777 x 1168 x 4608: 32 us whole, 25 in three; but 4096 x 4096
-// x 4096: 110 us whole, 162 in two.
+// Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 76 us whole,
+// 70 in ranges; 512 x 4096 x 8192: 52 us whole, 47 in four; but 4096 x 4096 x
+// 4096: 112 us whole, 162 in two.
 struct Cost {
   double tile_us, stage_us, rate;
-  int ring;
+  int ring, resident;   // stages of the ring; workgroups per compute unit (kResident)
 };
-constexpr Cost kCost[kNumCfg] = {{2.0, 1.12, 1330, 6}, {2.2, 1.28, 1425, 2}, {2.6, 0.88, 1570, 6},
-                                 {3.4, 0.56, 1250, 3}, {2.4, 0.79, 1140, 3}, {0.3, 0.45, 800, 4},
-                                 {0.2, 0.24, 450, 3}};
+constexpr Cost kCost[kNumBf] = {
+    {2.32, 1.114, 1379, 6, 1}, {1.70, 1.442, 4327, 2, 1}, {1.79, 0.932, 1475, 6, 1},
+    {2.04, 0.676, 1255, 3, 1}, {0.14, 0.633, 2515, 2, 2}, {1.25, 0.372, 995, 4, 1},
+    {0.12, 0.187, 592, 3, 3},  {0.15, 0.255, 724, 3, 2},  {0.38, 0.247, 752, 3, 2}};
 constexpr int64_t kMaxSlices = int64_t(1) << 29;   // bytes of workspace a split may take
 
 struct Choice {
@@ -39,28 +68,27 @@ struct Choice {
 int64_t range_bytes(int64_t kb, int chunks) { return (kb + 128 * chunks - 1) / (128 * chunks) * 128; }
 
 double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
-  const TileDesc& d = kCfgs[cfg];
+  const TileDesc& d = kBfTiles[cfg];
   const Cost& c = kCost[cfg];
-  const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * chunks;
-  const double tiles = (double)items;
-  const int resident = cfg == k64 ? 3 : cfg == k128 ? 2 : 1;   // as kResident
-  // tiles that share a compute unit overlap by about a quarter
-  const double rounds = resident == 1 ? (double)((items + kCUs - 1) / kCUs)
-                        : items <= kCUs ? 1.0
-                        : items <= kCUs * resident ? 1.0 + (tiles / kCUs - 1.0) * 0.75
-                                                   : tiles / kCUs;
-  const int64_t range = range_bytes(kb, chunks);
-  const int64_t stages = ((range + d.block_k - 1) / d.block_k + c.ring - 1) / c.ring * c.ring;
+  const int64_t range = range_bytes(kb, chunks), ranges = (kb + range - 1) / range;
+  const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * ranges;
+  const int64_t stages = (range / 128 + c.ring - 1) / c.ring * c.ring;
+  // a tile more on a compute unit that has one costs 0.86 of it
+  const double r = c.resident, q = (double)items / kCUs;
+  const double rounds = c.resident == 1 ? (double)((items + kCUs - 1) / kCUs)
+                        : q <= 1.0      ? 1.0
+                        : q <= r        ? 1.0 + (q - 1.0) * 0.86
+                                        : q * (1.0 + (r - 1.0) * 0.86) / r;
   // 128 operations per output and 128 bytes of K
   const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
-  const double us = 4.0 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power) * d.block_k / 128.0);
-  return chunks > 1 ? us + 1.8 + (double)chunks * (double)M * (double)N * 1.6e-6 : us;
+  const double us = 3.6 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
+  return ranges > 1 ? us + 3.0 + (double)ranges * (double)M * (double)N * 1.6e-6 : us;
 }
 
 Choice cheapest(int64_t M, int64_t N, int64_t kb) {
-  Choice best{kWhole256, 1};
+  Choice best{kBfWhole256, 1};
   double us = cost_us(best.cfg, 1, M, N, kb);
-  for (int cfg = 0; cfg < kNumCfg; ++cfg)
+  for (int cfg = 0; cfg < kNumBf; ++cfg)
     for (const int chunks : {1, 2, 3, 4, 6, 8}) {
       if (chunks > 1 && (kb < 512 * chunks || M * N * 4 * chunks > kMaxSlices)) break;
       const double c = cost_us(cfg, chunks, M, N, kb);
@@ -103,12 +131,10 @@ hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out,
   const int ranges = (int)((kb + range - 1) / range);
   if (ranges == 1 || slices == nullptr) {
     const KSplit whole{(int)kb, 1, 0};
-    return launch_cfg<OpB16, Epilogue::kBf16Plain>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, N,
-                                                   stream, whole);
+    return launch_bf16<Epilogue::kBf16Plain>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, stream, whole);
   }
   const KSplit ks{(int)kb, ranges, M * N};
-  return launch_cfg<OpB16, Epilogue::kRawI32>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, slices, {}}, M, N, range, N,
-                                              stream, ks);
+  return launch_bf16<Epilogue::kRawI32>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, slices, {}}, M, N, range, stream, ks);
 }
 
 }  // namespace w8a8

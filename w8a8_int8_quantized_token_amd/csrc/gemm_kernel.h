@@ -362,7 +362,7 @@ constexpr int out_columns(int bn) { return kGated<EPI> ? bn / 2 : bn; }
 // have them for the gated and bf16 products, so that one workgroup's epilogue
 // and stage waits run under another's MFMAs.
 template <class T, Epilogue EPI, class Op>
-constexpr int kResident = (!kGated<EPI> && !Op::kBf16) ? 1 : T::kLdsBytes <= 40 * 1024 ? 3 : T::kLdsBytes <= 80 * 1024 ? 2 : 1;
+constexpr int kResident = (!kGated<EPI> && !Op::kBf16) ? 1 : std::min(160 * 1024 / T::kLdsBytes, 3);
 
 // Persistent kernel: gridDim.x workgroups (at most kResident per CU) walk the work
 // items t = blockIdx.x, blockIdx.x + gridDim.x, ... (output tile t mod

@@ -1,8 +1,9 @@
 // bf16 x bf16 -> fp32 product on the kernel of gemm_kernel.h (out[m,n] =
 // bf16(sum_k a[m,k] b[n,k]), both operands contiguous along k): the products
-// of the backward passes.  v_mfma_f32_32x32x16_bf16 takes 16 bytes per lane
+// of the backward passes.  v_mfma_f32_16x16x32_bf16 takes 16 bytes per lane
 // and operand, as the int8 MFMA does, so stages, swizzle, ring and schedule
-// are the int8 ones with K counted in bytes; only the MFMA differs.
+// are the int8 ones with K counted in bytes; the MFMA, its fragments and the
+// epilogue differ.
 //
 // Few output tiles and a long sum (an input's gradient over few tokens) leave
 // compute units idle, so K is then cut into ranges whose fp32 sums go to
@@ -42,22 +43,23 @@ hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, in
 
 // Tile and number of K ranges, by a model of the time in us, fitted to
 // measurements on MI355X of every tile with 1 to 8 ranges at 35 shapes from 16
-// x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 8% of the
+// x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 10% of the
 // fastest at each, 1% in the mean):
-//   3.6 + rounds * (tile + stages * max(stage, power)) + join,
+//   3.77 + rounds * (tile + stages * max(stage, power)) + join,
 // stage the time of 128 K bytes of a tile alone on its compute unit, power
 // the same when `rate` TFLOP/s is what the whole chip's power limit allows.
 // Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 76 us whole,
-// 70 in ranges; 512 x 4096 x 8192: 52 us whole, 47 in four; but 4096 x 4096 x
-// 4096: 112 us whole, 162 in two.
+// 72 in four; 512 x 4096 x 8192: 51 us whole, 46 in four; but 4096 x 4096 x
+// 4096: 105 us whole, 160 in two.  (Operands from HBM; on repeated ones 4096 x
+// 4096 x 4096 takes 96 us, 1.43 PFLOP/s, and 16384 x 2048 x 4096 188 us.)
 struct Cost {
   double tile_us, stage_us, rate;
   int ring, resident;   // stages of the ring; workgroups per compute unit (kResident)
 };
 constexpr Cost kCost[kNumBf] = {
-    {2.32, 1.114, 1379, 6, 1}, {1.70, 1.442, 4327, 2, 1}, {1.79, 0.932, 1475, 6, 1},
-    {2.04, 0.676, 1255, 3, 1}, {0.14, 0.633, 2515, 2, 2}, {1.25, 0.372, 995, 4, 1},
-    {0.12, 0.187, 592, 3, 3},  {0.15, 0.255, 724, 3, 2},  {0.38, 0.247, 752, 3, 2}};
+    {5.27, 1.202, 1538, 6, 1}, {2.05, 1.409, 2032, 2, 1}, {2.07, 0.895, 1547, 6, 1},
+    {2.33, 0.802, 1829, 3, 1}, {0.11, 0.660, 1833, 2, 2}, {1.51, 0.380, 1035, 4, 1},
+    {0.09, 0.183, 601, 3, 3},  {0.16, 0.251, 721, 3, 2},  {0.23, 0.273, 768, 3, 2}};
 constexpr int64_t kMaxSlices = int64_t(1) << 29;   // bytes of workspace a split may take
 
 struct Choice {
@@ -73,16 +75,16 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   const int64_t range = range_bytes(kb, chunks), ranges = (kb + range - 1) / range;
   const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * ranges;
   const int64_t stages = (range / 128 + c.ring - 1) / c.ring * c.ring;
-  // a tile more on a compute unit that has one costs 0.86 of it
+  // a tile more on a compute unit that has one costs 0.88 of it
   const double r = c.resident, q = (double)items / kCUs;
   const double rounds = c.resident == 1 ? (double)((items + kCUs - 1) / kCUs)
                         : q <= 1.0      ? 1.0
-                        : q <= r        ? 1.0 + (q - 1.0) * 0.86
-                                        : q * (1.0 + (r - 1.0) * 0.86) / r;
+                        : q <= r        ? 1.0 + (q - 1.0) * 0.883
+                                        : q * (1.0 + (r - 1.0) * 0.883) / r;
   // 128 operations per output and 128 bytes of K
   const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
-  const double us = 3.6 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
-  return ranges > 1 ? us + 3.0 + (double)ranges * (double)M * (double)N * 1.6e-6 : us;
+  const double us = 3.77 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
+  return ranges > 1 ? us + 3.11 + (double)ranges * (double)M * (double)N * 1.41e-6 : us;
 }
 
 Choice cheapest(int64_t M, int64_t N, int64_t kb) {

@@ -256,12 +256,19 @@ struct OpF8 {
   typedef v8i Frag;
   typedef v16f Acc;
 };
+// bf16: a 32x32 tile as four 16x16 ones.  The package's power limit sets the
+// rate of a long product, and v_mfma_f32_16x16x32_bf16 moves half as many
+// accumulators per multiplication as the 32x32x16 form: on normally
+// distributed operands a loop of nothing but fragment reads and MFMAs runs at
+// 1.83 PFLOP/s on it and 1.64 on the other (both 2.3 on zeros).
 struct OpB16 {
   static constexpr bool kF8 = false;
   static constexpr bool kBf16 = true;
-  static constexpr int kStepK = 32;
+  static constexpr int kStepK = 32;   // bytes of K per row that one of its steps uses (see `frag2`)
   typedef v4i Frag;
-  typedef v16f Acc;
+  struct Acc {
+    f32x4 q[2][2];   // [16 tokens][16 channels]
+  };
 };
 
 // Output tile `t` (0 <= t < tiles_m * tiles_n) -> (first row, first channel).
@@ -422,8 +429,9 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // stage requests (twice as many each); the other half only read fragments
   // and run MFMAs.  Measured on MI355X: the K loop runs about 4% faster than
   // with every wavefront issuing.  (The 256x256 tile has no registers for
-  // the doubled request count, nor has the fp8 tile with the raw epilogue.)
-  constexpr bool kHalfDma = T::kSplit && T::BN < 256 && EPI != Epilogue::kRawI32;
+  // the doubled request count, nor have the fp8 tile with the raw epilogue
+  // and the bf16 tile.)
+  constexpr bool kHalfDma = T::kSplit && T::BN < 256 && EPI != Epilogue::kRawI32 && !Op::kBf16;
   constexpr int kDmaWaves = kHalfDma ? T::kWaves / 2 : T::kWaves;
   constexpr int DXk = T::BM / T::kDmaRows / kDmaWaves;   // X requests per DMA wavefront and stage
   constexpr int DWk = T::BN / T::kDmaRows / kDmaWaves;   // W requests
@@ -561,8 +569,20 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // fp8 fragments are twice as wide and single buffered, which keeps the
   // 128 accumulators and both operands within 256 VGPRs.  In K step s lane
   // half h reads chunks (2s + h)*CPS ... + CPS-1 of its row.
+  //
+  // bf16: a 16x16x32 MFMA takes 64 bytes of K, so a step is half of the
+  // token rows over 64 bytes: steps 2s and 2s + 1 share the channels'
+  // fragments fa[s & 1], and each has its own tokens' fb.
   constexpr int NB = Op::kF8 ? 1 : 2;
-  typename Op::Frag fa[NB][T::FN], fb[NB][T::FM];
+  constexpr int FA = Op::kBf16 ? 2 * T::FN : T::FN;   // fragments of a step's channels
+  static_assert(!Op::kBf16 || KSUB == 4, "bf16 fragments alternate over whole stages");
+  typename Op::Frag fa[NB][FA], fb[NB][T::FM];
+  // bf16: the channel whose fragment row this lane reads, of 32, first half.
+  // A lane's result holds 4 consecutive rows of each 16x16 tile; the rows are
+  // dealt out so that those of two neighbouring tiles are 8 consecutive
+  // channels (a 16-byte store), and so that 16 lanes' reads still fall into
+  // 16 slots: tile 0 has channels 0-3, 8-11, 20-23, 28-31, tile 1 the others.
+  [[maybe_unused]] const int chan16 = ((lane % 16) / 4) * 8 + ((lane % 16) / 8) * 4 + lane % 4;
   auto read_frag = [&](const int8_t* base, int r, int c) {
     typename Op::Frag f;
     if constexpr (CPS == 1) {
@@ -575,12 +595,24 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     return f;
   };
   auto frag2 = [&](const int8_t* xs, const int8_t* ws, int s, int slot) {
-    slot %= NB;
-    const int c = (s * 2 + khalf) * CPS;
+    if constexpr (Op::kBf16) {
+      const int c = s / 2 * 4 + lane / 16;
+      if (s % 2 == 0) {
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) fa[slot][j] = read_frag(ws, wn * T::TN + j * 32 + row_in, c);
+        for (int j = 0; j < FA; ++j)
+          fa[s / 2 % 2][j] = read_frag(ws, wn * T::TN + j / 2 * 32 + (j % 2 ? chan16 ^ 4 : chan16), c);
+      }
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) fb[slot][i] = read_frag(xs, wm * T::TM + i * 32 + row_in, c);
+      for (int i = 0; i < T::FM; ++i)
+        fb[s % 2][i] = read_frag(xs, wm * T::TM + (s % 2 * T::FM + i) * 16 + lane % 16, c);
+    } else {
+      slot %= NB;
+      const int c = (s * 2 + khalf) * CPS;
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) fa[slot][j] = read_frag(ws, wn * T::TN + j * 32 + row_in, c);
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i) fb[slot][i] = read_frag(xs, wm * T::TM + i * 32 + row_in, c);
+    }
   };
   auto frag = [&](const int8_t* buf, int s, int slot) { frag2(buf, buf + T::BM * T::BK, s, slot); };
   // fragments from an A slot and a B slot of the split ring
@@ -588,21 +620,31 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     if constexpr (kWAhead) frag2(bs, as, s, slot);
     else frag2(as, bs, s, slot);
   };
-  auto mfmas = [&](int slot) {
-    slot %= NB;
+  // the MFMAs of K step s of a stage
+  auto mfmas = [&](int s) {
+    if constexpr (Op::kBf16) {
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i)
+      for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j) {
-        if constexpr (Op::kF8)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fa[slot][j], fb[slot][i], acc[i][j], 0, 0, 0, 127, 0, 127);
-        else if constexpr (Op::kBf16)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, fa[slot][j]), __builtin_bit_cast(bf16x8, fb[slot][i]), acc[i][j], 0, 0, 0);
-        else
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[slot][j], fb[slot][i], acc[i][j], 0, 0, 0);
-      }
+        for (int j = 0; j < FA; ++j) {
+          const int r = s % 2 * T::FM + i;   // row tile of 16 tokens
+          f32x4& c = acc[r / 2][j / 2].q[r % 2][j % 2];
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[s / 2 % 2][j]),
+                                                      __builtin_bit_cast(bf16x8, fb[s % 2][i]), c, 0, 0, 0);
+        }
+    } else {
+      const int slot = s % NB;
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+          if constexpr (Op::kF8)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                fa[slot][j], fb[slot][i], acc[i][j], 0, 0, 0, 127, 0, 127);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[slot][j], fb[slot][i], acc[i][j], 0, 0, 0);
+        }
+    }
   };
 
   // Scheduling of the code after a barrier: the next stage's first fragment
@@ -611,18 +653,19 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // A requesting wavefront places ceil(requests / MFMAs) stage requests
   // after each MFMA; one that makes no requests only orders its fragment
   // reads before its MFMAs.
+  constexpr int kMfma = Op::kBf16 ? 2 : 1;   // MFMAs per 32x32 tile and K step
   auto interleave = [&](auto role) {
-    __builtin_amdgcn_sched_group_barrier(0x100, (T::FM + T::FN) * CPS, 0);   // fragment reads
+    __builtin_amdgcn_sched_group_barrier(0x100, (T::FM + FA) * CPS, 0);   // fragment reads
     if constexpr (decltype(role)::value) {
       constexpr int kPer = (DXk + DWk + T::FM * T::FN - 1) / (T::FM * T::FN);
 #pragma unroll
       for (int q = 0; q < T::FM * T::FN; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // one MFMA
+        __builtin_amdgcn_sched_group_barrier(0x008, kMfma, 0);         // one tile's MFMAs
         __builtin_amdgcn_sched_group_barrier(0x002, 3 * kPer, 0);      // address VALU
         __builtin_amdgcn_sched_group_barrier(0x020, kPer, 0);          // DMAs
       }
     } else {
-      __builtin_amdgcn_sched_group_barrier(0x008, T::FM * T::FN, 0);   // the MFMAs
+      __builtin_amdgcn_sched_group_barrier(0x008, kMfma * T::FM * T::FN, 0);   // the MFMAs
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -649,7 +692,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // stage k+1 has landed (one barrier), request stage k+S into `cur` and
   // start reading stage k+1's first fragments under the MFMAs of the last K
   // step.  A stage is thus requested a full S-1 steps before it is needed.
-  auto step = [&](const TileAddr& a, int8_t* cur, int8_t* nxt, int k, auto interior) {
+  auto step = [&](const TileAddr& a, int8_t* cur, int8_t* nxt, int k, auto interior) __attribute__((always_inline)) {
     if constexpr (NB == 1) {
 #pragma unroll
       for (int s = 0; s + 1 < KSUB; ++s) {
@@ -671,7 +714,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     for (int s = 0; s + 1 < KSUB; ++s) {
       frag(cur, s + 1, (s + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
-      mfmas(s & 1);
+      mfmas(s);
       __builtin_amdgcn_sched_barrier(0);
     }
     wait_lgkmcnt0();                 // this wavefront's reads of `cur` are done
@@ -679,7 +722,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     barrier();                       // ... and everyone's
     frag(nxt, 0, KSUB & 1);
     issue(a, cur, k + T::S, interior);
-    mfmas((KSUB - 1) & 1);
+    mfmas(KSUB - 1);
     interleave(kDmaRole);
   };
 
@@ -763,10 +806,10 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       }
       mfmas(0);
       if constexpr (kDma && decltype(pend_in)::value) {
-        __builtin_amdgcn_sched_group_barrier(0x100, (T::FM + T::FN) * CPS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (T::FM + (Op::kBf16 ? 0 : T::FN)) * CPS, 0);
 #pragma unroll
         for (int q = 0; q < T::FM * T::FN; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, kMfma, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
           __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
@@ -777,7 +820,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     for (int s = 1; s + 1 < KSUB; ++s) {
       frag_ab(ac, bc, s + 1, (s + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
-      mfmas(s & 1);
+      mfmas(s);
       __builtin_amdgcn_sched_barrier(0);
     }
     wait_lgkmcnt0();
@@ -792,7 +835,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       issue_b(a, bc, k + 2, interior);
       if constexpr (!decltype(pend_out)::value) issue_a(a, ac, k + 3, interior);
     }
-    mfmas((KSUB - 1) & 1);
+    mfmas(KSUB - 1);
     interleave(role);
   };
 
@@ -894,7 +937,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       frag(ring[0], 0, 0);
       const int KTr = (KT + T::S - 1) / T::S * T::S;   // padding stages read as zeros
       // S steps of the ring; the requests they make reach stage kt + 2S - 1
-      auto round = [&](int kt, auto interior) {
+      auto round = [&](int kt, auto interior) __attribute__((always_inline)) {
         if constexpr (T::S == 2) {
           step(cur, lds0, lds1, kt, interior);
           step(cur, lds1, lds0, kt + 1, interior);
@@ -997,25 +1040,59 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       // channels nj + 8g + 4*khalf + 0..3
       uint32_t w[4][2];
       auto pack = [&](int i, int j) {
-        const typename Op::Acc& c = acc[i][j];
-        // the fp32 output value (GELU applied for the gelu epilogue)
-        auto val = [&](int e, float s_w, float b) {
-          if constexpr (!kScaled<EPI>) return (float)c[e];
-          const float y = dequant((float)c[e], sa[i], s_w, b);
-          if constexpr (EPI == Epilogue::kBf16GeluScaleBias) return gelu(y);
-          else return y;
-        };
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const bf16x2 lo = __builtin_convertvector(
-              (f32x2{val(g * 4, sv[g][0], bv[g][0]), val(g * 4 + 1, sv[g][1], bv[g][1])}), bf16x2);
-          const bf16x2 hi = __builtin_convertvector(
-              (f32x2{val(g * 4 + 2, sv[g][2], bv[g][2]), val(g * 4 + 3, sv[g][3], bv[g][3])}), bf16x2);
-          w[g][0] = __builtin_bit_cast(uint32_t, lo);
-          w[g][1] = __builtin_bit_cast(uint32_t, hi);
+        if constexpr (!Op::kBf16) {
+          const typename Op::Acc& c = acc[i][j];
+          // the fp32 output value (GELU applied for the gelu epilogue)
+          auto val = [&](int e, float s_w, float b) {
+            if constexpr (!kScaled<EPI>) return (float)c[e];
+            const float y = dequant((float)c[e], sa[i], s_w, b);
+            if constexpr (EPI == Epilogue::kBf16GeluScaleBias) return gelu(y);
+            else return y;
+          };
+  #pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const bf16x2 lo = __builtin_convertvector(
+                (f32x2{val(g * 4, sv[g][0], bv[g][0]), val(g * 4 + 1, sv[g][1], bv[g][1])}), bf16x2);
+            const bf16x2 hi = __builtin_convertvector(
+                (f32x2{val(g * 4 + 2, sv[g][2], bv[g][2]), val(g * 4 + 3, sv[g][3], bv[g][3])}), bf16x2);
+            w[g][0] = __builtin_bit_cast(uint32_t, lo);
+            w[g][1] = __builtin_bit_cast(uint32_t, hi);
+          }
         }
       };
-      if constexpr (kGateFwd<EPI>) {
+      if constexpr (Op::kBf16) {
+        // Lane: token lane % 16 of each 16, channels 8 (lane / 16) + 0..7 of
+        // each 32 (see chan16), so a store instruction writes 16 whole
+        // 64-byte row pieces with no trip through LDS.
+        const int e_t = e_lane % 16, e_q = e_lane / 16;
+#pragma unroll
+        for (int r = 0; r < 2 * T::FM; ++r) {
+          const int mi = wm * T::TM + r * 16 + e_t;   // row within the block's
+#pragma unroll
+          for (int j = 0; j < T::FN; ++j) {
+            const f32x4(&q)[2] = acc[r / 2][j].q[r % 2];
+            const float f0[4] = {q[0][0], q[0][1], q[0][2], q[0][3]}, f1[4] = {q[1][0], q[1][1], q[1][2], q[1][3]};
+            const u32x2 t0 = pack4_bf16(f0), t1 = pack4_bf16(f1);
+            const u32x2 lo = e_q < 2 ? t0 : t1, hi = e_q < 2 ? t1 : t0;
+            const v4i v = v4i{(int)lo[0], (int)lo[1], (int)hi[0], (int)hi[1]};
+            const int n = n0 + wn * T::TN + j * 32 + 8 * e_q;
+            if (vec_store) {
+              if constexpr (kCountedStores) {
+                uint32_t off = n < N ? ((uint32_t)mi * (uint32_t)ldy + (uint32_t)n) * 2u : kOOB;
+                asm volatile("" : "+v"(off));
+                __builtin_amdgcn_raw_buffer_store_b128(v, y_rsrc, off, 0, kStoreNT);
+              } else if (m0 + mi < M && n < N) {
+                *reinterpret_cast<v4i*>(reinterpret_cast<uint16_t*>(out) + (int64_t)(m0 + mi) * ldy + n) = v;
+              }
+            } else if (m0 + mi < M) {
+              uint16_t* yrow = reinterpret_cast<uint16_t*>(out) + (int64_t)(m0 + mi) * ldy;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (n + e < N) yrow[n + e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
+            }
+          }
+        }
+      } else if constexpr (kGateFwd<EPI>) {
         // Both values of a channel are in one lane: act(gate) * up of 8
         // channels per lane and tile, the halves of the wavefront exchanged
         // so that each lane stores 16 bytes (8 consecutive channels of its
@@ -1269,6 +1346,31 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           issue_b(nxt, lds3, 0, kChecked);
         }
       }
+      // 4 accumulators for channels n ... n + 3 of row `crow`
+      auto put4 = [&](auto* crow, int n, auto a4) {
+        if (vec_store && n + 3 < N) {
+          *reinterpret_cast<decltype(a4)*>(crow + n) = a4;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) crow[n + e] = a4[e];
+        }
+      };
+      if constexpr (Op::kBf16) {
+#pragma unroll
+        for (int r = 0; r < 2 * T::FM; ++r) {
+          const int m = m0 + wm * T::TM + r * 16 + lane % 16;
+          if (m >= M) continue;
+          float* crow = reinterpret_cast<float*>(out) + (int64_t)c0 * ks.out_stride + (int64_t)m * ldy;
+#pragma unroll
+          for (int j = 0; j < T::FN; ++j) {
+            const f32x4(&q)[2] = acc[r / 2][j].q[r % 2];
+            const int n = n0 + wn * T::TN + j * 32 + lane / 16 * 8;
+            put4(crow, n, lane < 32 ? q[0] : q[1]);
+            put4(crow, n + 4, lane < 32 ? q[1] : q[0]);
+          }
+        }
+      } else
 #pragma unroll
       for (int i = 0; i < T::FM; ++i) {
         const int m = m0 + wm * T::TM + i * 32 + row_in;
@@ -1283,16 +1385,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
             // reinterpreted: bit-casting single fp32 elements of the fp8 MFMA's
             // result miscompiles (every element is taken to equal element 0).
             const v16i av = __builtin_bit_cast(v16i, acc[i][j]);
-            int32_t a4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a4[e] = av[g * 4 + e];
-            if (vec_store && n + 3 < N) {
-              *reinterpret_cast<v4i*>(crow + n) = v4i{a4[0], a4[1], a4[2], a4[3]};
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (n + e < N) crow[n + e] = a4[e];
-            }
+            put4(crow, n, v4i{av[g * 4], av[g * 4 + 1], av[g * 4 + 2], av[g * 4 + 3]});
           }
         }
       }

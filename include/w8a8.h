@@ -343,7 +343,8 @@ w8a8_status w8a8_gated_linear_dynamic(const uint16_t *x, const int8_t *wq, const
  * Without tokens (M = 0) dw and dbias are set to zeros.
  * Limits (W8A8_ERR_SHAPE): N at most 2^21 for dx, gated N at most 2^20 for any
  * output, M at most 2^21 for dw.  dy, bias and outputs 2-byte aligned
- * (16-byte aligned dy with N % 8 == 0 avoids a copy).  The workspace as above.
+ * (dy is copied where it is not 16-byte aligned, N % 8 != 0, or a long product
+ * of N % 64 != 0 repays it).  The workspace as above.
  */
 size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias);
 w8a8_status w8a8_linear_backward(const uint16_t *dy, const int8_t *xq, const float *x_scale,

@@ -307,8 +307,9 @@ def test_given_workspaces(w8):
     torch.cuda.synchronize()
     assert bool((room[need:] == 0xA5).all())
     with pytest.raises(w8.W8A8Error):
-        # (the size allows for a copy of dy, which this aligned dy does not need)
-        w8.linear_backward(dy, xq, xs, wq, ws, workspace=room[:need - 2 * M * N - 512])
+        # (the size allows for a copy of dy and longer rows, which this aligned
+        # dy does not need: less than its operands' own bytes)
+        w8.linear_backward(dy, xq, xs, wq, ws, workspace=room[:2 * (N * K + M * N + M * K) - 16])
     need = w8.lib.w8a8_linear_dynamic_workspace(M, N, K)
     room.fill_(0xA5)
     y = w8.linear_dynamic(x, wq, ws, workspace=room[:need])

@@ -109,12 +109,25 @@ struct BackPlan {
   int ranges_x, ranges_w;
   int64_t bytes;
 };
+// Rows of an operand laid out here are whole 128-byte lines, zeros past their
+// end: rows that start inside a line cost the product a quarter of its time
+// (2000 x 2000 x 5000: 53 us with rows of 5000 values, 41 with 5056; 333 x
+// 2064 x 3000: 18.1 and 13.6).
+constexpr int64_t kLine = 64;
+// Rows of dy that start inside a line are copied too where the product is long
+// enough (dx alone, us without and with the copy; M x N x K): 4096 x 5000 x 512
+// 45 and 42, 777 x 5000 x 2048 51 and 37; but 4096 x 5000 x 256 31 and 37, 4096
+// x 1000 x 1024 20 and 22, 100 x 5000 x 1024 16 and 22.
+bool copy_lines(int64_t M, int64_t N, int64_t K) {
+  return N % kLine != 0 && M >= 256 && N >= 2048 && K >= 512;
+}
+
 BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy) {
   BackPlan p{};
   const int64_t cols = (gated ? 2 : 1) * N;
-  p.ldy = up(N, 8);
-  p.ld = gated ? 2 * up(N, 16) : p.ldy;
-  p.mp = up(M, 8);
+  p.ldy = gated ? up(N, 8) : copy_dy ? up(N, kLine) : N;
+  p.ld = gated ? up(2 * N, kLine) : p.ldy;
+  p.mp = up(M, kLine);
   Pieces w;
   if (db) {
     p.sum_rows = gated ? w8a8::gated_grad_sum_rows(M, N, K)
@@ -173,7 +186,7 @@ w8a8_status check_back(const uint16_t* dy, const int8_t* xq, const float* x_scal
                        const uint16_t* dbias, int64_t M, int64_t N, int64_t K, bool gated) {
   if (!shape_ok(M, N, K, gated ? 2 : 1)) return W8A8_ERR_SHAPE;
   // (a gated gradient's epilogue addresses a tile's rows of dy the same way)
-  if (((dx || gated) && (gated ? 2 * up(N, 16) : up(N, 8)) > kMaxSummed) || (dw && up(M, 8) > kMaxSummed))
+  if (((dx || gated) && (gated ? up(2 * N, kLine) : up(N, kLine)) > kMaxSummed) || (dw && up(M, kLine) > kMaxSummed))
     return W8A8_ERR_SHAPE;
   const bool codes = dw || (gated && (dx || dbias)), weight = dx || (gated && (dw || dbias));
   if (M > 0) {
@@ -274,7 +287,8 @@ w8a8_status w8a8_gated_linear_dynamic(const uint16_t* x, const int8_t* wq, const
 // Both sizes allow for the copy of dy that an odd N or address needs.
 size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
   if (!shape_ok(M, N, K, 1) || M == 0) return 0;
-  return (size_t)back_plan(M, N, K, false, dx, dw, dbias, true).bytes;
+  const int64_t with = back_plan(M, N, K, false, dx, dw, dbias, true).bytes;
+  return (size_t)(N % 8 ? with : std::max(with, back_plan(M, N, K, false, dx, dw, dbias, false).bytes));
 }
 
 w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
@@ -283,7 +297,7 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
   w8a8_status st = check_back(dy, xq, x_scale, wq, w_scale, nullptr, dx, dw, dbias, M, N, K, false);
   if (st != W8A8_OK) return st;
   if (M == 0) return no_tokens(dw, dbias, N, K, stream);
-  const bool copy = N % 8 != 0 || !aligned(dy, 16);
+  const bool copy = N % 8 != 0 || !aligned(dy, 16) || (dx && copy_lines(M, N, K));
   const BackPlan p = back_plan(M, N, K, false, dx, dw, dbias, copy);
   st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;

@@ -25,8 +25,8 @@
 // first, and they come through the ring beside the weight.
 //
 // Measured (cold weights, one call after another): 1 x 65536 x 4096 49 us, 5.5
-// TB/s; 1 x 12288 x 4096 15.0 us; gated 1 x 12288 x 4096 22.4 us, 4.5 TB/s; 16
-// x 12288 x 4096 15 us after 4.3 us for the codes.
+// TB/s; 1 x 12288 x 4096 14 us; gated 1 x 12288 x 4096 21 us, 4.8 TB/s; 16
+// x 12288 x 4096 14 us after 4 us for the codes.
 #include "epilogue.h"
 #include "kernels.h"
 #include "quant_codes.h"

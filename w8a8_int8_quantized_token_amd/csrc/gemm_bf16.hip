@@ -16,15 +16,17 @@ namespace {
 // Tiles: the int8 product's large ones, and small ones with 128-byte stages
 // (64 values; the int8 ones have 64-byte stages, whose barrier every 256
 // cycles of MFMAs cost these a third: 777 x 1168 x 4608 on 64x64 tiles 31 us
-// with 64-byte stages, 20 with 128).
+// with 64-byte stages, 20 with 128).  Four of them: the smallest tile's time is
+// its requests' latency over the stages in flight (three 20.7 us, four 17.9,
+// six 18.3).
 using Cfg128s2 = Tile<128, 128, 128, 2, 2, 2>;
 using Cfg128s4 = Tile<128, 128, 128, 2, 2, 4>;
-using Cfg64s3 = Tile<64, 64, 128, 2, 2, 3>;
+using Cfg64s4 = Tile<64, 64, 128, 2, 2, 4>;
 using Cfg64x128 = Tile<64, 128, 128, 2, 2, 3>;
 using Cfg128x64 = Tile<128, 64, 128, 2, 2, 3>;
 enum BfCfg { kBf256, kBfWhole256, kBf192, kBf128x256, kBf128s2, kBf128s4, kBf64, kBf64x128, kBf128x64, kNumBf };
 const TileDesc kBfTiles[kNumBf] = {desc<CfgSplit>(), desc<CfgWhole>(), desc<Cfg192>(), desc<CfgTail>(), desc<Cfg128s2>(),
-                                   desc<Cfg128s4>(), desc<Cfg64s3>(), desc<Cfg64x128>(), desc<Cfg128x64>()};
+                                   desc<Cfg128s4>(), desc<Cfg64s4>(), desc<Cfg64x128>(), desc<Cfg128x64>()};
 
 template <Epilogue EPI>
 hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, hipStream_t s, KSplit ks) {
@@ -35,21 +37,21 @@ hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, in
     case kBf128x256: return launch_t<CfgTail, OpB16, EPI>(o, M, N, K, N, s, ks);
     case kBf128s2: return launch_t<Cfg128s2, OpB16, EPI>(o, M, N, K, N, s, ks);
     case kBf128s4: return launch_t<Cfg128s4, OpB16, EPI>(o, M, N, K, N, s, ks);
-    case kBf64: return launch_t<Cfg64s3, OpB16, EPI>(o, M, N, K, N, s, ks);
+    case kBf64: return launch_t<Cfg64s4, OpB16, EPI>(o, M, N, K, N, s, ks);
     case kBf64x128: return launch_t<Cfg64x128, OpB16, EPI>(o, M, N, K, N, s, ks);
     default: return launch_t<Cfg128x64, OpB16, EPI>(o, M, N, K, N, s, ks);
   }
 }
 
 // Tile and number of K ranges, by a model of the time in us, fitted to
-// measurements on MI355X of every tile with 1 to 8 ranges at 35 shapes from 16
-// x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 10% of the
+// measurements on MI355X of every tile with 1 to 8 ranges at 42 shapes from 16
+// x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 9% of the
 // fastest at each, 1% in the mean):
-//   3.77 + rounds * (tile + stages * max(stage, power)) + join,
+//   2.76 + rounds * (tile + stages * max(stage, power)) + join,
 // stage the time of 128 K bytes of a tile alone on its compute unit, power
 // the same when `rate` TFLOP/s is what the whole chip's power limit allows.
 // Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 76 us whole,
-// 72 in four; 512 x 4096 x 8192: 51 us whole, 46 in four; but 4096 x 4096 x
+// 72 in three; 512 x 4096 x 8192: 52 us whole, 48 in two; but 4096 x 4096 x
 // 4096: 105 us whole, 160 in two.  (Operands from HBM; on repeated ones 4096 x
 // 4096 x 4096 takes 96 us, 1.43 PFLOP/s, and 16384 x 2048 x 4096 188 us.)
 struct Cost {
@@ -57,9 +59,9 @@ struct Cost {
   int ring, resident;   // stages of the ring; workgroups per compute unit (kResident)
 };
 constexpr Cost kCost[kNumBf] = {
-    {5.27, 1.202, 1538, 6, 1}, {2.05, 1.409, 2032, 2, 1}, {2.07, 0.895, 1547, 6, 1},
-    {2.33, 0.802, 1829, 3, 1}, {0.11, 0.660, 1833, 2, 2}, {1.51, 0.380, 1035, 4, 1},
-    {0.09, 0.183, 601, 3, 3},  {0.16, 0.251, 721, 3, 2},  {0.23, 0.273, 768, 3, 2}};
+    {3.67, 1.226, 1391, 6, 1}, {2.52, 1.342, 3952, 2, 1}, {2.01, 0.984, 1446, 6, 1},
+    {1.38, 0.667, 1342, 3, 1}, {0.10, 0.610, 1493, 2, 2}, {1.59, 0.382, 1056, 4, 1},
+    {0.19, 0.172, 594, 4, 2},  {0.11, 0.258, 719, 3, 2},  {0.18, 0.291, 750, 3, 2}};
 constexpr int64_t kMaxSlices = int64_t(1) << 29;   // bytes of workspace a split may take
 
 struct Choice {
@@ -75,16 +77,16 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   const int64_t range = range_bytes(kb, chunks), ranges = (kb + range - 1) / range;
   const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * ranges;
   const int64_t stages = (range / 128 + c.ring - 1) / c.ring * c.ring;
-  // a tile more on a compute unit that has one costs 0.88 of it
+  // a tile more on a compute unit that has one costs 0.76 of it
   const double r = c.resident, q = (double)items / kCUs;
   const double rounds = c.resident == 1 ? (double)((items + kCUs - 1) / kCUs)
                         : q <= 1.0      ? 1.0
-                        : q <= r        ? 1.0 + (q - 1.0) * 0.883
-                                        : q * (1.0 + (r - 1.0) * 0.883) / r;
+                        : q <= r        ? 1.0 + (q - 1.0) * 0.76
+                                        : q * (1.0 + (r - 1.0) * 0.76) / r;
   // 128 operations per output and 128 bytes of K
   const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
-  const double us = 3.77 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
-  return ranges > 1 ? us + 3.11 + (double)ranges * (double)M * (double)N * 1.41e-6 : us;
+  const double us = 2.76 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
+  return ranges > 1 ? us + 4.65 + (double)ranges * (double)M * (double)N * 1.35e-6 : us;
 }
 
 Choice cheapest(int64_t M, int64_t N, int64_t kb) {

@@ -8,7 +8,7 @@
 //
 // Bound by its epilogue as much as by the matrix cores: 2 bytes in and 8 out
 // per channel and token besides 4K operations.  4096 x 8192 x 2048, all
-// outputs: 199 us (264 before the loads of dy ran ahead of the stores, the
+// outputs: 200 us (264 before the loads of dy ran ahead of the stores, the
 // stores were whole 64-byte pieces and the sums went through DPP), of which
 // the same product with the forward's epilogue is 134 and the 335 MB at the
 // rate of a large copy 62.

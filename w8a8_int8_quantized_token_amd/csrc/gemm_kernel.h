@@ -339,7 +339,7 @@ struct UpArgs {
 };
 // Gradient of the gated product.  For the gradients dg, du of the two
 // products' values, as far as wanted (OpI8Want):
-//   p    bf16 [M, ldp], ldp = 2 * (N rounded up to 16): dg * sw_gate of 16
+//   p    bf16 [M, ldp], ldp >= 2N a multiple of 64: dg * sw_gate of 16
 //        channels, then du * sw_up of the same 16, and so on (zeros for
 //        channels past N): the first operand of the input's gradient, whose
 //        other operand is then the codes themselves, in the same order;
@@ -1202,8 +1202,8 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
             swap_rows16(v0, v1);
             const int piece = e_kh + 2 * ((e_lane >> 4) & 1);
             const uint32_t o = (uint32_t)((row0(i) + (e_lane & 15)) * extra.ldp + 2 * nb + piece * 8) * 2u;
-            buffer_store16(v0, p_rsrc, nb < N ? o : kOOB);
-            buffer_store16(v1, p_rsrc, nb < N ? o + 32u * (uint32_t)extra.ldp : kOOB);
+            buffer_store16(v0, p_rsrc, 2 * nb < extra.ldp ? o : kOOB);
+            buffer_store16(v1, p_rsrc, 2 * nb < extra.ldp ? o + 32u * (uint32_t)extra.ldp : kOOB);
           }
           if constexpr (kWant & kWantQ) {
             // turned around in the wavefront's LDS region: 32 rows (16 gate

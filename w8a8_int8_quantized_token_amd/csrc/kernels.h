@@ -95,8 +95,8 @@ hipError_t launch_gated(int tile, GateAct act, const int8_t* xq, const float* sx
 // (rows 16-byte aligned; columns past N zeros or, N % 8 == 0, none), each
 // output as far as not null: p bf16 [M,ldp] (columns in blocks of 32: dg *
 // sw_gate of 16 channels, du * sw_up of the same, zeros past channel N; ldp =
-// 2 * (N rounded up to 16)), qt bf16 [2N,ldq] ((dg * sx)^T over (du * sx)^T,
-// zeros past column M; ldq = M rounded up to 8), sums fp32
+// 2N rounded up to 64), qt bf16 [2N,ldq] ((dg * sx)^T over (du * sx)^T,
+// zeros past column M; ldq = M rounded up to 64), sums fp32
 // [gated_grad_sum_rows(), 2N] (column sums over blocks of rows).
 int64_t gated_grad_sum_rows(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, int64_t ld_dy, const int8_t* xq, const float* sx,

@@ -14,6 +14,10 @@
 // reduction over the head's lanes.  All arithmetic is fp32, rounded to bf16
 // once.  The weight's gradient is kept in registers over a workgroup's heads
 // and joined by a second small kernel in a fixed order.
+//
+// Measured: 16384 tokens of 24 + 24 heads of 128 values 78 us, 5.2 TB/s (a
+// large copy 5.1 to 5.4); gradient of 8192 tokens of 32 + 8 heads 46 us, 5.5
+// TB/s, and 4.7 us for the second kernel.
 #include "kernels.h"
 
 #include <algorithm>
@@ -28,7 +32,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWave = 64;
-constexpr int kMaxSumBlocks = 1024;   // workgroups of the gradient kernel
+// Workgroups of the gradient kernel, each a row of weight sums (8192 x 40
+// heads: 1024 46 + 4.7 us, 512 53 + 4.7, 2048 47 + 5.4).
+constexpr int kMaxSumBlocks = 1024;
 
 __device__ __forceinline__ void unpack8(u32x4 v, float* f) {
 #pragma unroll

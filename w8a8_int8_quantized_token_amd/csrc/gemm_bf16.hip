@@ -44,24 +44,23 @@ hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, in
 }
 
 // Tile and number of K ranges, by a model of the time in us, fitted to
-// measurements on MI355X of every tile with 1 to 8 ranges at 42 shapes from 16
+// measurements on MI355X of every tile with 1 to 8 ranges at 44 shapes from 16
 // x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 9% of the
 // fastest at each, 1% in the mean):
-//   2.76 + rounds * (tile + stages * max(stage, power)) + join,
+//   3.77 + rounds * (tile + stages * max(stage, power)) + join,
 // stage the time of 128 K bytes of a tile alone on its compute unit, power
 // the same when `rate` TFLOP/s is what the whole chip's power limit allows.
-// Ranges pay where tiles leave units idle: 1037 x 2064 x 10944: 76 us whole,
-// 72 in three; 512 x 4096 x 8192: 52 us whole, 48 in two; but 4096 x 4096 x
-// 4096: 105 us whole, 160 in two.  (Operands from HBM; on repeated ones 4096 x
-// 4096 x 4096 takes 96 us, 1.43 PFLOP/s, and 16384 x 2048 x 4096 188 us.)
+// Ranges pay where tiles leave units idle: 128 x 8192 x 24576: 133 us whole, 92
+// in ranges; 512 x 512 x 8192: 23.8 us whole, 13.9 in ranges; but 4096 x 4096 x
+// 4096: 100 us whole, 149 in two.
 struct Cost {
   double tile_us, stage_us, rate;
   int ring, resident;   // stages of the ring; workgroups per compute unit (kResident)
 };
 constexpr Cost kCost[kNumBf] = {
-    {3.67, 1.226, 1391, 6, 1}, {2.52, 1.342, 3952, 2, 1}, {2.01, 0.984, 1446, 6, 1},
-    {1.38, 0.667, 1342, 3, 1}, {0.10, 0.610, 1493, 2, 2}, {1.59, 0.382, 1056, 4, 1},
-    {0.19, 0.172, 594, 4, 2},  {0.11, 0.258, 719, 3, 2},  {0.18, 0.291, 750, 3, 2}};
+    {3.98, 1.172, 1494, 6, 1}, {2.69, 1.244, 2705, 2, 1}, {3.03, 0.881, 1686, 6, 1},
+    {3.17, 0.576, 1497, 3, 1}, {0.11, 0.376, 842, 2, 2},  {1.78, 0.363, 1210, 4, 1},
+    {0.18, 0.166, 627, 4, 2},  {0.39, 0.235, 813, 3, 2},  {0.21, 0.260, 853, 3, 2}};
 constexpr int64_t kMaxSlices = int64_t(1) << 29;   // bytes of workspace a split may take
 
 struct Choice {
@@ -77,16 +76,16 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   const int64_t range = range_bytes(kb, chunks), ranges = (kb + range - 1) / range;
   const int64_t items = (M + d.block_m - 1) / d.block_m * ((N + d.block_n - 1) / d.block_n) * ranges;
   const int64_t stages = (range / 128 + c.ring - 1) / c.ring * c.ring;
-  // a tile more on a compute unit that has one costs 0.76 of it
+  // a tile more on a compute unit that has one costs 0.72 of it
   const double r = c.resident, q = (double)items / kCUs;
   const double rounds = c.resident == 1 ? (double)((items + kCUs - 1) / kCUs)
                         : q <= 1.0      ? 1.0
-                        : q <= r        ? 1.0 + (q - 1.0) * 0.76
-                                        : q * (1.0 + (r - 1.0) * 0.76) / r;
+                        : q <= r        ? 1.0 + (q - 1.0) * 0.717
+                                        : q * (1.0 + (r - 1.0) * 0.717) / r;
   // 128 operations per output and 128 bytes of K
   const double power = (double)std::min<int64_t>(items, kCUs) * (double)(d.block_m * d.block_n) * 128.0 / (c.rate * 1e6);
-  const double us = 2.76 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
-  return ranges > 1 ? us + 4.65 + (double)ranges * (double)M * (double)N * 1.35e-6 : us;
+  const double us = 3.77 + rounds * (c.tile_us + (double)stages * std::max(c.stage_us, power));
+  return ranges > 1 ? us + 2.5 + (double)ranges * (double)M * (double)N * 1.35e-6 : us;
 }
 
 Choice cheapest(int64_t M, int64_t N, int64_t kb) {

@@ -170,6 +170,28 @@ def test_linear_backward(w8, M, N, K):
         assert torch.equal(bits(alone[i]), bits(got[i])), name
 
 
+# shapes of dx whose product takes each of its tiles whole or in ranges of the
+# sum, and on both sides of copying dy for the sake of its rows' alignment
+TILES = [(10079, 1026, 1216), (3872, 201, 3488), (4925, 278, 2272), (987, 520, 6544), (4500, 8, 144),
+         (397, 1021, 5920), (186, 141, 8336), (69, 135, 8720),
+         (434, 10056, 9104), (2088, 9573, 2208), (6308, 12097, 160), (66, 11925, 6032), (84, 8175, 2528),
+         (67, 4974, 7904), (1, 2197, 2624), (2545, 2170, 16), (1, 1296, 16), (300, 2056, 512), (300, 2056, 496)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_input_gradient_on_every_tile(w8, M, N, K):
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    ws = torch.rand(N, generator=g, device=DEV) * 0.02 + 1e-3
+    dy = torch.randn(M, N, generator=g, device=DEV).to(BF)
+    w = wq.to(ref.F64) * ws.to(ref.F64)[:, None]
+    want = dy.to(ref.F64) @ w
+    mag = dy.to(ref.F64).abs() @ w.abs()
+    got = w8.linear_backward(dy, None, None, wq, ws, dw=False, dbias=False)[0]
+    ref.check(got, want.cpu(), grad_slack(mag.cpu(), N), "dx")
+    assert torch.equal(bits(w8.linear_backward(dy, None, None, wq, ws, dw=False, dbias=False)[0]), bits(got))
+
+
 def test_linear_backward_of_an_unaligned_dy(w8):
     M, N, K = 40, 64, 96
     g = gen(5)
@@ -346,3 +368,26 @@ def test_outputs_at_odd_addresses(w8, M, N, K):
     for f, n in ((w8.linear_dynamic, 2 * N), (w8.gated_linear_dynamic, N)):
         room = torch.empty(M * n + 1, dtype=BF, device=DEV)
         assert torch.equal(bits(f(x, wq, ws, b, y=room[1:].view(M, n))), bits(f(x, wq, ws, b)))
+
+
+@pytest.mark.parametrize("M,N,K", [(10079, 1026, 1216), (3872, 201, 3488), (4925, 278, 2272), (987, 520, 6544),
+                                   (4500, 8, 144), (434, 10056, 9104), (66, 11925, 6032)])
+def test_input_gradient_at_an_odd_address(w8, M, N, K):
+    """On large tiles, nothing written around it (ranges of the sum are not
+    joined at an odd address: the sums run in another order)."""
+    g = torch.Generator(device=DEV).manual_seed(M)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    ws = torch.rand(N, generator=g, device=DEV) * 0.02 + 1e-3
+    dy = torch.randn(M, N, generator=g, device=DEV).to(BF)
+    room = torch.full((M * K + 9,), -7.0, dtype=BF, device=DEV)
+    need = w8.lib.w8a8_linear_backward_workspace(M, N, K, 1, 0, 0)
+    space = torch.empty(need, dtype=torch.uint8, device=DEV)
+    status = w8.lib.w8a8_linear_backward(dy.data_ptr(), None, None, wq.data_ptr(), ws.data_ptr(),
+                                         room[1:].data_ptr(), None, None, M, N, K, space.data_ptr(), need,
+                                         torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    got = room[1:1 + M * K].view(M, K)
+    w = wq.to(ref.F64) * ws.to(ref.F64)[:, None]
+    mag = dy.to(ref.F64).abs() @ w.abs()
+    ref.check(got, (dy.to(ref.F64) @ w).cpu(), grad_slack(mag.cpu(), N), "dx")
+    assert float(room[0]) == -7.0 and bool((room[1 + M * K:] == -7.0).all())

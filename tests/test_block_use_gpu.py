@@ -434,3 +434,23 @@ def test_native_and_checked_calls_agree(w8):
                 bad(**o)
     with pytest.raises(w8.W8A8Error):
         w8.linear_dynamic(x[:, :24].contiguous(), wq[:, :24].contiguous(), ws)      # K not a multiple of 16
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (17, 31, 48), (65, 40, 272), (100, 72, 256), (129, 1001, 400), (300, 2056, 512),
+                                   (70, 5466, 2064), (777, 33, 144)])
+def test_what_a_workspace_held_does_not_matter(w8, M, N, K):
+    """Workspaces of NaNs: the padding of laid-out rows is written, not assumed."""
+    g = torch.Generator().manual_seed(M + N)
+    wq, ws = [t.to(DEV) for t in ref.codes_of(torch.randn(2 * N, K, generator=g).to(BF))]
+    xq, xs = [t.to(DEV) for t in ref.codes_of(torch.randn(M, K, generator=g).to(BF))]
+    for f, size, n, rows in ((w8.linear_backward, w8.lib.w8a8_linear_backward_workspace, 2 * N, 2 * N),
+                             (w8.gated_linear_backward, w8.lib.w8a8_gated_linear_backward_workspace, N, N)):
+        dy = torch.randn(M, n, generator=g).to(BF).to(DEV)
+        for want in ((1, 1, 1), (1, 0, 0), (0, 1, 0)):
+            flags = dict(zip(("dx", "dw", "dbias"), map(bool, want)))
+            space = torch.full((size(M, rows, K, *want),), 0xFF, dtype=torch.uint8, device=DEV)
+            got, fresh = f(dy, xq, xs, wq, ws, workspace=space, **flags), f(dy, xq, xs, wq, ws, **flags)
+            for a, b in zip(got, fresh):
+                assert (a is None) == (b is None)
+                if a is not None:
+                    assert bool(torch.isfinite(a).all()) and same(a, b)

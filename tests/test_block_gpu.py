@@ -144,7 +144,7 @@ def test_gated_extremes(w8):
 # ---- backward ----
 
 BACK = [(1, 1, 16), (8, 8, 32), (9, 7, 48), (65, 33, 272), (130, 96, 128), (300, 257, 528), (777, 1001, 400),
-        (64, 2048, 256), (2049, 64, 144)]
+        (64, 2048, 256), (2049, 64, 144), (3, 1601, 2000), (40, 1999, 1568)]
 
 
 def grad_slack(mag, n):
@@ -171,11 +171,14 @@ def test_linear_backward(w8, M, N, K):
 
 
 # shapes of dx whose product takes each of its tiles whole or in ranges of the
-# sum, and on both sides of copying dy for the sake of its rows' alignment
+# sum, on both sides of copying dy for the sake of its rows' alignment, and few
+# tokens of a large weight
 TILES = [(10079, 1026, 1216), (3872, 201, 3488), (4925, 278, 2272), (987, 520, 6544), (4500, 8, 144),
          (397, 1021, 5920), (186, 141, 8336), (69, 135, 8720),
          (434, 10056, 9104), (2088, 9573, 2208), (6308, 12097, 160), (66, 11925, 6032), (84, 8175, 2528),
-         (67, 4974, 7904), (1, 2197, 2624), (2545, 2170, 16), (1, 1296, 16), (300, 2056, 512), (300, 2056, 496)]
+         (67, 4974, 7904), (1, 2197, 2624), (2545, 2170, 16), (1, 1296, 16), (300, 2056, 512), (300, 2056, 496),
+         (1, 2501, 2624), (15, 1200, 5008), (16, 6001, 1008), (17, 9000, 752), (32, 12504, 496), (33, 3333, 1904),
+         (48, 23001, 272), (64, 777, 8208), (65, 777, 8208)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)

@@ -437,7 +437,7 @@ def test_native_and_checked_calls_agree(w8):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (17, 31, 48), (65, 40, 272), (100, 72, 256), (129, 1001, 400), (300, 2056, 512),
-                                   (70, 5466, 2064), (777, 33, 144)])
+                                   (70, 5466, 2064), (777, 33, 144), (5, 1500, 2064), (33, 3077, 1040), (64, 750, 4112)])
 def test_what_a_workspace_held_does_not_matter(w8, M, N, K):
     """Workspaces of NaNs: the padding of laid-out rows is written, not assumed."""
     g = torch.Generator().manual_seed(M + N)

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libw8a8.so")
 CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["quantize_rows.hip", "dequantize_rows.hip", "gemm_i8.hip", "splitk_reduce.hip",
            "mfma_ceiling.hip", "w8a8_api.hip", "gemm_gated.hip", "gemm_gated_grad.hip", "gemm_bf16.hip",
-           "backward_layout.hip", "few_tokens.hip", "qk_norm_rope.hip", "block_api.hip"]
+           "backward_layout.hip", "few_grad.hip", "few_tokens.hip", "qk_norm_rope.hip", "block_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -107,6 +107,7 @@ struct BackPlan {
   int64_t first, wt, slices_x;
   int64_t second, xt, slices_w;
   int ranges_x, ranges_w;
+  bool few;                   // dx straight from the codes (few_grad.hip): no wt
   int64_t bytes;
 };
 // Rows of an operand laid out here are whole 128-byte lines, zeros past their
@@ -114,6 +115,12 @@ struct BackPlan {
 // (2000 x 2000 x 5000: 53 us with rows of 5000 values, 41 with 5056; 333 x
 // 2064 x 3000: 18.1 and 13.6).
 constexpr int64_t kLine = 64;
+// Few tokens' dx comes from the codes as they are (its join writes 16 bytes at
+// a time) where turning them costs more than its slices do: from 6 million
+// codes on (us turned and as they are: 29 tokens, 2776 x 2592 20.2 and 15.9,
+// 12000 x 5408 75 and 30; gated, 26 tokens, 2 x 2749 x 1872 32.1 and 31.4; but
+// 600 x 5440 11.9 and 13.4, gated 2 x 722 x 2176 22.8 and 26.7).
+bool few_rows(int64_t M, int64_t rows, int64_t K) { return M <= w8a8::kFewGradTokens && rows * K >= 6000000; }
 // Rows of dy that start inside a line are copied too where the product is long
 // enough (dx alone, us without and with the copy; M x N x K): 4096 x 5000 x 512
 // 45 and 42, 777 x 5000 x 2048 51 and 37; but 4096 x 5000 x 256 31 and 37, 4096
@@ -122,8 +129,9 @@ bool copy_lines(int64_t M, int64_t N, int64_t K) {
   return N % kLine != 0 && M >= 256 && N >= 2048 && K >= 512;
 }
 
-BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy) {
+BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy, bool few) {
   BackPlan p{};
+  p.few = dx && few;
   const int64_t cols = (gated ? 2 : 1) * N;
   p.ldy = gated ? up(N, 8) : copy_dy ? up(N, kLine) : N;
   p.ld = gated ? up(2 * N, kLine) : p.ldy;
@@ -134,12 +142,12 @@ BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw
                        : (M + w8a8::transpose_sum_span(M, N) - 1) / w8a8::transpose_sum_span(M, N);
     p.sums = w.add(4 * p.sum_rows * cols);
   }
-  if (copy_dy && (gated || dx)) p.copy = w.add(2 * M * p.ldy);
+  if (copy_dy && (gated || (dx && !few))) p.copy = w.add(2 * M * p.ldy);
   if (dx) {
     if (gated) p.first = w.add(2 * M * p.ld);
-    p.wt = w.add(2 * K * p.ld);
-    p.ranges_x = w8a8::gemm_bf16_slices(M, K, p.ld);
-    if (p.ranges_x > 1) p.slices_x = w.add(4 * M * K * p.ranges_x);
+    if (!few) p.wt = w.add(2 * K * p.ld);
+    p.ranges_x = few ? w8a8::few_grad_slices(M, N, K, gated) : w8a8::gemm_bf16_slices(M, K, p.ld);
+    if (few || p.ranges_x > 1) p.slices_x = w.add(4 * M * K * p.ranges_x);
   }
   if (dw) {
     p.second = w.add(2 * cols * p.mp);
@@ -151,18 +159,32 @@ BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw
   return p;
 }
 
+// The largest of the plans that calls of these sizes may take, as their
+// addresses are.
+size_t back_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db) {
+  int64_t most = 0;
+  for (const bool copy : {true, false})
+    for (const bool few : {false, true})
+      if ((copy || N % 8 == 0) && (!few || few_rows(M, gated ? 2 * N : N, K))) most = std::max(most, back_plan(M, N, K, gated, dx, dw, db, copy, few).bytes);
+  return (size_t)most;
+}
+
 // The products of a backward pass and what comes after them: dx [M,K] from
-// first [M,ld] and wt [K,ld], dw [cols,K] from second [cols,mp] and xt [K,mp],
+// first [M,ld] and wt [K,ld] (few tokens: the codes and scales), dw [cols,K] from second [cols,mp] and xt [K,mp],
 // dbias [cols] from the sums.
-hipError_t products(const BackPlan& p, void* ws, const uint16_t* first, uint16_t* dx, uint16_t* dw, uint16_t* dbias,
-                    int64_t M, int64_t cols, int64_t K, hipStream_t stream) {
+hipError_t products(const BackPlan& p, void* ws, const uint16_t* first, const int8_t* wq, const float* w_scale,
+                    bool gated, uint16_t* dx, uint16_t* dw, uint16_t* dbias, int64_t M, int64_t cols, int64_t K,
+                    hipStream_t stream) {
   w8a8::JoinJob jobs[w8a8::kMaxJobs];
   int n = 0;
   hipError_t e = hipSuccess;
   if (dx) {
     // the join writes 16 bytes at a time
-    float* slices = p.ranges_x > 1 && aligned(dx, 16) ? at<float>(ws, p.slices_x) : nullptr;
-    e = w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.wt), dx, slices, M, K, p.ld, stream);
+    float* slices = p.few || (p.ranges_x > 1 && aligned(dx, 16)) ? at<float>(ws, p.slices_x) : nullptr;
+    if (p.few)
+      e = gated ? w8a8::launch_few_grad(first, p.ld, wq, nullptr, slices, M, cols / 2, K, true, stream)
+                : w8a8::launch_few_grad(first, cols, wq, w_scale, slices, M, cols, K, false, stream);
+    else e = w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.wt), dx, slices, M, K, p.ld, stream);
     if (slices) jobs[n++] = {slices, dx, p.ranges_x, M * K, true, 0};
   }
   if (dw && e == hipSuccess) {
@@ -287,8 +309,7 @@ w8a8_status w8a8_gated_linear_dynamic(const uint16_t* x, const int8_t* wq, const
 // Both sizes allow for the copy of dy that an odd N or address needs.
 size_t w8a8_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
   if (!shape_ok(M, N, K, 1) || M == 0) return 0;
-  const int64_t with = back_plan(M, N, K, false, dx, dw, dbias, true).bytes;
-  return (size_t)(N % 8 ? with : std::max(with, back_plan(M, N, K, false, dx, dw, dbias, false).bytes));
+  return back_workspace(M, N, K, false, dx, dw, dbias);
 }
 
 w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
@@ -297,8 +318,9 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
   w8a8_status st = check_back(dy, xq, x_scale, wq, w_scale, nullptr, dx, dw, dbias, M, N, K, false);
   if (st != W8A8_OK) return st;
   if (M == 0) return no_tokens(dw, dbias, N, K, stream);
+  const bool few = dx && few_rows(M, N, K) && aligned(dx, 16);
   const bool copy = N % 8 != 0 || !aligned(dy, 16) || (dx && copy_lines(M, N, K));
-  const BackPlan p = back_plan(M, N, K, false, dx, dw, dbias, copy);
+  const BackPlan p = back_plan(M, N, K, false, dx, dw, dbias, copy, few);
   st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;
   if (!dx && !dw && !dbias) return W8A8_OK;
@@ -306,7 +328,7 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
   Job jobs[w8a8::kMaxJobs];
   int n = 0;
   const uint16_t* first = dy;
-  if (dx) {
+  if (dx && !few) {
     if (copy) {
       jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(workspace, p.copy), nullptr, M, N, p.ldy, 0};
       first = at<uint16_t>(workspace, p.copy);
@@ -317,13 +339,13 @@ w8a8_status w8a8_linear_backward(const uint16_t* dy, const int8_t* xq, const flo
     jobs[n++] = {Job::kTurnValues, dy, nullptr, dw ? at<uint16_t>(workspace, p.second) : nullptr,
                  dbias ? at<float>(workspace, p.sums) : nullptr, M, N, p.mp, w8a8::transpose_sum_span(M, N)};
   if (dw) jobs[n++] = {Job::kTurnCodes, xq, x_scale, at<uint16_t>(workspace, p.xt), nullptr, M, K, p.mp, 0};
-  TRY(w8a8::launch_prepare(jobs, n, stream));
-  return launched(products(p, workspace, first, dx, dw, dbias, M, N, K, stream));
+  if (n > 0) TRY(w8a8::launch_prepare(jobs, n, stream));
+  return launched(products(p, workspace, first, wq, w_scale, false, dx, dw, dbias, M, N, K, stream));
 }
 
 size_t w8a8_gated_linear_backward_workspace(int64_t M, int64_t N, int64_t K, int dx, int dw, int dbias) {
   if (!shape_ok(M, N, K, 2) || M == 0) return 0;
-  return (size_t)back_plan(M, N, K, true, dx, dw, dbias, true).bytes;
+  return back_workspace(M, N, K, true, dx, dw, dbias);
 }
 
 w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
@@ -336,7 +358,8 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, con
   if (M == 0) return no_tokens(dw, dbias, 2 * N, K, stream);
   if (!dx && !dw && !dbias) return W8A8_OK;
   const bool copy = N % 8 != 0 || !aligned(dy, 16);
-  const BackPlan p = back_plan(M, N, K, true, dx, dw, dbias, copy);
+  const bool few = dx && few_rows(M, 2 * N, K) && aligned(dx, 16);
+  const BackPlan p = back_plan(M, N, K, true, dx, dw, dbias, copy, few);
   st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;
   uint16_t* first = dx ? at<uint16_t>(workspace, p.first) : nullptr;
@@ -349,12 +372,12 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t* dy, const int8_t* xq, con
     jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(workspace, p.copy), nullptr, M, N, p.ldy, 0};
     dy = at<uint16_t>(workspace, p.copy);
   }
-  if (dx) jobs[n++] = {Job::kTurnPaired, wq, nullptr, at<uint16_t>(workspace, p.wt), nullptr, 2 * N, K, p.ld, 0};
+  if (dx && !few) jobs[n++] = {Job::kTurnPaired, wq, nullptr, at<uint16_t>(workspace, p.wt), nullptr, 2 * N, K, p.ld, 0};
   if (dw) jobs[n++] = {Job::kTurnCodes, xq, nullptr, at<uint16_t>(workspace, p.xt), nullptr, M, K, p.mp, 0};
   if (n > 0) TRY(w8a8::launch_prepare(jobs, n, stream));
   TRY(w8a8::launch_gated_grad(static_cast<GateAct>(act), dy, p.ldy, xq, x_scale, wq, w_scale, bias, first, p.ld,
                               second, p.mp, sums, M, N, K, stream));
-  return launched(products(p, workspace, first, dx, dw, dbias, M, 2 * N, K, stream));
+  return launched(products(p, workspace, first, wq, w_scale, true, dx, dw, dbias, M, 2 * N, K, stream));
 }
 
 w8a8_status w8a8_qk_norm_rope(const uint16_t* q, int64_t q_row, int64_t q_head, const uint16_t* k, int64_t k_row,

@@ -131,6 +131,13 @@ struct JoinJob {
   bool slices;           // few long rows (a product's slices, n % 8 == 0), or many short ones
   int64_t blocks;        // set by the launch
 };
+// The input's gradient of few tokens from the codes as they are: fp32 slices
+// [few_grad_slices()][M][K] for launch_finish to join.  d is dy [M,N] (any
+// address; `scale` that of the rows of q), or gated launch_gated_grad's p.
+constexpr int64_t kFewGradTokens = 64;
+int few_grad_slices(int64_t M, int64_t N, int64_t K, bool gated);
+hipError_t launch_few_grad(const uint16_t* d, int64_t ldd, const int8_t* q, const float* scale, float* slices,
+                           int64_t M, int64_t N, int64_t K, bool gated, hipStream_t stream);
 int64_t transpose_sum_span(int64_t R, int64_t C);   // kTurnValues' rows of one block of sums
 hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream);
 hipError_t launch_finish(const JoinJob* jobs, int n, hipStream_t stream);

@@ -333,8 +333,10 @@ w8a8_status w8a8_gated_linear_dynamic(const uint16_t *x, const int8_t *wq, const
  *   dbias[n] = bf16( sum_m dy[m,n] ).
  * Each output is bf16 and is left out where its pointer is NULL; dx needs wq
  * and w_scale, dw needs xq and x_scale.  Sums are fp32 (bf16 matrix cores);
- * the values w and x are rounded to bf16 once before their products.  Results
- * do not depend on timing (no atomics).
+ * the values w and x are rounded to bf16 once before their products (for up to
+ * 64 tokens of a large weight and 16-byte aligned dx, dy * w_scale in the place
+ * of w; the codes are then exact).  Results do not depend on timing (no
+ * atomics).
  * The gated form has wq [2N,K], w_scale, bias and dbias [2N] and dw [2N,K] as
  * w8a8_gated_linear; it needs all of xq, x_scale, wq, w_scale and the
  * forward's bias, forms g and u again from them, and

@@ -225,7 +225,7 @@ def cases(w8, seed):
         return [t.to(DEV) for t in ref.codes_of(torch.randn(r, k, generator=g).to(BF))]
 
     out = []
-    for M, N, K in [(1, 200, 512), (20, 136, 1024), (64, 256, 4096), (200, 264, 256)]:
+    for M, N, K in [(1, 200, 512), (20, 136, 1024), (64, 256, 4096), (200, 264, 256), (33, 3000, 2048)]:
         w, s = q(N, K)
         w2, s2 = q(2 * N, K)
         b, b2 = bf(N), bf(2 * N)

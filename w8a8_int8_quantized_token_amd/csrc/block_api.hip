@@ -160,12 +160,14 @@ BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw
 }
 
 // The largest of the plans that calls of these sizes may take, as their
-// addresses are.
+// addresses are (without the copy of dy a plan is smaller unless its rows, and
+// with them its ranges, are others).
 size_t back_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db) {
   int64_t most = 0;
   for (const bool copy : {true, false})
     for (const bool few : {false, true})
-      if ((copy || N % 8 == 0) && (!few || few_rows(M, gated ? 2 * N : N, K))) most = std::max(most, back_plan(M, N, K, gated, dx, dw, db, copy, few).bytes);
+      if ((copy || (!gated && N % 8 == 0 && N % kLine != 0)) && (!few || few_rows(M, gated ? 2 * N : N, K)))
+        most = std::max(most, back_plan(M, N, K, gated, dx, dw, db, copy, few).bytes);
   return (size_t)most;
 }
 

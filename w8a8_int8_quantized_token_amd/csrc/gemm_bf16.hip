@@ -108,11 +108,11 @@ Choice choose(int64_t M, int64_t N, int64_t kb) {
     int64_t M, N, kb;
     Choice c;
   };
-  thread_local Entry last[4] = {};
+  thread_local Entry last[8] = {};
   thread_local unsigned next = 0;
   for (const Entry& e : last)
     if (e.M == M && e.N == N && e.kb == kb) return e.c;
-  Entry& e = last[next++ % 4];
+  Entry& e = last[next++ % 8];
   e = {M, N, kb, cheapest(M, N, kb)};
   return e.c;
 }

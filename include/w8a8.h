@@ -374,14 +374,15 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t *dy, const int8_t *xq,
  *   or NULL: m mod P, one sequence of P tokens after another).
  * Arithmetic in fp32, rounded to bf16 once.  A row whose position is outside
  * [0, P) (padding) gets zeros in every head, and in the gradients, and adds
- * nothing to the weights' gradients.  q_out and k_out may be q and k (same
+ * nothing to the weights' gradients, also where rot = 0 (the norm alone; P is
+ * then looked at only where positions are given).  q_out and k_out may be q and k (same
  * strides); Hq or Hk may be 0 (its pointers are then not looked at).
  * The gradient takes the outputs' gradients dq, dk and the inputs q, k, and
  * writes dq_in, dk_in (bf16; they may be dq, dk or q, k with the same strides)
  * and, where not NULL, dq_weight, dk_weight (fp32 [D], summed over rows and
  * heads in a fixed order; they need the workspace).
  * Contract: 16 <= D <= 1024, D and rot multiples of 16, 0 <= rot <= D,
- * M * (Hq + Hk) * (D/16 rounded up to a power of two) <= 2^31, P < 2^31,
+ * M * (Hq + Hk) * (D/16 rounded up to a power of two) <= 2^31, 1 <= P < 2^31,
  * eps >= 0; all bf16 and table pointers 16-byte aligned, strides multiples of
  * 8, weight gradients and positions 4-byte aligned.
  */

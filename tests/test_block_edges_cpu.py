@@ -1,0 +1,33 @@
+"""Host-side checks at the edges of the operators around the linear: refusals
+before any launch (fake pointers, never dereferenced) and which form a call
+takes, by its workspace."""
+import pytest
+
+A = 0x10000
+NULL, SHAPE, ALIGN, ARG = 1, 2, 3, 5
+
+
+@pytest.fixture(scope="module")
+def w8():
+    import w8a8_int8_quantized_token_amd as pkg
+    return pkg
+
+
+def test_positions_without_a_rotation_need_a_table_size(w8):
+    """rot = 0: P counts where positions are given (rows outside [0, P) are
+    padding), and nowhere else."""
+    v = (512, 64)
+
+    def call(pos, P, M=0, rot=0):
+        return w8.lib.w8a8_qk_norm_rope(A, *v, A, *v, A, A, None, None, pos, A, *v, A, *v, M, P, 4, 2, 64, rot, 1e-6,
+                                        0, None)
+
+    def back(pos, P):
+        return w8.lib.w8a8_qk_norm_rope_backward(A, *v, A, *v, A, *v, A, *v, A, A, None, None, pos, A, *v, A, *v, None,
+                                                 None, 0, P, 4, 2, 64, 0, 1e-6, 0, None, 0, None)
+
+    for P in (0, -1, 2 ** 31):
+        assert call(A, P) == back(A, P) == SHAPE and call(None, P) == back(None, P) == 0
+        assert call(None, P, rot=16) == SHAPE
+    assert call(A, 1) == back(A, 1) == 0
+    assert call(A + 2, 4, M=4) == ALIGN

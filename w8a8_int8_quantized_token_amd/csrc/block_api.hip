@@ -237,9 +237,13 @@ w8a8_status check_workspace(const void* ws, size_t have, int64_t need) {
 
 // ---- norm and rotation ----
 
+// Without a rotation positions still say which rows are padding; without
+// positions either, every row is at some position of any table.
+bool positions_matter(int64_t rot, const int32_t* positions) { return rot > 0 || positions != nullptr; }
+
 w8a8_status check_rope(const w8a8::RopeArgs& a, int64_t Hq, int64_t Hk, int64_t D, int64_t rot) {
   if (a.M < 0 || a.M > kMaxRows || Hq < 0 || Hk < 0 || Hq + Hk < 1 || Hq + Hk > 65536 || D < 16 || D > 1024 ||
-      D % 16 != 0 || rot < 0 || rot > D || rot % 16 != 0 || (rot > 0 && (a.P < 1 || a.P > INT32_MAX)))
+      D % 16 != 0 || rot < 0 || rot > D || rot % 16 != 0 || a.P < 1 || a.P > INT32_MAX)
     return W8A8_ERR_SHAPE;
   int64_t lanes = 1;
   while (lanes * 16 < D) lanes *= 2;
@@ -389,8 +393,8 @@ w8a8_status w8a8_qk_norm_rope(const uint16_t* q, int64_t q_row, int64_t q_head, 
                               int64_t P, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, float eps, int interleaved,
                               hipStream_t stream) {
   w8a8::RopeArgs a{view(q, q_row, q_head), view(k, k_row, k_head), view(q_out, q_out_row, q_out_head),
-                   view(k_out, k_out_row, k_out_head), q_weight, k_weight, cos, sin, rot > 0 ? positions : nullptr,
-                   M, rot > 0 ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
+                   view(k_out, k_out_row, k_out_head), q_weight, k_weight, cos, sin, positions,
+                   M, positions_matter(rot, positions) ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
   w8a8_status st = check_rope(a, Hq, Hk, D, rot);
   if (st != W8A8_OK || M == 0) return st;
   st = check_rope_ptrs(a);
@@ -411,8 +415,8 @@ w8a8_status w8a8_qk_norm_rope_backward(
     float* dq_weight, float* dk_weight, int64_t M, int64_t P, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
     float eps, int interleaved, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   w8a8::RopeArgs a{view(q, q_row, q_head), view(k, k_row, k_head), view(dq, dq_row, dq_head),
-                   view(dk, dk_row, dk_head), q_weight, k_weight, cos, sin, rot > 0 ? positions : nullptr,
-                   M, rot > 0 ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
+                   view(dk, dk_row, dk_head), q_weight, k_weight, cos, sin, positions,
+                   M, positions_matter(rot, positions) ? P : 1, (int)Hq, (int)Hk, (int)D, (int)rot, eps};
   w8a8_status st = check_rope(a, Hq, Hk, D, rot);
   if (st != W8A8_OK) return st;
   if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return W8A8_ERR_ALIGN;

@@ -55,3 +55,21 @@ def test_padding_rows_without_a_rotation(w8, interleaved):
             assert not got[i][pad].any() and same(got[i][keep], part[i])
             # the same terms in another order: fp32 sums of M heads' products
             assert torch.allclose(got[2 + i], part[2 + i], rtol=1e-4, atol=1e-4 * float(part[2 + i].abs().max()))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_padding_rows_are_zeros_whatever_the_tables_hold(w8, interleaved):
+    M, P, H, D = 9, 6, 2, 64
+    g = torch.Generator().manual_seed(2)
+    q, k = bf(g, M, H, D), bf(g, M, H, D)
+    cos, sin = torch.rand(P, 16, generator=g).to(DEV), torch.rand(P, 16, generator=g).to(DEV)
+    cos[0], sin[0] = float("inf"), float("nan")       # a row that no token is at
+    pos = torch.randint(1, P, (M,), generator=g, dtype=torch.int32)
+    pos[4], pos[8] = -1, P
+    q[4], k[8] = float("nan"), float("inf")
+    out = w8.qk_norm_rope(q, k, None, None, cos, sin, pos.to(DEV), interleaved=interleaved)
+    back = w8.qk_norm_rope_backward(q, k, q, k, None, None, cos, sin, pos.to(DEV), interleaved=interleaved)
+    keep = [0, 1, 2, 3, 5, 6, 7]
+    for t in (*out, *back[:2]):
+        assert not t[[4, 8]].any() and bool(torch.isfinite(t[keep]).all())
+    assert bool(torch.isfinite(back[2]).all()) and bool(torch.isfinite(back[3]).all())

@@ -150,8 +150,11 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeArgs a, uint32_
   if (!on) return;
   const float r = __builtin_amdgcn_rsqf(sq / (float)a.D + a.eps);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = turned ? v[e] * r * w[e] : 0.0f;
+  for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
   turn<kInterleaved, false>(v, c, s);
+  // (chosen after the turn: a padding row's angles are the table's first row's)
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = turned ? v[e] : 0.0f;
   *reinterpret_cast<u32x4*>(y + lo) = pack8(v);
   *reinterpret_cast<u32x4*>(y + hi) = pack8(v + 8);
 }

@@ -73,3 +73,65 @@ def test_padding_rows_are_zeros_whatever_the_tables_hold(w8, interleaved):
     for t in (*out, *back[:2]):
         assert not t[[4, 8]].any() and bool(torch.isfinite(t[keep]).all())
     assert bool(torch.isfinite(back[2]).all()) and bool(torch.isfinite(back[3]).all())
+
+
+# ---- the QKV module ----
+
+def qkv_module(w8, seed, norms=True):
+    K, Hq, Hk, D = 64, 4, 2, 32
+    torch.manual_seed(seed)
+    proj = torch.nn.Linear(K, (Hq + 2 * Hk) * D, device=DEV, dtype=BF)
+    w = [(1 + 0.2 * torch.randn(D, device=DEV)).to(BF) if norms else None for _ in range(2)]
+    return w8.W8A8QKV(w8.W8A8Linear.from_linear(proj), Hq, Hk, *w)
+
+
+def turns(P):
+    a = torch.rand(P, 16, device=DEV) * 6
+    return a.cos(), a.sin()
+
+
+@pytest.mark.parametrize("grads", [False, True])
+def test_each_sequence_of_a_batch_starts_at_position_0(w8, grads):
+    """Tables longer than the sequences: a token's position is its index in
+    its own sequence."""
+    B, S, P = 3, 19, 64
+    m = qkv_module(w8, 3)
+    cos, sin = turns(P)
+    x = torch.randn(2, B, S, 64, device=DEV).to(BF).requires_grad_(grads)
+    with torch.set_grad_enabled(grads):
+        got = m(x, cos, sin)
+        for i in range(2):
+            for b in range(B):
+                one = m(x[i, b], cos, sin)
+                for g, w in zip(got, one):
+                    assert same(g[i, b], w), (i, b)
+    pos = torch.arange(S, dtype=torch.int32, device=DEV).expand(2, B, S).contiguous()
+    for g, w in zip(got, m(x, cos, sin, pos)):
+        assert same(g, w)
+
+
+def test_sequences_longer_than_the_tables(w8):
+    m = qkv_module(w8, 4)
+    cos, sin = turns(8)
+    x = torch.randn(2, 16, 64, device=DEV).to(BF)
+    with torch.no_grad():
+        # whole runs of the table, in a batch or not, and one sequence alone
+        flat = m(x.reshape(32, 64), cos, sin)
+        for a, b in zip(m(x, cos, sin), flat):
+            assert same(a.reshape(b.shape), b)
+        for a, b in zip(m(x[:1, :13], cos, sin), m(x[0, :13], cos, sin)):
+            assert same(a[0], b)
+        # a second sequence would start inside a run
+        with pytest.raises(ValueError, match="position"):
+            m(x[:, :13].contiguous(), cos, sin)
+        assert m(x[:, :0], cos, sin)[0].shape == (2, 0, 4, 32)
+        with pytest.raises(ValueError):
+            m(x, cos, sin[:7])
+        with pytest.raises(TypeError):
+            m(x, None, sin)
+        with pytest.raises(w8.W8A8Error):
+            m(x, cos[:0], sin[:0])
+        # nothing to turn: no positions, whatever the tables' length
+        none = torch.empty(5, 0, device=DEV)
+        for a, b in zip(m(x, none, none), m(x.reshape(32, 64), none, none)):
+            assert same(a.reshape(b.shape), b)

@@ -101,9 +101,28 @@ class W8A8QKV(torch.nn.Module):
             self.register_parameter(name, None if w is None else
                                     torch.nn.Parameter(w.detach().to(torch.bfloat16).contiguous()))
 
+    @staticmethod
+    def _tables(tokens: int, sequences: int, cos: torch.Tensor, sin: torch.Tensor):
+        """The tables cut to the sequences' length, so that row mod P of the
+        flattened batch is the index in a sequence."""
+        if any(not isinstance(t, torch.Tensor) or t.dim() != 2 for t in (cos, sin)) or cos.shape != sin.shape or \
+                cos.numel() == 0:
+            return cos, sin     # what is wrong is named by the call, and without a rotation there are no positions
+        P = cos.shape[0]
+        if sequences > 1 and tokens > P and tokens % P:
+            raise ValueError(f"sequences of {tokens} tokens are no whole runs of the {P} positions of cos and sin: "
+                             "give each token's position")
+        if 0 < tokens < P:
+            return cos[:tokens], sin[:tokens]
+        return cos, sin
+
     def forward(self, x: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor | None = None):
         """x [..., features] -> q [..., Hq, D], k and v [..., Hk, D]; cos, sin
-        fp32 [P, rot/2], positions int32, one per token (None: token mod P)."""
+        fp32 [P, rot/2], positions int32, one per token.  Without positions a
+        token is at its index in its sequence (the last dimension before the
+        features), in sequences longer than the tables at that index mod P."""
+        if positions is None and x.dim() > 2:
+            cos, sin = self._tables(x.shape[-2], x.shape[:-2].numel(), cos, sin)
         qkv = self.proj(x).reshape(-1, self.proj.out_features)
         if positions is not None:
             positions = positions.reshape(-1)

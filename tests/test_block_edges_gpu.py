@@ -135,3 +135,17 @@ def test_sequences_longer_than_the_tables(w8):
         none = torch.empty(5, 0, device=DEV)
         for a, b in zip(m(x, none, none), m(x.reshape(32, 64), none, none)):
             assert same(a.reshape(b.shape), b)
+
+
+@pytest.mark.parametrize("grads", [False, True])
+@pytest.mark.parametrize("norms", [False, True])
+def test_what_a_hook_on_the_projection_keeps(w8, grads, norms):
+    m = qkv_module(w8, 5, norms)
+    cos, sin = turns(7)
+    kept = []
+    m.proj.register_forward_hook(lambda mod, args, out: kept.append((out, out.detach().clone())))
+    x = torch.randn(2, 7, 64, device=DEV).to(BF).requires_grad_(grads)
+    with torch.set_grad_enabled(grads):
+        m(x, cos, sin)
+    out, then = kept[0]
+    assert same(out, then)

@@ -133,8 +133,8 @@ class W8A8QKV(torch.nn.Module):
                                                  self.eps, self.interleaved)
         else:
             q, k, v = autograd._split(qkv, self.heads)
-            # in place: the packed rows are this call's own
-            block_ops.qk_norm_rope(q, k, self.q_weight, self.k_weight, cos, sin, positions, self.eps,
-                                   self.interleaved, q_out=q, k_out=k)
+            # not in place: a hook on the projection may keep its output
+            q, k = block_ops.qk_norm_rope(q, k, self.q_weight, self.k_weight, cos, sin, positions, self.eps,
+                                          self.interleaved)
         lead = x.shape[:-1]
         return tuple(t.reshape(*lead, *t.shape[1:]) for t in (q, k, v))

@@ -149,3 +149,16 @@ def test_what_a_hook_on_the_projection_keeps(w8, grads, norms):
         m(x, cos, sin)
     out, then = kept[0]
     assert same(out, then)
+
+
+def test_gradients_that_arrive_at_odd_addresses(w8):
+    m = qkv_module(w8, 6)
+    cos, sin = turns(5)
+    x = torch.randn(5, 64, device=DEV).to(BF).requires_grad_()
+    out = m(x, cos, sin)
+    ds = [torch.randn_like(t) for t in out]
+    odd = [torch.empty(t.numel() + 1, dtype=BF, device=DEV)[1:].view(t.shape).copy_(t) for t in ds]
+    leaves = [x, m.q_weight, m.k_weight]
+    want = torch.autograd.grad(out, leaves, ds, retain_graph=True)
+    got = torch.autograd.grad(out, leaves, odd)
+    assert all(same(a, b) for a, b in zip(got, want))

@@ -27,6 +27,13 @@ def _not_captured(name: str) -> None:
                            "*_backward entry points instead")
 
 
+def _aligned(grad):
+    """An output's gradient, contiguous and at an address that 16-byte loads
+    take: it may arrive as a piece of a larger tensor."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _FrozenLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, wq, w_scale, bias):
@@ -104,7 +111,7 @@ class _QKNormRope(torch.autograd.Function):
         dqkv = torch.empty_like(qkv)
         gq, gk, gv = _split(dqkv, ctx.heads)
         weights = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
-        _, _, gqw, gkw = block_ops.qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), q, k, q_weight, k_weight,
+        _, _, gqw, gkw = block_ops.qk_norm_rope_backward(_aligned(dq), _aligned(dk), q, k, q_weight, k_weight,
                                                          cos, sin, positions, ctx.eps, ctx.interleaved, weights,
                                                          q_grad=gq, k_grad=gk)
         gv.copy_(dv)

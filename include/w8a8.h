@@ -279,16 +279,19 @@ w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int
 
 /*
  * The linear from bf16 activations: w8a8_quantize_act and w8a8_linear (or
- * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  For
- * at most 16 tokens whose codes take at most 22 KB (one token of K = 22272,
- * five of 4096) it is one launch that reads the weight once and needs no
- * workspace; otherwise the codes are made in the workspace first (then the
- * few-token kernel up to 32 tokens, the K-split or the tiled kernel, by shape).
+ * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  Up to
+ * 32 tokens take a kernel that reads the weight once: up to 16 tokens where
+ * K >= 768 or N <= 8192 + 16 K, more where K >= 256 and N <= 16 min(K, 1024); it
+ * is one launch that needs no workspace for at most 16 tokens whose codes take
+ * at most 22 KB (one token of K = 22272, five of 4096).  Otherwise the codes are
+ * made in the workspace first (then the same kernel, the K-split or the tiled
+ * kernel, by shape).
  *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;
  *   y bf16 [M,N] 2-byte aligned; workspace of at least
- *   w8a8_linear_dynamic_workspace(M, N, K) bytes, 16-byte aligned (may be
- *   NULL where that is 0).  The workspace belongs to the call until its work
- *   on the stream is done: calls that may overlap need one each.
+ *   w8a8_linear_dynamic_workspace(M, N, K) bytes, 16-byte aligned (it may be
+ *   less, or NULL, where that one launch can do without).  The workspace
+ *   belongs to the call until its work on the stream is done: calls that may
+ *   overlap need one each.
  */
 size_t w8a8_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K);
 w8a8_status w8a8_linear_dynamic(const uint16_t *x, const int8_t *wq, const float *w_scale,

@@ -31,3 +31,15 @@ def test_positions_without_a_rotation_need_a_table_size(w8):
         assert call(None, P, rot=16) == SHAPE
     assert call(A, 1) == back(A, 1) == 0
     assert call(A + 2, 4, M=4) == ALIGN
+
+
+@pytest.mark.parametrize("name", ["linear", "gated_linear"])
+def test_which_few_tokens_take_the_few_token_kernel(w8, name):
+    """Up to 16 tokens with codes that fit it need no workspace there; many
+    channels of a short K are left to the tiled kernel, whose codes do."""
+    ws = getattr(w8.lib, f"w8a8_{name}_dynamic_workspace")
+    for M in (1, 5, 16):
+        for K in (16, 64, 256, 512, 752):
+            assert ws(M, 8192 + 16 * K, K) == 0
+            assert ws(M, 8192 + 16 * K + 1, K) >= M * K + 4 * M
+        assert ws(M, 2 ** 20, 768) == 0

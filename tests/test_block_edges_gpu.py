@@ -162,3 +162,29 @@ def test_gradients_that_arrive_at_odd_addresses(w8):
     want = torch.autograd.grad(out, leaves, ds, retain_graph=True)
     got = torch.autograd.grad(out, leaves, odd)
     assert all(same(a, b) for a, b in zip(got, want))
+
+
+# ---- few tokens ----
+
+@pytest.mark.parametrize("M", [1, 3, 16, 17, 32])
+@pytest.mark.parametrize("N,K", [(8448, 16), (8449, 16), (12289, 256), (4096, 256), (4097, 256), (150003, 768)])
+def test_either_side_of_the_few_token_kernel(w8, M, N, K):
+    """The same bits by quantize + linear, by the kernel chosen, and (up to 16
+    tokens) by the few-token kernel without a workspace, or with one too small
+    for the other; the largest weight has more groups of channels to a
+    workgroup than their scales fit LDS at once."""
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    for per, f, raw in ((1, w8.linear, w8.lib.w8a8_linear_dynamic),
+                        (2, w8.gated_linear, w8.lib.w8a8_gated_linear_dynamic)):
+        wq = torch.randint(-127, 128, (per * N, K), generator=g, device=DEV, dtype=torch.int8)
+        ws = torch.rand(per * N, generator=g, device=DEV) * 0.01
+        b = torch.randn(per * N, generator=g, device=DEV).to(BF)
+        x = torch.randn(M, K, generator=g, device=DEV).to(BF)
+        want = f(*w8.quantize_act(x), wq, ws, b)
+        assert same((w8.linear_dynamic if per == 1 else w8.gated_linear_dynamic)(x, wq, ws, b), want)
+        small = torch.empty(16, dtype=torch.uint8, device=DEV)
+        for space, size in ((None, 0), (small.data_ptr(), 16)) if M <= 16 else ():
+            y = torch.full((M, N), 7.0, dtype=BF, device=DEV)
+            status = raw(x.data_ptr(), wq.data_ptr(), ws.data_ptr(), b.data_ptr(), y.data_ptr(), M, N, K, 0, space,
+                         size, torch.cuda.current_stream().cuda_stream)
+            assert status == 0 and same(y, want)

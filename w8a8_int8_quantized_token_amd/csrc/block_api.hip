@@ -45,10 +45,32 @@ struct DynamicPlan {
   int64_t xq, xs, slices;
   int64_t bytes;
 };
-DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated) {
+// Where the few-token kernel is the faster one.  It walks 16 channels at a time,
+// one group to a compute unit up to 4096 channels, and a group takes 0.8 us (1.2
+// beyond 16 tokens) however short K is, so many channels of a short K go to the
+// tiled kernel; beyond 16 tokens short rows do too, as the codes are a launch of
+// their own there.  Cold weights, us (quantize + tiled / few tokens):
+//   1 and 16 tokens, K = 64: 8192 channels 5.8 / 5.7 and 6.4 / 6.3, 12288 6.0 / 6.3
+//   and 6.5 / 7.1, 65536 11.7 / 16.4 and 12.2 / 17.4; K = 256: 12288 6.7 / 6.5 and
+//   7.0 / 7.2, 16384 6.7 / 7.2 and 7.1 / 8.0; K = 512: 16384 8.2 / 8.2 and 8.7 / 9.0,
+//   32768 10.4 / 11.5 and 10.8 / 12.4; K = 768: 32768 11.9 / 11.8 and 12.4 / 13.1,
+//   65536 18.7 / 18.8 and 19.4 / 20.5; K = 4096: 65536 56 / 47 and 57 / 57;
+//   17 and 32 tokens, K = 64: 512 channels 5.8 / 6.2 and 5.6 / 6.2; K = 256: 4096
+//   6.8 / 6.6 and 6.9 / 6.7, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 16384 11.8 / 11.9
+//   and 12.0 / 12.4, 32768 15.1 / 16.8 and 15.5 / 17.9; K = 2048: 16384 17.9 / 15.7 and
+//   18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K = 8192: 16384 54 / 34 and 54 /
+//   38, 32768 59 / 59 and 61 / 67.
+bool few_tokens_pay(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16) return K >= 768 || N <= 8192 + 16 * K;
+  return K >= 256 && N <= 16 * std::min<int64_t>(K, 1024);
+}
+// `room`: there is a workspace; without one the few-token kernel takes what
+// needs none.
+DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated, bool room) {
   DynamicPlan p{};
-  p.few = M <= w8a8::kFewTokens;
-  p.codes = !p.few || !w8a8::few_tokens_in_lds(M, K);
+  const bool in_lds = w8a8::few_tokens_in_lds(M, K);
+  p.few = M <= w8a8::kFewTokens && (few_tokens_pay(M, N, K) || (in_lds && !room));
+  p.codes = !p.few || !in_lds;
   p.splits = 1;
   p.tile = -1;
   Pieces w;
@@ -70,7 +92,8 @@ w8a8_status dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, c
   if (!shape_ok(M, N, K, gated ? 2 : 1)) return W8A8_ERR_SHAPE;
   if (act < 0 || act > 1) return W8A8_ERR_ARG;
   if (M == 0) return W8A8_OK;
-  const DynamicPlan p = dynamic_plan(M, N, K, gated);
+  DynamicPlan p = dynamic_plan(M, N, K, gated, true);
+  if (!ws || !aligned(ws, 16) || ws_bytes < (size_t)p.bytes) p = dynamic_plan(M, N, K, gated, false);
   if (!x || !wq || !w_scale || !y || (p.bytes && !ws)) return W8A8_ERR_NULL;
   if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(w_scale, 4) || !aligned(y, 2) || (bias && !aligned(bias, 2)) ||
       (p.bytes && !aligned(ws, 16)))
@@ -273,7 +296,7 @@ w8a8::RopeView view(const uint16_t* p, int64_t row, int64_t head) { return {cons
 extern "C" {
 
 size_t w8a8_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K) {
-  return shape_ok(M, N, K, 1) ? (size_t)dynamic_plan(M, N, K, false).bytes : 0;
+  return shape_ok(M, N, K, 1) ? (size_t)dynamic_plan(M, N, K, false, true).bytes : 0;
 }
 
 w8a8_status w8a8_linear_dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale, const uint16_t* bias,
@@ -303,7 +326,7 @@ w8a8_status w8a8_gated_linear(const int8_t* xq, const float* x_scale, const int8
 }
 
 size_t w8a8_gated_linear_dynamic_workspace(int64_t M, int64_t N, int64_t K) {
-  return shape_ok(M, N, K, 2) ? (size_t)dynamic_plan(M, N, K, true).bytes : 0;
+  return shape_ok(M, N, K, 2) ? (size_t)dynamic_plan(M, N, K, true, true).bytes : 0;
 }
 
 w8a8_status w8a8_gated_linear_dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale,

@@ -281,9 +281,10 @@ w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int
  * The linear from bf16 activations: w8a8_quantize_act and w8a8_linear (or
  * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  Up to
  * 32 tokens take a kernel that reads the weight once: up to 16 tokens where
- * K >= 768 or N <= 8192 + 16 K, more where K >= 256 and N <= 16 min(K, 1024); it
+ * K >= 768 or N <= 8192 + 16 K, more where K >= 256 and N <= 8 min(K, 2048); it
  * is one launch that needs no workspace for at most 16 tokens whose codes take
- * at most 22 KB (one token of K = 22272, five of 4096).  Otherwise the codes are
+ * at most 22 KB (one token of K = 22272, five of 4096; with more, 9 to 16
+ * tokens take it only where N <= 40960 or K >= 8192).  Otherwise the codes are
  * made in the workspace first (then the same kernel, the K-split or the tiled
  * kernel, by shape).
  *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;

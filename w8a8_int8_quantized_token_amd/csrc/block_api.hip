@@ -54,22 +54,28 @@ struct DynamicPlan {
 //   and 6.5 / 7.1, 65536 11.7 / 16.4 and 12.2 / 17.4; K = 256: 12288 6.7 / 6.5 and
 //   7.0 / 7.2, 16384 6.7 / 7.2 and 7.1 / 8.0; K = 512: 16384 8.2 / 8.2 and 8.7 / 9.0,
 //   32768 10.4 / 11.5 and 10.8 / 12.4; K = 768: 32768 11.9 / 11.8 and 12.4 / 13.1,
-//   65536 18.7 / 18.8 and 19.4 / 20.5; K = 4096: 65536 56 / 47 and 57 / 57;
-//   17 and 32 tokens, K = 64: 512 channels 5.8 / 6.2 and 5.6 / 6.2; K = 256: 4096
-//   6.8 / 6.6 and 6.9 / 6.7, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 16384 11.8 / 11.9
-//   and 12.0 / 12.4, 32768 15.1 / 16.8 and 15.5 / 17.9; K = 2048: 16384 17.9 / 15.7 and
-//   18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K = 8192: 16384 54 / 34 and 54 /
-//   38, 32768 59 / 59 and 61 / 67.
-bool few_tokens_pay(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return K >= 768 || N <= 8192 + 16 * K;
-  return K >= 256 && N <= 16 * std::min<int64_t>(K, 1024);
+//   65536 18.7 / 18.8 and 19.4 / 20.5;
+//   12 and 16 tokens whose codes come from memory, K = 4096: 32768 37 / 31 and 37 /
+//   32, 40960 73 / 36 and 73 / 37, 65536 57 / 53 and 57 / 56; K = 5120: 50000 52 / 53
+//   and 52 / 57, 65536 62 / 64 and 62 / 70; K = 8192: 65536 114 / 92 and 115 / 98
+//   (8 tokens, K = 5120: 65536 61 / 61);
+//   17 and 32 tokens, K = 64: 512 channels 5.8 / 6.2 and 5.6 / 6.2; K = 256: 2048
+//   6.8 / 6.7 and 6.9 / 6.8, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 8192 11.3 / 9.4
+//   and 11.5 / 9.6, 16384 11.8 / 11.9 and 12.0 / 12.4 (warm 9.3 / 10.9 and 9.5 / 11.3);
+//   K = 2048: 16384 17.9 / 15.7 and 18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K =
+//   8192: 16384 54 / 34 and 54 / 38, 32768 59 / 59 and 61 / 67.
+bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool in_lds) {
+  if (M > 16) return K >= 256 && N <= 8 * std::min<int64_t>(K, 2048);
+  if (M > 8 && !in_lds && N > 40960 && K < 8192) return false;
+  return K >= 768 || N <= 8192 + 16 * K;
 }
+
 // `room`: there is a workspace; without one the few-token kernel takes what
 // needs none.
 DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated, bool room) {
   DynamicPlan p{};
   const bool in_lds = w8a8::few_tokens_in_lds(M, K);
-  p.few = M <= w8a8::kFewTokens && (few_tokens_pay(M, N, K) || (in_lds && !room));
+  p.few = M <= w8a8::kFewTokens && (few_tokens_pay(M, N, K, in_lds) || (in_lds && !room));
   p.codes = !p.few || !in_lds;
   p.splits = 1;
   p.tile = -1;

@@ -43,3 +43,13 @@ def test_which_few_tokens_take_the_few_token_kernel(w8, name):
             assert ws(M, 8192 + 16 * K, K) == 0
             assert ws(M, 8192 + 16 * K + 1, K) >= M * K + 4 * M
         assert ws(M, 2 ** 20, 768) == 0
+
+
+def test_which_linears_are_cut_into_k_ranges(w8):
+    """Ranges need slices beside the codes: for K from 6144 on or up to 64
+    tokens, where the linear has few tiles."""
+    def slices(M, N, K):
+        return w8.lib.w8a8_linear_dynamic_workspace(M, N, K) - (M * K + 4 * M + 255) // 256 * 256 >= 8 * M * N
+
+    assert slices(64, 2048, 4096) and slices(33, 512, 5120) and slices(512, 2048, 6144) and slices(256, 2048, 8192)
+    assert not slices(65, 2048, 4096) and not slices(512, 2048, 4096) and not slices(256, 512, 6128)

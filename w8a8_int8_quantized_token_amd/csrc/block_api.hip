@@ -70,6 +70,13 @@ bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool in_lds) {
   return K >= 768 || N <= 8192 + 16 * K;
 }
 
+// More tokens: K ranges where the linear is hardly ever faster whole, be the weight
+// cold or warm (us whole / in ranges, cold; warm): 256 x 2048 x 6144 38.9 / 28.5; 27.9 /
+// 27.7, 64 x 2048 x 4096 27.8 / 20.6; 19.1 / 18.9, but 512 x 2048 x 4096 27.8 / 29.3;
+// 21.6 / 27.9, 256 x 512 x 4096 20.7 / 23.7; 20.1 / 22.1, 192 x 2048 x 5120 33.6 /
+// 28.8; 23.8 / 27.6.  (At the worst of it, 1024 x 1024 x 6144, 40.3 / 35.5; 30.9 / 35.7.)
+bool ranges_pay(int64_t M, int64_t K) { return K >= 6144 || M <= 64; }
+
 // `room`: there is a workspace; without one the few-token kernel takes what
 // needs none.
 DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated, bool room) {
@@ -84,7 +91,7 @@ DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated, bool room)
     p.xq = w.add(M * K);
     p.xs = w.add(4 * M);
   }
-  if (!p.few && !gated) {
+  if (!p.few && !gated && ranges_pay(M, K)) {
     p.splits = w8a8::select_splitk(M, N, K, &p.tile);
     if (p.splits > 1) p.slices = w.add((int64_t)w8a8_linear_splitk_workspace(M, N, p.splits));
   }

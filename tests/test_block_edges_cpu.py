@@ -1,6 +1,11 @@
 """Host-side checks at the edges of the operators around the linear: refusals
 before any launch (fake pointers, never dereferenced) and which form a call
 takes, by its workspace."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 
 A = 0x10000
@@ -53,3 +58,15 @@ def test_which_linears_are_cut_into_k_ranges(w8):
 
     assert slices(64, 2048, 4096) and slices(33, 512, 5120) and slices(512, 2048, 6144) and slices(256, 2048, 8192)
     assert not slices(65, 2048, 4096) and not slices(512, 2048, 4096) and not slices(256, 512, 6128)
+
+
+@pytest.mark.parametrize("stale", [False, True])
+def test_native_calls_that_are_missing_or_do_not_load(tmp_path, stale):
+    name = "w8a8_int8_quantized_token_amd"
+    here = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), name)
+    shutil.copytree(here, tmp_path / name, ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__", "_calls.so"))
+    if stale:
+        (tmp_path / name / "_calls.so").write_bytes(b"no library")
+    r = subprocess.run([sys.executable, "-c", f"import {name}"], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 1
+    assert "ImportError" in r.stderr and "_calls.so is not built or does not load" in r.stderr and "build.py" in r.stderr

@@ -1,7 +1,8 @@
-"""ctypes loader for libw8a8.so (built in-tree by ``build.py``).
+"""Loaders for libw8a8.so (ctypes) and _calls.so (the binding's native calls),
+both built in-tree by ``build.py``.
 
-There is no fallback: if the library is missing or does not load, importing
-the package raises, so nothing silently runs on another path.
+There is no fallback: if one is missing or does not load, importing the
+package raises, so nothing silently runs on another path.
 """
 from __future__ import annotations
 
@@ -9,6 +10,8 @@ import ctypes
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw8a8.so")
+
+CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
 
 # Status codes of include/w8a8.h
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_LAUNCH, ERR_ARG, ERR_SCRATCH = range(7)
@@ -20,6 +23,17 @@ class W8A8Error(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {status_str(status)} (status {status})")
+
+
+def load_calls():
+    """The module of the native calls, which is tied to the torch it was built
+    against."""
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise ImportError(f"{CALLS_PATH} is not built or does not load (it belongs to the torch and Python it was "
+                          "built against); run `python w8a8_int8_quantized_token_amd/build.py`") from e
+    return _calls
 
 
 def _load() -> ctypes.CDLL:

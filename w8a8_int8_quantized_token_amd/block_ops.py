@@ -16,9 +16,9 @@ from __future__ import annotations
 
 import torch
 
-from . import _calls
-from ._lib import check, lib
+from ._lib import check, lib, load_calls
 
+_calls = load_calls()
 ACTS = {"silu": 0, "gelu": 1}
 
 

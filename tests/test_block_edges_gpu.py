@@ -189,3 +189,45 @@ def test_either_side_of_the_few_token_kernel(w8, M, N, K):
             status = raw(x.data_ptr(), wq.data_ptr(), ws.data_ptr(), b.data_ptr(), y.data_ptr(), M, N, K, 0, space,
                          size, torch.cuda.current_stream().cuda_stream)
             assert status == 0 and same(y, want)
+
+
+# ---- backward nodes under a capture ----
+
+def test_every_backward_node_refuses_a_capture(w8, monkeypatch):
+    """Each node is run with the stream said to be capturing (no capture is
+    made): it raises before it launches anything, and no leaf gets a gradient."""
+    K = 64
+    torch.manual_seed(7)
+    lin = torch.nn.Linear(K, K, device=DEV, dtype=BF)
+    linear = w8.W8A8Linear.from_linear(lin)
+    mlp = w8.W8A8GatedMLP.from_linears(lin, lin, lin)
+    qkv = qkv_module(w8, 8)
+    cos, sin = turns(4)
+    qkv_only = torch.randn(4, qkv.proj.out_features, device=DEV).to(BF)
+    w, w2 = torch.randn(K, K, device=DEV).to(BF), torch.randn(2 * K, K, device=DEV).to(BF)
+
+    class Projection(torch.nn.Module):      # gives the norm's node a leaf of its own
+        out_features = qkv.proj.out_features
+
+        def forward(self, x):
+            return x
+
+    alone = w8.W8A8QKV(Projection(), 4, 2, qkv.q_weight, qkv.k_weight)
+    for name, f, inputs in (
+            ("linear", lambda x: linear(x), [torch.randn(4, K, device=DEV).to(BF)]),
+            ("mlp", lambda x: mlp(x), [torch.randn(4, K, device=DEV).to(BF)]),
+            ("linear_ste", lambda x, w: w8.linear_ste(x, w), [torch.randn(4, K, device=DEV).to(BF), w]),
+            ("gated_linear_ste", lambda x, w: w8.gated_linear_ste(x, w), [torch.randn(4, K, device=DEV).to(BF), w2]),
+            ("qkv", lambda x: torch.cat(qkv(x, cos, sin), 1), [torch.randn(4, K, device=DEV).to(BF)]),
+            ("norm", lambda x: torch.cat(alone(x, cos, sin), 1), [qkv_only])):
+        leaves = [t.requires_grad_() for t in inputs]
+        y = f(*leaves).sum()
+        with monkeypatch.context() as p:
+            p.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+            with pytest.raises(RuntimeError, match="cannot be captured"):
+                y.backward()
+        torch.cuda.synchronize()
+        assert all(t.grad is None for t in leaves), name
+        f(*leaves).sum().backward()
+        assert all(t.grad is not None for t in leaves), name
+    assert qkv.q_weight.grad is not None and alone.q_weight.grad is not None

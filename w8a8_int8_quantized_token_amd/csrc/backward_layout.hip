@@ -201,26 +201,33 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare p) {
   }
 }
 
-// Eight outputs per thread and step (n % 8 == 0), eight slices' loads in
-// flight: with one at a time the join of few outputs takes a memory latency
-// for each of its slices (46 of 1 x 512 values: 15 us).
+// Eight outputs per thread and step (n % 8 == 0).  Up to eight slices' loads are
+// in flight: with one at a time the join of few outputs takes a memory latency
+// for each of its slices (46 of 1 x 512 values: 15 us).  Only slices that are
+// there are read (two of 4096 x 2048 values: 17 us, and 36 when eight are always
+// read).
+template <int kSlices>
+__device__ __forceinline__ void add_slices(const f32x4* p, int64_t stride, f32x4& lo, f32x4& hi) {
+  f32x4 v[kSlices][2];
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) {
+    v[i][0] = __builtin_nontemporal_load(p + i * stride);
+    v[i][1] = __builtin_nontemporal_load(p + i * stride + 1);
+  }
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) lo += v[i][0], hi += v[i][1];
+}
 __device__ void join_slices(const JoinJob& j, int64_t block) {
-  const int64_t groups = j.n / 8;
+  const int64_t groups = j.n / 8, stride = j.n / 4;
   const f32x4* part = reinterpret_cast<const f32x4*>(j.part);
   for (int64_t g = block * kThreads + threadIdx.x; g < groups; g += j.blocks * kThreads) {
     f32x4 lo = f32x4{0, 0, 0, 0}, hi = lo;
-    for (int64_t c = 0; c < j.P; c += 8) {
-      f32x4 v[8][2];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const f32x4* p = part + ((c + i < j.P ? c + i : c) * j.n + g * 8) / 4;
-        v[i][0] = __builtin_nontemporal_load(p);
-        v[i][1] = __builtin_nontemporal_load(p + 1);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < j.P) lo += v[i][0], hi += v[i][1];
-    }
+    const f32x4* p = part + g * 2;
+    int64_t left = j.P;
+    for (; left >= 8; left -= 8, p += 8 * stride) add_slices<8>(p, stride, lo, hi);
+    if (left & 4) add_slices<4>(p, stride, lo, hi), p += 4 * stride;
+    if (left & 2) add_slices<2>(p, stride, lo, hi), p += 2 * stride;
+    if (left & 1) add_slices<1>(p, stride, lo, hi);
     *reinterpret_cast<u32x4*>(j.out + g * 8) = u32x4{pack2(lo[0], lo[1]), pack2(lo[2], lo[3]), pack2(hi[0], hi[1]), pack2(hi[2], hi[3])};
   }
 }

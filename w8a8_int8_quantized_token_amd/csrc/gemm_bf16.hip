@@ -48,8 +48,15 @@ hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, in
 // x 1024 x 2048 to 8192 x 4096 x 24576 (its choice was within 9% of the
 // fastest at each, 1% in the mean):
 //   3.77 + rounds * (tile + stages * max(stage, power)) + join,
-// stage the time of 128 K bytes of a tile alone on its compute unit, power
-// the same when `rate` TFLOP/s is what the whole chip's power limit allows.
+// stage the time of 128 K bytes of a tile alone on its compute unit, power the
+// same at `rate` TFLOP/s over the whole chip.  All are fitted numbers, no
+// properties of the chip: a rate above the 1.83 PFLOP/s that a loop of nothing
+// but fragment reads and MFMAs reaches (the whole 256x256 ring's) never binds, and
+// that tile's times are its stages' alone.  The measurements are of products by
+// themselves with their operands just laid out; in a whole backward pass large
+// ones take longer (4096^3 86 us by the model, 96 alone, 103 to 109 in the pass),
+// and a choice by a percent says nothing there: 4096 x 2048 x 16384 is 191 as two
+// ranges by the model and 192 whole on 128x256 tiles; the two ranges take 256 + 17.
 // Ranges pay where tiles leave units idle: 128 x 8192 x 24576: 133 us whole, 92
 // in ranges; 512 x 512 x 8192: 23.8 us whole, 13.9 in ranges; but 4096 x 4096 x
 // 4096: 100 us whole, 149 in two.

@@ -6,10 +6,12 @@
 // values of a channel and neither product leaves the registers.
 //
 // Bound by the matrix cores at many tokens (4MNK operations against
-// MK + 2NK + 2MN bytes): 8192 x 12288 x 4096 680 to 710 us, 2.3 to 2.4 POPS at
-// the package's power limit, where the linear of the same 24576 rows takes 820
-// us for its twice as many outputs.  Tiles by the linear's cost model for 2N
-// channels.
+// MK + 2NK + 2MN bytes): 8192 x 12288 x 4096 675 to 730 us, 2.3 to 2.4 POPS at
+// the package's power limit (1.67 GHz, matrix pipes busy 0.66 of the cycles), where
+// the linear of the same 24576 rows takes 820 us for its twice as many outputs.
+// Tiles by the linear's cost model for 2N channels, which counts one workgroup per
+// compute unit; the smaller tiles have two or three here, so for a few hundred
+// tokens its rounds are too many.
 #include "gemm_kernel.h"
 
 namespace w8a8 {

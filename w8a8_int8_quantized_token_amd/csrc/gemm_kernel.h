@@ -232,8 +232,8 @@ __device__ __forceinline__ void barrier() {
 // Operand types.  int8: v_mfma_i32_32x32x32_i8, 16 K bytes per lane and
 // step, int32 accumulators.  fp8 (e4m3): v_mfma_f32_32x32x64_f8f6f4 (the
 // scaled form with unit E8M0 scales, 127), 32 K bytes per lane and step,
-// fp32 accumulators.  bf16: v_mfma_f32_32x32x16_bf16, 16 K bytes (8 values)
-// per lane and step like int8, fp32 accumulators; K counts bytes for it too.
+// fp32 accumulators.  bf16: v_mfma_f32_16x16x32_bf16, 16 K bytes (8 values)
+// per lane and MFMA like int8, fp32 accumulators; K counts bytes for it too.
 // All take the lane's row of A and of B at the same K
 // positions, so any fixed assignment of K bytes to (lane half, byte) that is
 // the same for both operands gives the same dot products.

@@ -281,12 +281,12 @@ w8a8_status w8a8_mfma_ceiling(const int8_t *xq, const int8_t *wq, int64_t M, int
  * The linear from bf16 activations: w8a8_quantize_act and w8a8_linear (or
  * w8a8_linear_gelu when `gelu` is non-zero) in one call, the same bits.  Up to
  * 32 tokens take a kernel that reads the weight once: up to 16 tokens where
- * K >= 768 or N <= 8192 + 16 K, more where K >= 256 and N <= 8 min(K, 2048); it
- * is one launch that needs no workspace for at most 16 tokens whose codes take
- * at most 22 KB (one token of K = 22272, five of 4096; with more, 9 to 16
- * tokens take it only where N <= 40960 or K >= 8192).  Otherwise the codes are
- * made in the workspace first (then the same kernel, the K-split or the tiled
- * kernel, by shape).
+ * K >= 768 or N <= 8192 + 16 K, more where K >= 256 and N <= 8 min(K, 2048)
+ * (gated: or K >= 4096).  It is one launch that needs no workspace for at most
+ * 16 tokens whose codes take at most 22 KB (one token of K = 22272, five of
+ * 4096); for larger codes of 9 to 16 tokens the linear takes it only where
+ * N <= 40960 or K >= 8192.  Otherwise the codes are made in the workspace first
+ * (then the same kernel, the K-split or the tiled kernel, by shape).
  *   x bf16 [M,K] 16-byte aligned; wq [N,K], w_scale [N], bias [N] or NULL;
  *   y bf16 [M,N] 2-byte aligned; workspace of at least
  *   w8a8_linear_dynamic_workspace(M, N, K) bytes, 16-byte aligned (it may be
@@ -381,9 +381,9 @@ w8a8_status w8a8_gated_linear_backward(const uint16_t *dy, const int8_t *xq,
  * Arithmetic in fp32, rounded to bf16 once.  A row whose position is outside
  * [0, P) (padding) gets zeros in every head, and in the gradients, and adds
  * nothing to the weights' gradients, also where rot = 0 (the norm alone; P is
- * then looked at only where positions are given).  q_out and k_out may be q and k (same
- * strides) and overlap nothing otherwise, nor each other; Hq or Hk may be 0 (its
- * pointers are then not looked at).
+ * then looked at only where positions are given).  q_out and k_out may be q and
+ * k (same strides) and overlap nothing otherwise, nor each other; Hq or Hk may
+ * be 0 (its pointers are then not looked at).
  * The gradient takes the outputs' gradients dq, dk and the inputs q, k, and
  * writes dq_in, dk_in (bf16; they may be dq, dk or q, k with the same strides)
  * and, where not NULL, dq_weight, dk_weight (fp32 [D], summed over rows and

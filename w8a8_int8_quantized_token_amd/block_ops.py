@@ -293,7 +293,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float 
     first 2 * cos.shape[1] values by cos, sin fp32 [P, rot/2] at each row's
     position (int32 [M]; None: row mod P).  q_weight, k_weight: bf16 [D] or
     None.  Returns (q_out, k_out), new dense tensors unless given; they may be
-    q and k themselves.  Rows at a position outside [0, P) become zeros, also
+    q and k themselves and overlap nothing otherwise.  Rows at a position outside [0, P) become zeros, also
     where the tables have no columns (the norm alone)."""
     if q_out is None and k_out is None:
         out = _calls.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)

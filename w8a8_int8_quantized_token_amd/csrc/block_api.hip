@@ -63,10 +63,15 @@ struct DynamicPlan {
 //   6.8 / 6.7 and 6.9 / 6.8, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 8192 11.3 / 9.4
 //   and 11.5 / 9.6, 16384 11.8 / 11.9 and 12.0 / 12.4 (warm 9.3 / 10.9 and 9.5 / 11.3);
 //   K = 2048: 16384 17.9 / 15.7 and 18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K =
-//   8192: 16384 54 / 34 and 54 / 38, 32768 59 / 59 and 61 / 67.
-bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool in_lds) {
-  if (M > 16) return K >= 256 && N <= 8 * std::min<int64_t>(K, 2048);
-  if (M > 8 && !in_lds && N > 40960 && K < 8192) return false;
+//   8192: 16384 54 / 34 and 54 / 38, 32768 59 / 59 and 61 / 67;
+//   gated, where long rows go on paying: 12 and 16 tokens, K = 2048: 65536 channels
+//   54 / 47 and 54 / 49, K = 4096: 65536 119 / 95 and 118 / 97; 17 and 32 tokens, K =
+//   2048: 16384 22.1 / 21.7 and 22.8 / 22.7, 65536 55 / 59 and 55 / 62, K = 4096: 24576
+//   47 / 41 and 50 / 44, 65536 118 / 104 and 120 / 112, K = 8192: 32768 111 / 94 and 112 /
+//   105.
+bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds) {
+  if (M > 16) return K >= 256 && (N <= 8 * std::min<int64_t>(K, 2048) || (gated && K >= 4096));
+  if (!gated && M > 8 && !in_lds && N > 40960 && K < 8192) return false;
   return K >= 768 || N <= 8192 + 16 * K;
 }
 
@@ -82,7 +87,7 @@ bool ranges_pay(int64_t M, int64_t K) { return K >= 6144 || M <= 64; }
 DynamicPlan dynamic_plan(int64_t M, int64_t N, int64_t K, bool gated, bool room) {
   DynamicPlan p{};
   const bool in_lds = w8a8::few_tokens_in_lds(M, K);
-  p.few = M <= w8a8::kFewTokens && (few_tokens_pay(M, N, K, in_lds) || (in_lds && !room));
+  p.few = M <= w8a8::kFewTokens && (few_tokens_pay(M, N, K, gated, in_lds) || (in_lds && !room));
   p.codes = !p.few || !in_lds;
   p.splits = 1;
   p.tile = -1;

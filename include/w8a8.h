@@ -412,6 +412,79 @@ w8a8_status w8a8_qk_norm_rope_backward(
     int64_t Hk, int64_t D, int64_t rot, float eps, int interleaved, void *workspace,
     size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * The residual's addition, the root-mean-square norm of each row and its
+ * quantization in one pass, in front of a linear.  For rows of K values:
+ *   h = bf16(x + residual)                     (residual NULL: h = x),
+ *   v = fl32(h * weight)                       (weight NULL: ones),
+ *   s = fl32(max|v| / 127), xq = rne(fl32(v / s)) in [-127, 127]
+ *   (fp8 non-zero: / 448 and e4m3 codes, as w8a8_quantize_act_fp8),
+ *   x_scale = fl32(s / sqrt(mean(h^2) + eps)),
+ * so xq * x_scale is the normed row quantized as w8a8_quantize_act would the
+ * fp32 values: the norm's factor is common to a row, cancels in the codes and
+ * goes into the scale.  Codes are exact functions of the inputs; mean(h^2) is
+ * an fp32 sum.  A row whose s is zero (all zeros) has zero codes and scale.
+ * h is written where it is not NULL; it may be x or residual and overlaps
+ * nothing otherwise, and no other output overlaps anything.
+ * The gradient, the rounding to codes passed straight through, for dn (of the
+ * normed row) and dh (of h, from what else reads it; may be NULL):
+ *   r = 1 / sqrt(mean(h^2) + eps), hh = h r,
+ *   dx = bf16( dh + r (dn weight - hh mean(dn weight hh)) )  (x and residual),
+ *   dweight = sum over rows of dn hh, fp32, in a fixed order (may be NULL; it
+ *   needs the workspace; zeros without rows).
+ * dx may be dn, dh or h and overlaps nothing otherwise.  Arithmetic is fp32, each bf16
+ * output rounded once.  Of a row of zeros with eps = 0, r is taken as 0.
+ * Contract: 16 <= K <= 32768, K % 16 == 0; M times 64 (K <= 4096), 256 (K <=
+ * 16384) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; finite inputs whose
+ * squares' sum and products with the weight are finite in fp32; all bf16
+ * pointers and the codes 16-byte aligned, scales and dweight 4-byte aligned.
+ */
+w8a8_status w8a8_add_rms_norm_quantize(const uint16_t *x, const uint16_t *residual,
+                                       const uint16_t *weight, uint16_t *h, void *xq,
+                                       float *x_scale, int64_t M, int64_t K, float eps, int fp8,
+                                       hipStream_t stream);
+size_t w8a8_add_rms_norm_backward_workspace(int64_t M, int64_t K);
+w8a8_status w8a8_add_rms_norm_backward(const uint16_t *dn, const uint16_t *dh, const uint16_t *h,
+                                       const uint16_t *weight, uint16_t *dx, float *dweight,
+                                       int64_t M, int64_t K, float eps, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The linear with a low-rank adapter for each token, of a set of L adapters of
+ * rank R that share the weight: a bf16 [L,R,K], b bf16 [L,N,R], scaling fp32
+ * [L], ids int32 [M] (the token's adapter; outside [0, L): none).  With
+ * i = ids[m] and x = xq * x_scale:
+ *   t[m,r] = bf16( scaling[i] * sum_k x[m,k] * a[i][r,k] ),
+ *   y[m,n] = bf16( v + sum_r t[m,r] * b[i][n,r] ),  v the fp32 value of w8a8_linear.
+ * Sums are fp32; t is rounded because it is an operand of the bf16 matrix
+ * cores.  A token without an adapter has the bits of w8a8_linear, and no
+ * token's result depends on another adapter's values (be they NaN) or on its
+ * neighbours.  Adapters of different ranks are padded with zeros.  Any order
+ * of ids is right; long runs of tokens with the same adapter are the fast one.
+ * The dynamic form takes bf16 activations, with the same bits as
+ * w8a8_quantize_act and w8a8_linear_adapters: two launches for a few tokens.
+ * Contract as for w8a8_linear, and 8 <= R <= 128, R % 8 == 0, 1 <= L <= 65536;
+ * a and b 16-byte aligned, scaling and ids 4-byte aligned.  Workspace as for
+ * w8a8_linear_dynamic (always needed).  `tile` as for w8a8_linear_tile, for
+ * tests and sweeps: every tile gives the same bits as each other (a few tokens'
+ * kernel and the K split, which tile < 0 may choose, sum the adapters' products
+ * in another order).
+ */
+size_t w8a8_linear_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int dynamic);
+w8a8_status w8a8_linear_adapters(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                                 const float *w_scale, const uint16_t *bias, const uint16_t *a,
+                                 const uint16_t *b, const float *scaling, const int32_t *ids,
+                                 uint16_t *y, int64_t M, int64_t N, int64_t K, int64_t R,
+                                 int64_t L, int tile, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+w8a8_status w8a8_linear_adapters_dynamic(const uint16_t *x, const int8_t *wq,
+                                         const float *w_scale, const uint16_t *bias,
+                                         const uint16_t *a, const uint16_t *b,
+                                         const float *scaling, const int32_t *ids, uint16_t *y,
+                                         int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                                         void *workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -82,6 +82,12 @@ def _load() -> ctypes.CDLL:
         "w8a8_qk_norm_rope_backward_workspace": (sz, [i64, i64, i64, i64]),
         "w8a8_qk_norm_rope_backward": (st, [*view, *view, *view, *view, p, p, p, p, p, *view, *view, p, p, i64,
                                             i64, i64, i64, i64, i64, ctypes.c_float, i32, p, sz, p]),
+        "w8a8_add_rms_norm_quantize": (st, [p, p, p, p, p, p, i64, i64, ctypes.c_float, i32, p]),
+        "w8a8_add_rms_norm_backward_workspace": (sz, [i64, i64]),
+        "w8a8_add_rms_norm_backward": (st, [p, p, p, p, p, p, i64, i64, ctypes.c_float, p, sz, p]),
+        "w8a8_linear_adapters_workspace": (sz, [i64, i64, i64, i64, i32]),
+        "w8a8_linear_adapters": (st, [p] * 10 + [i64] * 5 + [i32, p, sz, p]),
+        "w8a8_linear_adapters_dynamic": (st, [p] * 9 + [i64] * 5 + [p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

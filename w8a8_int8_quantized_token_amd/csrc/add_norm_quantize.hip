@@ -1,0 +1,387 @@
+// The residual's addition, the root-mean-square norm of each row and its codes
+// in one pass, and the gradient.  For rows x, residual [K] and a weight w:
+//   h = bf16(x + residual),  v = fl32(h w),  s = fl32(max|v| / 127),
+//   q = rne(fl32(v / s))  (e4m3: / 448 and the e4m3 rounding),
+//   scale = fl32(s / rms),  rms = sqrt(mean(h^2) + eps).
+// The normed value v / rms is never formed: its factor 1 / rms is common to the
+// row, so it cancels in v / s and goes into the scale.  h w is exact (8 + 8
+// bits), so the codes depend on no order of summation; the sum of squares
+// enters the scale alone.
+//
+// Gradient with the rounding to codes passed straight through, for dn (of the
+// normed row) and dh (of h, from what else reads it), r = 1 / rms, hh = h r:
+//   dx = dresidual = dh + r (dn w - hh mean(dn w hh)),
+//   dw = sum over rows of dn hh.
+//
+// Bound by memory: 7 bytes per value forward (3 without a residual), 8 backward
+// (6 without dh).  A row stays in registers between its reductions and its
+// codes.
+#include "kernels.h"
+#include "quant_codes.h"
+
+#include <algorithm>
+
+namespace w8a8 {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWave = 64;
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+__device__ __forceinline__ float wave_maxf(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+
+// fl32(v / s) for any fp32 |v| <= 448 s, from the correctly rounded r = 1 / s:
+// one correction step brings v r within a step of the quotient, and the second
+// then rounds it correctly (Markstein's theorem).  (For the bf16 v of
+// quant_codes.h one step gives the same codes; v has twice their bits here.)
+__device__ __forceinline__ float quotient(float v, float s, float r) {
+  float q = v * r;
+  q = fmaf(fmaf(-q, s, v), r, q);
+  return fmaf(fmaf(-q, s, v), r, q);
+}
+template <bool F8>
+__device__ __forceinline__ u32x2 quantize8(const float* v, const RowScale& rs) {
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = quotient(v[e] * rs.xs, rs.ss, rs.r);
+    constexpr float kTop = F8 ? 448.0f : 127.0f;
+    f[e] = __builtin_amdgcn_fmed3f(F8 ? q : __builtin_rintf(q), -kTop, kTop);
+    if (F8) f[e] = __builtin_copysignf(f[e], v[e]);   // (the correction turns -0 into +0)
+  }
+  if constexpr (F8) {
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
+    return u32x2{(uint32_t)lo, (uint32_t)hi};
+  }
+  return u32x2{pack4((int)f[0], (int)f[1], (int)f[2], (int)f[3]), pack4((int)f[4], (int)f[5], (int)f[6], (int)f[7])};
+}
+
+struct Norm {
+  const u32x4 *x, *residual, *weight;   // rows of `chunks` 16-byte pieces; residual, weight or null
+  u32x4* h;                             // or null
+  u32x2* q;
+  float* scale;
+  int64_t M;
+  int chunks;
+  float eps;
+};
+
+// kWaves wavefronts to a row (below four of them: four rows to a workgroup),
+// kPieces 16-byte pieces to a lane.
+template <int kWaves, int kPieces, bool F8>
+__global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel(Norm a) {
+  constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves, kStride = kWaves * kWave;
+  __shared__ f32x2 part[kRows > 1 ? 1 : kWaves];
+  const int tid = threadIdx.x % kStride;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kStride;
+  if (kRows > 1 && row >= a.M) return;   // whole wavefronts, and no barriers with several rows
+  const int64_t base = row * a.chunks;
+
+  u32x4 h[kPieces], w[kPieces], other[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = tid + i * kStride;
+    h[i] = other[i] = u32x4{0, 0, 0, 0};
+    w[i] = u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};   // ones
+    if (c < a.chunks) {
+      h[i] = __builtin_nontemporal_load(a.x + base + c);
+      if (a.residual != nullptr) other[i] = __builtin_nontemporal_load(a.residual + base + c);
+      if (a.weight != nullptr) w[i] = a.weight[c];
+    }
+  }
+  float sq = 0.0f, top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if (a.residual != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        h[i][e] = pack2(low(h[i][e]) + low(other[i][e]), high(h[i][e]) + high(other[i][e]));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = low(h[i][e]), hi = high(h[i][e]);
+      sq = fmaf(lo, lo, sq);
+      sq = fmaf(hi, hi, sq);
+      top = fmaxf(top, fmaxf(fabsf(lo * low(w[i][e])), fabsf(hi * high(w[i][e]))));
+    }
+  }
+  if (a.h != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = tid + i * kStride;
+      if (c < a.chunks) a.h[base + c] = h[i];
+    }
+  }
+  sq = wave_sum(sq);
+  top = wave_maxf(top);
+  if constexpr (kWaves > 1) {
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = f32x2{sq, top};
+    __syncthreads();
+    sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+      const f32x2 p = part[k];
+      sq += p[0];
+      top = fmaxf(top, p[1]);
+    }
+  }
+  const RowScale rs = row_scale_of<F8>(top);
+  const bool zero = rs.s == 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = tid + i * kStride;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = low(h[i][e]) * low(w[i][e]);
+      v[2 * e + 1] = high(h[i][e]) * high(w[i][e]);
+    }
+    if (c < a.chunks) a.q[base + c] = zero ? u32x2{0, 0} : quantize8<F8>(v, rs);
+  }
+  if (tid == 0) a.scale[row] = zero ? 0.0f : rs.s / sqrtf(sq / (float)(a.chunks * 8) + a.eps);
+}
+
+template <int kWaves, int kPieces>
+hipError_t forward(const Norm& a, bool fp8, hipStream_t s) {
+  constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
+  const dim3 grid((unsigned)((a.M + kRows - 1) / kRows)), block(kWave * (kWaves > 4 ? kWaves : 4));
+  if (fp8) hipLaunchKernelGGL((norm_kernel<kWaves, kPieces, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_kernel<kWaves, kPieces, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+// ---- gradient ----
+
+struct NormGrad {
+  const u32x4 *dn, *dh, *h, *weight;   // dh, weight or null
+  u32x4* dx;
+  float* part;   // [gridDim.x][8 * chunks], or null
+  int64_t M;
+  int chunks;
+  float eps;
+};
+
+// A workgroup takes every gridDim.x-th row and keeps its rows' sums for the
+// weight's gradient in registers.  kAhead: the next row's loads are in flight
+// meanwhile.  Long rows leave no registers for that, and the longest
+// (kReload) none for the row itself, which is then read again after the
+// reductions (from the cache).
+enum class Rows { kAhead, kKept, kReload };
+template <int kThreads, int kPieces, Rows kRows>
+__global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGrad a) {
+  constexpr int kWaves = kThreads / kWave;
+  constexpr u32x4 kZeros = {0, 0, 0, 0}, kOnes = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+  __shared__ f32x2 part[2][kWaves];
+  const int tid = threadIdx.x;
+  float sum[kPieces][8];
+  u32x4 w[kPieces];
+  auto weight = [&](int i) __attribute__((always_inline)) {
+    const int c = tid + i * kThreads;
+    return a.weight != nullptr && c < a.chunks ? a.weight[c] : kOnes;
+  };
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if constexpr (kRows != Rows::kReload) w[i] = weight(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[i][e] = 0.0f;
+  }
+  struct Piece {
+    u32x4 h, dn, dh;
+  };
+  auto load = [&](int64_t row, int i, Piece& p) __attribute__((always_inline)) {
+    const int c = tid + i * kThreads;
+    p.h = p.dn = p.dh = kZeros;
+    if (c < a.chunks && row < a.M) {
+      const int64_t at = row * a.chunks + c;
+      p.h = __builtin_nontemporal_load(a.h + at);
+      p.dn = __builtin_nontemporal_load(a.dn + at);
+      if (a.dh != nullptr) p.dh = __builtin_nontemporal_load(a.dh + at);
+    }
+  };
+  Piece now[kPieces];
+  [[maybe_unused]] Piece next[kPieces];
+  auto load_row = [&](int64_t row, Piece* p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) load(row, i, p[i]);
+  };
+  if constexpr (kRows == Rows::kAhead) load_row(blockIdx.x, now);
+  int parity = 0;
+  const float n = (float)(a.chunks * 8);
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+    if constexpr (kRows == Rows::kAhead) load_row(row + gridDim.x, next);
+    else if constexpr (kRows == Rows::kKept) load_row(row, now);
+    float sq = 0.0f, along = 0.0f;
+    auto reduce = [&](const Piece& p, u32x4 wt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float h0 = low(p.h[e]), h1 = high(p.h[e]);
+        sq = fmaf(h0, h0, sq);
+        sq = fmaf(h1, h1, sq);
+        along = fmaf(low(p.dn[e]) * low(wt[e]), h0, along);
+        along = fmaf(high(p.dn[e]) * high(wt[e]), h1, along);
+      }
+    };
+    if constexpr (kRows == Rows::kReload) {
+#pragma unroll 1
+      for (int i = 0; i < kPieces; ++i) {
+        Piece p;
+        load(row, i, p);
+        reduce(p, weight(i));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) reduce(now[i], w[i]);
+    }
+    sq = wave_sum(sq);
+    along = wave_sum(along);
+    // (two buffers: a wavefront is at most one barrier ahead of another)
+    if (tid % kWave == 0) part[parity][tid / kWave] = f32x2{sq, along};
+    __syncthreads();
+    sq = along = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) sq += part[parity][k][0], along += part[parity][k][1];
+    parity ^= 1;
+    const float power = sq / n + a.eps;
+    const float r = power > 0.0f ? 1.0f / sqrtf(power) : 0.0f;
+    const float t = along * r / n;   // mean(dn w hh)
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = tid + i * kThreads;
+      Piece p;
+      u32x4 wt;
+      if constexpr (kRows == Rows::kReload) {
+        load(row, i, p);
+        wt = weight(i);
+      } else {
+        p = now[i];
+        wt = w[i];
+      }
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float h0 = low(p.h[e]) * r, h1 = high(p.h[e]) * r;
+        const float d0 = low(p.dn[e]), d1 = high(p.dn[e]);
+        sum[i][2 * e] = fmaf(d0, h0, sum[i][2 * e]);
+        sum[i][2 * e + 1] = fmaf(d1, h1, sum[i][2 * e + 1]);
+        const float g0 = fmaf(d0, low(wt[e]), -(h0 * t)), g1 = fmaf(d1, high(wt[e]), -(h1 * t));
+        o[e] = pack2(fmaf(r, g0, low(p.dh[e])), fmaf(r, g1, high(p.dh[e])));
+      }
+      if (c < a.chunks) a.dx[row * a.chunks + c] = o;
+      if constexpr (kRows == Rows::kAhead) now[i] = next[i];
+    }
+  }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = tid + i * kThreads;
+    if (c < a.chunks) {
+      f32x4* p = reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.x * a.chunks + c) * 8);
+      p[0] = f32x4{sum[i][0], sum[i][1], sum[i][2], sum[i][3]};
+      p[1] = f32x4{sum[i][4], sum[i][5], sum[i][6], sum[i][7]};
+    }
+  }
+}
+
+// part [rows][K] -> out [K], in a fixed order: 32 columns to a workgroup, 32
+// groups of threads walk the rows with eight loads in flight each.
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(const float* __restrict__ part, int rows, int K,
+                                                               float* __restrict__ out) {
+  constexpr int kGroups = kSumThreads / 32;
+  __shared__ float lds[kGroups][33];
+  const int l = threadIdx.x % 32, g = threadIdx.x / 32, e = blockIdx.x * 32 + l;
+  float s = 0.0f;
+  if (e < K)
+    for (int b = g; b < rows; b += 8 * kGroups) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = b + i * kGroups < rows ? part[(int64_t)(b + i * kGroups) * K + e] : 0.0f;
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+  lds[g][l] = s;
+  __syncthreads();
+  if (g == 0 && e < K) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) t += lds[i][l];
+    out[e] = t;
+  }
+}
+
+// Threads of the gradient's workgroups, 16 values to a thread where K allows.
+int grad_threads(int64_t K) { return K <= 4096 ? 256 : K <= 16384 ? 512 : 1024; }
+
+template <int kThreads, int kPieces, Rows kRows>
+hipError_t backward(const NormGrad& a, int rows, hipStream_t s) {
+  hipLaunchKernelGGL((norm_grad_kernel<kThreads, kPieces, kRows>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// A launch has under 2^32 threads.
+bool norm_fits(int64_t M, int64_t K) {
+  return K <= kMaxNorm && M * (K <= 4096 ? kWave : K <= 16384 ? 4 * kWave : 16 * kWave) < (int64_t(1) << 32) - 1024;
+}
+
+hipError_t launch_add_norm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h,
+                                    void* q, float* scale, int64_t M, int64_t K, float eps, bool fp8, hipStream_t s) {
+  const auto in = [](const uint16_t* p) { return reinterpret_cast<const u32x4*>(p); };
+  const Norm a{in(x), in(residual), in(weight), reinterpret_cast<u32x4*>(h), static_cast<u32x2*>(q), scale, M, (int)(K / 8), eps};
+  if (K > 16384) return forward<16, 4>(a, fp8, s);
+  if (K <= 4096 && M >= 1024) {
+    const int pieces = (a.chunks + kWave - 1) / kWave;
+    if (pieces <= 1) return forward<1, 1>(a, fp8, s);
+    if (pieces <= 2) return forward<1, 2>(a, fp8, s);
+    if (pieces <= 4) return forward<1, 4>(a, fp8, s);
+    if (pieces <= 6) return forward<1, 6>(a, fp8, s);
+    return forward<1, 8>(a, fp8, s);
+  }
+  const int pieces = (a.chunks + 4 * kWave - 1) / (4 * kWave);
+  if (pieces <= 1) return forward<4, 1>(a, fp8, s);
+  if (pieces <= 2) return forward<4, 2>(a, fp8, s);
+  if (pieces <= 3) return forward<4, 3>(a, fp8, s);
+  if (pieces <= 4) return forward<4, 4>(a, fp8, s);
+  if (pieces <= 6) return forward<4, 6>(a, fp8, s);
+  return forward<4, 8>(a, fp8, s);
+}
+
+int64_t norm_grad_rows(int64_t M, int64_t K) { return std::min<int64_t>(M, 256 * 1024 / grad_threads(K)); }
+
+hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                                uint16_t* dx, float* part, float* dweight, int64_t M, int64_t K, float eps,
+                                hipStream_t s) {
+  const auto in = [](const uint16_t* p) { return reinterpret_cast<const u32x4*>(p); };
+  const NormGrad a{in(dn), in(dh), in(h), in(weight), reinterpret_cast<u32x4*>(dx), part, M, (int)(K / 8), eps};
+  const int rows = (int)norm_grad_rows(M, K);
+  hipError_t e;
+  if (K <= 2048) e = backward<256, 1, Rows::kAhead>(a, rows, s);
+  else if (K <= 4096) e = backward<256, 2, Rows::kAhead>(a, rows, s);
+  else if (K <= 8192) e = backward<512, 2, Rows::kAhead>(a, rows, s);
+  else if (K <= 16384) e = backward<512, 4, Rows::kKept>(a, rows, s);
+  else e = backward<1024, 4, Rows::kReload>(a, rows, s);
+  if (e != hipSuccess || part == nullptr) return e;
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((K + 31) / 32)), dim3(kSumThreads), 0, s, part, rows, (int)K, dweight);
+  return hipGetLastError();
+}
+
+}  // namespace w8a8

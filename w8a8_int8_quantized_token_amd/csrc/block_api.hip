@@ -1,6 +1,6 @@
 // C ABI of the operators around the linear (few-token forms, gated product,
-// backward passes, norm and rotation of queries and keys): argument checks,
-// workspace layout and launches.  Semantics are documented in include/w8a8.h;
+// backward passes, norm and rotation of queries and keys, norm with codes,
+// low-rank adapters): argument checks, workspace layout and launches.  Semantics are documented in include/w8a8.h;
 // checks always complete before anything is launched.
 #include "../../include/w8a8.h"
 #include "kernels.h"
@@ -276,6 +276,101 @@ w8a8_status check_workspace(const void* ws, size_t have, int64_t need) {
 #define TRY(call) \
   if ((call) != hipSuccess) return W8A8_ERR_LAUNCH
 
+// ---- low-rank adapters ----
+
+constexpr int64_t kMaxRank = 128, kMaxAdapters = 65536;
+
+bool adapters_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  return shape_ok(M, N, K, 1) && R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxAdapters;
+}
+
+// Launches of the linear with adapters: the first products t (which make the
+// codes of few tokens on the way), then one of the linear's kernels with t.
+struct AdapterPlan {
+  bool quantize, in_down;   // codes are made here; by the first product
+  bool few;                 // the few-token kernel
+  int splits, tile;         // otherwise the linear's plan
+  int64_t xq, xs, t, slices;
+  int64_t bytes;
+};
+AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int64_t R, bool dynamic, bool y_aligned, int tile) {
+  AdapterPlan p{};
+  p.quantize = dynamic;
+  p.in_down = dynamic && w8a8::down_quantizes(M, K);
+  p.few = tile < 0 && M <= w8a8::kFewTokens && few_tokens_pay(M, N, K, false, false) && w8a8::few_tokens_low_fit(M, N);
+  p.splits = 1;
+  p.tile = tile;
+  Pieces w;
+  if (dynamic) {
+    p.xq = w.add(M * K);
+    p.xs = w.add(4 * M);
+  }
+  p.t = w.add(2 * M * up(R, 16));
+  if (!p.few && tile < 0 && y_aligned && ranges_pay(M, K)) {   // the split's second pass writes 16 bytes at a time
+    p.splits = w8a8::select_splitk(M, N, K, &p.tile);
+    if (p.splits > 1) p.slices = w.add((int64_t)w8a8_linear_splitk_workspace(M, N, p.splits));
+    else p.tile = -1;
+  }
+  p.bytes = w.bytes;
+  return p;
+}
+
+w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                     const uint16_t* bias, const uint16_t* a, const uint16_t* b, const float* scaling,
+                     const int32_t* ids, uint16_t* y, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                     bool dynamic, int tile, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!adapters_ok(M, N, K, R, L)) return W8A8_ERR_SHAPE;
+  if (tile >= w8a8::num_tiles()) return W8A8_ERR_ARG;
+  if (M == 0) return W8A8_OK;
+  if ((dynamic ? !x : !xq || !x_scale) || !wq || !w_scale || !a || !b || !scaling || !ids || !y) return W8A8_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(x_scale, 4) || !aligned(wq, 16) || !aligned(w_scale, 4) ||
+      !aligned(bias, 2) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scaling, 4) || !aligned(ids, 4) ||
+      !aligned(y, 2))
+    return W8A8_ERR_ALIGN;
+  const AdapterPlan p = adapter_plan(M, N, K, R, dynamic, aligned(y, 16), tile);
+  const w8a8_status st = check_workspace(ws, ws_bytes, p.bytes);
+  if (st != W8A8_OK) return st;
+  uint16_t* t = at<uint16_t>(ws, p.t);
+  int8_t* codes = dynamic ? at<int8_t>(ws, p.xq) : nullptr;
+  float* code_scale = dynamic ? at<float>(ws, p.xs) : nullptr;
+  if (dynamic) {
+    if (!p.in_down) TRY(w8a8::launch_quantize_rows(x, codes, code_scale, M, K, stream));
+    xq = codes;
+    x_scale = code_scale;
+  }
+  w8a8::Down d{};
+  d.x = p.in_down ? static_cast<const void*>(x) : xq;
+  d.scale = x_scale;
+  d.codes = codes;
+  d.code_scale = code_scale;
+  d.p = a;
+  d.p_stride = R * K;
+  d.ids = ids;
+  d.scaling = scaling;
+  d.t = t;
+  d.M = M;
+  d.K = d.ldp = (int)K;
+  d.R = (int)R;
+  d.ldt = (int)up(R, 16);
+  d.count = (int)L;
+  TRY(w8a8::launch_down(p.in_down ? w8a8::DownRows::kQuantize : w8a8::DownRows::kCodes, d, stream));
+  const w8a8::Low low{t, b, ids, up(R, 16), R, L};
+  if (p.few) return launched(w8a8::launch_few_tokens_low(xq, x_scale, wq, w_scale, bias, low, y, M, N, K, stream));
+  if (p.splits > 1) {
+    int32_t* slices = at<int32_t>(ws, p.slices);
+    TRY(w8a8::launch_gemm_partials(p.tile, xq, wq, slices, M, N, K, p.splits, stream));
+    return launched(w8a8::launch_splitk_reduce_low(slices, p.splits, x_scale, w_scale, bias, low, y, M, N, stream));
+  }
+  return launched(w8a8::launch_gemm_low(p.tile, xq, x_scale, wq, w_scale, bias, low, y, M, N, K, stream));
+}
+
+// ---- norm with codes ----
+
+w8a8_status check_norm(int64_t M, int64_t K, float eps) {
+  if (M < 0 || M > kMaxRows || K < 16 || K % 16 != 0 || !w8a8::norm_fits(M, K)) return W8A8_ERR_SHAPE;
+  return eps >= 0.0f ? W8A8_OK : W8A8_ERR_ARG;
+}
+
 // ---- norm and rotation ----
 
 // Without a rotation positions still say which rows are padding; without
@@ -478,6 +573,62 @@ w8a8_status w8a8_qk_norm_rope_backward(
   }
   return launched(w8a8::launch_norm_rope_grad(a, oq, ok, interleaved != 0, sums ? static_cast<float*>(workspace) : nullptr,
                                               dq_weight, dk_weight, stream));
+}
+
+w8a8_status w8a8_add_rms_norm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h,
+                                       void* xq, float* x_scale, int64_t M, int64_t K, float eps, int fp8,
+                                       hipStream_t stream) {
+  const w8a8_status st = check_norm(M, K, eps);
+  if (st != W8A8_OK || M == 0) return st;
+  if (!x || !xq || !x_scale) return W8A8_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(xq, 16) ||
+      !aligned(x_scale, 4))
+    return W8A8_ERR_ALIGN;
+  return launched(w8a8::launch_add_norm_quantize(x, residual, weight, h, xq, x_scale, M, K, eps, fp8 != 0, stream));
+}
+
+size_t w8a8_add_rms_norm_backward_workspace(int64_t M, int64_t K) {
+  return M >= 1 && check_norm(M, K, 0.0f) == W8A8_OK ? (size_t)(4 * K * w8a8::norm_grad_rows(M, K)) : 0;
+}
+
+w8a8_status w8a8_add_rms_norm_backward(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                                       uint16_t* dx, float* dweight, int64_t M, int64_t K, float eps, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  w8a8_status st = check_norm(M, K, eps);
+  if (st != W8A8_OK) return st;
+  if (!aligned(dweight, 4)) return W8A8_ERR_ALIGN;
+  if (M == 0) return dweight ? launched(w8a8::launch_zero(dweight, 2 * K, stream)) : W8A8_OK;
+  if (!dn || !h || !dx) return W8A8_ERR_NULL;
+  if (!aligned(dn, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dx, 16))
+    return W8A8_ERR_ALIGN;
+  if (dweight) {
+    st = check_workspace(workspace, workspace_bytes, (int64_t)w8a8_add_rms_norm_backward_workspace(M, K));
+    if (st != W8A8_OK) return st;
+  }
+  return launched(w8a8::launch_add_norm_grad(dn, dh, h, weight, dx, dweight ? static_cast<float*>(workspace) : nullptr,
+                                             dweight, M, K, eps, stream));
+}
+
+// Any address of y: the K split of an aligned one needs the most.
+size_t w8a8_linear_adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int dynamic) {
+  return adapters_ok(M, N, K, R, 1) && M > 0 ? (size_t)adapter_plan(M, N, K, R, dynamic != 0, true, -1).bytes : 0;
+}
+
+w8a8_status w8a8_linear_adapters(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                                 const uint16_t* bias, const uint16_t* a, const uint16_t* b, const float* scaling,
+                                 const int32_t* ids, uint16_t* y, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                                 int tile, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return adapters(nullptr, xq, x_scale, wq, w_scale, bias, a, b, scaling, ids, y, M, N, K, R, L, false, tile, workspace,
+                  workspace_bytes, stream);
+}
+
+w8a8_status w8a8_linear_adapters_dynamic(const uint16_t* x, const int8_t* wq, const float* w_scale,
+                                         const uint16_t* bias, const uint16_t* a, const uint16_t* b,
+                                         const float* scaling, const int32_t* ids, uint16_t* y, int64_t M, int64_t N,
+                                         int64_t K, int64_t R, int64_t L, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+  return adapters(x, nullptr, nullptr, wq, w_scale, bias, a, b, scaling, ids, y, M, N, K, R, L, true, -1, workspace,
+                  workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -56,7 +56,7 @@ enum class FewAct { kNone, kGelu, kSiluGate, kGeluGate };
 // multiple of 16 bytes (16 lanes read the same chunk of 16 rows).
 __host__ __device__ constexpr int64_t code_row(int64_t K) { return (K + kPiece - 1) / kPiece * kPiece + 16; }
 
-template <int MT, FewAct ACT, bool kCodes>
+template <int MT, FewAct ACT, bool kCodes, bool kLow = false>
 struct Few {
   static constexpr bool kGate = ACT == FewAct::kSiluGate || ACT == FewAct::kGeluGate;
   static constexpr int NW = kGate ? 2 : 1;                 // weight rows per channel
@@ -70,8 +70,13 @@ struct Few {
   static constexpr int kSlotBytes = kWaves * kTiles * kPieceBytes;
   static constexpr int kSlots = kTiles == 1 ? 6 : kTiles == 2 ? 4 : kTiles == 3 ? 3 : 2;   // as LDS allows
   static constexpr int kAhead = kThreads / (kRows * NW);   // groups whose scales are in LDS
-  static constexpr int kLds = kSlots * kSlotBytes + (kCodes ? 0 : kCodeBytes) + 12 * kThreads + 64;
+  // Low-rank adapters: the tokens' shares of the workgroup's groups, fp32, made
+  // before the first piece is needed.
+  static constexpr int kLowGroup = MT * 16 * kRows * 4;   // bytes of a group
+  static constexpr int kLowGroups = kLow ? (MT == 1 ? 24 : 4) : 0;
+  static constexpr int kLds = kSlots * kSlotBytes + (kCodes ? 0 : kCodeBytes) + 12 * kThreads + 64 + kLowGroups * kLowGroup;
   static_assert(kCodes || MT == 1, "codes in LDS are one tile of tokens");
+  static_assert(!kLow || (kCodes && ACT == FewAct::kNone), "adapters beside the plain linear, from codes");
   static_assert(kLds <= 160 * 1024, "LDS budget");
   static_assert(NV * kWave * 16 <= kTiles * kPieceBytes, "a wavefront's sums fit its part of a slot");
 };
@@ -174,18 +179,19 @@ __device__ __forceinline__ uint32_t wave_max_dpp(uint32_t v) {
 }
 
 // kCodes: the codes and scales come from memory (xq, sx); otherwise from x.
-template <int MT, FewAct ACT, bool kCodes>
-__global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_kernel(
+template <int MT, FewAct ACT, bool kCodes, bool kLow>
+__global__ __launch_bounds__((Few<MT, ACT, kCodes, kLow>::kThreads)) void few_tokens_kernel(
     const uint16_t* __restrict__ x, const int8_t* __restrict__ xq, const float* __restrict__ sx,
     const int8_t* __restrict__ W, const float* __restrict__ sw, const uint16_t* __restrict__ bias,
-    uint16_t* __restrict__ y, int M, int64_t N, int K, int groups) {
-  using F = Few<MT, ACT, kCodes>;
+    uint16_t* __restrict__ y, int M, int64_t N, int K, int groups, Low low) {
+  using F = Few<MT, ACT, kCodes, kLow>;
   constexpr int NW = F::NW, S = F::kSlots, kWaves = F::kWaves, kThreads = F::kThreads;
   __shared__ __attribute__((aligned(16))) int8_t ring[S * F::kSlotBytes];
   __shared__ __attribute__((aligned(16))) int8_t codes[kCodes ? 16 : kCodeBytes];
   __shared__ float sx_lds[kThreads];
   __shared__ __attribute__((aligned(16))) float s_lds[kThreads], b_lds[kThreads];
   __shared__ __attribute__((aligned(16))) uint32_t amax_lds[8];
+  __shared__ __attribute__((aligned(16))) float low_lds[kLow ? F::kLowGroups * F::kLowGroup / 4 : 4];
 
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -311,6 +317,31 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
     }
     if (P > 1 && wave / P >= M) barrier();
   }
+  if constexpr (kLow) {
+    // A thread for a token and a channel of one of this workgroup's groups
+    // (neighbouring threads: neighbouring rows of b).  The first pieces of the
+    // weight are on the way meanwhile.
+    const int all = mine * M * kRows;
+    for (int i = tid; i < all; i += kThreads) {
+      const int c = i % kRows, mt = i / kRows % M, gi = i / kRows / M;
+      const int64_t n = min(((int64_t)blockIdx.x + (int64_t)gi * gridDim.x) * kRows + c, N - 1);
+      const int id = low.ids[mt];
+      float v = 0.0f;
+      if (id >= 0 && id < low.count) {
+        const uint16_t* b = low.b + (id * N + n) * low.R;
+        const uint16_t* t = low.t + mt * low.ldt;
+        for (int r = 0; r < (int)low.R; r += 8) {
+          const u32x4 bv = *reinterpret_cast<const u32x4*>(b + r), tv = *reinterpret_cast<const u32x4*>(t + r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v = fmaf(__uint_as_float(tv[e] << 16), __uint_as_float(bv[e] << 16), v);
+            v = fmaf(__uint_as_float(tv[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), v);
+          }
+        }
+      }
+      lds_write(lds_address(low_lds + (gi * MT * 16 + mt) * kRows + c), __float_as_uint(v));
+    }
+  }
   barrier();
 
   v4i acc[NW][MT];
@@ -341,6 +372,7 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
     const int tok = mine_t * 16 + l16;
     v4i sum[NW];
     f32x4 swv[NW], bv[NW];
+    [[maybe_unused]] f32x4 lowv;
     float sa = 0.0f;
     if (mine_t < MT) {
 #pragma unroll
@@ -358,6 +390,8 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
         bv[i] = __builtin_bit_cast(f32x4, lds_read16(lds_address(b_lds + e0)));
       }
       sa = __uint_as_float(lds_read_word(lds_address(sx_lds + tok)));
+      if constexpr (kLow)
+        lowv = __builtin_bit_cast(f32x4, lds_read16(lds_address(low_lds + (gi * MT * 16 + tok) * kRows + 4 * h)));
     }
     barrier();   // read: the slot may be requested again, the scales replaced
     if (mine_t < MT) {
@@ -367,6 +401,7 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float v = dequant((float)sum[0][e], sa, swv[0][e], bv[0][e]);
+          if constexpr (kLow) v += lowv[e];
           if constexpr (ACT == FewAct::kGelu) v = gelu(v);
           if constexpr (F::kGate) {
             const float up = dequant((float)sum[NW - 1][e], sa, swv[NW - 1][e], bv[NW - 1][e]);
@@ -431,13 +466,15 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes>::kThreads)) void few_tokens_k
   wait_vmcnt<0>();   // no request may write LDS after the workgroup ends
 }
 
-template <int MT, FewAct ACT, bool kCodes>
+template <int MT, FewAct ACT, bool kCodes, bool kLow = false>
 hipError_t launch(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
-                  const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+                  const uint16_t* bias, uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t stream,
+                  const Low& low = Low{}) {
   const int64_t groups = (N + kRows - 1) / kRows;
   const int64_t grid = std::min<int64_t>(groups, 256);   // one workgroup per compute unit
-  hipLaunchKernelGGL((few_tokens_kernel<MT, ACT, kCodes>), dim3((unsigned)grid), dim3(Few<MT, ACT, kCodes>::kThreads), 0, stream, x, xq, sx,
-                     wq, sw, bias, y, (int)M, N, (int)K, (int)groups);
+  hipLaunchKernelGGL((few_tokens_kernel<MT, ACT, kCodes, kLow>), dim3((unsigned)grid),
+                     dim3(Few<MT, ACT, kCodes, kLow>::kThreads), 0, stream, x, xq, sx, wq, sw, bias, y, (int)M, N, (int)K,
+                     (int)groups, low);
   return hipGetLastError();
 }
 
@@ -450,6 +487,19 @@ hipError_t launch_act(const uint16_t* x, const int8_t* xq, const float* sx, cons
 }
 
 }  // namespace
+
+bool few_tokens_low_fit(int64_t M, int64_t N) {
+  const int64_t groups = (N + kRows - 1) / kRows, per = (groups + 255) / 256;
+  return per <= (M <= 16 ? Few<1, FewAct::kNone, true, true>::kLowGroups : Few<2, FewAct::kNone, true, true>::kLowGroups);
+}
+
+hipError_t launch_few_tokens_low(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                 const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                                 hipStream_t s) {
+  if (M < 1 || M > kFewTokens || !few_tokens_low_fit(M, N)) return hipErrorInvalidValue;
+  return M <= 16 ? launch<1, FewAct::kNone, true, true>(nullptr, xq, sx, wq, sw, bias, y, M, N, K, s, low)
+                 : launch<2, FewAct::kNone, true, true>(nullptr, xq, sx, wq, sw, bias, y, M, N, K, s, low);
+}
 
 bool few_tokens_in_lds(int64_t M, int64_t K) { return M <= 16 && M * code_row(K) <= kCodeBytes; }
 

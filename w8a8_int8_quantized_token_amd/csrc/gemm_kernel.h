@@ -319,8 +319,13 @@ template <Epilogue EPI>
 constexpr bool kGateGrad = EPI == Epilogue::kSiluGateGrad || EPI == Epilogue::kGeluGateGrad;
 template <Epilogue EPI>
 constexpr bool kGated = kGateFwd<EPI> || kGateGrad<EPI>;
+// With the tokens' low-rank adapters (LowArgs) added to the fp32 value.
 template <Epilogue EPI>
-constexpr bool kScaled = EPI != Epilogue::kRawI32 && EPI != Epilogue::kBf16Plain;
+constexpr bool kLow = EPI == Epilogue::kBf16ScaleBiasLow || EPI == Epilogue::kBf16PlainLow || EPI == Epilogue::kRawLow;
+template <Epilogue EPI>
+constexpr bool kRaw = EPI == Epilogue::kRawI32 || EPI == Epilogue::kRawLow;
+template <Epilogue EPI>
+constexpr bool kScaled = !kRaw<EPI> && EPI != Epilogue::kBf16Plain && EPI != Epilogue::kBf16PlainLow;
 
 // Extra arguments of an epilogue (none for the plain ones).
 struct NoExtra {
@@ -357,9 +362,20 @@ struct GradArgs : UpArgs {
   int ldq;
   float* dbp;
 };
+// Low-rank adapters: token m adds sum_r t[m, r] * b[id][n, r], id = ids[m], to
+// output channel n, and nothing where id is outside [0, count).
+struct LowArgs {
+  const uint16_t* t;    // bf16 [M, ldt], ldt a multiple of 16, zeros from column R on
+  const uint16_t* b;    // bf16 [count][channels][R], R a multiple of 8
+  const int32_t* ids;   // [M]
+  int64_t b_stride;     // values from one adapter's b to the next one's
+  int ldt, R, count;
+  void columns_from(int64_t n, int64_t) { b += n * R; }
+};
 template <Epilogue EPI>
 using EpiArgs = std::conditional_t<kGateGrad<EPI>, GradArgs,
-                                   std::conditional_t<kGated<EPI>, UpArgs, NoExtra>>;
+                                   std::conditional_t<kGated<EPI>, UpArgs,
+                                                      std::conditional_t<kLow<EPI>, LowArgs, NoExtra>>>;
 
 // Output channels of a tile whose W operand has `bn` rows.
 template <Epilogue EPI>
@@ -431,7 +447,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // with every wavefront issuing.  (The 256x256 tile has no registers for
   // the doubled request count, nor have the fp8 tile with the raw epilogue
   // and the bf16 tile.)
-  constexpr bool kHalfDma = T::kSplit && T::BN < 256 && EPI != Epilogue::kRawI32 && !Op::kBf16;
+  constexpr bool kHalfDma = T::kSplit && T::BN < 256 && !kRaw<EPI> && !Op::kBf16;
   constexpr int kDmaWaves = kHalfDma ? T::kWaves / 2 : T::kWaves;
   constexpr int DXk = T::BM / T::kDmaRows / kDmaWaves;   // X requests per DMA wavefront and stage
   constexpr int DWk = T::BN / T::kDmaRows / kDmaWaves;   // W requests
@@ -447,7 +463,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // the plain path (vec_store = 0) when BM * ldy * 2 >= 2^31.
   // (The gated forward makes one store per 32x32 tile; its gradient's stores
   // depend on what is wanted and are waited for.)
-  constexpr bool kCountedStores = T::kSplit && EPI != Epilogue::kRawI32 && !kGateGrad<EPI>;
+  constexpr bool kCountedStores = T::kSplit && !kRaw<EPI> && !kGateGrad<EPI>;
   constexpr int kStores = (kGated<EPI> ? 1 : 2) * T::FM * T::FN;   // store instructions per wavefront and tile
   const int dma_r = (wave % kDmaWaves) * T::kDmaRows + lane / T::CPR;
   const int col = swz<T::CPR>(dma_r, lane % T::CPR) * 16;   // K byte offset within a stage
@@ -760,6 +776,102 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     }
   };
 
+  // ---- low-rank adapters ----
+  // The adapters' share of a tile, t b^T, added to its fp32 values, which are
+  // in the accumulators: one pass for each adapter that the wavefront's tokens
+  // have.  Where they do not all have the same one, only the lanes whose token
+  // has it take a sub-tile's result (a lane's token is the same in all of its
+  // values): an adapter's values, whatever they are, reach no other adapter's
+  // tokens.
+  constexpr int kLowRows = Op::kBf16 ? 16 : 32, kLowM = T::TM / kLowRows;   // row tiles of a wavefront
+  constexpr int kLowN = Op::kBf16 ? 2 * T::FN : T::FN;                      // fragments of its channels
+  constexpr int kLowStep = Op::kBf16 ? 32 : 16;                            // ranks of an MFMA
+  auto add_low = [&](const TileAddr& at) __attribute__((always_inline)) {
+    if constexpr (kLow<EPI>) {
+      int e_lane = lane;
+      asm volatile("" : "+v"(e_lane));   // addresses formed here, not before the K loop
+      const int l_row = e_lane % kLowRows, l_r = 8 * (e_lane / kLowRows);
+      const int first_m = at.m0 + wm * T::TM + l_row;
+      int id[kLowM];
+#pragma unroll
+      for (int i = 0; i < kLowM; ++i) {
+        const int m = first_m + i * kLowRows, v = extra.ids[min(m, M - 1)];
+        id[i] = m < M && v >= 0 && v < extra.count ? v : -1;
+      }
+      // the tile's rows of t and an adapter's rows of b as buffer ranges: rows
+      // past M and N and ranks past R are zeros
+      const __amdgpu_buffer_rsrc_t rt = buffer_range(extra.t + (int64_t)at.m0 * extra.ldt, min(T::BM, M - at.m0) * extra.ldt);
+      const int chans = min(T::BN, N - at.n0) * extra.R;
+      __amdgpu_buffer_rsrc_t rb;
+      auto frag_t = [&](int i, int r0) {   // tokens
+        const uint32_t o = (uint32_t)((wm * T::TM + i * kLowRows + l_row) * extra.ldt + r0 + l_r) * 2u;
+        return buffer_load16(rt, r0 + l_r < extra.ldt ? o : kOOB);
+      };
+      auto frag_b = [&](int j, int r0) {   // channels
+        int c;
+        if constexpr (Op::kBf16) {
+          const int dealt = (l_row / 4) * 8 + (l_row / 8) * 4 + l_row % 4 - (l_row / 8) * 16;
+          c = j / 2 * 32 + (j % 2 ? dealt ^ 4 : dealt);
+        } else {
+          c = j * 32 + l_row;
+        }
+        const uint32_t o = (uint32_t)((wn * T::TN + c) * extra.R + r0 + l_r) * 2u;
+        return buffer_load16(rb, r0 + l_r < extra.R ? o : kOOB);
+      };
+      auto product = [&](v4i b, v4i t, auto v) {
+        const bf16x8 fb8 = __builtin_bit_cast(bf16x8, b), ft8 = __builtin_bit_cast(bf16x8, t);
+        if constexpr (Op::kBf16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb8, ft8, v, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb8, ft8, v, 0, 0, 0);
+      };
+      auto get = [&](int i, int j) {
+        if constexpr (Op::kBf16) return acc[i / 2][j / 2].q[i % 2][j % 2];
+        else return __builtin_bit_cast(v16f, acc[i][j]);
+      };
+      auto set = [&](int i, int j, auto v) {
+        if constexpr (Op::kBf16) acc[i / 2][j / 2].q[i % 2][j % 2] = v;
+        else acc[i][j] = __builtin_bit_cast(v16i, v);
+      };
+      uint64_t left[kLowM];   // lanes whose adapter is still to come
+      uint64_t any = 0;
+#pragma unroll
+      for (int i = 0; i < kLowM; ++i) {
+        left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+        any |= left[i];
+      }
+      while (any != 0) {
+        int a = 0;
+#pragma unroll
+        for (int i = kLowM - 1; i >= 0; --i)
+          if (left[i] != 0) a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(left[i]));
+        any = 0;
+#pragma unroll
+        for (int i = 0; i < kLowM; ++i) {
+          left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == a);
+          any |= left[i];
+        }
+        rb = buffer_range(extra.b + a * extra.b_stride + (int64_t)at.n0 * extra.R, chans);
+        for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
+          v4i ft[kLowM], fn[kLowN];
+#pragma unroll
+          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
+#pragma unroll
+          for (int j = 0; j < kLowN; ++j) fn[j] = frag_b(j, r0);
+#pragma unroll
+          for (int i = 0; i < kLowM; ++i)
+#pragma unroll
+            for (int j = 0; j < kLowN; ++j) {
+              auto v = get(i, j);
+              const auto d = product(fn[j], ft[i], decltype(v){});
+#pragma unroll
+              for (int e = 0; e < (Op::kBf16 ? 4 : 16); ++e) v[e] += id[i] == a ? d[e] : 0.0f;
+              set(i, j, v);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+      }
+    }
+  };
+
   // Split-ring step k: A_k in `ac`, B_k in `bc`, stage k+1 in `an`/`bn1`.
   // After the barrier that frees A_k's and B_k's slots, B_{k+2} and then
   // A_{k+3} are requested into them: at the next barrier only the B part
@@ -965,6 +1077,9 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
 
     const int m0 = cur.m0, n0 = cur.n0;
     [[maybe_unused]] const int c0 = cur.c;
+    if constexpr (kLow<EPI> && Op::kBf16) {
+      if (c0 == 0) add_low(cur);   // a split product: into the first range's sums
+    }
     // output rows of this tile as a buffer range (bf16, ldy apart)
     __amdgpu_buffer_rsrc_t y_rsrc;
     if constexpr (kCountedStores)
@@ -975,7 +1090,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     const bool has_next = t_next < nitems;
 
     // ---- epilogue: lane holds token m, channels n = base + 8*g + 4*khalf + 0..3 ----
-    if constexpr (EPI != Epilogue::kRawI32) {
+    if constexpr (!kRaw<EPI>) {
       // Lane-derived epilogue addresses are recomputed per tile (the opaque
       // copy of the lane id keeps them from being hoisted out of the tile
       // loop, where they would occupy registers through the K loop).
@@ -1036,6 +1151,19 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           bv[g] = *reinterpret_cast<const f32x4*>(b_lds + nj + g * 8 + e_kh * 4);
         }
       };
+      if constexpr (kLow<EPI> && !Op::kBf16) {
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+          load_sb(j);
+#pragma unroll
+          for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[i][j][e] = __float_as_int(dequant((float)acc[i][j][e], sa[i], sv[e / 4][e % 4], bv[e / 4][e % 4]));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        add_low(cur);
+      }
       // 4 bf16 outputs (two packed words) of each run g of output tile (i, j):
       // channels nj + 8g + 4*khalf + 0..3
       uint32_t w[4][2];
@@ -1045,6 +1173,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           // the fp32 output value (GELU applied for the gelu epilogue)
           auto val = [&](int e, float s_w, float b) {
             if constexpr (!kScaled<EPI>) return (float)c[e];
+            if constexpr (kLow<EPI>) return __int_as_float(c[e]);   // the value already
             const float y = dequant((float)c[e], sa[i], s_w, b);
             if constexpr (EPI == Epilogue::kBf16GeluScaleBias) return gelu(y);
             else return y;
@@ -1448,7 +1577,7 @@ struct Operands {
     o.w += n * K;
     if (sw) o.sw += n;
     if (bias) o.bias += n;
-    o.out = static_cast<char*>(out) + n * (EPI == Epilogue::kRawI32 ? 4 : 2);
+    o.out = static_cast<char*>(out) + n * (kRaw<EPI> ? 4 : 2);
     o.extra.columns_from(n, K);
     return o;
   }
@@ -1469,7 +1598,7 @@ hipError_t launch_t(const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, int
   const uintptr_t a = reinterpret_cast<uintptr_t>(o.out);
   // 16-byte stores; the split ring's buffer stores take 32-bit offsets
   // within a tile's rows
-  const int vec = EPI == Epilogue::kRawI32
+  const int vec = kRaw<EPI>
                       ? (ldy % 4 == 0) && (a % 16 == 0)
                       : (ldy % 8 == 0) && (a % 16 == 0) && (int64_t)T::BM * ldy * 2 < (int64_t(1) << 31);
   hipLaunchKernelGGL((gemm_i8_kernel<T, EPI, Op>), grid, block, 0, stream, o.x, o.w, o.sx, o.sw,

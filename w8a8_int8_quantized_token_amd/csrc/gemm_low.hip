@@ -1,0 +1,15 @@
+// The int8 linear with low-rank adapters on the kernel of gemm_kernel.h:
+//   y = bf16(((acc*sx)*sw)+b + sum_r t[m,r] b[id(m)][n,r]).
+#include "gemm_kernel.h"
+
+namespace w8a8 {
+
+hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                           const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                           hipStream_t stream) {
+  const LowArgs args{low.t, low.b, low.ids, N * low.R, (int)low.ldt, (int)low.R, (int)low.count};
+  if (tile < 0) tile = choose_tile(M, N, K);
+  return launch_plan<OpI8, Epilogue::kBf16ScaleBiasLow>(tile, {xq, wq, sx, sw, bias, y, args}, M, N, K, stream);
+}
+
+}  // namespace w8a8

@@ -40,9 +40,12 @@ int select_splitk(int64_t M, int64_t N, int64_t K, int* tile);
 // kBf16Plain: the accumulators rounded to bf16.
 // Gated (two products, gate and up, with values g and u as above):
 // k*Gate: y = bf16(act(g) * u); k*GateGrad: the gradients of g and u.
+// k*Low: kBf16ScaleBias, kBf16Plain, or the fp32 sums, with the tokens'
+// low-rank adapters added before the rounding.
 enum class Epilogue {
   kBf16ScaleBias, kBf16GeluScaleBias, kRawI32, kBf16Plain,
-  kSiluGate, kGeluGate, kSiluGateGrad, kGeluGateGrad
+  kSiluGate, kGeluGate, kSiluGateGrad, kGeluGateGrad,
+  kBf16ScaleBiasLow, kBf16PlainLow, kRawLow
 };
 
 // int8 GEMM acc[m,n] = sum_k xq[m,k] * wq[n,k] with the chosen epilogue.
@@ -172,5 +175,67 @@ hipError_t launch_norm_rope(const RopeArgs& a, bool interleaved, hipStream_t str
 int64_t norm_rope_grad_rows(int64_t M, int64_t Hq, int64_t Hk, int D);
 hipError_t launch_norm_rope_grad(const RopeArgs& a, const RopeView& dq, const RopeView& dk, bool interleaved,
                                  float* part, float* dqw, float* dkw, hipStream_t stream);
+
+// The residual's addition, norm and codes of rows of at most kMaxNorm values
+// (add_norm_quantize.hip): residual, weight and h (the sum's output) may be
+// null; q int8 or, fp8, e4m3 codes.  The gradient's part fp32
+// [norm_grad_rows(), K] and dweight fp32 [K], or both null.
+constexpr int64_t kMaxNorm = 32768;
+bool norm_fits(int64_t M, int64_t K);
+hipError_t launch_add_norm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h,
+                                    void* q, float* scale, int64_t M, int64_t K, float eps, bool fp8,
+                                    hipStream_t stream);
+int64_t norm_grad_rows(int64_t M, int64_t K);
+hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                                uint16_t* dx, float* part, float* dweight, int64_t M, int64_t K, float eps,
+                                hipStream_t stream);
+
+// Low-rank adapters of a product's tokens: token m adds
+// sum_r t[m,r] * b[ids[m]][n,r] to output n, and nothing where ids[m] is
+// outside [0, count).  t bf16 [M,ldt], ldt = R rounded up to 16, zeros past
+// column R; b bf16 [count,N,R], 16-byte aligned; R a multiple of 8.
+struct Low {
+  const uint16_t *t, *b;
+  const int32_t* ids;
+  int64_t ldt, R, count;
+};
+hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                           const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                           hipStream_t stream);
+
+// An adapter's first product (adapter_down.hip): t bf16 [M,ldt] from x [M,K]
+// and p [count][R][ldp] (adapters p_stride apart; rows 16-byte aligned, ldp a
+// multiple of 16 and at least K, zeros past column K).  Codes: scale [M];
+// quantizing x (where down_quantizes()): codes [M,K] and code_scale [M] are
+// outputs; bf16 values: x at any 2-byte address, rows of K.  t2, where not
+// null: the same times scale2[m].
+constexpr int64_t kDownRows = 256;   // up to here a workgroup for each row
+enum class DownRows { kCodes, kQuantize, kValues };
+struct Down {
+  const void* x;
+  const float* scale;
+  int8_t* codes;
+  float* code_scale;
+  const uint16_t* p;
+  int64_t p_stride;
+  const int32_t* ids;
+  const float* scaling;
+  uint16_t *t, *t2;
+  const float* scale2;
+  int64_t M;
+  int K, ldp, R, ldt, count;
+};
+bool down_quantizes(int64_t M, int64_t K);
+hipError_t launch_down(DownRows rows, const Down& a, hipStream_t stream);
+
+// The linear with adapters for at most kFewTokens tokens, from codes, where
+// few_tokens_low_fit(); and the K split's second pass with them.
+bool few_tokens_low_fit(int64_t M, int64_t N);
+hipError_t launch_few_tokens_low(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                 const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                                 hipStream_t stream);
+hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const float* sx, const float* sw,
+                                    const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N,
+                                    hipStream_t stream);
 
 }  // namespace w8a8

@@ -28,11 +28,13 @@ constexpr int kThreads = 256;
 
 // kVec: channel scales and bias are read as 16-byte vectors (both 16-byte
 // aligned); otherwise one element at a time.
+// Low-rank adapters (kBf16ScaleBiasLow): the token's share of its 8 channels
+// is summed here, 8 rows of b by one of t.
 template <Epilogue EPI, bool kVec>
 __global__ __launch_bounds__(kThreads) void splitk_reduce_kernel(
     const int32_t* __restrict__ part, int chunks, int64_t slice, const float* __restrict__ sx,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
-    int64_t groups_per_row, int64_t groups) {
+    int64_t groups_per_row, int64_t groups, Low low) {
   for (int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x; g < groups;
        g += (int64_t)gridDim.x * kThreads) {
     const int64_t m = g / groups_per_row;
@@ -66,6 +68,28 @@ __global__ __launch_bounds__(kThreads) void splitk_reduce_kernel(
         bv[e] = bias != nullptr ? __uint_as_float((uint32_t)bias[n + e] << 16) : 0.0f;
       }
     }
+    [[maybe_unused]] float share[8];
+    if constexpr (EPI == Epilogue::kBf16ScaleBiasLow) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) share[e] = 0.0f;
+      const int id = low.ids[m];
+      if (id >= 0 && id < low.count) {
+        const uint16_t* t = low.t + m * low.ldt;
+        const uint16_t* b = low.b + (id * groups_per_row * 8 + n) * low.R;
+        for (int r = 0; r < (int)low.R; r += 8) {
+          const u32x4 tv = *reinterpret_cast<const u32x4*>(t + r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const u32x4 bw = *reinterpret_cast<const u32x4*>(b + e * low.R + r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              share[e] = fmaf(__uint_as_float(tv[i] << 16), __uint_as_float(bw[i] << 16), share[e]);
+              share[e] = fmaf(__uint_as_float(tv[i] & 0xffff0000u), __uint_as_float(bw[i] & 0xffff0000u), share[e]);
+            }
+          }
+        }
+      }
+    }
     uint32_t w[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -75,6 +99,7 @@ __global__ __launch_bounds__(kThreads) void splitk_reduce_kernel(
         const int e = 2 * q + h;
         const float r = dequant((float)acc[e], sa, swv[e], bv[e]);
         v[h] = EPI == Epilogue::kBf16GeluScaleBias ? gelu(r) : r;
+        if constexpr (EPI == Epilogue::kBf16ScaleBiasLow) v[h] += share[e];
       }
       w[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2));
     }
@@ -82,33 +107,41 @@ __global__ __launch_bounds__(kThreads) void splitk_reduce_kernel(
   }
 }
 
-}  // namespace
-
-hipError_t launch_splitk_reduce(Epilogue epi, const int32_t* partials, int chunks, const float* sx,
-                                const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
-                                int64_t N, hipStream_t stream) {
-  if (N % 8 != 0 || chunks < 1 || epi == Epilogue::kRawI32) return hipErrorInvalidValue;
+template <Epilogue EPI>
+hipError_t launch(const int32_t* partials, int chunks, const float* sx, const float* sw, const uint16_t* bias,
+                  uint16_t* y, int64_t M, int64_t N, const Low& low, hipStream_t stream) {
   const int64_t gpr = N / 8, groups = M * gpr;
   const int64_t blocks = std::min<int64_t>((groups + kThreads - 1) / kThreads, int64_t(1) << 20);
   const bool vec = reinterpret_cast<uintptr_t>(sw) % 16 == 0 &&
                    (bias == nullptr || reinterpret_cast<uintptr_t>(bias) % 16 == 0);
   const dim3 grid((unsigned)blocks), block(kThreads);
-  if (epi == Epilogue::kBf16GeluScaleBias) {
-    if (vec)
-      hipLaunchKernelGGL((splitk_reduce_kernel<Epilogue::kBf16GeluScaleBias, true>), grid, block, 0,
-                         stream, partials, chunks, M * N, sx, sw, bias, y, gpr, groups);
-    else
-      hipLaunchKernelGGL((splitk_reduce_kernel<Epilogue::kBf16GeluScaleBias, false>), grid, block, 0,
-                         stream, partials, chunks, M * N, sx, sw, bias, y, gpr, groups);
-  } else {
-    if (vec)
-      hipLaunchKernelGGL((splitk_reduce_kernel<Epilogue::kBf16ScaleBias, true>), grid, block, 0, stream,
-                         partials, chunks, M * N, sx, sw, bias, y, gpr, groups);
-    else
-      hipLaunchKernelGGL((splitk_reduce_kernel<Epilogue::kBf16ScaleBias, false>), grid, block, 0,
-                         stream, partials, chunks, M * N, sx, sw, bias, y, gpr, groups);
-  }
+  if (vec)
+    hipLaunchKernelGGL((splitk_reduce_kernel<EPI, true>), grid, block, 0, stream, partials, chunks, M * N, sx, sw, bias,
+                       y, gpr, groups, low);
+  else
+    hipLaunchKernelGGL((splitk_reduce_kernel<EPI, false>), grid, block, 0, stream, partials, chunks, M * N, sx, sw, bias,
+                       y, gpr, groups, low);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_splitk_reduce(Epilogue epi, const int32_t* partials, int chunks, const float* sx,
+                                const float* sw, const uint16_t* bias, uint16_t* y, int64_t M,
+                                int64_t N, hipStream_t stream) {
+  if (N % 8 != 0 || chunks < 1) return hipErrorInvalidValue;
+  if (epi == Epilogue::kBf16GeluScaleBias)
+    return launch<Epilogue::kBf16GeluScaleBias>(partials, chunks, sx, sw, bias, y, M, N, Low{}, stream);
+  if (epi == Epilogue::kBf16ScaleBias)
+    return launch<Epilogue::kBf16ScaleBias>(partials, chunks, sx, sw, bias, y, M, N, Low{}, stream);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const float* sx, const float* sw,
+                                    const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N,
+                                    hipStream_t stream) {
+  if (N % 8 != 0 || chunks < 1) return hipErrorInvalidValue;
+  return launch<Epilogue::kBf16ScaleBiasLow>(partials, chunks, sx, sw, bias, y, M, N, low, stream);
 }
 
 }  // namespace w8a8

@@ -1,4 +1,4 @@
-// The plain calls of block_ops.py in one native step.  Through Python checks
+// The plain calls of block_ops.py and adapter_ops.py in one native step.  Through Python checks
 // and ctypes a call of these entry points costs 9 to 25 us of host time, more
 // than many of them run for; here it costs a third of that.
 //
@@ -6,7 +6,7 @@
 // call if it is an ordinary one: contiguous tensors of the right types and
 // sizes on the current device.  Anything else (a wrong argument, another
 // device, an error status, an exception) gives None with nothing launched, and
-// the caller goes through block_ops.py's checks, which name what is wrong or
+// the caller goes through the Python checks, which name what is wrong or
 // make the call.  Work is enqueued on torch's current stream; outputs and
 // workspaces come from torch's allocator.
 #include <torch/csrc/autograd/python_variable.h>
@@ -91,6 +91,11 @@ int integer(PyObject* o) {
   const long v = PyLong_AsLong(o);
   if ((v == -1 && PyErr_Occurred()) || v < INT_MIN || v > INT_MAX) throw Refused{};
   return (int)v;
+}
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+  return (float)v;
 }
 void two_dims(const at::Tensor& t) {
   if (t.dim() != 2) throw Refused{};
@@ -196,9 +201,7 @@ struct Rope {
     cos = c.at<float>(a[4], at::kFloat, {P, half});
     sin = c.at<float>(a[5], at::kFloat, {P, half});
     positions = c.at_or_null<int32_t>(a[6], at::kInt, {M});
-    const double e = PyFloat_AsDouble(a[7]);
-    if (e == -1.0 && PyErr_Occurred()) throw Refused{};
-    eps = (float)e;
+    eps = real(a[7]);
     interleaved = flag(a[8]);
   }
 };
@@ -245,8 +248,98 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// x, residual, weight, eps, fp8
+PyObject* add_rms_norm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return plain(n, 5, [&] {
+    const at::Tensor& x = tensor(a[0]);
+    two_dims(x);
+    Call c(x);
+    const int64_t M = x.size(0), K = x.size(1);
+    const auto* px = c.at<uint16_t>(a[0], at::kBFloat16, {M, K});
+    const auto* pr = c.at_or_null<uint16_t>(a[1], at::kBFloat16, {M, K});
+    const auto* pw = c.at_or_null<uint16_t>(a[2], at::kBFloat16, {K});
+    const float eps = real(a[3]);
+    const bool fp8 = flag(a[4]);
+    at::Tensor q = c.empty({M, K}, fp8 ? at::kByte : at::kChar), s = c.empty({M}, at::kFloat), h;
+    if (pr != nullptr) h = c.empty({M, K}, at::kBFloat16);
+    launched(w8a8_add_rms_norm_quantize(px, pr, pw, bits(h), q.data_ptr(), static_cast<float*>(s.data_ptr()), M, K, eps,
+                                        fp8, c.stream));
+    return tuple({std::move(q), std::move(s), pr != nullptr ? std::move(h) : x});
+  });
+}
+
+// dn, h, weight, eps, dh, whether dweight
+PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return plain(n, 6, [&] {
+    const at::Tensor& h = tensor(a[1]);
+    two_dims(h);
+    Call c(h);
+    const int64_t M = h.size(0), K = h.size(1);
+    const auto* pdn = c.at<uint16_t>(a[0], at::kBFloat16, {M, K});
+    const auto* ph = c.at<uint16_t>(a[1], at::kBFloat16, {M, K});
+    const auto* pw = c.at_or_null<uint16_t>(a[2], at::kBFloat16, {K});
+    const float eps = real(a[3]);
+    const auto* pdh = c.at_or_null<uint16_t>(a[4], at::kBFloat16, {M, K});
+    at::Tensor dx = c.empty({M, K}, at::kBFloat16), dw;
+    size_t need = 0;
+    if (flag(a[5])) {
+      dw = c.empty({K}, at::kFloat);
+      need = w8a8_add_rms_norm_backward_workspace(M, K);
+    }
+    void* ws = c.workspace(need);
+    launched(w8a8_add_rms_norm_backward(pdn, pdh, ph, pw, bits(dx), dw.defined() ? static_cast<float*>(dw.data_ptr()) : nullptr,
+                                        M, K, eps, ws, need, c.stream));
+    return tuple({std::move(dx), std::move(dw)});
+  });
+}
+
+// The adapters of a call: a, b, ids, scaling
+struct Adapters {
+  int64_t R, L;
+  const uint16_t *a, *b;
+  const int32_t* ids;
+  const float* scaling;
+  Adapters(const Call& c, PyObject* const* o, int64_t M, int64_t N, int64_t K) {
+    const at::Tensor& t = tensor(o[0]);
+    if (t.dim() != 3) throw Refused{};
+    L = t.size(0), R = t.size(1);
+    a = c.at<uint16_t>(o[0], at::kBFloat16, {L, R, K});
+    b = c.at<uint16_t>(o[1], at::kBFloat16, {L, N, R});
+    ids = c.at<int32_t>(o[2], at::kInt, {M});
+    scaling = c.at<float>(o[3], at::kFloat, {L});
+  }
+};
+
+// x or xq, x_scale or None (x is bf16), wq, w_scale, bias, a, b, ids, scaling
+PyObject* linear_adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return plain(n, 9, [&] {
+    const at::Tensor &x = tensor(a[0]), &w = tensor(a[2]);
+    two_dims(x);
+    two_dims(w);
+    Call c(x);
+    const bool dynamic = a[1] == Py_None;
+    const int64_t M = x.size(0), K = x.size(1), N = w.size(0);
+    const uint16_t* px = dynamic ? c.at<uint16_t>(a[0], at::kBFloat16, {M, K}) : nullptr;
+    const int8_t* pq = dynamic ? nullptr : c.at<int8_t>(a[0], at::kChar, {M, K});
+    const float* pxs = c.at_or_null<float>(a[1], at::kFloat, {M});
+    const auto* pw = c.at<int8_t>(a[2], at::kChar, {N, K});
+    const auto* ps = c.at<float>(a[3], at::kFloat, {N});
+    const auto* pb = c.at_or_null<uint16_t>(a[4], at::kBFloat16, {N});
+    const Adapters ad(c, a + 5, M, N, K);
+    at::Tensor y = c.empty({M, N}, at::kBFloat16);
+    const size_t need = w8a8_linear_adapters_workspace(M, N, K, ad.R, dynamic);
+    void* ws = c.workspace(need);
+    launched(dynamic ? w8a8_linear_adapters_dynamic(px, pw, ps, pb, ad.a, ad.b, ad.scaling, ad.ids, bits(y), M, N, K, ad.R,
+                                                    ad.L, ws, need, c.stream)
+                     : w8a8_linear_adapters(pq, pxs, pw, ps, pb, ad.a, ad.b, ad.scaling, ad.ids, bits(y), M, N, K, ad.R,
+                                            ad.L, -1, ws, need, c.stream));
+    return wrap(std::move(y));
+  });
+}
+
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(dynamic), METHOD(backward), METHOD(qk_norm_rope), METHOD(qk_norm_rope_backward),
+                         METHOD(add_rms_norm_quantize), METHOD(add_rms_norm_backward), METHOD(linear_adapters),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

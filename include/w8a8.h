@@ -485,6 +485,32 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t *x, const int8_t *wq,
                                          void *workspace, size_t workspace_bytes,
                                          hipStream_t stream);
 
+/*
+ * Gradients of w8a8_linear_adapters for dy bf16 [M,N], on frozen codes of the
+ * weight, the rounding of the activations to codes passed straight through.
+ * With i = ids[m], x and t as above and
+ *   u[m,r] = bf16( scaling[i] * sum_n dy[m,n] * b[i][n,r] ):
+ *   dx[m,k]    = bf16( sum_n dy[m,n] * w[n,k] + sum_r u[m,r] * a[i][r,k] ),
+ *   da[i][r,k] = bf16( sum over the adapter's tokens of u[m,r] * x[m,k] ),
+ *   db[i][n,r] = bf16( sum over the adapter's tokens of dy[m,n] * t[m,r] ),
+ * bf16 [M,K], [L,R,K] and [L,N,R]; an adapter without tokens gets zeros.  Each
+ * is left out where its pointer is NULL; dx needs wq, w_scale, a and b, da needs
+ * b, xq and x_scale, db needs a, xq and x_scale.  Sums are fp32, on operands
+ * rounded to bf16 once (of da, u times x's scale); no atomics, the same bits
+ * from call to call.  Contract as for w8a8_linear_adapters and
+ * w8a8_linear_backward; da and db 16-byte aligned.
+ */
+size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R,
+                                               int64_t L, int dx, int da, int db);
+w8a8_status w8a8_linear_adapters_backward(const uint16_t *dy, const int8_t *xq,
+                                          const float *x_scale, const int8_t *wq,
+                                          const float *w_scale, const uint16_t *a,
+                                          const uint16_t *b, const float *scaling,
+                                          const int32_t *ids, uint16_t *dx, uint16_t *da,
+                                          uint16_t *db, int64_t M, int64_t N, int64_t K, int64_t R,
+                                          int64_t L, void *workspace, size_t workspace_bytes,
+                                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

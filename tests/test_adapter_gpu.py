@@ -284,3 +284,135 @@ def test_outputs_workspaces_and_addresses(w8):
             assert (space[need:] == fill).all()
     e = torch.empty(0, 256, dtype=BF, device=DEV)
     assert w8.linear_adapters_dynamic(e, wq, ws, a, b, ids[:0], scaling, bias).shape == (0, 96)
+
+
+# ---- adapters, gradients ----
+
+# every path of dx (few tokens from the codes, tiles whole and in ranges, dy copied or not), rows and blocks of the
+# first products, every shape of the matrices' gradients, parts of long lists, adapters without tokens
+GRADS = [(1, 16, 1, 8, 1, "one"), (3, 784, 77, 24, 5, "mixed"), (64, 256, 512, 16, 1, "one"), (29, 2592, 2776, 16, 3, "mixed"),
+         (64, 2592, 2776, 40, 9, "mixed"), (100, 1024, 5000, 8, 2, "runs"), (257, 512, 300, 72, 4, "runs"),
+         (300, 1168, 1203, 40, 9, "mixed"), (777, 528, 603, 128, 70, "mixed"), (1037, 272, 5466, 8, 3, "mixed"),
+         (2048, 1024, 1024, 16, 1, "one"), (2100, 512, 2048, 64, 4, "runs"), (3000, 2064, 264, 32, 2, "mixed"),
+         (500, 64, 64, 16, 5, "none"), (1300, 1040, 1000, 24, 2, "runs"), (4500, 96, 130, 48, 3, "mixed")]
+
+
+def grad_inputs(M, K, N, R, L, kind, seed):
+    x, wq, ws, a, b, ids, scaling, _ = adapter_inputs(M, K, N, R, L, kind, seed)
+    xq, xs = ref.codes_of(x)
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(seed + 1)).to(BF)
+    return dy, xq, xs, wq, ws, a, b, ids, scaling
+
+
+@pytest.mark.parametrize("M,K,N,R,L,kind", GRADS)
+def test_adapter_gradients(w8, M, K, N, R, L, kind):
+    inputs = grad_inputs(M, K, N, R, L, kind, M + K + N)
+    got = w8.linear_adapters_backward(*dev(*inputs))
+    for g, (want, off), name in zip(got, aref.grads(*inputs), ("dx", "da", "db")):
+        assert g.shape == want.shape and g.dtype == BF
+        # the operands' roundings add about as much as the output's own, each of an rms of half a step / sqrt(3)
+        ref.check(g, want, off, name, rms_steps=2.0)
+    again = w8.linear_adapters_backward(*dev(*inputs))
+    assert all(same(a, b) for a, b in zip(got, again))
+    for asked in [(True, False, False), (False, True, False), (False, False, True), (True, False, True)]:
+        some = w8.linear_adapters_backward(*dev(*inputs), *asked)
+        for g, s, wanted in zip(got, some, asked):
+            assert (s is None) == (not wanted)
+            assert s is None or same(s, g)
+    for i in range(L):
+        if not (inputs[7] == i).any():
+            assert not got[1][i].any() and not got[2][i].any()
+
+
+def test_tokens_without_adapters_have_the_linears_gradient(w8):
+    for M, N, K in [(40, 2776, 2592), (300, 520, 256), (700, 2048, 512)]:
+        inputs = dev(*grad_inputs(M, K, N, 16, 3, "none", 3))
+        dx, da, db = w8.linear_adapters_backward(*inputs)
+        want = w8.linear_backward(*inputs[:5], dw=False, dbias=False)[0]
+        # (the same sums; the tiles of a large product may be others, and with them the sums' order)
+        ref.check(dx, want.cpu().double(), 2 * N * U * float(want.abs().max()) * 4, "dx", rms_steps=1.5)
+        assert not da.any() and not db.any()
+
+
+def test_adapter_gradients_against_differences(w8):
+    """The formulas themselves: the gradients of sum(dy * y) in 64 bits by central differences."""
+    M, K, N, R, L = 5, 32, 24, 8, 2
+    inputs = grad_inputs(M, K, N, R, L, "mixed", 77)
+    dy, xq, xs, wq, ws, a, b, ids, scaling = inputs
+    x0 = xq.double() * xs.double()[:, None]
+    w = wq.double() * ws.double()[:, None]
+
+    def loss(x, a, b):
+        y = x @ w.T
+        for i in range(L):
+            at = ids == i
+            y[at] += scaling[i].double() * (x[at] @ a[i].T) @ b[i].T
+        return (y * dy.double()).sum()
+
+    got = w8.linear_adapters_backward(*dev(*inputs))
+    args = [x0, a.double(), b.double()]
+    offs = [o for _, o in aref.grads(*inputs)]
+    g = torch.Generator().manual_seed(1)
+    for k, (t, grad, off) in enumerate(zip(args, got, offs)):
+        for _ in range(6):
+            at = tuple(int(torch.randint(0, n, (1,), generator=g)) for n in t.shape)
+            e = torch.zeros_like(t)
+            e[at] = 1e-3
+            up_, down_ = [list(args), list(args)]
+            up_[k], down_[k] = t + e, t - e
+            d = float((loss(*up_) - loss(*down_)) / 2e-3)
+            assert abs(float(grad[at]) - d) <= float(off[at]) + 2 ** -8 * abs(d) + 1e-9, (k, at)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 96, 64), (64, 2776, 2592), (700, 520, 512)])
+def test_other_adapters_do_not_matter_to_gradients(w8, M, N, K):
+    dy, xq, xs, wq, ws, a, b, ids, scaling = grad_inputs(M, K, N, 16, 4, "mixed", 5)
+    got = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, ids, scaling))
+    bad_a, bad_b, bad_s = a.clone(), b.clone(), scaling.clone()
+    bad_a[1, 3], bad_b[1, 5], bad_s[1] = float("nan"), float("inf"), float("nan")
+    bad = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, bad_a, bad_b, ids, bad_s))
+    keep = (ids != 1).nonzero().flatten().to(DEV)
+    assert same(bad[0][keep], got[0][keep])
+    others = [0, 2, 3]
+    assert same(bad[1][others], got[1][others]) and same(bad[2][others], got[2][others])
+    # a NaN token is its own adapter's trouble alone
+    xs2 = xs.clone()
+    m = int((ids == 2).nonzero()[0])
+    xs2[m] = float("nan")
+    bad = w8.linear_adapters_backward(*dev(dy, xq, xs2, wq, ws, a, b, ids, scaling))
+    others = [0, 1, 3]
+    assert same(bad[0], got[0]) and same(bad[1][others], got[1][others]) and same(bad[2][others], got[2][others])
+
+
+def test_gradient_workspaces_and_addresses(w8):
+    for M, N, K in [(50, 2776, 2592), (300, 520, 256), (600, 77, 128)]:
+        dy, xq, xs, wq, ws, a, b, ids, scaling = dev(*grad_inputs(M, K, N, 24, 3, "mixed", 8))
+        want = w8.linear_adapters_backward(dy, xq, xs, wq, ws, a, b, ids, scaling)
+        need = w8.lib.w8a8_linear_adapters_backward_workspace(M, N, K, 24, 3, 1, 1, 1)
+        for fill in (0, 255):
+            space = torch.full((need + 32,), fill, dtype=torch.uint8, device=DEV)
+            got = w8.linear_adapters_backward(dy, xq, xs, wq, ws, a, b, ids, scaling, workspace=space[:need])
+            assert all(same(x, y) for x, y in zip(got, want)) and (space[need:] == fill).all()
+        # dy at an odd address
+        room = torch.empty(M * N + 1, dtype=BF, device=DEV)
+        odd = room[1:].view(M, N)
+        odd.copy_(dy)
+        got = w8.linear_adapters_backward(odd, xq, xs, wq, ws, a, b, ids, scaling)
+        assert same(got[1], want[1]) and same(got[2], want[2])
+        ref.check(got[0], want[0].cpu().double(), 2 * N * U * float(want[0].abs().max()) * 4, "dx", rms_steps=1.5)
+    e = torch.empty(0, 77, dtype=BF, device=DEV)
+    dx, da, db = w8.linear_adapters_backward(e, xq[:0], xs[:0], wq, ws, a, b, ids[:0], scaling)
+    assert dx.shape == (0, 128) and not da.any() and not db.any() and da.shape == a.shape and db.shape == b.shape
+
+
+@pytest.mark.parametrize("M,K,N,R,L,kind", SHAPES + GRADS)
+def test_the_adapters_share_alone(w8, M, K, N, R, L, kind):
+    """A weight of scale zero leaves the adapters' products and their rounding."""
+    x, wq, ws, a, b, ids, scaling, _ = adapter_inputs(M, K, N, R, L, kind, M + K + N + R)
+    xq, xs = ref.codes_of(x)
+    ws = torch.zeros_like(ws)
+    y = w8.linear_adapters(*dev(xq, xs, wq, ws, a, b, ids, scaling))
+    ref.check(y, *aref.linear(xq, xs, wq, ws, a, b, ids, scaling, None), "y", rms_steps=2.0)
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(M)).to(BF)
+    dx = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, ids, scaling), da=False, db=False)[0]
+    ref.check(dx, *aref.grads(dy, xq, xs, wq, ws, a, b, ids, scaling)[0], "dx", rms_steps=2.0)

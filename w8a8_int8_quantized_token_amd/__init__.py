@@ -9,7 +9,8 @@ Ideogram 4.0" (arXiv 2606.14598).
 from ._lib import LIB_PATH, MAX_K, W8A8Error, lib, status_str
 from .block_ops import (gated_linear, gated_linear_backward, gated_linear_dynamic, linear_backward, linear_dynamic,
                         qk_norm_rope, qk_norm_rope_backward)
-from .adapter_ops import (add_rms_norm_backward, add_rms_norm_quantize, linear_adapters, linear_adapters_dynamic)
+from .adapter_ops import (add_rms_norm_backward, add_rms_norm_quantize, linear_adapters, linear_adapters_backward,
+                          linear_adapters_dynamic)
 from .autograd import gated_linear_ste, linear_ste
 from .module import W8A8GatedMLP, W8A8Linear, W8A8QKV
 from .ops import (dequantize_rows, gemm_f32_fp8, gemm_i32, linear, linear_fp8, linear_splitk,
@@ -22,7 +23,8 @@ __all__ = ["LIB_PATH", "MAX_K", "W8A8Error", "W8A8GatedMLP", "W8A8Linear", "W8A8
            "add_rms_norm_quantize", "dequant_bf16_linear",
            "dequantize_rows", "gated_linear", "gated_linear_backward", "gated_linear_dynamic", "gated_linear_ste",
            "gemm_f32_fp8", "gemm_i32",
-           "lib", "linear", "linear_adapters", "linear_adapters_dynamic", "linear_backward", "linear_dynamic",
+           "lib", "linear", "linear_adapters", "linear_adapters_backward",
+           "linear_adapters_dynamic", "linear_backward", "linear_dynamic",
            "linear_fp8", "linear_splitk", "linear_ste",
            "mfma_ceiling", "select_splitk", "splitk_workspace_bytes",
            "num_tiles", "qk_norm_rope", "qk_norm_rope_backward", "quantize_act", "quantize_act_fp8", "quantize_weight",

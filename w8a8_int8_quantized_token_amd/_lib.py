@@ -87,6 +87,8 @@ def _load() -> ctypes.CDLL:
         "w8a8_add_rms_norm_backward": (st, [p, p, p, p, p, p, i64, i64, ctypes.c_float, p, sz, p]),
         "w8a8_linear_adapters_workspace": (sz, [i64, i64, i64, i64, i32]),
         "w8a8_linear_adapters": (st, [p] * 10 + [i64] * 5 + [i32, p, sz, p]),
+        "w8a8_linear_adapters_backward_workspace": (sz, [i64] * 5 + [i32] * 3),
+        "w8a8_linear_adapters_backward": (st, [p] * 12 + [i64] * 5 + [p, sz, p]),
         "w8a8_linear_adapters_dynamic": (st, [p] * 9 + [i64] * 5 + [p, sz, p]),
     }
     for name, (res, args) in sig.items():

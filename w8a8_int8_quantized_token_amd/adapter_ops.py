@@ -117,3 +117,33 @@ def linear_adapters_dynamic(x, wq, w_scale, a, b, ids, scaling, bias=None, y=Non
     pws, nws, workspace = _workspace(workspace, lib.w8a8_linear_adapters_workspace(M, N, K, R, 1), dev)
     _call(dev, lib.w8a8_linear_adapters_dynamic, px, pw, ps, pb, *low, py, M, N, K, R, L, pws, nws)
     return y
+
+
+def linear_adapters_backward(dy, xq, x_scale, wq, w_scale, a, b, ids, scaling, dx: bool = True, da: bool = True,
+                             db: bool = True, workspace=None):
+    """Gradients of ``linear_adapters`` for dy bf16 [M,N] on frozen codes of the
+    weight, the rounding of the activations passed straight through: (dx bf16
+    [M,K], da bf16 [L,R,K], db bf16 [L,N,R]), None where not asked for.  xq and
+    x_scale may be None without da and db."""
+    if workspace is None:
+        grads = _calls.linear_adapters_backward(dy, xq, x_scale, wq, w_scale, a, b, ids, scaling, dx, da, db)
+        if grads is not None:
+            return grads
+    pdy, M, N, dev = _matrix(dy, BF, "dy")
+    K = _rows(wq, "wq")[1]
+    pw = _on(wq, torch.int8, (N, K), "wq", dev)
+    ps = _on(w_scale, torch.float32, (N,), "w_scale", dev)
+    if xq is None and x_scale is None and not da and not db:
+        pxq = pxs = None
+    else:
+        pxq = _on(xq, torch.int8, (M, K), "xq", dev)
+        pxs = _on(x_scale, torch.float32, (M,), "x_scale", dev)
+    low, R, L = _adapters(a, b, ids, scaling, M, N, K, dev)
+    gx = _empty((M, K), BF, dev) if dx else None
+    ga = _empty((L, R, K), BF, dev) if da else None
+    gb = _empty((L, N, R), BF, dev) if db else None
+    need = lib.w8a8_linear_adapters_backward_workspace(M, N, K, R, L, bool(dx), bool(da), bool(db))
+    pws, nws, workspace = _workspace(workspace, need, dev)
+    _call(dev, lib.w8a8_linear_adapters_backward, pdy, pxq, pxs, pw, ps, *low, _ptr(gx), _ptr(ga), _ptr(gb), M, N, K, R,
+          L, pws, nws)
+    return gx, ga, gb

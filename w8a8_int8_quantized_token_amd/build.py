@@ -20,7 +20,7 @@ CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["quantize_rows.hip", "dequantize_rows.hip", "gemm_i8.hip", "splitk_reduce.hip",
            "mfma_ceiling.hip", "w8a8_api.hip", "gemm_gated.hip", "gemm_gated_grad.hip", "gemm_bf16.hip",
            "backward_layout.hip", "few_grad.hip", "few_tokens.hip", "qk_norm_rope.hip", "block_api.hip",
-           "add_norm_quantize.hip", "adapter_down.hip", "gemm_low.hip"]
+           "add_norm_quantize.hip", "adapter_down.hip", "adapter_grad.hip", "gemm_low.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

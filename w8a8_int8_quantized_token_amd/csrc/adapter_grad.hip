@@ -1,0 +1,260 @@
+// Gradients of the low-rank adapters' two matrices: for each adapter i, over its
+// rows m (tokens),
+//   out[i][r, c] = sum_m v[m, r] x[m, c],
+// v bf16 [M, ldt] (t or u, which have the scalings), x the activations' codes
+// (v then has their scales too) or the output's gradient in bf16.  fp32 sums on
+// the bf16 matrix cores, both operands exact.
+//
+// The rows of an adapter come as a list (`lists`, made beside the operands'
+// layout), so ids may be in any order; a row's values lie together, and only
+// the row's address is looked up.
+//
+// Bound by reading x once.  A wavefront takes 32 rows of the list at a time and
+// 16 * KB columns: a lane loads KB columns of each of 8 rows, and value j of
+// those 8 rows is its fragment of column KB * (lane % 16) + j for
+// v_mfma_f32_16x16x32_bf16; v's ranks are dealt to the lanes the same way.  No
+// transposition goes through LDS.  The list is cut into parts where columns and
+// adapters leave compute units idle; the wavefronts' sums are joined through
+// LDS and the parts' go to slices for launch_finish, each in a fixed order.
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace w8a8 {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kWave = 64, kWaves = 8, kThreads = kWave * kWaves;
+constexpr int kRows = 32;    // rows of the list of a step
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+// The 16-bit values j of two rows' words.
+__device__ __forceinline__ uint32_t pair(uint32_t first, uint32_t second, int j) {
+  return __builtin_amdgcn_perm(second, first, j % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// KR ranks to a lane (16 KR of a workgroup), KB columns.
+template <int KR, int KB, bool kCodes>
+__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
+  constexpr int kWords = kCodes ? KB / 4 : KB / 2;   // of a lane's columns in a row
+  constexpr int kSums = KR * KB * kWave;              // f32x4 of a wavefront's sums
+  constexpr int kAtOnce = KR * KB <= 16 ? 4 : KR * KB <= 32 ? 2 : 1;   // wavefronts' sums in LDS at once
+  __shared__ f32x4 part[kAtOnce * kSums];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int l16 = lane % 16, h = lane / 16;
+  unsigned block = blockIdx.x;
+  const int cb = (int)(block % (unsigned)a.col_blocks);
+  block /= (unsigned)a.col_blocks;
+  const int rb = (int)(block % (unsigned)a.rank_blocks);
+  block /= (unsigned)a.rank_blocks;
+  const int slice = (int)(block % (unsigned)a.parts), id = (int)(block / (unsigned)a.parts);
+  const int64_t col = (int64_t)cb * 16 * KB + l16 * KB;
+  const int rank = rb * 16 * KR + l16 * KR;
+  // this part's rows of the adapter's list
+  const int from = a.starts[id], to = a.starts[id + 1];
+  const int per = (to - from + a.parts - 1) / a.parts;
+  const int first = from + slice * per, last = min(first + per, to);
+
+  f32x4 acc[KR][KB];
+#pragma unroll
+  for (int r = 0; r < KR; ++r)
+#pragma unroll
+    for (int j = 0; j < KB; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+
+  struct Step {
+    uint32_t x[8][kWords];
+    uint32_t v[8][(KR + 1) / 2];
+  };
+  // Places past the part's end: the last row again, with zeros of v.
+  auto load = [&](int p0, Step& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + 8 * h + i;
+      const int64_t m = a.list[min(p, last - 1)];
+      if constexpr (kCodes) {
+        const int8_t* row = static_cast<const int8_t*>(a.x) + m * a.C;
+        __builtin_memcpy(s.x[i], __builtin_assume_aligned(row + min(col, a.C - KB), KB), KB);
+      } else {
+        const uint16_t* row = static_cast<const uint16_t*>(a.x) + m * a.C;
+        if (col + KB <= a.C) {
+          __builtin_memcpy(s.x[i], row + col, 2 * KB);
+        } else {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            const uint32_t lo = col + 2 * w < a.C ? row[col + 2 * w] : 0;
+            const uint32_t hi = col + 2 * w + 1 < a.C ? row[col + 2 * w + 1] : 0;
+            s.x[i][w] = lo | hi << 16;
+          }
+        }
+      }
+      const uint16_t* v = a.v + m * a.ldt + min(rank, a.ldt - KR);
+      if constexpr (KR == 1) {
+        s.v[i][0] = *v;
+      } else {
+        __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
+      }
+#pragma unroll
+      for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = p < last ? s.v[i][w] : 0;
+    }
+  };
+  auto multiply = [&](const Step& s) __attribute__((always_inline)) {
+    u32x4 fv[KR];
+#pragma unroll
+    for (int r = 0; r < KR; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) fv[r][q] = pair(s.v[2 * q][r / 2], s.v[2 * q + 1][r / 2], r);
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      u32x4 fx;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (kCodes)
+          fx[q] = pack2((float)(int8_t)(s.x[2 * q][j / 4] >> (8 * (j % 4))),
+                        (float)(int8_t)(s.x[2 * q + 1][j / 4] >> (8 * (j % 4))));
+        else fx[q] = pair(s.x[2 * q][j / 2], s.x[2 * q + 1][j / 2], j);
+      }
+#pragma unroll
+      for (int r = 0; r < KR; ++r)
+        acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[r]),
+                                                            __builtin_bit_cast(bf16x8, fx), acc[r][j], 0, 0, 0);
+    }
+  };
+  const int mine = first + wave * kRows;
+  if (mine < last) {
+    Step now, next;
+    load(mine, now);
+    for (int p = mine; p < last; p += kWaves * kRows) {
+      if (p + kWaves * kRows < last) load(p + kWaves * kRows, next);
+      multiply(now);
+      now = next;
+    }
+  }
+  // the other wavefronts' sums onto the first's, in order
+#pragma unroll
+  for (int w0 = 1; w0 < kWaves; w0 += kAtOnce) {
+    if (wave >= w0 && wave < w0 + kAtOnce) {
+#pragma unroll
+      for (int r = 0; r < KR; ++r)
+#pragma unroll
+        for (int j = 0; j < KB; ++j) part[(wave - w0) * kSums + (r * KB + j) * kWave + lane] = acc[r][j];
+    }
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 0; w < kAtOnce; ++w)
+        if (w0 + w < kWaves) {
+#pragma unroll
+          for (int r = 0; r < KR; ++r)
+#pragma unroll
+            for (int j = 0; j < KB; ++j) acc[r][j] += part[w * kSums + (r * KB + j) * kWave + lane];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+  // lane: column col + j, ranks KR (4h + e) + r of the block's
+  float* out = a.slices + ((int64_t)slice * a.count + id) * a.R * a.C;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r0 = rb * 16 * KR + KR * (4 * h + e);
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+      if (r0 + r >= a.R) continue;
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (col + j < a.C) out[kCodes ? (r0 + r) * a.C + col + j : (col + j) * a.R + r0 + r] = acc[r][j][e];
+    }
+  }
+}
+
+// Ranks and columns of a lane: as many sums as registers allow.
+struct Shape {
+  int kr, kb;
+};
+Shape shape_of(int R, bool codes) {
+  if (R <= 16) return {1, codes ? 16 : 8};
+  if (R <= 32) return {2, codes ? 16 : 8};
+  return {4, codes ? 8 : 4};
+}
+
+// Parts of the lists: about two workgroups per compute unit, each wavefront a
+// step or more.
+int parts_of(int64_t M, int64_t C, int R, int count, bool codes) {
+  const Shape s = shape_of(R, codes);
+  const int64_t blocks = (C + 16 * s.kb - 1) / (16 * s.kb) * ((R + 16 * s.kr - 1) / (16 * s.kr)) * count;
+  return (int)std::max<int64_t>(1, std::min((512 + blocks - 1) / blocks, (M + kWaves * kRows - 1) / (kWaves * kRows)));
+}
+
+template <int KR, int KB, bool kCodes>
+hipError_t launch(AdapterGrad a, hipStream_t stream) {
+  a.col_blocks = (int)((a.C + 16 * KB - 1) / (16 * KB));
+  a.rank_blocks = (a.R + 16 * KR - 1) / (16 * KR);
+  const int64_t blocks = (int64_t)a.col_blocks * a.rank_blocks * a.parts * a.count;
+  if (blocks * kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((adapter_grad_kernel<KR, KB, kCodes>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ---- the adapters' share of few rows' input gradient ----
+
+// out fp32 [M, C] = sum_r u[m, r] p[id][r, c]: a thread for 8 columns of a row.
+constexpr int kUpThreads = 256;
+__global__ __launch_bounds__(kUpThreads) void adapter_up_kernel(const uint16_t* __restrict__ u, int ldt,
+                                                                const uint16_t* __restrict__ p,
+                                                                const int32_t* __restrict__ ids, int count, int R,
+                                                                int64_t C, float* __restrict__ out) {
+  const int64_t m = blockIdx.y, c = ((int64_t)blockIdx.x * kUpThreads + threadIdx.x) * 8;
+  if (c >= C) return;
+  const int id = ids[m];
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+  if (id >= 0 && id < count) {
+    const uint16_t* row = p + (int64_t)id * R * C + c;
+#pragma unroll 8
+    for (int r = 0; r < R; ++r) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(row + r * C);
+      const float f = __uint_as_float((uint32_t)u[m * ldt + r] << 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[2 * e] = fmaf(f, __uint_as_float(w[e] << 16), s[2 * e]);
+        s[2 * e + 1] = fmaf(f, __uint_as_float(w[e] & 0xffff0000u), s[2 * e + 1]);
+      }
+    }
+  }
+  f32x4* o = reinterpret_cast<f32x4*>(out + m * C + c);
+  o[0] = f32x4{s[0], s[1], s[2], s[3]};
+  o[1] = f32x4{s[4], s[5], s[6], s[7]};
+}
+
+}  // namespace
+
+int adapter_grad_parts(int64_t M, int64_t C, int64_t R, int64_t count, bool codes) {
+  return parts_of(M, C, (int)R, (int)count, codes);
+}
+
+hipError_t launch_adapter_grad(AdapterGrad a, bool codes, hipStream_t s) {
+  const Shape k = shape_of(a.R, codes);
+  if (codes) {
+    if (k.kr == 1) return launch<1, 16, true>(a, s);
+    return k.kr == 2 ? launch<2, 16, true>(a, s) : launch<4, 8, true>(a, s);
+  }
+  if (k.kr == 1) return launch<1, 8, false>(a, s);
+  return k.kr == 2 ? launch<2, 8, false>(a, s) : launch<4, 4, false>(a, s);
+}
+
+hipError_t launch_adapter_up(const uint16_t* u, int64_t ldt, const uint16_t* p, const int32_t* ids, int64_t count,
+                             int64_t R, int64_t M, int64_t C, float* out, hipStream_t s) {
+  const dim3 grid((unsigned)((C / 8 + kUpThreads - 1) / kUpThreads), (unsigned)M);
+  hipLaunchKernelGGL(adapter_up_kernel, grid, dim3(kUpThreads), 0, s, u, (int)ldt, p, ids, (int)count, (int)R, C, out);
+  return hipGetLastError();
+}
+
+}  // namespace w8a8

@@ -2,7 +2,7 @@
 // product kernel wants both operands contiguous along the summed index, but
 // the input's gradient sums over output channels (rows of the weight) and the
 // weight's gradient over tokens (rows of the activations).  Before the
-// products, one launch of up to four jobs (`prepare`):
+// products, one launch of up to six jobs (`prepare`):
 //   turn_codes:  int8 [R,C] (times scale[r]) -> bf16 [C, ld], zeros past
 //     column R; or, `paired`, the R = 2N rows of a stacked [gate; up] weight
 //     with 16 gate columns, the 16 up columns of the same channels, and so on
@@ -10,6 +10,8 @@
 //   turn_values: bf16 [R,C] -> bf16 [C, ld] (zeros past column R), and the
 //     fp32 sums of each column over blocks of rows;
 //   pad_rows:    bf16 [R,C] -> bf16 [R, ld], zeros past column C;
+//   turn_each:   as turn_values without sums, for several matrices;
+//   lists:       the rows of each id, in order (low-rank adapters);
 // after them one launch of up to three (`finish`):
 //   join_slices: the fp32 slices of a product split along its sum -> bf16;
 //   sum_rows:    fp32 [P,C] -> bf16 [C], summed over P in a fixed order.
@@ -186,6 +188,54 @@ __device__ void pad_rows(const LayoutJob& j, int64_t block) {
   }
 }
 
+// A wavefront for an id: where its list starts (the rows with smaller ids),
+// then its rows in order.  Four loads in flight in each pass.
+__device__ void make_lists(const LayoutJob& j, int64_t block) {
+  const int lane = threadIdx.x % 64;
+  const int id = (int)(block * (kThreads / 64) + threadIdx.x / 64), count = (int)j.C, M = (int)j.R;
+  if (id >= count) return;   // whole wavefronts
+  const int32_t* ids = static_cast<const int32_t*>(j.in);
+  constexpr int kLoads = 4;
+  int before = 0, own = 0;
+  for (int m0 = 0; m0 < M; m0 += 64 * kLoads) {
+    int v[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = m0 + i * 64 + lane < M ? ids[m0 + i * 64 + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      before += __popcll(__builtin_amdgcn_ballot_w64(v[i] >= 0 && v[i] < id));
+      own += __popcll(__builtin_amdgcn_ballot_w64(v[i] == id));
+    }
+  }
+  if (lane == 0) {
+    j.starts[id] = before;
+    if (id == count - 1) j.starts[count] = before + own;
+  }
+  if (own == 0) return;
+  int at = before;
+  for (int m0 = 0; m0 < M; m0 += 64 * kLoads) {
+    int v[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = m0 + i * 64 + lane < M ? ids[m0 + i * 64 + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint64_t hits = __builtin_amdgcn_ballot_w64(v[i] == id);
+      if (v[i] == id) j.list[at + __popcll(hits & ((uint64_t(1) << lane) - 1))] = m0 + i * 64 + lane;
+      at += __popcll(hits);
+    }
+  }
+}
+
+// One of `batch` matrices, each as turn_values without sums.
+__device__ void turn_each(const LayoutJob& j, int64_t block, Lds& lds) {
+  const int64_t per = (j.C + kT - 1) / kT * ((j.ld + j.span - 1) / j.span), k = block / per;
+  LayoutJob one = j;
+  one.in = static_cast<const uint16_t*>(j.in) + k * j.R * j.C;
+  one.out = j.out + k * j.C * j.ld;
+  one.sums = nullptr;
+  turn_values(one, block - k * per, lds);
+}
+
 struct Prepare {
   LayoutJob job[kMaxJobs];
   int64_t end[kMaxJobs];   // workgroups up to and with each job
@@ -201,6 +251,8 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare p) {
     case LayoutJob::kTurnCodes: turn_codes<false>(j, block, lds); break;
     case LayoutJob::kTurnPaired: turn_codes<true>(j, block, lds); break;
     case LayoutJob::kTurnValues: turn_values(j, block, lds); break;
+    case LayoutJob::kTurnEach: turn_each(j, block, lds); break;
+    case LayoutJob::kLists: make_lists(j, block); break;
     default: pad_rows(j, block); break;
   }
 }
@@ -304,6 +356,8 @@ hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream) {
       const auto tiles = [](int64_t v, int64_t t) { return (v + t - 1) / t; };
       end += j.kind == LayoutJob::kPadRows      ? tiles(j.R * (j.ld / 8), kPadBlock)
              : j.kind == LayoutJob::kTurnValues ? tiles(j.C, kT) * tiles(j.R, j.span)
+             : j.kind == LayoutJob::kTurnEach   ? tiles(j.C, kT) * tiles(j.ld, j.span) * j.batch
+             : j.kind == LayoutJob::kLists      ? tiles(j.C, kThreads / 64)
                                                 : tiles(j.C, kCodeCols) * tiles(j.ld, kCodeRows);
     }
     p.end[k] = end;

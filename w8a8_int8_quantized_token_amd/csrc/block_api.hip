@@ -170,7 +170,8 @@ bool copy_lines(int64_t M, int64_t N, int64_t K) {
   return N % kLine != 0 && M >= 256 && N >= 2048 && K >= 512;
 }
 
-BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy, bool few) {
+BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw, bool db, bool copy_dy, bool few,
+                   bool low = false) {
   BackPlan p{};
   p.few = dx && few;
   const int64_t cols = (gated ? 2 : 1) * N;
@@ -187,7 +188,8 @@ BackPlan back_plan(int64_t M, int64_t N, int64_t K, bool gated, bool dx, bool dw
   if (dx) {
     if (gated) p.first = w.add(2 * M * p.ld);
     if (!few) p.wt = w.add(2 * K * p.ld);
-    p.ranges_x = few ? w8a8::few_grad_slices(M, N, K, gated) : w8a8::gemm_bf16_slices(M, K, p.ld);
+    // few tokens with adapters: their share is a slice of its own
+    p.ranges_x = few ? w8a8::few_grad_slices(M, N, K, gated) + low : w8a8::gemm_bf16_slices(M, K, p.ld, low);
     if (few || p.ranges_x > 1) p.slices_x = w.add(4 * M * K * p.ranges_x);
   }
   if (dw) {
@@ -227,12 +229,12 @@ hipError_t products(const BackPlan& p, void* ws, const uint16_t* first, const in
     if (p.few)
       e = gated ? w8a8::launch_few_grad(first, p.ld, wq, nullptr, slices, M, cols / 2, K, true, stream)
                 : w8a8::launch_few_grad(first, cols, wq, w_scale, slices, M, cols, K, false, stream);
-    else e = w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.wt), dx, slices, M, K, p.ld, stream);
+    else e = w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.wt), dx, slices, M, K, p.ld, nullptr, stream);
     if (slices) jobs[n++] = {slices, dx, p.ranges_x, M * K, true, 0};
   }
   if (dw && e == hipSuccess) {
     float* slices = p.ranges_w > 1 && aligned(dw, 16) ? at<float>(ws, p.slices_w) : nullptr;
-    e = w8a8::launch_gemm_bf16(at<uint16_t>(ws, p.second), at<uint16_t>(ws, p.xt), dw, slices, cols, K, p.mp, stream);
+    e = w8a8::launch_gemm_bf16(at<uint16_t>(ws, p.second), at<uint16_t>(ws, p.xt), dw, slices, cols, K, p.mp, nullptr, stream);
     if (slices) jobs[n++] = {slices, dw, p.ranges_w, cols * K, true, 0};
   }
   if (dbias) jobs[n++] = {at<float>(ws, p.sums), dbias, p.sum_rows, cols, false, 0};
@@ -362,6 +364,48 @@ w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, 
     return launched(w8a8::launch_splitk_reduce_low(slices, p.splits, x_scale, w_scale, bias, low, y, M, N, stream));
   }
   return launched(w8a8::launch_gemm_low(p.tile, xq, x_scale, wq, w_scale, bias, low, y, M, N, K, stream));
+}
+
+// Workspace of the adapters' gradients: that of dx by itself, the adapters'
+// matrices turned (b: the first operand's rows contiguous along the channels;
+// a: along the ranks), the rows of each adapter, t, u, and u with the codes'
+// scales, and the slices of the matrices' gradients.
+struct AdapterBackPlan {
+  BackPlan x;
+  int64_t ldt, ldn;
+  int64_t bt, at, list, starts, t, u, v, slices_a, slices_b;
+  int parts_a, parts_b;
+  int64_t bytes;
+};
+AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, bool dx, bool da, bool db,
+                                  bool copy_dy, bool few) {
+  AdapterBackPlan p{};
+  p.x = back_plan(M, N, K, false, dx, false, false, copy_dy, few, true);
+  p.ldt = up(R, 16);
+  p.ldn = up(N, 16);
+  Pieces w;
+  w.bytes = p.x.bytes;
+  if (dx || da) {
+    p.bt = w.add(2 * L * R * p.ldn);
+    p.u = w.add(2 * M * p.ldt);
+  }
+  if (dx && !few) p.at = w.add(2 * L * K * R);
+  if (da || db) {
+    p.list = w.add(4 * M);
+    p.starts = w.add(4 * (L + 1));
+  }
+  if (da) {
+    p.v = w.add(2 * M * p.ldt);
+    p.parts_a = w8a8::adapter_grad_parts(M, K, R, L, true);
+    p.slices_a = w.add(4 * p.parts_a * L * R * K);
+  }
+  if (db) {
+    p.t = w.add(2 * M * p.ldt);
+    p.parts_b = w8a8::adapter_grad_parts(M, N, R, L, false);
+    p.slices_b = w.add(4 * p.parts_b * L * R * N);
+  }
+  p.bytes = w.bytes;
+  return p;
 }
 
 // ---- norm with codes ----
@@ -629,6 +673,118 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t* x, const int8_t* wq, co
                                          hipStream_t stream) {
   return adapters(x, nullptr, nullptr, wq, w_scale, bias, a, b, scaling, ids, y, M, N, K, R, L, true, -1, workspace,
                   workspace_bytes, stream);
+}
+
+size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int dx, int da,
+                                               int db) {
+  if (!adapters_ok(M, N, K, R, L) || M == 0) return 0;
+  int64_t most = 0;   // the largest of the plans that calls of these sizes may take, as their addresses are
+  for (const bool copy : {true, false})
+    for (const bool few : {false, true})
+      if ((copy || (N % 8 == 0 && N % kLine != 0)) && (!few || few_rows(M, N, K)))
+        most = std::max(most, adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few).bytes);
+  return (size_t)most;
+}
+
+w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, const float* x_scale, const int8_t* wq,
+                                          const float* w_scale, const uint16_t* a, const uint16_t* b,
+                                          const float* scaling, const int32_t* ids, uint16_t* dx, uint16_t* da,
+                                          uint16_t* db, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!adapters_ok(M, N, K, R, L) || (dx && up(N, kLine) > kMaxSummed)) return W8A8_ERR_SHAPE;
+  if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(da, 16) || !aligned(db, 16)) return W8A8_ERR_ALIGN;
+  if (M == 0) {
+    if (da) TRY(w8a8::launch_zero(da, L * R * K, stream));
+    if (db) TRY(w8a8::launch_zero(db, L * R * N, stream));
+    return W8A8_OK;
+  }
+  if (!dx && !da && !db) return W8A8_OK;
+  const bool codes = da || db;   // the activations
+  if (!dy || !scaling || !ids || (codes && (!xq || !x_scale)) || (dx && (!wq || !w_scale)) || ((dx || db) && !a) ||
+      ((dx || da) && !b))
+    return W8A8_ERR_NULL;
+  if (!aligned(scaling, 4) || !aligned(ids, 4) || !aligned(a, 16) || !aligned(b, 16) ||
+      (codes && (!aligned(xq, 16) || !aligned(x_scale, 4))) || (dx && (!aligned(wq, 16) || !aligned(w_scale, 4))))
+    return W8A8_ERR_ALIGN;
+  const bool few = dx && few_rows(M, N, K) && aligned(dx, 16);
+  const bool copy = N % 8 != 0 || !aligned(dy, 16) || (dx && copy_lines(M, N, K));
+  const AdapterBackPlan p = adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few);
+  const w8a8_status st = check_workspace(workspace, workspace_bytes, p.bytes);
+  if (st != W8A8_OK) return st;
+  using Job = w8a8::LayoutJob;
+  void* const ws = workspace;
+  uint16_t *bt = at<uint16_t>(ws, p.bt), *a_turned = at<uint16_t>(ws, p.at), *t = at<uint16_t>(ws, p.t),
+           *u = at<uint16_t>(ws, p.u), *v = at<uint16_t>(ws, p.v);
+  int32_t *list = at<int32_t>(ws, p.list), *starts = at<int32_t>(ws, p.starts);
+  Job jobs[w8a8::kMaxJobs];
+  int n = 0;
+  const uint16_t* first = dy;
+  if (dx && !few) {
+    if (copy) {
+      jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(ws, p.x.copy), nullptr, M, N, p.x.ldy, 0};
+      first = at<uint16_t>(ws, p.x.copy);
+    }
+    jobs[n++] = {Job::kTurnCodes, wq, w_scale, at<uint16_t>(ws, p.x.wt), nullptr, N, K, p.x.ld, 0};
+    jobs[n++] = {Job::kTurnEach, a, nullptr, a_turned, nullptr, R, K, R, 64, L};
+  }
+  if (dx || da) jobs[n++] = {Job::kTurnEach, b, nullptr, bt, nullptr, N, R, p.ldn, 64, L};
+  if (codes) jobs[n++] = {Job::kLists, ids, nullptr, nullptr, nullptr, M, L, 0, 0, 0, list, starts};
+  if (n > 0) TRY(w8a8::launch_prepare(jobs, n, stream));
+  w8a8::Down d{};
+  d.ids = ids;
+  d.scaling = scaling;
+  d.M = M;
+  d.R = (int)R;
+  d.ldt = (int)p.ldt;
+  d.count = (int)L;
+  if (db) {
+    d.x = xq;
+    d.scale = x_scale;
+    d.p = a;
+    d.p_stride = R * K;
+    d.K = d.ldp = (int)K;
+    d.t = t;
+    TRY(w8a8::launch_down(w8a8::DownRows::kCodes, d, stream));
+  }
+  if (dx || da) {
+    d.x = dy;
+    d.scale = nullptr;
+    d.p = bt;
+    d.p_stride = R * p.ldn;
+    d.K = (int)N;
+    d.ldp = (int)p.ldn;
+    d.t = u;
+    if (da) {
+      d.t2 = v;
+      d.scale2 = x_scale;
+    }
+    TRY(w8a8::launch_down(w8a8::DownRows::kValues, d, stream));
+  }
+  w8a8::JoinJob join[w8a8::kMaxJobs];
+  int joins = 0;
+  if (dx) {
+    // the join writes 16 bytes at a time
+    float* slices = few || (p.x.ranges_x > 1 && aligned(dx, 16)) ? at<float>(ws, p.x.slices_x) : nullptr;
+    if (few) {
+      TRY(w8a8::launch_few_grad(dy, N, wq, w_scale, slices, M, N, K, false, stream));
+      TRY(w8a8::launch_adapter_up(u, p.ldt, a, ids, L, R, M, K, slices + (p.x.ranges_x - 1) * M * K, stream));
+    } else {
+      const w8a8::Low low{u, a_turned, ids, p.ldt, R, L};
+      TRY(w8a8::launch_gemm_bf16(first, at<uint16_t>(ws, p.x.wt), dx, slices, M, K, p.x.ld, &low, stream));
+    }
+    if (slices) join[joins++] = {slices, dx, p.x.ranges_x, M * K, true, 0};
+  }
+  if (da) {
+    w8a8::AdapterGrad g{xq, v, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
+    TRY(w8a8::launch_adapter_grad(g, true, stream));
+    join[joins++] = {g.slices, da, p.parts_a, L * R * K, true, 0};
+  }
+  if (db) {
+    w8a8::AdapterGrad g{dy, t, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
+    TRY(w8a8::launch_adapter_grad(g, false, stream));
+    join[joins++] = {g.slices, db, p.parts_b, L * R * N, true, 0};
+  }
+  return joins > 0 ? launched(w8a8::launch_finish(join, joins, stream)) : W8A8_OK;
 }
 
 }  // extern "C"

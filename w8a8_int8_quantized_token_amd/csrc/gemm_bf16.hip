@@ -28,8 +28,25 @@ enum BfCfg { kBf256, kBfWhole256, kBf192, kBf128x256, kBf128s2, kBf128s4, kBf64,
 const TileDesc kBfTiles[kNumBf] = {desc<CfgSplit>(), desc<CfgWhole>(), desc<Cfg192>(), desc<CfgTail>(), desc<Cfg128s2>(),
                                    desc<Cfg128s4>(), desc<Cfg64s4>(), desc<Cfg64x128>(), desc<Cfg128x64>()};
 
+// Tiles with adapters: those whose K loop has the registers for it.
+bool low_tile(int cfg, bool raw) { return cfg != kBf256 && cfg != kBf192 && (cfg != kBfWhole256 || !raw); }
+
 template <Epilogue EPI>
 hipError_t launch_bf16(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, hipStream_t s, KSplit ks) {
+  if constexpr (kLow<EPI>) {
+    if (!low_tile(cfg, EPI == Epilogue::kRawLow)) return hipErrorInvalidValue;
+    switch (cfg) {
+      case kBfWhole256:
+        if constexpr (EPI != Epilogue::kRawLow) return launch_t<CfgWhole, OpB16, EPI>(o, M, N, K, N, s, ks);
+        else return hipErrorInvalidValue;
+      case kBf128x256: return launch_t<CfgTail, OpB16, EPI>(o, M, N, K, N, s, ks);
+      case kBf128s2: return launch_t<Cfg128s2, OpB16, EPI>(o, M, N, K, N, s, ks);
+      case kBf128s4: return launch_t<Cfg128s4, OpB16, EPI>(o, M, N, K, N, s, ks);
+      case kBf64: return launch_t<Cfg64s4, OpB16, EPI>(o, M, N, K, N, s, ks);
+      case kBf64x128: return launch_t<Cfg64x128, OpB16, EPI>(o, M, N, K, N, s, ks);
+      default: return launch_t<Cfg128x64, OpB16, EPI>(o, M, N, K, N, s, ks);
+    }
+  } else
   switch (cfg) {
     case kBf256: return launch_t<CfgSplit, OpB16, EPI>(o, M, N, K, N, s, ks);
     case kBfWhole256: return launch_t<CfgWhole, OpB16, EPI>(o, M, N, K, N, s, ks);
@@ -95,11 +112,12 @@ double cost_us(int cfg, int chunks, int64_t M, int64_t N, int64_t kb) {
   return ranges > 1 ? us + 2.5 + (double)ranges * (double)M * (double)N * 1.35e-6 : us;
 }
 
-Choice cheapest(int64_t M, int64_t N, int64_t kb) {
+Choice cheapest(int64_t M, int64_t N, int64_t kb, bool low) {
   Choice best{kBfWhole256, 1};
   double us = cost_us(best.cfg, 1, M, N, kb);
   for (int cfg = 0; cfg < kNumBf; ++cfg)
     for (const int chunks : {1, 2, 3, 4, 6, 8}) {
+      if (low && !low_tile(cfg, chunks > 1)) continue;
       if (chunks > 1 && (kb < 512 * chunks || M * N * 4 * chunks > kMaxSlices)) break;
       const double c = cost_us(cfg, chunks, M, N, kb);
       if (c < us * 0.999) best = {cfg, chunks}, us = c;
@@ -110,40 +128,46 @@ Choice cheapest(int64_t M, int64_t N, int64_t kb) {
 // The model takes about a microsecond, and a backward pass asks three times
 // for each of its products (workspace size, layout, launch): the last shapes'
 // choices are kept per thread.
-Choice choose(int64_t M, int64_t N, int64_t kb) {
+Choice choose(int64_t M, int64_t N, int64_t kb, bool low) {
   struct Entry {
     int64_t M, N, kb;
+    bool low;
     Choice c;
   };
   thread_local Entry last[8] = {};
   thread_local unsigned next = 0;
   for (const Entry& e : last)
-    if (e.M == M && e.N == N && e.kb == kb) return e.c;
+    if (e.M == M && e.N == N && e.kb == kb && e.low == low) return e.c;
   Entry& e = last[next++ % 8];
-  e = {M, N, kb, cheapest(M, N, kb)};
+  e = {M, N, kb, low, cheapest(M, N, kb, low)};
   return e.c;
 }
 
 }  // namespace
 
-int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad) {
+int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad, bool low) {
   const int64_t kb = 2 * Kpad;
-  const int64_t range = range_bytes(kb, choose(M, N, kb).chunks);
+  const int64_t range = range_bytes(kb, choose(M, N, kb, low).chunks);
   return (int)((kb + range - 1) / range);
 }
 
 hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, float* slices, int64_t M,
-                            int64_t N, int64_t Kpad, hipStream_t stream) {
+                            int64_t N, int64_t Kpad, const Low* low, hipStream_t stream) {
   const int64_t kb = 2 * Kpad;   // bytes per row
   const int8_t *pa = reinterpret_cast<const int8_t*>(a), *pb = reinterpret_cast<const int8_t*>(b);
-  const Choice c = choose(M, N, kb);
+  const Choice c = choose(M, N, kb, low != nullptr);
   const int64_t range = range_bytes(kb, c.chunks);
   const int ranges = (int)((kb + range - 1) / range);
-  if (ranges == 1 || slices == nullptr) {
-    const KSplit whole{(int)kb, 1, 0};
-    return launch_bf16<Epilogue::kBf16Plain>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, stream, whole);
+  const KSplit whole{(int)kb, 1, 0}, ks{(int)kb, ranges, M * N};
+  const bool one = ranges == 1 || slices == nullptr;
+  if (low != nullptr) {
+    const LowArgs args{low->t, low->b, low->ids, N * low->R, (int)low->ldt, (int)low->R, (int)low->count};
+    if (one)
+      return launch_bf16<Epilogue::kBf16PlainLow>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, args}, M, N, kb, stream, whole);
+    return launch_bf16<Epilogue::kRawLow>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, slices, args}, M, N, range, stream, ks);
   }
-  const KSplit ks{(int)kb, ranges, M * N};
+  if (one)
+    return launch_bf16<Epilogue::kBf16Plain>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, out, {}}, M, N, kb, stream, whole);
   return launch_bf16<Epilogue::kRawI32>(c.cfg, {pa, pb, nullptr, nullptr, nullptr, slices, {}}, M, N, range, stream, ks);
 }
 

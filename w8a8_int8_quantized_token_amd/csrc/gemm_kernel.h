@@ -810,7 +810,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       auto frag_b = [&](int j, int r0) {   // channels
         int c;
         if constexpr (Op::kBf16) {
-          const int dealt = (l_row / 4) * 8 + (l_row / 8) * 4 + l_row % 4 - (l_row / 8) * 16;
+          const int dealt = (l_row / 4) * 8 + (l_row / 8) * 4 + l_row % 4;   // as chan16
           c = j / 2 * 32 + (j % 2 ? dealt ^ 4 : dealt);
         } else {
           c = j * 32 + l_row;
@@ -851,22 +851,24 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
         }
         rb = buffer_range(extra.b + a * extra.b_stride + (int64_t)at.n0 * extra.R, chans);
         for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
-          v4i ft[kLowM], fn[kLowN];
-#pragma unroll
-          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
+          // (two row tiles' fragments at a time: all of them spill)
+          v4i fn[kLowN], ft[2];
+          ft[0] = frag_t(0, r0);
 #pragma unroll
           for (int j = 0; j < kLowN; ++j) fn[j] = frag_b(j, r0);
 #pragma unroll
-          for (int i = 0; i < kLowM; ++i)
+          for (int i = 0; i < kLowM; ++i) {
+            if (i + 1 < kLowM) ft[(i + 1) % 2] = frag_t(i + 1, r0);
 #pragma unroll
             for (int j = 0; j < kLowN; ++j) {
               auto v = get(i, j);
-              const auto d = product(fn[j], ft[i], decltype(v){});
+              const auto d = product(fn[j], ft[i % 2], decltype(v){});
 #pragma unroll
               for (int e = 0; e < (Op::kBf16 ? 4 : 16); ++e) v[e] += id[i] == a ? d[e] : 0.0f;
               set(i, j, v);
               __builtin_amdgcn_sched_barrier(0);
             }
+          }
         }
       }
     }
@@ -988,9 +990,19 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) acc[i][j] = typename Op::Acc{};
 
+    // bf16: the adapters' share is where the sums start (added after the K loop,
+    // the whole-stage 256x256 tile spills inside it); a split product has it in
+    // the first range's
+    auto start_low = [&]() __attribute__((always_inline)) {
+      if constexpr (kLow<EPI> && Op::kBf16) {
+        if (cur.c == 0) add_low(cur);
+      }
+    };
+
     // ---- K loop ----
     if constexpr (!kEpiOwn) load_scalars(cur);
     if constexpr (T::kSplit) {
+      start_low();
       const int KT6 = (KT + 5) / 6 * 6;   // padding stages read as zeros
       // six steps of the ring; the requests they make reach stage kt + 8
       auto kloop = [&](auto role) __attribute__((always_inline)) {
@@ -1044,6 +1056,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     } else {
 #pragma unroll
       for (int s = 0; s < T::S; ++s) issue(cur, ring[s], s, kChecked);
+      start_low();
       wait_vmcnt<(T::S - 1) * T::D>();
       barrier();
       frag(ring[0], 0, 0);
@@ -1077,9 +1090,6 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
 
     const int m0 = cur.m0, n0 = cur.n0;
     [[maybe_unused]] const int c0 = cur.c;
-    if constexpr (kLow<EPI> && Op::kBf16) {
-      if (c0 == 0) add_low(cur);   // a split product: into the first range's sums
-    }
     // output rows of this tile as a buffer range (bf16, ldy apart)
     __amdgpu_buffer_rsrc_t y_rsrc;
     if constexpr (kCountedStores)
@@ -1628,7 +1638,10 @@ template <class Op, Epilogue EPI>
 hipError_t launch_cfg(int cfg, const Operands<EPI>& o, int64_t M, int64_t N, int64_t K, int64_t ldy,
                       hipStream_t s, KSplit ks) {
   switch (cfg) {
-    case kSplit256: return launch_t<CfgSplit, Op, EPI>(o, M, N, K, ldy, s, ks);
+    case kSplit256:
+      // (with adapters its K loop spills; launch_gemm_low takes the next one)
+      if constexpr (kLow<EPI>) return hipErrorInvalidValue;
+      else return launch_t<CfgSplit, Op, EPI>(o, M, N, K, ldy, s, ks);
     case kWhole256: return launch_t<CfgWhole, Op, EPI>(o, M, N, K, ldy, s, ks);
     case k192: return launch_t<Cfg192, Op, EPI>(o, M, N, K, ldy, s, ks);
     case kTail128x256: return launch_t<CfgTail, Op, EPI>(o, M, N, K, ldy, s, ks);

@@ -9,6 +9,10 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
                            hipStream_t stream) {
   const LowArgs args{low.t, low.b, low.ids, N * low.R, (int)low.ldt, (int)low.R, (int)low.count};
   if (tile < 0) tile = choose_tile(M, N, K);
+  // the plans of the 256x256 split ring are those of its whole-stage form here
+  if (tile < kNumPlans && kPlans[tile].main == kSplit256) tile += 2;
+  static_assert(kPlans[2].main == kWhole256 && kPlans[3].main == kWhole256 && kPlans[2].tail == kPlans[0].tail &&
+                    kPlans[3].tail == kPlans[1].tail, "the order of the plans");
   return launch_plan<OpI8, Epilogue::kBf16ScaleBiasLow>(tile, {xq, wq, sx, sw, bias, y, args}, M, N, K, stream);
 }
 

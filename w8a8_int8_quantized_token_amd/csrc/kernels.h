@@ -107,25 +107,40 @@ hipError_t launch_gated_grad(GateAct act, const uint16_t* dy, int64_t ld_dy, con
                              int64_t ldp, uint16_t* qt, int64_t ldq, float* sums, int64_t M,
                              int64_t N, int64_t K, hipStream_t stream);
 
+// Low-rank adapters of a product's tokens: token m adds
+// sum_r t[m,r] * b[ids[m]][n,r] to output n, and nothing where ids[m] is
+// outside [0, count).  t bf16 [M,ldt], ldt = R rounded up to 16, zeros past
+// column R; b bf16 [count,N,R], 16-byte aligned; R a multiple of 8.
+struct Low {
+  const uint16_t *t, *b;
+  const int32_t* ids;
+  int64_t ldt, R, count;
+};
+
 // out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; N and Kpad
 // multiples of 8, rows 16-byte aligned.  The sum is cut into gemm_bf16_slices()
 // ranges; where they are more than one, their fp32 sums go to slices [ranges,
 // M, N] for a JoinJob (out must then be 16-byte aligned) and out is not
-// written; with slices null the product is made whole.
-int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad);
+// written; with slices null the product is made whole.  low: null, or adapters
+// whose share is added (to the first range's sums).
+int gemm_bf16_slices(int64_t M, int64_t N, int64_t Kpad, bool low = false);
 hipError_t launch_gemm_bf16(const uint16_t* a, const uint16_t* b, uint16_t* out, float* slices, int64_t M,
-                            int64_t N, int64_t Kpad, hipStream_t stream);
+                            int64_t N, int64_t Kpad, const Low* low, hipStream_t stream);
 
 // Operand layout of the backward products and the joins after them (see
 // backward_layout.hip): one launch each for up to kMaxJobs jobs.
-constexpr int kMaxJobs = 4;
+constexpr int kMaxJobs = 6;
 struct LayoutJob {
-  enum Kind { kTurnCodes, kTurnPaired, kTurnValues, kPadRows } kind;
-  const void* in;        // [R,C]: int8 codes or bf16 values
+  enum Kind { kTurnCodes, kTurnPaired, kTurnValues, kPadRows, kTurnEach, kLists } kind;
+  const void* in;        // [R,C]: int8 codes or bf16 values; kTurnEach: `batch` of them; kLists: ids int32 [R]
   const float* scale;    // codes: [R] or null
-  uint16_t* out;         // [C,ld] (kPadRows: [R,ld])
+  uint16_t* out;         // [C,ld] (kPadRows: [R,ld]); kTurnEach: `batch` of them
   float* sums;           // kTurnValues: [ceil(R / span), C] or null
   int64_t R, C, ld, span;
+  int64_t batch;
+  // kLists: the rows whose id is i, in order, at list[starts[i]] ...
+  // list[starts[i + 1] - 1], for i below C
+  int32_t *list, *starts;
 };
 struct JoinJob {
   const float* part;     // [P, n]
@@ -190,15 +205,7 @@ hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const ui
                                 uint16_t* dx, float* part, float* dweight, int64_t M, int64_t K, float eps,
                                 hipStream_t stream);
 
-// Low-rank adapters of a product's tokens: token m adds
-// sum_r t[m,r] * b[ids[m]][n,r] to output n, and nothing where ids[m] is
-// outside [0, count).  t bf16 [M,ldt], ldt = R rounded up to 16, zeros past
-// column R; b bf16 [count,N,R], 16-byte aligned; R a multiple of 8.
-struct Low {
-  const uint16_t *t, *b;
-  const int32_t* ids;
-  int64_t ldt, R, count;
-};
+// The int8 linear with adapters, by tile (< 0 chooses).
 hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                            const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
                            hipStream_t stream);
@@ -237,5 +244,24 @@ hipError_t launch_few_tokens_low(const int8_t* xq, const float* sx, const int8_t
 hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const float* sx, const float* sw,
                                     const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N,
                                     hipStream_t stream);
+
+// Gradients of an adapter's matrix (adapter_grad.hip): slices fp32 [parts][count]
+// [R][C] from codes x [M,C] (rows 16-byte aligned), or [parts][count][C][R] from
+// bf16 x (any 2-byte address), for a JoinJob.  v bf16 [M,ldt]; list [M] and
+// starts [count + 1]: the rows of each adapter (LayoutJob::kLists).  parts =
+// adapter_grad_parts(); col_blocks and rank_blocks are set by the launch.
+struct AdapterGrad {
+  const void* x;
+  const uint16_t* v;
+  const int32_t *list, *starts;
+  float* slices;
+  int64_t C;
+  int ldt, R, count, parts, col_blocks, rank_blocks;
+};
+int adapter_grad_parts(int64_t M, int64_t C, int64_t R, int64_t count, bool codes);
+hipError_t launch_adapter_grad(AdapterGrad a, bool codes, hipStream_t stream);
+// out fp32 [M,C] = sum_r u[m,r] p[ids[m]][r,c] (p bf16 [count,R,C], C % 16 == 0), for few rows.
+hipError_t launch_adapter_up(const uint16_t* u, int64_t ldt, const uint16_t* p, const int32_t* ids, int64_t count,
+                             int64_t R, int64_t M, int64_t C, float* out, hipStream_t stream);
 
 }  // namespace w8a8

@@ -337,9 +337,38 @@ PyObject* linear_adapters(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// dy, xq, x_scale, wq, w_scale, a, b, ids, scaling, dx, da, db
+PyObject* linear_adapters_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return plain(n, 12, [&] {
+    const at::Tensor &dy = tensor(a[0]), &w = tensor(a[3]);
+    two_dims(dy);
+    two_dims(w);
+    Call c(dy);
+    const bool dx = flag(a[9]), da = flag(a[10]), db = flag(a[11]);
+    const int64_t M = dy.size(0), N = dy.size(1), K = w.size(1);
+    const auto* pdy = c.at<uint16_t>(a[0], at::kBFloat16, {M, N});
+    const bool no_x = !da && !db && a[1] == Py_None && a[2] == Py_None;
+    const auto* pxq = no_x ? nullptr : c.at<int8_t>(a[1], at::kChar, {M, K});
+    const auto* pxs = no_x ? nullptr : c.at<float>(a[2], at::kFloat, {M});
+    const auto* pw = c.at<int8_t>(a[3], at::kChar, {N, K});
+    const auto* ps = c.at<float>(a[4], at::kFloat, {N});
+    const Adapters ad(c, a + 5, M, N, K);
+    at::Tensor gx, ga, gb;
+    if (dx) gx = c.empty({M, K}, at::kBFloat16);
+    if (da) ga = c.empty({ad.L, ad.R, K}, at::kBFloat16);
+    if (db) gb = c.empty({ad.L, N, ad.R}, at::kBFloat16);
+    const size_t need = w8a8_linear_adapters_backward_workspace(M, N, K, ad.R, ad.L, dx, da, db);
+    void* ws = c.workspace(need);
+    launched(w8a8_linear_adapters_backward(pdy, pxq, pxs, pw, ps, ad.a, ad.b, ad.scaling, ad.ids, bits(gx), bits(ga),
+                                           bits(gb), M, N, K, ad.R, ad.L, ws, need, c.stream));
+    return tuple({std::move(gx), std::move(ga), std::move(gb)});
+  });
+}
+
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(dynamic), METHOD(backward), METHOD(qk_norm_rope), METHOD(qk_norm_rope_backward),
                          METHOD(add_rms_norm_quantize), METHOD(add_rms_norm_backward), METHOD(linear_adapters),
+                         METHOD(linear_adapters_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

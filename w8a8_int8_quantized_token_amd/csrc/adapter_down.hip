@@ -70,13 +70,13 @@ __device__ __forceinline__ int adapter_of(const Down& a, int64_t m) {
 
 // ---- one row per workgroup ----
 
-using Rows = DownRows;
+enum class Rows { kCodes, kQuantize, kValues };
 constexpr int kRanks = 16;          // of a workgroup, two per wavefront
 constexpr int kKeep = 4;            // pieces of 8 values that a thread quantizes
 constexpr int kMaxFused = kKeep * kThreads * 8;
 
 template <Rows R>
-__global__ __launch_bounds__(kThreads) void down_row_kernel(Down a) {
+__device__ __forceinline__ void down_row(const Down& a) {
   __shared__ __attribute__((aligned(16))) u32x2 codes[R == Rows::kQuantize ? kMaxFused / 8 : 1];
   __shared__ uint32_t amax[kWaves];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -164,55 +164,60 @@ __global__ __launch_bounds__(kThreads) void down_row_kernel(Down a) {
   if (lane == 0) {
     *reinterpret_cast<uint32_t*>(a.t + m * a.ldt + r0) = pack2(sum[0], sum[1]);
     if (a.t2 != nullptr) {
-      const float s2 = a.scale2[m];
+      const float s2 = id >= 0 ? a.scale2[m] : 0.0f;
       *reinterpret_cast<uint32_t*>(a.t2 + m * a.ldt + r0) = pack2(sum[0] * s2, sum[1] * s2);
     }
   }
 }
 
+template <Rows R>
+__global__ __launch_bounds__(kThreads) void down_row_kernel(Down a) {
+  down_row<R>(a);
+}
+
 // ---- 32 rows per workgroup ----
 
 constexpr int kBlockRows = 32, kStepK = 64;
+// LDS of a workgroup: the wavefronts' sums.
+template <int kTiles>
+using Sums = f32x4[kWaves][kTiles][2][kWave];
 
 // 64 values of k at a time: a lane has 16 consecutive ones of a row, the first
 // and the last eight of them for two MFMAs; both operands are dealt alike.
-template <Rows R, int kTiles>
-__global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
-  __shared__ f32x4 part[kWaves][kTiles][2][kWave];
+// kDepth steps of loads are in flight (with one, 8192 rows of 4096 codes take
+// 26 us, the latency of eight loads one after another).
+// The adapters of a workgroup's rows are shared out over `slots` workgroups.
+template <Rows R, int kTiles, int kDepth>
+__device__ __forceinline__ void down_block(const Down& a, int64_t block, int rank_block, int slot, int slots,
+                                           Sums<kTiles>& part) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int l16 = lane % 16, h = lane / 16;
-  const int64_t m0 = (int64_t)blockIdx.x * kBlockRows;
-  const int first = blockIdx.y * kTiles * 16;   // rank
+  const int64_t m0 = block * kBlockRows;
+  const int first = rank_block * kTiles * 16;   // rank
   int id[2];
   int64_t row[2];
+  bool mine[2];   // this workgroup writes the row
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t m = m0 + i * 16 + l16;
     row[i] = min(m, a.M - 1);
     id[i] = m < a.M ? adapter_of(a, m) : -1;
+    mine[i] = id[i] < 0 && slot == 0;
   }
   f32x4 res[kTiles][2];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) res[t][0] = res[t][1] = f32x4{0, 0, 0, 0};
 
+  constexpr int kWords = R == Rows::kValues ? 2 : 1;
   struct Step {
-    u32x4 p[kTiles][2], x[2][2];
+    u32x4 p[kTiles][2], x[2][kWords];
   };
   auto load = [&](const uint16_t* p, int s, Step& v) __attribute__((always_inline)) {
     const int k = s * kStepK + 16 * h;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const int r = min(first + t * 16 + l16, a.R - 1);
-      v.p[t][0] = v.p[t][1] = kZeros;
-      if (k < a.K) {   // (rows of p are whole pieces of 16 values)
-        const u32x4* from = reinterpret_cast<const u32x4*>(p + (int64_t)r * a.ldp + k);
-        v.p[t][0] = from[0];
-        v.p[t][1] = from[1];
-      }
-    }
-#pragma unroll
     for (int i = 0; i < 2; ++i) {
-      v.x[i][0] = v.x[i][1] = kZeros;
+#pragma unroll
+      for (int g = 0; g < kWords; ++g) v.x[i][g] = kZeros;
       if (k < a.K) {
         if constexpr (R == Rows::kValues) {
           const uint16_t* from = static_cast<const uint16_t*>(a.x) + row[i] * a.K;
@@ -223,34 +228,42 @@ __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
         }
       }
     }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int r = min(first + t * 16 + l16, a.R - 1);
+      v.p[t][0] = v.p[t][1] = kZeros;
+      if (k < a.K) {   // (rows of p are whole pieces of 16 values)
+        const u32x4* from = reinterpret_cast<const u32x4*>(p + (int64_t)r * a.ldp + k);
+        v.p[t][0] = from[0];
+        v.p[t][1] = from[1];
+      }
+    }
   };
   uint64_t left[2] = {__builtin_amdgcn_ballot_w64(id[0] >= 0), __builtin_amdgcn_ballot_w64(id[1] >= 0)};
   const int steps = (a.K + kStepK - 1) / kStepK;
-  while ((left[0] | left[1]) != 0) {
+  for (int pass = 0; (left[0] | left[1]) != 0; ++pass) {
     const int ad = left[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
                                 : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
 #pragma unroll
     for (int i = 0; i < 2; ++i) left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == ad);
+    if (pass % slots != slot) continue;
     const uint16_t* p = a.p + ad * a.p_stride;
     f32x4 acc[kTiles][2];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
-    Step now, next;
-    load(p, wave, now);
-    for (int s = wave; s < steps; s += kWaves) {
-      load(p, s + kWaves, next);
+    auto multiply = [&](const Step& v) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         u32x4 x[2];
         if constexpr (R == Rows::kValues) {
-          x[0] = now.x[i][0];
-          x[1] = now.x[i][1];
+          x[0] = v.x[i][0];
+          x[1] = v.x[i][kWords - 1];
         } else {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float f[8];
-            codes4(now.x[i][0][2 * g], f);
-            codes4(now.x[i][0][2 * g + 1], f + 4);
+            codes4(v.x[i][0][2 * g], f);
+            codes4(v.x[i][0][2 * g + 1], f + 4);
             x[g] = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
           }
         }
@@ -258,18 +271,31 @@ __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
           for (int g = 0; g < 2; ++g)
-            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.p[t][g]),
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.p[t][g]),
                                                                 __builtin_bit_cast(bf16x8, x[g]), acc[t][i], 0, 0, 0);
       }
-      now = next;
+    };
+    Step ring[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(p, wave + d * kWaves, ring[d]);
+    for (int s = wave; s < steps; s += kDepth * kWaves) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {   // (steps past the end are zeros)
+        multiply(ring[d]);
+        load(p, s + (kDepth + d) * kWaves, ring[d]);
+      }
     }
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int i = 0; i < 2; ++i) {
+      mine[i] |= id[i] == ad;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) res[t][i][e] = id[i] == ad ? acc[t][i][e] : res[t][i][e];
+    }
   }
+  // (the same in all wavefronts)
+  if (__builtin_amdgcn_ballot_w64(mine[0] || mine[1]) == 0) return;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -280,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
   const int t = wave / 2, i = wave % 2;
   const int64_t m = m0 + i * 16 + l16;
   const int r = first + t * 16 + 4 * h;
-  if (m >= a.M || r >= a.ldt) return;
+  if (m >= a.M || r >= a.ldt || !(i ? mine[1] : mine[0])) return;
   f32x4 sum = part[0][t][i][lane];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum += part[w][t][i][lane];
@@ -293,39 +319,88 @@ __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
   for (int e = 0; e < 4; ++e) sum[e] = on ? sum[e] * scale * f : 0.0f;
   *reinterpret_cast<u32x2*>(a.t + m * a.ldt + r) = u32x2{pack2(sum[0], sum[1]), pack2(sum[2], sum[3])};
   if (a.t2 != nullptr) {
-    const float s2 = a.scale2[m];
+    const float s2 = on ? a.scale2[m] : 0.0f;
     *reinterpret_cast<u32x2*>(a.t2 + m * a.ldt + r) =
         u32x2{pack2(sum[0] * s2, sum[1] * s2), pack2(sum[2] * s2, sum[3] * s2)};
   }
 }
 
-template <Rows R>
-hipError_t launch(const Down& a, hipStream_t s) {
-  if (a.M <= kDownRows) {
-    hipLaunchKernelGGL((down_row_kernel<R>), dim3((unsigned)a.M, (unsigned)(a.ldt / kRanks)), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
-  }
-  if constexpr (R != Rows::kQuantize) {
-    const unsigned blocks = (unsigned)((a.M + kBlockRows - 1) / kBlockRows);
-    if (a.R <= 16) hipLaunchKernelGGL((down_block_kernel<R, 1>), dim3(blocks), dim3(kThreads), 0, s, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((down_block_kernel<R, 2>), dim3(blocks), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((down_block_kernel<R, 4>), dim3(blocks, (unsigned)((a.R + 63) / 64)), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
-  }
-  return hipErrorInvalidValue;
+// Steps in flight, as registers allow.
+template <Rows R, int kTiles>
+constexpr int kDepthOf = kTiles == 1 ? 4 : kTiles == 2 ? 3 : 2;
+
+// grid (blocks of rows, blocks of ranks, slots); two products share a launch,
+// of codes and of values (b, the last grid.z = slots ones).
+template <int kTiles>
+__global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
+  __shared__ Sums<kTiles> part;
+  down_block<Rows::kCodes, kTiles, kDepthOf<Rows::kCodes, kTiles>>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, part);
+}
+template <int kTiles>
+__global__ __launch_bounds__(kThreads) void down_block_kernel2(Down codes, Down values, int slots) {
+  __shared__ Sums<kTiles> part;
+  const int z = blockIdx.z;
+  if (codes.M > 0 && z >= slots)   // (the longer rows first)
+    down_block<Rows::kCodes, kTiles, kDepthOf<Rows::kCodes, kTiles>>(codes, blockIdx.x, blockIdx.y, z - slots, slots, part);
+  else
+    down_block<Rows::kValues, kTiles, kDepthOf<Rows::kValues, kTiles>>(values, blockIdx.x, blockIdx.y, z, slots, part);
+}
+template <int kUnused>
+__global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down values) {
+  if (blockIdx.z == 0) down_row<Rows::kValues>(values);
+  else down_row<Rows::kCodes>(codes);
+}
+
+// Workgroups that share out the adapters of a block of rows: more where blocks
+// leave compute units idle.
+int slots_of(const Down& a) {
+  const int64_t blocks = (a.M + kBlockRows - 1) / kBlockRows * ((a.R + 63) / 64);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.count, 1024 / blocks, 16}));
+}
+dim3 block_grid(const Down& a, int tiles, int z) {
+  return dim3((unsigned)((a.M + kBlockRows - 1) / kBlockRows), (unsigned)((a.R + 16 * tiles - 1) / (16 * tiles)), (unsigned)z);
 }
 
 }  // namespace
 
 bool down_quantizes(int64_t M, int64_t K) { return M <= kDownRows && K <= kMaxFused; }
 
-hipError_t launch_down(DownRows rows, const Down& a, hipStream_t stream) {
+hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
   if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0) return hipErrorInvalidValue;
-  switch (rows) {
-    case Rows::kCodes: return launch<Rows::kCodes>(a, stream);
-    case Rows::kQuantize: return down_quantizes(a.M, a.K) ? launch<Rows::kQuantize>(a, stream) : hipErrorInvalidValue;
-    default: return launch<Rows::kValues>(a, stream);
+  const dim3 threads(kThreads), rows((unsigned)a.M, (unsigned)(a.ldt / kRanks));
+  if (quantize) {
+    if (!down_quantizes(a.M, a.K)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(down_row_kernel<Rows::kQuantize>, rows, threads, 0, s, a);
+  } else if (a.M <= kDownRows) {
+    hipLaunchKernelGGL(down_row_kernel<Rows::kCodes>, rows, threads, 0, s, a);
+  } else {
+    const int slots = slots_of(a);
+    if (a.R <= 16) hipLaunchKernelGGL(down_block_kernel<1>, block_grid(a, 1, slots), threads, 0, s, a);
+    else if (a.R <= 32) hipLaunchKernelGGL(down_block_kernel<2>, block_grid(a, 2, slots), threads, 0, s, a);
+    else hipLaunchKernelGGL(down_block_kernel<4>, block_grid(a, 4, slots), threads, 0, s, a);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s) {
+  if (values == nullptr) return codes != nullptr ? launch_down(*codes, false, s) : hipSuccess;
+  const Down& v = *values;
+  Down c{};   // (M = 0: none)
+  if (codes != nullptr) c = *codes;
+  if (v.M < 1 || v.R < 8 || v.R % 8 != 0 || v.ldt < v.R || v.ldt % 16 != 0 ||
+      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)))
+    return hipErrorInvalidValue;
+  const dim3 threads(kThreads);
+  const int both = c.M > 0 ? 2 : 1;
+  if (v.M <= kDownRows) {
+    hipLaunchKernelGGL(down_row_kernel2<0>, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
+    return hipGetLastError();
+  }
+  const int slots = slots_of(v);
+  if (v.R <= 16) hipLaunchKernelGGL(down_block_kernel2<1>, block_grid(v, 1, both * slots), threads, 0, s, c, v, slots);
+  else if (v.R <= 32) hipLaunchKernelGGL(down_block_kernel2<2>, block_grid(v, 2, both * slots), threads, 0, s, c, v, slots);
+  else hipLaunchKernelGGL(down_block_kernel2<4>, block_grid(v, 4, both * slots), threads, 0, s, c, v, slots);
+  return hipGetLastError();
 }
 
 }  // namespace w8a8

@@ -188,35 +188,53 @@ __device__ void pad_rows(const LayoutJob& j, int64_t block) {
   }
 }
 
-// A wavefront for an id: where its list starts (the rows with smaller ids),
-// then its rows in order.  Four loads in flight in each pass.
-__device__ void make_lists(const LayoutJob& j, int64_t block) {
-  const int lane = threadIdx.x % 64;
-  const int id = (int)(block * (kThreads / 64) + threadIdx.x / 64), count = (int)j.C, M = (int)j.R;
-  if (id >= count) return;   // whole wavefronts
+// A workgroup for an id: where its list starts (the rows with smaller ids), then
+// its rows in order, each wavefront a quarter of them.  Two passes over the
+// ids with sixteen loads in flight (one wavefront with four: 25 us for 4096 ids,
+// the longest part of the launch).
+__device__ void make_lists(const LayoutJob& j, int64_t block, Lds& lds) {
+  constexpr int kLoads = 16, kWaves = kThreads / 64;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int id = (int)block, count = (int)j.C, M = (int)j.R;
   const int32_t* ids = static_cast<const int32_t*>(j.in);
-  constexpr int kLoads = 4;
-  int before = 0, own = 0;
-  for (int m0 = 0; m0 < M; m0 += 64 * kLoads) {
-    int v[kLoads];
+  const int per = (M + kWaves * 64 - 1) / (kWaves * 64) * 64;   // rows of a wavefront
+  const int first = wave * per, last = min(first + per, M);
+  auto load = [&](int m0, int (&v)[kLoads]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i] = m0 + i * 64 + lane < M ? ids[m0 + i * 64 + lane] : -1;
+    for (int i = 0; i < kLoads; ++i) {
+      const int m = m0 + i * 64 + lane;
+      v[i] = m < last ? ids[m] : -1;
+    }
+  };
+  int before = 0, own = 0;
+  for (int m0 = first; m0 < last; m0 += 64 * kLoads) {
+    int v[kLoads];
+    load(m0, v);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       before += __popcll(__builtin_amdgcn_ballot_w64(v[i] >= 0 && v[i] < id));
       own += __popcll(__builtin_amdgcn_ballot_w64(v[i] == id));
     }
   }
-  if (lane == 0) {
-    j.starts[id] = before;
-    if (id == count - 1) j.starts[count] = before + own;
-  }
-  if (own == 0) return;
-  int at = before;
-  for (int m0 = 0; m0 < M; m0 += 64 * kLoads) {
-    int v[kLoads];
+  int (*const counts)[2] = reinterpret_cast<int (*)[2]>(&lds);
+  if (lane == 0) counts[wave][0] = before, counts[wave][1] = own;
+  __syncthreads();
+  int start = 0, at = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i] = m0 + i * 64 + lane < M ? ids[m0 + i * 64 + lane] : -1;
+  for (int w = 0; w < kWaves; ++w) {
+    start += counts[w][0];
+    if (w < wave) at += counts[w][1];
+    all += counts[w][1];
+  }
+  if (threadIdx.x == 0) {
+    j.starts[id] = start;
+    if (id == count - 1) j.starts[count] = start + all;
+  }
+  at += start;
+  if (own == 0) return;
+  for (int m0 = first; m0 < last; m0 += 64 * kLoads) {
+    int v[kLoads];
+    load(m0, v);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const uint64_t hits = __builtin_amdgcn_ballot_w64(v[i] == id);
@@ -252,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare p) {
     case LayoutJob::kTurnPaired: turn_codes<true>(j, block, lds); break;
     case LayoutJob::kTurnValues: turn_values(j, block, lds); break;
     case LayoutJob::kTurnEach: turn_each(j, block, lds); break;
-    case LayoutJob::kLists: make_lists(j, block); break;
+    case LayoutJob::kLists: make_lists(j, block, lds); break;
     default: pad_rows(j, block); break;
   }
 }
@@ -357,7 +375,7 @@ hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream) {
       end += j.kind == LayoutJob::kPadRows      ? tiles(j.R * (j.ld / 8), kPadBlock)
              : j.kind == LayoutJob::kTurnValues ? tiles(j.C, kT) * tiles(j.R, j.span)
              : j.kind == LayoutJob::kTurnEach   ? tiles(j.C, kT) * tiles(j.ld, j.span) * j.batch
-             : j.kind == LayoutJob::kLists      ? tiles(j.C, kThreads / 64)
+             : j.kind == LayoutJob::kLists      ? j.C
                                                 : tiles(j.C, kCodeCols) * tiles(j.ld, kCodeRows);
     }
     p.end[k] = end;

@@ -355,7 +355,7 @@ w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, 
   d.R = (int)R;
   d.ldt = (int)up(R, 16);
   d.count = (int)L;
-  TRY(w8a8::launch_down(p.in_down ? w8a8::DownRows::kQuantize : w8a8::DownRows::kCodes, d, stream));
+  TRY(w8a8::launch_down(d, p.in_down, stream));
   const w8a8::Low low{t, b, ids, up(R, 16), R, L};
   if (p.few) return launched(w8a8::launch_few_tokens_low(xq, x_scale, wq, w_scale, bias, low, y, M, N, K, stream));
   if (p.splits > 1) {
@@ -737,29 +737,24 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   d.R = (int)R;
   d.ldt = (int)p.ldt;
   d.count = (int)L;
-  if (db) {
-    d.x = xq;
-    d.scale = x_scale;
-    d.p = a;
-    d.p_stride = R * K;
-    d.K = d.ldp = (int)K;
-    d.t = t;
-    TRY(w8a8::launch_down(w8a8::DownRows::kCodes, d, stream));
+  w8a8::Down dt = d, du = d;
+  dt.x = xq;
+  dt.scale = x_scale;
+  dt.p = a;
+  dt.p_stride = R * K;
+  dt.K = dt.ldp = (int)K;
+  dt.t = t;
+  du.x = dy;
+  du.p = bt;
+  du.p_stride = R * p.ldn;
+  du.K = (int)N;
+  du.ldp = (int)p.ldn;
+  du.t = u;
+  if (da) {
+    du.t2 = v;
+    du.scale2 = x_scale;
   }
-  if (dx || da) {
-    d.x = dy;
-    d.scale = nullptr;
-    d.p = bt;
-    d.p_stride = R * p.ldn;
-    d.K = (int)N;
-    d.ldp = (int)p.ldn;
-    d.t = u;
-    if (da) {
-      d.t2 = v;
-      d.scale2 = x_scale;
-    }
-    TRY(w8a8::launch_down(w8a8::DownRows::kValues, d, stream));
-  }
+  TRY(w8a8::launch_down_pair(db ? &dt : nullptr, dx || da ? &du : nullptr, stream));
   w8a8::JoinJob join[w8a8::kMaxJobs];
   int joins = 0;
   if (dx) {

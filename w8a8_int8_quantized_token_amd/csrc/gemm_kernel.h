@@ -200,6 +200,12 @@ __device__ __forceinline__ float keep_half(float a, float b, int hi, F partner) 
   return keep + __uint_as_float(partner(__float_as_uint(send)));
 }
 
+// Larger ones of the two 16-bit halves of two words.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
 // Buffer accesses (kept out of the kernel's lambdas like dma16): a range of
 // `n` bf16 values, 16-byte loads and stores at byte offsets in it; loads past
 // its end give zeros, stores past it are dropped.
@@ -778,11 +784,13 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
 
   // ---- low-rank adapters ----
   // The adapters' share of a tile, t b^T, added to its fp32 values, which are
-  // in the accumulators: one pass for each adapter that the wavefront's tokens
-  // have.  Where they do not all have the same one, only the lanes whose token
-  // has it take a sub-tile's result (a lane's token is the same in all of its
-  // values): an adapter's values, whatever they are, reach no other adapter's
-  // tokens.
+  // in the accumulators: for 16 (bf16 32) ranks at a time one pass for each
+  // adapter that the wavefront's tokens have, with the other tokens' rows of t
+  // taken as zeros; the next adapter's fragments are on the way meanwhile.  (A
+  // zero times an infinity or a NaN would reach the other tokens, so where an
+  // adapter's fragments of b hold one they are taken as zeros and its own
+  // tokens' of t as NaNs.)  The bf16 tiles have no registers for that: there
+  // each product is made by itself and taken by the adapter's tokens alone.
   constexpr int kLowRows = Op::kBf16 ? 16 : 32, kLowM = T::TM / kLowRows;   // row tiles of a wavefront
   constexpr int kLowN = Op::kBf16 ? 2 * T::FN : T::FN;                      // fragments of its channels
   constexpr int kLowStep = Op::kBf16 ? 32 : 16;                            // ranks of an MFMA
@@ -802,71 +810,95 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
       // past M and N and ranks past R are zeros
       const __amdgpu_buffer_rsrc_t rt = buffer_range(extra.t + (int64_t)at.m0 * extra.ldt, min(T::BM, M - at.m0) * extra.ldt);
       const int chans = min(T::BN, N - at.n0) * extra.R;
-      __amdgpu_buffer_rsrc_t rb;
       auto frag_t = [&](int i, int r0) {   // tokens
         const uint32_t o = (uint32_t)((wm * T::TM + i * kLowRows + l_row) * extra.ldt + r0 + l_r) * 2u;
         return buffer_load16(rt, r0 + l_r < extra.ldt ? o : kOOB);
       };
-      auto frag_b = [&](int j, int r0) {   // channels
-        int c;
-        if constexpr (Op::kBf16) {
-          const int dealt = (l_row / 4) * 8 + (l_row / 8) * 4 + l_row % 4;   // as chan16
-          c = j / 2 * 32 + (j % 2 ? dealt ^ 4 : dealt);
-        } else {
-          c = j * 32 + l_row;
+      auto frags_b = [&](int a, int r0, v4i (&f)[kLowN]) {   // channels
+        const __amdgpu_buffer_rsrc_t rb = buffer_range(extra.b + a * extra.b_stride + (int64_t)at.n0 * extra.R, chans);
+#pragma unroll
+        for (int j = 0; j < kLowN; ++j) {
+          int c;
+          if constexpr (Op::kBf16) {
+            const int dealt = (l_row / 4) * 8 + (l_row / 8) * 4 + l_row % 4;   // as chan16
+            c = j / 2 * 32 + (j % 2 ? dealt ^ 4 : dealt);
+          } else {
+            c = j * 32 + l_row;
+          }
+          const uint32_t o = (uint32_t)((wn * T::TN + c) * extra.R + r0 + l_r) * 2u;
+          f[j] = buffer_load16(rb, r0 + l_r < extra.R ? o : kOOB);
         }
-        const uint32_t o = (uint32_t)((wn * T::TN + c) * extra.R + r0 + l_r) * 2u;
-        return buffer_load16(rb, r0 + l_r < extra.R ? o : kOOB);
-      };
-      auto product = [&](v4i b, v4i t, auto v) {
-        const bf16x8 fb8 = __builtin_bit_cast(bf16x8, b), ft8 = __builtin_bit_cast(bf16x8, t);
-        if constexpr (Op::kBf16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb8, ft8, v, 0, 0, 0);
-        else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb8, ft8, v, 0, 0, 0);
-      };
-      auto get = [&](int i, int j) {
-        if constexpr (Op::kBf16) return acc[i / 2][j / 2].q[i % 2][j % 2];
-        else return __builtin_bit_cast(v16f, acc[i][j]);
-      };
-      auto set = [&](int i, int j, auto v) {
-        if constexpr (Op::kBf16) acc[i / 2][j / 2].q[i % 2][j % 2] = v;
-        else acc[i][j] = __builtin_bit_cast(v16i, v);
       };
       uint64_t left[kLowM];   // lanes whose adapter is still to come
-      uint64_t any = 0;
-#pragma unroll
-      for (int i = 0; i < kLowM; ++i) {
-        left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
-        any |= left[i];
-      }
-      while (any != 0) {
-        int a = 0;
+      auto next_adapter = [&]() {   // -1: none
+        int a = -1;
 #pragma unroll
         for (int i = kLowM - 1; i >= 0; --i)
           if (left[i] != 0) a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(left[i]));
-        any = 0;
 #pragma unroll
-        for (int i = 0; i < kLowM; ++i) {
-          left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == a);
-          any |= left[i];
+        for (int i = 0; i < kLowM; ++i) left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == a);
+        return a;
+      };
+      for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
+#pragma unroll
+        for (int i = 0; i < kLowM; ++i) left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+        constexpr bool kAhead = !Op::kBf16;
+        v4i ft[kAhead ? kLowM : 2], fn[kLowN];
+        [[maybe_unused]] v4i ahead[kLowN];
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
         }
-        rb = buffer_range(extra.b + a * extra.b_stride + (int64_t)at.n0 * extra.R, chans);
-        for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
-          // (two row tiles' fragments at a time: all of them spill)
-          v4i fn[kLowN], ft[2];
-          ft[0] = frag_t(0, r0);
+        int a = next_adapter();
+        if constexpr (kAhead)
+          if (a >= 0) frags_b(a, r0, ahead);
+        while (a >= 0) {
+          const int now = a;
+          a = next_adapter();
+          if constexpr (kAhead) {
 #pragma unroll
-          for (int j = 0; j < kLowN; ++j) fn[j] = frag_b(j, r0);
+            for (int j = 0; j < kLowN; ++j) fn[j] = ahead[j];
+            if (a >= 0) frags_b(a, r0, ahead);
+          } else {
+            ft[0] = frag_t(0, r0);
+            frags_b(now, r0, fn);
+          }
+          if constexpr (Op::kBf16) {
+            // each product by itself, and only the adapter's own tokens take it
 #pragma unroll
-          for (int i = 0; i < kLowM; ++i) {
-            if (i + 1 < kLowM) ft[(i + 1) % 2] = frag_t(i + 1, r0);
+            for (int i = 0; i < kLowM; ++i) {
+              if (i + 1 < kLowM) ft[(i + 1) % 2] = frag_t(i + 1, r0);
 #pragma unroll
-            for (int j = 0; j < kLowN; ++j) {
-              auto v = get(i, j);
-              const auto d = product(fn[j], ft[i % 2], decltype(v){});
+              for (int j = 0; j < kLowN; ++j) {
+                const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, fn[j]), __builtin_bit_cast(bf16x8, ft[i % 2]), f32x4{0, 0, 0, 0}, 0, 0, 0);
+                f32x4& c = acc[i / 2][j / 2].q[i % 2][j % 2];
 #pragma unroll
-              for (int e = 0; e < (Op::kBf16 ? 4 : 16); ++e) v[e] += id[i] == a ? d[e] : 0.0f;
-              set(i, j, v);
-              __builtin_amdgcn_sched_barrier(0);
+                for (int e = 0; e < 4; ++e) c[e] += id[i] == now ? d[e] : 0.0f;
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          } else {
+            uint32_t most = 0;   // largest magnitudes of both halves of the words
+#pragma unroll
+            for (int j = 0; j < kLowN; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fn[j][e] & 0x7fff7fffu);
+            const bool drop = __builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0;
+#pragma unroll
+            for (int j = 0; j < kLowN; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) fn[j][e] = drop ? 0 : fn[j][e];
+#pragma unroll
+            for (int i = 0; i < kLowM; ++i) {
+              v4i t;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[e] = id[i] == now ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
+#pragma unroll
+              for (int j = 0; j < kLowN; ++j)
+                acc[i][j] = __builtin_bit_cast(
+                    v16i, __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fn[j]), __builtin_bit_cast(bf16x8, t),
+                                                                  __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
             }
           }
         }

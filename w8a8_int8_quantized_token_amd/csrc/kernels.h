@@ -217,7 +217,6 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
 // outputs; bf16 values: x at any 2-byte address, rows of K.  t2, where not
 // null: the same times scale2[m].
 constexpr int64_t kDownRows = 256;   // up to here a workgroup for each row
-enum class DownRows { kCodes, kQuantize, kValues };
 struct Down {
   const void* x;
   const float* scale;
@@ -233,7 +232,10 @@ struct Down {
   int K, ldp, R, ldt, count;
 };
 bool down_quantizes(int64_t M, int64_t K);
-hipError_t launch_down(DownRows rows, const Down& a, hipStream_t stream);
+hipError_t launch_down(const Down& a, bool quantize, hipStream_t stream);
+// Products of codes and of bf16 values (each null for none) in one launch, of
+// the same M, R and ldt.
+hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t stream);
 
 // The linear with adapters for at most kFewTokens tokens, from codes, where
 // few_tokens_low_fit(); and the K split's second pass with them.

@@ -13,7 +13,7 @@
 // with the lanes along k (M K R fused multiply-adds, and P read once for each
 // row, from L2 where rows share an adapter).  More rows: a workgroup takes 32
 // of them on the bf16 matrix cores (codes are exact in bf16), its wavefronts
-// every eighth 64 values of k, and goes through the adapters that its rows
+// a range of k each, and goes through the adapters that its rows
 // have one after another; a row takes the sums of its own adapter alone.
 #include "kernels.h"
 #include "quant_codes.h"
@@ -177,19 +177,25 @@ __global__ __launch_bounds__(kThreads) void down_row_kernel(Down a) {
 
 // ---- 32 rows per workgroup ----
 
-constexpr int kBlockRows = 32, kStepK = 64;
+constexpr int kBlockRows = 32;
 // LDS of a workgroup: the wavefronts' sums.
 template <int kTiles>
 using Sums = f32x4[kWaves][kTiles][2][kWave];
 
-// 64 values of k at a time: a lane has 16 consecutive ones of a row, the first
-// and the last eight of them for two MFMAs; both operands are dealt alike.
-// kDepth steps of loads are in flight (with one, 8192 rows of 4096 codes take
-// 26 us, the latency of eight loads one after another).
+// A step is 64 or 128 values of k, a quarter of them in a row in each lane
+// (both operands are dealt alike), 16 bytes for an MFMA.  Each wavefront has a
+// range of k of its own, and blocks start at different places of it: rows are
+// whole pages or parts of them apart, and wavefronts that all read the same
+// place of every row keep a few memory channels busy (8192 rows of 4096 codes: 26
+// us).  kDepth steps of loads are in flight.
 // The adapters of a workgroup's rows are shared out over `slots` workgroups.
-template <Rows R, int kTiles, int kDepth>
+template <Rows R, int kTiles>
 __device__ __forceinline__ void down_block(const Down& a, int64_t block, int rank_block, int slot, int slots,
                                            Sums<kTiles>& part) {
+  constexpr bool kCodes = R == Rows::kCodes;
+  constexpr int kMma = kCodes && kTiles < 4 ? 4 : 2;     // MFMAs of a step and tile
+  constexpr int kLane = kMma * 8, kStepK = 4 * kLane;    // values of a lane and of a step
+  constexpr int kDepth = kTiles == 1 ? 3 : 2;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int l16 = lane % 16, h = lane / 16;
   const int64_t m0 = block * kBlockRows;
@@ -208,39 +214,41 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t block, int ran
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) res[t][0] = res[t][1] = f32x4{0, 0, 0, 0};
 
-  constexpr int kWords = R == Rows::kValues ? 2 : 1;
+  constexpr int kWords = kCodes ? kMma / 2 : kMma;   // 16-byte words of a lane's values of x
   struct Step {
-    u32x4 p[kTiles][2], x[2][kWords];
+    u32x4 p[kTiles][kMma], x[2][kWords];
   };
-  auto load = [&](const uint16_t* p, int s, Step& v) __attribute__((always_inline)) {
-    const int k = s * kStepK + 16 * h;
+  const int steps = (a.K + kStepK - 1) / kStepK, per = (steps + kWaves - 1) / kWaves;
+  const int from = wave * per, here = max(min(per, steps - from), 0);   // this wavefront's steps
+  const int turn = here * (int)(block % 4) / 4;
+  // Step n of the wavefront's; past its end zeros.
+  auto load = [&](const uint16_t* p, int n, Step& v) __attribute__((always_inline)) {
+    int s = n + turn;
+    s = from + (s < here ? s : s - here);
+    const int k = n < here ? s * kStepK + kLane * h : a.ldp;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int g = 0; g < kWords; ++g) v.x[i][g] = kZeros;
-      if (k < a.K) {
-        if constexpr (R == Rows::kValues) {
-          const uint16_t* from = static_cast<const uint16_t*>(a.x) + row[i] * a.K;
-          v.x[i][0] = load8(from, k, a.K);
-          v.x[i][1] = load8(from, k + 8, a.K);
-        } else {
-          v.x[i][0] = *reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(a.x) + row[i] * a.K + k);
+      for (int g = 0; g < kWords; ++g) {
+        v.x[i][g] = kZeros;
+        const int at = k + g * (kCodes ? 16 : 8);
+        if (at < a.K) {
+          if constexpr (kCodes)
+            v.x[i][g] = *reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(a.x) + row[i] * a.K + at);
+          else v.x[i][g] = load8(static_cast<const uint16_t*>(a.x) + row[i] * a.K, at, a.K);
         }
       }
-    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       const int r = min(first + t * 16 + l16, a.R - 1);
-      v.p[t][0] = v.p[t][1] = kZeros;
-      if (k < a.K) {   // (rows of p are whole pieces of 16 values)
-        const u32x4* from = reinterpret_cast<const u32x4*>(p + (int64_t)r * a.ldp + k);
-        v.p[t][0] = from[0];
-        v.p[t][1] = from[1];
+#pragma unroll
+      for (int g = 0; g < kMma; ++g) {
+        v.p[t][g] = kZeros;
+        if (k + 8 * g < a.ldp) v.p[t][g] = *reinterpret_cast<const u32x4*>(p + (int64_t)r * a.ldp + k + 8 * g);
       }
     }
   };
   uint64_t left[2] = {__builtin_amdgcn_ballot_w64(id[0] >= 0), __builtin_amdgcn_ballot_w64(id[1] >= 0)};
-  const int steps = (a.K + kStepK - 1) / kStepK;
   for (int pass = 0; (left[0] | left[1]) != 0; ++pass) {
     const int ad = left[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
                                 : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
@@ -254,35 +262,35 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t block, int ran
     auto multiply = [&](const Step& v) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        u32x4 x[2];
-        if constexpr (R == Rows::kValues) {
-          x[0] = v.x[i][0];
-          x[1] = v.x[i][kWords - 1];
-        } else {
+        u32x4 x[kMma];
+        if constexpr (kCodes) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
+          for (int g = 0; g < kMma; ++g) {
             float f[8];
-            codes4(v.x[i][0][2 * g], f);
-            codes4(v.x[i][0][2 * g + 1], f + 4);
+            codes4(v.x[i][g / 2][2 * (g % 2)], f);
+            codes4(v.x[i][g / 2][2 * (g % 2) + 1], f + 4);
             x[g] = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
           }
+        } else {
+#pragma unroll
+          for (int g = 0; g < kMma; ++g) x[g] = v.x[i][g];
         }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < kMma; ++g)
             acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.p[t][g]),
                                                                 __builtin_bit_cast(bf16x8, x[g]), acc[t][i], 0, 0, 0);
       }
     };
     Step ring[kDepth];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(p, wave + d * kWaves, ring[d]);
-    for (int s = wave; s < steps; s += kDepth * kWaves) {
+    for (int d = 0; d < kDepth; ++d) load(p, d, ring[d]);
+    for (int n = 0; n < here; n += kDepth) {
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {   // (steps past the end are zeros)
+      for (int d = 0; d < kDepth; ++d) {
         multiply(ring[d]);
-        load(p, s + (kDepth + d) * kWaves, ring[d]);
+        load(p, n + kDepth + d, ring[d]);
       }
     }
 #pragma unroll
@@ -325,25 +333,21 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t block, int ran
   }
 }
 
-// Steps in flight, as registers allow.
-template <Rows R, int kTiles>
-constexpr int kDepthOf = kTiles == 1 ? 4 : kTiles == 2 ? 3 : 2;
-
 // grid (blocks of rows, blocks of ranks, slots); two products share a launch,
 // of codes and of values (b, the last grid.z = slots ones).
 template <int kTiles>
 __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
   __shared__ Sums<kTiles> part;
-  down_block<Rows::kCodes, kTiles, kDepthOf<Rows::kCodes, kTiles>>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, part);
+  down_block<Rows::kCodes, kTiles>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, part);
 }
 template <int kTiles>
 __global__ __launch_bounds__(kThreads) void down_block_kernel2(Down codes, Down values, int slots) {
   __shared__ Sums<kTiles> part;
   const int z = blockIdx.z;
   if (codes.M > 0 && z >= slots)   // (the longer rows first)
-    down_block<Rows::kCodes, kTiles, kDepthOf<Rows::kCodes, kTiles>>(codes, blockIdx.x, blockIdx.y, z - slots, slots, part);
+    down_block<Rows::kCodes, kTiles>(codes, blockIdx.x, blockIdx.y, z - slots, slots, part);
   else
-    down_block<Rows::kValues, kTiles, kDepthOf<Rows::kValues, kTiles>>(values, blockIdx.x, blockIdx.y, z, slots, part);
+    down_block<Rows::kValues, kTiles>(values, blockIdx.x, blockIdx.y, z, slots, part);
 }
 template <int kUnused>
 __global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down values) {
@@ -351,11 +355,11 @@ __global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down va
   else down_row<Rows::kCodes>(codes);
 }
 
-// Workgroups that share out the adapters of a block of rows: more where blocks
-// leave compute units idle.
+// Workgroups that share out the adapters of a block of rows, where blocks leave
+// compute units idle (one with nothing to do still takes 2 us).
 int slots_of(const Down& a) {
   const int64_t blocks = (a.M + kBlockRows - 1) / kBlockRows * ((a.R + 63) / 64);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.count, 1024 / blocks, 16}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.count, 256 / blocks, 16}));
 }
 dim3 block_grid(const Down& a, int tiles, int z) {
   return dim3((unsigned)((a.M + kBlockRows - 1) / kBlockRows), (unsigned)((a.R + 16 * tiles - 1) / (16 * tiles)), (unsigned)z);

@@ -40,16 +40,23 @@ __device__ __forceinline__ uint32_t pair(uint32_t first, uint32_t second, int j)
   return __builtin_amdgcn_perm(second, first, j % 2 ? 0x07060302u : 0x05040100u);
 }
 
+// Rows of the list that are in LDS at once: looked up in memory, each would
+// wait for the loads of x that were sent before it.
+constexpr int kListed = 8 * kWaves * kRows;
+
+template <int KR, int KB>
+struct Lds {
+  f32x4 part[KR * KB <= 16 ? 4 : KR * KB <= 32 ? 2 : 1][KR * KB * kWave];
+  int32_t list[kListed];
+};
+
 // KR ranks to a lane (16 KR of a workgroup), KB columns.
 template <int KR, int KB, bool kCodes>
-__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
+__device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned block, Lds<KR, KB>& lds) {
   constexpr int kWords = kCodes ? KB / 4 : KB / 2;   // of a lane's columns in a row
-  constexpr int kSums = KR * KB * kWave;              // f32x4 of a wavefront's sums
-  constexpr int kAtOnce = KR * KB <= 16 ? 4 : KR * KB <= 32 ? 2 : 1;   // wavefronts' sums in LDS at once
-  __shared__ f32x4 part[kAtOnce * kSums];
+  constexpr int kAtOnce = sizeof(lds.part) / sizeof(lds.part[0]);   // wavefronts' sums in LDS at once
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int l16 = lane % 16, h = lane / 16;
-  unsigned block = blockIdx.x;
   const int cb = (int)(block % (unsigned)a.col_blocks);
   block /= (unsigned)a.col_blocks;
   const int rb = (int)(block % (unsigned)a.rank_blocks);
@@ -60,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
   // this part's rows of the adapter's list
   const int from = a.starts[id], to = a.starts[id + 1];
   const int per = (to - from + a.parts - 1) / a.parts;
-  const int first = from + slice * per, last = min(first + per, to);
+  const int first = min(from + slice * per, to), last = min(first + per, to);
 
   f32x4 acc[KR][KB];
 #pragma unroll
@@ -72,12 +79,12 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
     uint32_t x[8][kWords];
     uint32_t v[8][(KR + 1) / 2];
   };
-  // Places past the part's end: the last row again, with zeros of v.
-  auto load = [&](int p0, Step& s) __attribute__((always_inline)) {
+  // Places past the `n` listed ones: the last row again, with zeros of v.
+  auto load = [&](int p0, int n, Step& s) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int p = p0 + 8 * h + i;
-      const int64_t m = a.list[min(p, last - 1)];
+      const int64_t m = lds.list[min(p, n - 1)];
       if constexpr (kCodes) {
         const int8_t* row = static_cast<const int8_t*>(a.x) + m * a.C;
         __builtin_memcpy(s.x[i], __builtin_assume_aligned(row + min(col, a.C - KB), KB), KB);
@@ -101,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
         __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
       }
 #pragma unroll
-      for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = p < last ? s.v[i][w] : 0;
+      for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = p < n ? s.v[i][w] : 0;
     }
   };
   auto multiply = [&](const Step& s) __attribute__((always_inline)) {
@@ -126,14 +133,19 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
                                                             __builtin_bit_cast(bf16x8, fx), acc[r][j], 0, 0, 0);
     }
   };
-  const int mine = first + wave * kRows;
-  if (mine < last) {
-    Step now, next;
-    load(mine, now);
-    for (int p = mine; p < last; p += kWaves * kRows) {
-      if (p + kWaves * kRows < last) load(p + kWaves * kRows, next);
-      multiply(now);
-      now = next;
+  for (int base = first; base < last; base += kListed) {
+    const int n = min(kListed, last - base);
+    if (base > first) __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) lds.list[i] = a.list[base + i];
+    __syncthreads();
+    if (wave * kRows < n) {
+      Step now, next;
+      load(wave * kRows, n, now);
+      for (int p = wave * kRows; p < n; p += kWaves * kRows) {
+        if (p + kWaves * kRows < n) load(p + kWaves * kRows, n, next);
+        multiply(now);
+        now = next;
+      }
     }
   }
   // the other wavefronts' sums onto the first's, in order
@@ -143,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
 #pragma unroll
       for (int r = 0; r < KR; ++r)
 #pragma unroll
-        for (int j = 0; j < KB; ++j) part[(wave - w0) * kSums + (r * KB + j) * kWave + lane] = acc[r][j];
+        for (int j = 0; j < KB; ++j) lds.part[wave - w0][(r * KB + j) * kWave + lane] = acc[r][j];
     }
     __syncthreads();
     if (wave == 0) {
@@ -153,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
 #pragma unroll
           for (int r = 0; r < KR; ++r)
 #pragma unroll
-            for (int j = 0; j < KB; ++j) acc[r][j] += part[w * kSums + (r * KB + j) * kWave + lane];
+            for (int j = 0; j < KB; ++j) acc[r][j] += lds.part[w][(r * KB + j) * kWave + lane];
         }
     }
     __syncthreads();
@@ -174,32 +186,38 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad a) {
   }
 }
 
-// Ranks and columns of a lane: as many sums as registers allow.
-struct Shape {
-  int kr, kb;
-};
-Shape shape_of(int R, bool codes) {
-  if (R <= 16) return {1, codes ? 16 : 8};
-  if (R <= 32) return {2, codes ? 16 : 8};
-  return {4, codes ? 8 : 4};
+// The gradients of both matrices in one launch: b's workgroups, whose rows are
+// longer, before a's.
+template <int KR, int KA, int KB>
+__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, AdapterGrad gb, unsigned blocks_b) {
+  __shared__ union {
+    Lds<KR, KA> a;
+    Lds<KR, KB> b;
+  } lds;
+  if (blockIdx.x < blocks_b) adapter_grad<KR, KB, false>(gb, blockIdx.x, lds.b);
+  else adapter_grad<KR, KA, true>(ga, blockIdx.x - blocks_b, lds.a);
 }
 
-// Parts of the lists: about two workgroups per compute unit, each wavefront a
-// step or more.
+// Ranks of a lane, and columns: as many sums as registers allow.
+int ranks_of(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+int columns_of(int R, bool codes) { return R <= 32 ? (codes ? 16 : 8) : codes ? 8 : 4; }
+
+int64_t col_blocks_of(int64_t C, int R, bool codes) { return (C + 16 * columns_of(R, codes) - 1) / (16 * columns_of(R, codes)); }
+int64_t rank_blocks_of(int R) { return (R + 16 * ranks_of(R) - 1) / (16 * ranks_of(R)); }
+
+// Parts of the lists: about one workgroup per compute unit for both gradients
+// (b's has twice the bytes), each wavefront a step or more.
 int parts_of(int64_t M, int64_t C, int R, int count, bool codes) {
-  const Shape s = shape_of(R, codes);
-  const int64_t blocks = (C + 16 * s.kb - 1) / (16 * s.kb) * ((R + 16 * s.kr - 1) / (16 * s.kr)) * count;
-  return (int)std::max<int64_t>(1, std::min((512 + blocks - 1) / blocks, (M + kWaves * kRows - 1) / (kWaves * kRows)));
+  const int64_t blocks = col_blocks_of(C, R, codes) * rank_blocks_of(R) * count, want = codes ? 96 : 160;
+  return (int)std::max<int64_t>(1, std::min(want / blocks, (M + kWaves * kRows - 1) / (kWaves * kRows)));
 }
 
-template <int KR, int KB, bool kCodes>
-hipError_t launch(AdapterGrad a, hipStream_t stream) {
-  a.col_blocks = (int)((a.C + 16 * KB - 1) / (16 * KB));
-  a.rank_blocks = (a.R + 16 * KR - 1) / (16 * KR);
-  const int64_t blocks = (int64_t)a.col_blocks * a.rank_blocks * a.parts * a.count;
-  if (blocks * kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((adapter_grad_kernel<KR, KB, kCodes>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+// Workgroups of one of the gradients (none: 0).
+int64_t set_blocks(AdapterGrad& g, bool codes) {
+  if (g.slices == nullptr) return 0;
+  g.col_blocks = (int)col_blocks_of(g.C, g.R, codes);
+  g.rank_blocks = (int)rank_blocks_of(g.R);
+  return (int64_t)g.col_blocks * g.rank_blocks * g.parts * g.count;
 }
 
 // ---- the adapters' share of few rows' input gradient ----
@@ -240,14 +258,25 @@ int adapter_grad_parts(int64_t M, int64_t C, int64_t R, int64_t count, bool code
   return parts_of(M, C, (int)R, (int)count, codes);
 }
 
-hipError_t launch_adapter_grad(AdapterGrad a, bool codes, hipStream_t s) {
-  const Shape k = shape_of(a.R, codes);
-  if (codes) {
-    if (k.kr == 1) return launch<1, 16, true>(a, s);
-    return k.kr == 2 ? launch<2, 16, true>(a, s) : launch<4, 8, true>(a, s);
+bool adapter_grads_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t count) {
+  int64_t blocks = 0;
+  for (const bool codes : {true, false}) {
+    const int64_t C = codes ? K : N;
+    blocks += col_blocks_of(C, (int)R, codes) * rank_blocks_of((int)R) * count * parts_of(M, C, (int)R, (int)count, codes);
   }
-  if (k.kr == 1) return launch<1, 8, false>(a, s);
-  return k.kr == 2 ? launch<2, 8, false>(a, s) : launch<4, 4, false>(a, s);
+  return blocks * kThreads < (int64_t(1) << 32);   // threads of a launch
+}
+
+hipError_t launch_adapter_grads(AdapterGrad ga, AdapterGrad gb, hipStream_t s) {
+  const int64_t na = set_blocks(ga, true), nb = set_blocks(gb, false);
+  if (na + nb == 0) return hipSuccess;
+  const dim3 grid((unsigned)(na + nb)), block(kThreads);
+  switch (ranks_of(na ? ga.R : gb.R)) {
+    case 1: hipLaunchKernelGGL((adapter_grad_kernel<1, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    case 2: hipLaunchKernelGGL((adapter_grad_kernel<2, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    default: hipLaunchKernelGGL((adapter_grad_kernel<4, 8, 4>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_adapter_up(const uint16_t* u, int64_t ldt, const uint16_t* p, const int32_t* ids, int64_t count,

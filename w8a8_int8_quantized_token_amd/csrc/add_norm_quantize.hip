@@ -365,7 +365,7 @@ hipError_t launch_add_norm_quantize(const uint16_t* x, const uint16_t* residual,
   return forward<4, 8>(a, fp8, s);
 }
 
-int64_t norm_grad_rows(int64_t M, int64_t K) { return std::min<int64_t>(M, 256 * 1024 / grad_threads(K)); }
+int64_t norm_grad_rows(int64_t M, int64_t K) { return std::min<int64_t>(M, 128 * 1024 / grad_threads(K)); }
 
 hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                                 uint16_t* dx, float* part, float* dweight, int64_t M, int64_t K, float eps,

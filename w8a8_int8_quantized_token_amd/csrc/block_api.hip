@@ -286,6 +286,11 @@ bool adapters_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   return shape_ok(M, N, K, 1) && R >= 8 && R <= kMaxRank && R % 8 == 0 && L >= 1 && L <= kMaxAdapters;
 }
 
+bool adapters_back_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, bool dx) {
+  return adapters_ok(M, N, K, R, L) && !(dx && up(N, kLine) > kMaxSummed) &&
+         w8a8::adapter_grads_fit(std::max<int64_t>(M, 1), N, K, R, L);
+}
+
 // Launches of the linear with adapters: the first products t (which make the
 // codes of few tokens on the way), then one of the linear's kernels with t.
 struct AdapterPlan {
@@ -677,7 +682,7 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t* x, const int8_t* wq, co
 
 size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, int dx, int da,
                                                int db) {
-  if (!adapters_ok(M, N, K, R, L) || M == 0) return 0;
+  if (!adapters_back_ok(M, N, K, R, L, dx) || M == 0) return 0;
   int64_t most = 0;   // the largest of the plans that calls of these sizes may take, as their addresses are
   for (const bool copy : {true, false})
     for (const bool few : {false, true})
@@ -691,7 +696,7 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
                                           const float* scaling, const int32_t* ids, uint16_t* dx, uint16_t* da,
                                           uint16_t* db, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
                                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  if (!adapters_ok(M, N, K, R, L) || (dx && up(N, kLine) > kMaxSummed)) return W8A8_ERR_SHAPE;
+  if (!adapters_back_ok(M, N, K, R, L, dx)) return W8A8_ERR_SHAPE;
   if (!aligned(dy, 2) || !aligned(dx, 2) || !aligned(da, 16) || !aligned(db, 16)) return W8A8_ERR_ALIGN;
   if (M == 0) {
     if (da) TRY(w8a8::launch_zero(da, L * R * K, stream));
@@ -769,16 +774,16 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
     }
     if (slices) join[joins++] = {slices, dx, p.x.ranges_x, M * K, true, 0};
   }
+  w8a8::AdapterGrad ga{}, gb{};
   if (da) {
-    w8a8::AdapterGrad g{xq, v, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
-    TRY(w8a8::launch_adapter_grad(g, true, stream));
-    join[joins++] = {g.slices, da, p.parts_a, L * R * K, true, 0};
+    ga = {xq, v, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
+    join[joins++] = {ga.slices, da, p.parts_a, L * R * K, true, 0};
   }
   if (db) {
-    w8a8::AdapterGrad g{dy, t, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
-    TRY(w8a8::launch_adapter_grad(g, false, stream));
-    join[joins++] = {g.slices, db, p.parts_b, L * R * N, true, 0};
+    gb = {dy, t, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
+    join[joins++] = {gb.slices, db, p.parts_b, L * R * N, true, 0};
   }
+  TRY(w8a8::launch_adapter_grads(ga, gb, stream));
   return joins > 0 ? launched(w8a8::launch_finish(join, joins, stream)) : W8A8_OK;
 }
 

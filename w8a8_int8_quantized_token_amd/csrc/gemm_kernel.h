@@ -794,7 +794,8 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   constexpr int kLowRows = Op::kBf16 ? 16 : 32, kLowM = T::TM / kLowRows;   // row tiles of a wavefront
   constexpr int kLowN = Op::kBf16 ? 2 * T::FN : T::FN;                      // fragments of its channels
   constexpr int kLowStep = Op::kBf16 ? 32 : 16;                            // ranks of an MFMA
-  auto add_low = [&](const TileAddr& at) __attribute__((always_inline)) {
+  // `before`: called once the first pass's loads are on the way.
+  auto add_low = [&](const TileAddr& at, auto before) __attribute__((always_inline)) {
     if constexpr (kLow<EPI>) {
       int e_lane = lane;
       asm volatile("" : "+v"(e_lane));   // addresses formed here, not before the K loop
@@ -830,6 +831,10 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
         }
       };
       uint64_t left[kLowM];   // lanes whose adapter is still to come
+      auto all_left = [&]() {
+#pragma unroll
+        for (int i = 0; i < kLowM; ++i) left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+      };
       auto next_adapter = [&]() {   // -1: none
         int a = -1;
 #pragma unroll
@@ -839,32 +844,17 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
         for (int i = 0; i < kLowM; ++i) left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == a);
         return a;
       };
-      for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
-#pragma unroll
-        for (int i = 0; i < kLowM; ++i) left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
-        constexpr bool kAhead = !Op::kBf16;
-        v4i ft[kAhead ? kLowM : 2], fn[kLowN];
-        [[maybe_unused]] v4i ahead[kLowN];
-        if constexpr (kAhead) {
-#pragma unroll
-          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
-        }
-        int a = next_adapter();
-        if constexpr (kAhead)
-          if (a >= 0) frags_b(a, r0, ahead);
-        while (a >= 0) {
-          const int now = a;
-          a = next_adapter();
-          if constexpr (kAhead) {
-#pragma unroll
-            for (int j = 0; j < kLowN; ++j) fn[j] = ahead[j];
-            if (a >= 0) frags_b(a, r0, ahead);
-          } else {
+      if constexpr (Op::kBf16) {
+        // each product by itself, and only the adapter's own tokens take it
+        for (int r0 = 0; r0 < extra.R; r0 += kLowStep) {
+          all_left();
+          int a = next_adapter();
+          while (a >= 0) {
+            const int now = a;
+            a = next_adapter();
+            v4i ft[2], fn[kLowN];
             ft[0] = frag_t(0, r0);
             frags_b(now, r0, fn);
-          }
-          if constexpr (Op::kBf16) {
-            // each product by itself, and only the adapter's own tokens take it
 #pragma unroll
             for (int i = 0; i < kLowM; ++i) {
               if (i + 1 < kLowM) ft[(i + 1) % 2] = frag_t(i + 1, r0);
@@ -878,29 +868,54 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
                 __builtin_amdgcn_sched_barrier(0);
               }
             }
-          } else {
-            uint32_t most = 0;   // largest magnitudes of both halves of the words
-#pragma unroll
-            for (int j = 0; j < kLowN; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fn[j][e] & 0x7fff7fffu);
-            const bool drop = __builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0;
-#pragma unroll
-            for (int j = 0; j < kLowN; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) fn[j][e] = drop ? 0 : fn[j][e];
-#pragma unroll
-            for (int i = 0; i < kLowM; ++i) {
-              v4i t;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) t[e] = id[i] == now ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
-#pragma unroll
-              for (int j = 0; j < kLowN; ++j)
-                acc[i][j] = __builtin_bit_cast(
-                    v16i, __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fn[j]), __builtin_bit_cast(bf16x8, t),
-                                                                  __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
-            }
           }
+        }
+      } else {
+        all_left();
+        int a = next_adapter();
+        v4i ft[kLowM], fn[kLowN], ahead[kLowN];
+        auto load_t = [&](int r0) {
+#pragma unroll
+          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
+        };
+        if (a >= 0) {
+          load_t(0);
+          frags_b(a, 0, ahead);
+        }
+        before();
+        for (int r0 = 0; a >= 0;) {
+#pragma unroll
+          for (int j = 0; j < kLowN; ++j) fn[j] = ahead[j];
+          const int now = a, r_now = r0;
+          a = next_adapter();
+          if (a < 0 && r0 + kLowStep < extra.R) {   // the next ranks, from the first adapter on
+            r0 += kLowStep;
+            all_left();
+            a = next_adapter();
+          }
+          if (a >= 0) frags_b(a, r0, ahead);
+          uint32_t most = 0;   // largest magnitudes of both halves of the words
+#pragma unroll
+          for (int j = 0; j < kLowN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fn[j][e] & 0x7fff7fffu);
+          const bool drop = __builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0;
+#pragma unroll
+          for (int j = 0; j < kLowN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fn[j][e] = drop ? 0 : fn[j][e];
+#pragma unroll
+          for (int i = 0; i < kLowM; ++i) {
+            v4i t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = id[i] == now ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
+#pragma unroll
+            for (int j = 0; j < kLowN; ++j)
+              acc[i][j] = __builtin_bit_cast(
+                  v16i, __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fn[j]), __builtin_bit_cast(bf16x8, t),
+                                                                __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
+          }
+          if (a >= 0 && r0 != r_now) load_t(r0);
         }
       }
     }
@@ -1027,7 +1042,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
     // the first range's
     auto start_low = [&]() __attribute__((always_inline)) {
       if constexpr (kLow<EPI> && Op::kBf16) {
-        if (cur.c == 0) add_low(cur);
+        if (cur.c == 0) add_low(cur, [] {});
       }
     };
 
@@ -1194,17 +1209,19 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
         }
       };
       if constexpr (kLow<EPI> && !Op::kBf16) {
+        add_low(cur, [&]() __attribute__((always_inline)) {
+          // the fp32 values in the accumulators' place
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j) {
-          load_sb(j);
+          for (int j = 0; j < T::FN; ++j) {
+            load_sb(j);
 #pragma unroll
-          for (int i = 0; i < T::FM; ++i)
+            for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[i][j][e] = __float_as_int(dequant((float)acc[i][j][e], sa[i], sv[e / 4][e % 4], bv[e / 4][e % 4]));
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        add_low(cur);
+              for (int e = 0; e < 16; ++e)
+                acc[i][j][e] = __float_as_int(dequant((float)acc[i][j][e], sa[i], sv[e / 4][e % 4], bv[e / 4][e % 4]));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        });
       }
       // 4 bf16 outputs (two packed words) of each run g of output tile (i, j):
       // channels nj + 8g + 4*khalf + 0..3

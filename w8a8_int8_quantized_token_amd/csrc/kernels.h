@@ -261,7 +261,9 @@ struct AdapterGrad {
   int ldt, R, count, parts, col_blocks, rank_blocks;
 };
 int adapter_grad_parts(int64_t M, int64_t C, int64_t R, int64_t count, bool codes);
-hipError_t launch_adapter_grad(AdapterGrad a, bool codes, hipStream_t stream);
+bool adapter_grads_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t count);
+// Both gradients, each left out where its slices are null.
+hipError_t launch_adapter_grads(AdapterGrad codes, AdapterGrad values, hipStream_t stream);
 // out fp32 [M,C] = sum_r u[m,r] p[ids[m]][r,c] (p bf16 [count,R,C], C % 16 == 0), for few rows.
 hipError_t launch_adapter_up(const uint16_t* u, int64_t ldt, const uint16_t* p, const int32_t* ids, int64_t count,
                              int64_t R, int64_t M, int64_t C, float* out, hipStream_t stream);

@@ -15,6 +15,7 @@
 // of them on the bf16 matrix cores (codes are exact in bf16), its wavefronts
 // a range of k each, and goes through the adapters that its rows
 // have one after another; a row takes the sums of its own adapter alone.
+#include "adapter_sum.h"
 #include "kernels.h"
 #include "quant_codes.h"
 
@@ -33,22 +34,6 @@ constexpr u32x4 kZeros = {0, 0, 0, 0};
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-}
-__device__ __forceinline__ void unpack8(u32x4 v, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(v[i] << 16);
-    f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void codes4(uint32_t w, float* f) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w >> (8 * e));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
 }
 // Eight bf16 values of a row of K from column k on, zeros past its end, from
 // any 2-byte address.
@@ -79,28 +64,37 @@ template <Rows R>
 __device__ __forceinline__ void down_row(const Down& a) {
   __shared__ __attribute__((aligned(16))) u32x2 codes[R == Rows::kQuantize ? kMaxFused / 8 : 1];
   __shared__ uint32_t amax[kWaves];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t m = blockIdx.x;
-  const int id = adapter_of(a, m);
   const int pieces = (a.K + 7) / 8;
-  float scale = 1.0f;
-  if constexpr (R == Rows::kCodes) scale = a.scale[m];
+  const int r0 = blockIdx.y * kRanks + 2 * wave;   // this wavefront's two ranks (R is even)
+  [[maybe_unused]] u32x4 v[kKeep];
   if constexpr (R == Rows::kQuantize) {
     const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + m * a.K);
-    u32x4 v[kKeep];
-    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
       const int c = threadIdx.x + i * kThreads;
       v[i] = c < pieces ? x[c] : kZeros;
+    }
+  }
+  const int id = adapter_of(a, m);
+  float scale = 1.0f;
+  if constexpr (R == Rows::kCodes) scale = a.scale[m];
+  const bool on = id >= 0 && r0 < a.R;
+  const RankRows rows(a.p + max(id, 0) * a.p_stride + (int64_t)min(r0, a.R - 2) * a.ldp, a.ldp, pieces, on);
+  RankPieces w;   // the first ones are on the way while the codes are made
+  rows.load(lane, w);
+  if constexpr (R == Rows::kQuantize) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = absmax_bits(top, v[i][e]);
-    }
     top = wave_max(max(top & 0xffffu, top >> 16));
     if (lane == 0) amax[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = max(top, amax[w]);
+    for (int k = 0; k < kWaves; ++k) top = max(top, amax[k]);
     const RowScale rs = row_scale<false>(top);
     scale = top ? rs.s : 0.0f;
 #pragma unroll
@@ -115,51 +109,31 @@ __device__ __forceinline__ void down_row(const Down& a) {
     if (blockIdx.y == 0 && threadIdx.x == 0) a.code_scale[m] = scale;
     __syncthreads();
   }
-  const int r0 = blockIdx.y * kRanks + 2 * wave;   // this wavefront's two ranks (R is even)
   float sum[2] = {0.0f, 0.0f};
-  if (id >= 0 && r0 < a.R) {
-    const uint16_t* p0 = a.p + id * a.p_stride + (int64_t)r0 * a.ldp;
-    const uint16_t* p1 = p0 + a.ldp;
-    constexpr int kSteps = 4;
-    for (int c0 = lane; c0 < pieces; c0 += kSteps * kWave) {
-      u32x4 w[kSteps][2], v[kSteps];
+  if (on) {
+    for (int c0 = lane; c0 < pieces; c0 += kSumSteps * kWave) {
+      if (c0 > lane) rows.load(c0, w);
+      float x[kSumSteps][8];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int s = 0; s < kSumSteps; ++s) {
         const int c = c0 + s * kWave;
-        w[s][0] = w[s][1] = v[s] = kZeros;
-        if (c < pieces) {
-          w[s][0] = *reinterpret_cast<const u32x4*>(p0 + c * 8);
-          w[s][1] = *reinterpret_cast<const u32x4*>(p1 + c * 8);
-          if constexpr (R == Rows::kValues) {
-            v[s] = load8(static_cast<const uint16_t*>(a.x) + m * a.K, c * 8, a.K);
-          } else {
-            u32x2 q;
+        if constexpr (R == Rows::kValues) {
+          unpack8(c < pieces ? load8(static_cast<const uint16_t*>(a.x) + m * a.K, c * 8, a.K) : kZeros, x[s]);
+        } else {
+          u32x2 q = u32x2{0, 0};
+          if (c < pieces) {
             if constexpr (R == Rows::kQuantize) q = codes[c];
             else q = reinterpret_cast<const u32x2*>(static_cast<const int8_t*>(a.x) + m * a.K)[c];
-            v[s][0] = q[0], v[s][1] = q[1];
           }
+          codes4(q[0], x[s]);
+          codes4(q[1], x[s] + 4);
         }
       }
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        float x[8], y[8];
-        if constexpr (R == Rows::kValues) {
-          unpack8(v[s], x);
-        } else {
-          codes4(v[s][0], x);
-          codes4(v[s][1], x + 4);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          unpack8(w[s][k], y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum[k] = fmaf(x[e], y[e], sum[k]);
-        }
-      }
+      add_ranks(w, x, sum);
     }
     const float f = a.scaling[id];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) sum[k] = wave_sum(sum[k]) * scale * f;
+    for (int k = 0; k < 2; ++k) sum[k] = sum_lanes(sum[k]) * scale * f;
   }
   if (lane == 0) {
     *reinterpret_cast<uint32_t*>(a.t + m * a.ldt + r0) = pack2(sum[0], sum[1]);

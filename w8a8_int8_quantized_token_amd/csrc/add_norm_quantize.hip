@@ -20,6 +20,7 @@
 #include "quant_codes.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w8a8 {
 namespace {
@@ -35,15 +36,27 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
+// Sum and maximum over the wavefront by DPP exchanges: six trips through LDS
+// take longer than a short row.
+template <class F>
+__device__ __forceinline__ float over_lanes(float v, F f) {
+  auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v = f(v, dpp(v, std::integral_constant<int, 0xB1>{}));    // quad_perm [1,0,3,2]
+  v = f(v, dpp(v, std::integral_constant<int, 0x4E>{}));    // quad_perm [2,3,0,1]
+  v = f(v, dpp(v, std::integral_constant<int, 0x141>{}));   // row_half_mirror
+  v = f(v, dpp(v, std::integral_constant<int, 0x140>{}));   // row_mirror
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
+  return over_lanes(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_maxf(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  return v;
+  return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // fl32(v / s) for any fp32 |v| <= 448 s, from the correctly rounded r = 1 / s:

@@ -295,7 +295,7 @@ bool adapters_back_ok(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, boo
 // codes of few tokens on the way), then one of the linear's kernels with t.
 struct AdapterPlan {
   bool quantize, in_down;   // codes are made here; by the first product
-  bool few;                 // the few-token kernel
+  bool few, alone;          // the few-token kernel; it makes codes and t itself
   int splits, tile;         // otherwise the linear's plan
   int64_t xq, xs, t, slices;
   int64_t bytes;
@@ -305,8 +305,10 @@ AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int64_t R, bool dynami
   p.quantize = dynamic;
   p.in_down = dynamic && w8a8::down_quantizes(M, K);
   p.few = tile < 0 && M <= w8a8::kFewTokens && few_tokens_pay(M, N, K, false, false) && w8a8::few_tokens_low_fit(M, N);
+  p.alone = p.few && dynamic && w8a8::few_tokens_low_from_x(M, N, K, R);
   p.splits = 1;
   p.tile = tile;
+  if (p.alone) return p;
   Pieces w;
   if (dynamic) {
     p.xq = w.add(M * K);
@@ -337,6 +339,10 @@ w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, 
   const AdapterPlan p = adapter_plan(M, N, K, R, dynamic, aligned(y, 16), tile);
   const w8a8_status st = check_workspace(ws, ws_bytes, p.bytes);
   if (st != W8A8_OK) return st;
+  if (p.alone) {
+    const w8a8::Low low{nullptr, b, ids, 0, R, L, a, scaling};
+    return launched(w8a8::launch_few_tokens_low_from_x(x, wq, w_scale, bias, low, y, M, N, K, stream));
+  }
   uint16_t* t = at<uint16_t>(ws, p.t);
   int8_t* codes = dynamic ? at<int8_t>(ws, p.xq) : nullptr;
   float* code_scale = dynamic ? at<float>(ws, p.xs) : nullptr;

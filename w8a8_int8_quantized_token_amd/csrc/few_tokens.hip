@@ -18,6 +18,11 @@
 // codes as the second; the partial sums of the wavefronts are exact int32 and
 // are joined through LDS.
 //
+// Low-rank adapters: their shares t b^T of the workgroup's groups are made at
+// the start, while the first pieces of the weight are on the way; for a single
+// token or a short one so are t themselves, by every workgroup, which costs less
+// than the launch that makes them for more tokens.
+//
 // Codes: up to kCodeBytes of them (one token of K = 22272, or five of 4096)
 // are made by every workgroup for itself while its first pieces are on the
 // way, and stay in LDS: one launch.  More tokens would make that the
@@ -27,6 +32,7 @@
 // Measured (cold weights, one call after another): 1 x 65536 x 4096 49 us, 5.5
 // TB/s; 1 x 12288 x 4096 14 us; gated 1 x 12288 x 4096 21 us, 4.8 TB/s; 16
 // x 12288 x 4096 14 us after 4 us for the codes.
+#include "adapter_sum.h"
 #include "epilogue.h"
 #include "kernels.h"
 #include "quant_codes.h"
@@ -47,6 +53,7 @@ constexpr int kRows = 16;            // output channels of a group
 constexpr int kPiece = 128;          // bytes of K of a piece
 constexpr int kPieceBytes = kRows * kPiece;
 constexpr int kCodeBytes = 22 * 1024;
+constexpr int kFewRank = 64;               // ranks of adapters whose first products are made here
 constexpr uint32_t kOOB = 0x80000000u;    // buffer offset past any range: reads as zeros
 constexpr int kRsrcWord3 = 0x00020000;
 
@@ -74,9 +81,12 @@ struct Few {
   // before the first piece is needed.
   static constexpr int kLowGroup = MT * 16 * kRows * 4;   // bytes of a group
   static constexpr int kLowGroups = kLow ? (MT == 1 ? 24 : 4) : 0;
-  static constexpr int kLds = kSlots * kSlotBytes + (kCodes ? 0 : kCodeBytes) + 12 * kThreads + 64 + kLowGroups * kLowGroup;
+  // from bf16 activations: the adapters' first products too
+  static constexpr int kLowT = kLow && !kCodes ? 16 * kFewRank * 2 : 0;
+  static constexpr int kLds =
+      kSlots * kSlotBytes + (kCodes ? 0 : kCodeBytes) + 12 * kThreads + 64 + kLowGroups * kLowGroup + kLowT;
   static_assert(kCodes || MT == 1, "codes in LDS are one tile of tokens");
-  static_assert(!kLow || (kCodes && ACT == FewAct::kNone), "adapters beside the plain linear, from codes");
+  static_assert(!kLow || ACT == FewAct::kNone, "adapters beside the plain linear");
   static_assert(kLds <= 160 * 1024, "LDS budget");
   static_assert(NV * kWave * 16 <= kTiles * kPieceBytes, "a wavefront's sums fit its part of a slot");
 };
@@ -116,6 +126,11 @@ __device__ __forceinline__ void lds_write(uint32_t a, uint32_t v) {
 __device__ __forceinline__ uint32_t lds_read_word(uint32_t a) {
   uint32_t r;
   asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(r) : "v"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ u32x2 lds_read8(uint32_t a) {
+  u32x2 r;
+  asm volatile("ds_read_b64 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(r) : "v"(a) : "memory");
   return r;
 }
 __device__ __forceinline__ v4i lds_read16(uint32_t a) {
@@ -192,6 +207,7 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes, kLow>::kThreads)) void few_to
   __shared__ __attribute__((aligned(16))) float s_lds[kThreads], b_lds[kThreads];
   __shared__ __attribute__((aligned(16))) uint32_t amax_lds[8];
   __shared__ __attribute__((aligned(16))) float low_lds[kLow ? F::kLowGroups * F::kLowGroup / 4 : 4];
+  __shared__ __attribute__((aligned(16))) uint16_t t_lds[kLow && !kCodes ? F::kLowT / 2 : 8];
 
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -264,6 +280,9 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes, kLow>::kThreads)) void few_to
   else load_x(wave / P);
   const int64_t n_first = scale_row(0);
   const float first_scale = sw[n_first];
+  auto share_id = [&](int i) { return kLow ? low.ids[i / kRows % M] : 0; };
+  [[maybe_unused]] int first_id = 0;
+  if constexpr (kLow) first_id = share_id(min(tid, mine * M * kRows - 1));
   const uint16_t* const bias_or = bias != nullptr ? bias : reinterpret_cast<const uint16_t*>(sw);
   const uint32_t first_bias = bias_or[n_first];
   __builtin_amdgcn_sched_barrier(0);
@@ -273,6 +292,47 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes, kLow>::kThreads)) void few_to
   lds_write(lds_address(s_lds + tid), __float_as_uint(first_scale));
   lds_write(lds_address(b_lds + tid), bias != nullptr ? first_bias << 16 : 0u);
   if constexpr (kCodes) lds_write(lds_address(sx_lds + tid), __float_as_uint(token_scale));
+
+  // Adapters' shares: a thread for a token and a channel of one of this
+  // workgroup's groups (neighbouring threads: neighbouring rows of b).  The
+  // first one's rows are on the way while the codes and t are made.
+  constexpr int kSharePieces = kLow ? 2 : 1;   // of 8 ranks at a time
+  [[maybe_unused]] const int low_all = kLow ? mine * M * kRows : 0;
+  [[maybe_unused]] const uint16_t *share_b = nullptr, *share_row = nullptr;
+  [[maybe_unused]] u32x4 share_w[kSharePieces], share_t[kSharePieces];
+  [[maybe_unused]] bool share_on = false;
+  auto load_ranks_of_share = [&](int r) __attribute__((always_inline)) {
+    // (branch-free: ranks past the last are not used)
+#pragma unroll
+    for (int p = 0; p < kSharePieces; ++p) {
+      const int at = min(r + 8 * p, (int)low.R - 8);
+      share_w[p] = *reinterpret_cast<const u32x4*>(share_b + at);
+      if constexpr (kCodes) share_t[p] = *reinterpret_cast<const u32x4*>(share_row + at);
+    }
+  };
+  auto load_share = [&](int i, int id) __attribute__((always_inline)) {
+    const int64_t n = min(((int64_t)blockIdx.x + (int64_t)(i / kRows / M) * gridDim.x) * kRows + i % kRows, N - 1);
+    share_on = id >= 0 && id < low.count;
+    share_b = low.b + ((share_on ? id : 0) * N + n) * low.R;
+    if constexpr (kCodes) share_row = low.t + i / kRows % M * low.ldt;
+    load_ranks_of_share(0);
+  };
+  if constexpr (kLow) load_share(min(tid, low_all - 1), first_id);
+
+  // Adapters from bf16 activations: a wavefront takes a token and two ranks at a
+  // time, as the first product's own kernel does; its first pieces are on the
+  // way while the codes are made.
+  [[maybe_unused]] RankPieces ranks;
+  [[maybe_unused]] RankRows rank_rows(nullptr, 0, 0, false);
+  [[maybe_unused]] int rank_id = -1;
+  [[maybe_unused]] const int pairs = kLow && !kCodes ? (int)low.R / 2 : 1, eighths = K / 8;
+  auto start_pair = [&](int i) __attribute__((always_inline)) {
+    rank_id = low.ids[i / pairs];
+    if (rank_id >= low.count) rank_id = -1;
+    rank_rows = RankRows(low.a + ((int64_t)max(rank_id, 0) * low.R + i % pairs * 2) * K, K, eighths, rank_id >= 0);
+    rank_rows.load(lane, ranks);
+  };
+  if constexpr (kLow && !kCodes) start_pair(min(wave, M * pairs - 1));
 
   if constexpr (!kCodes) {
     // ---- the tokens' codes ----
@@ -317,29 +377,58 @@ __global__ __launch_bounds__((Few<MT, ACT, kCodes, kLow>::kThreads)) void few_to
     }
     if (P > 1 && wave / P >= M) barrier();
   }
-  if constexpr (kLow) {
-    // A thread for a token and a channel of one of this workgroup's groups
-    // (neighbouring threads: neighbouring rows of b).  The first pieces of the
-    // weight are on the way meanwhile.
-    const int all = mine * M * kRows;
-    for (int i = tid; i < all; i += kThreads) {
-      const int c = i % kRows, mt = i / kRows % M, gi = i / kRows / M;
-      const int64_t n = min(((int64_t)blockIdx.x + (int64_t)gi * gridDim.x) * kRows + c, N - 1);
-      const int id = low.ids[mt];
-      float v = 0.0f;
-      if (id >= 0 && id < low.count) {
-        const uint16_t* b = low.b + (id * N + n) * low.R;
-        const uint16_t* t = low.t + mt * low.ldt;
-        for (int r = 0; r < (int)low.R; r += 8) {
-          const u32x4 bv = *reinterpret_cast<const u32x4*>(b + r), tv = *reinterpret_cast<const u32x4*>(t + r);
+  if constexpr (kLow && !kCodes) {
+    barrier();   // the codes and scales are there
+    for (int i = wave; i < M * pairs; i += kWaves) {
+      if (i > wave) start_pair(i);
+      const int m = i / pairs;
+      float sum[2] = {0.0f, 0.0f};
+      if (rank_id >= 0) {
+        const uint32_t row = lds_address(codes) + (uint32_t)(m * code_row(K));
+        for (int c0 = lane; c0 < eighths; c0 += kSumSteps * kWave) {
+          if (c0 > lane) rank_rows.load(c0, ranks);
+          float v[kSumSteps][8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v = fmaf(__uint_as_float(tv[e] << 16), __uint_as_float(bv[e] << 16), v);
-            v = fmaf(__uint_as_float(tv[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), v);
+          for (int s = 0; s < kSumSteps; ++s) {
+            const int c = c0 + s * kWave;
+            const u32x2 q = lds_read8(row + (uint32_t)min(c, eighths - 1) * 8);   // (past the row: times zeros)
+            codes4(q[0], v[s]);
+            codes4(q[1], v[s] + 4);
+          }
+          add_ranks(ranks, v, sum);
+        }
+        const float sa = __uint_as_float(lds_read_word(lds_address(sx_lds + m))), f = low.scaling[rank_id];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sum[k] = sum_lanes(sum[k]) * sa * f;
+      }
+      if (lane == 0)
+        lds_write(lds_address(t_lds + m * kFewRank + i % pairs * 2),
+                  __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{sum[0], sum[1]}), bf16x2)));
+    }
+    barrier();
+  }
+  if constexpr (kLow) {
+    for (int i = tid; i < low_all; i += kThreads) {
+      if (i > tid) load_share(i, share_id(i));
+      float v = 0.0f;
+      if (share_on) {
+        for (int r = 0; r < (int)low.R; r += 8 * kSharePieces) {
+          if (r > 0) load_ranks_of_share(r);
+#pragma unroll
+          for (int p = 0; p < kSharePieces; ++p) {
+            if (r + 8 * p >= (int)low.R) continue;
+            u32x4 tv;
+            if constexpr (kCodes) tv = share_t[p];
+            else tv = __builtin_bit_cast(u32x4, lds_read16(lds_address(t_lds + i / kRows % M * kFewRank + r + 8 * p)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v = fmaf(__uint_as_float(tv[e] << 16), __uint_as_float(share_w[p][e] << 16), v);
+              v = fmaf(__uint_as_float(tv[e] & 0xffff0000u), __uint_as_float(share_w[p][e] & 0xffff0000u), v);
+            }
           }
         }
       }
-      lds_write(lds_address(low_lds + (gi * MT * 16 + mt) * kRows + c), __float_as_uint(v));
+      lds_write(lds_address(low_lds + (i / kRows / M * MT * 16 + i / kRows % M) * kRows + i % kRows), __float_as_uint(v));
     }
   }
   barrier();
@@ -487,6 +576,18 @@ hipError_t launch_act(const uint16_t* x, const int8_t* xq, const float* sx, cons
 }
 
 }  // namespace
+
+// Where every workgroup makes the first products for itself: the codes fit LDS,
+// and the adapters' rows that each has to read are as few as a launch costs.
+bool few_tokens_low_from_x(int64_t M, int64_t N, int64_t K, int64_t R) {
+  return few_tokens_in_lds(M, K) && R <= kFewRank && M * R * K <= 65536 && few_tokens_low_fit(M, N);
+}
+
+hipError_t launch_few_tokens_low_from_x(const uint16_t* x, const int8_t* wq, const float* sw, const uint16_t* bias,
+                                        const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  if (M < 1 || !few_tokens_low_from_x(M, N, K, low.R)) return hipErrorInvalidValue;
+  return launch<1, FewAct::kNone, false, true>(x, nullptr, nullptr, wq, sw, bias, y, M, N, K, s, low);
+}
 
 bool few_tokens_low_fit(int64_t M, int64_t N) {
   const int64_t groups = (N + kRows - 1) / kRows, per = (groups + 255) / 256;

@@ -115,6 +115,8 @@ struct Low {
   const uint16_t *t, *b;
   const int32_t* ids;
   int64_t ldt, R, count;
+  const uint16_t* a;      // where t is made on the way (few tokens): a bf16 [count,R,K]
+  const float* scaling;   // and scaling [count]
 };
 
 // out bf16 [M,N] = a [M,Kpad] * b [N,Kpad]^T, bf16 with fp32 sums; N and Kpad
@@ -243,6 +245,10 @@ bool few_tokens_low_fit(int64_t M, int64_t N);
 hipError_t launch_few_tokens_low(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                  const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
                                  hipStream_t stream);
+bool few_tokens_low_from_x(int64_t M, int64_t N, int64_t K, int64_t R);   // from bf16 x, t made on the way
+hipError_t launch_few_tokens_low_from_x(const uint16_t* x, const int8_t* wq, const float* sw, const uint16_t* bias,
+                                        const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                                        hipStream_t stream);
 hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const float* sx, const float* sw,
                                     const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N,
                                     hipStream_t stream);

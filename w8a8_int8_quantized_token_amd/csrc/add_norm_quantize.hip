@@ -68,24 +68,33 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
   q = fmaf(fmaf(-q, s, v), r, q);
   return fmaf(fmaf(-q, s, v), r, q);
 }
+// Codes of 8 values.  No clamp: |v| <= amax, so the quotient is at most a step
+// above 127 (448), which rounds to it.  The even rounding to an integer is the
+// addition of 1.5 * 2^23, whose sum has the code in its lowest byte.
 template <bool F8>
 __device__ __forceinline__ u32x2 quantize8(const float* v, const RowScale& rs) {
   float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = quotient(v[e] * rs.xs, rs.ss, rs.r);
-    constexpr float kTop = F8 ? 448.0f : 127.0f;
-    f[e] = __builtin_amdgcn_fmed3f(F8 ? q : __builtin_rintf(q), -kTop, kTop);
-    if (F8) f[e] = __builtin_copysignf(f[e], v[e]);   // (the correction turns -0 into +0)
-  }
+  for (int e = 0; e < 8; ++e) f[e] = quotient(v[e], rs.ss, rs.r);
   if constexpr (F8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __builtin_copysignf(f[e], v[e]);   // (the correction turns -0 into +0)
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
     hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
     return u32x2{(uint32_t)lo, (uint32_t)hi};
   }
-  return u32x2{pack4((int)f[0], (int)f[1], (int)f[2], (int)f[3]), pack4((int)f[4], (int)f[5], (int)f[6], (int)f[7])};
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = __float_as_uint(f[4 * i + e] + 12582912.0f);
+    const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
+    w[i] = lo | hi;
+  }
+  return u32x2{w[0], w[1]};
 }
 
 struct Norm {
@@ -167,6 +176,10 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
     for (int e = 0; e < 4; ++e) {
       v[2 * e] = low(h[i][e]) * low(w[i][e]);
       v[2 * e + 1] = high(h[i][e]) * high(w[i][e]);
+    }
+    if (rs.xs != 1.0f) {   // a row of tiny numbers
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= rs.xs;
     }
     if (c < a.chunks) a.q[base + c] = zero ? u32x2{0, 0} : quantize8<F8>(v, rs);
   }

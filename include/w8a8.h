@@ -139,6 +139,10 @@ w8a8_status w8a8_dequantize_rows(const int8_t *q, const float *scale, int64_t R,
  *                                    * w_scale[n] ) + float(bias[n]) ) )
  * Each fp32 operation is rounded separately (no fused multiply-add), so y is
  * a deterministic function of the inputs.  bias may be NULL (treated as 0).
+ * Up to 32 tokens go to the kernel of w8a8_linear_dynamic (from codes, no
+ * workspace) where it is the faster one, with the same bits; a tile id given to
+ * w8a8_linear_tile is always that tile.  So do w8a8_linear_gelu and
+ * w8a8_gated_linear.
  * Abstract: int8 x int8 -> int32 on the matrix cores, per-token x per-channel
  * dequantization and bias folded into the epilogue, bf16 out.
  * Inputs xq [M,K], x_scale [M], wq [N,K], w_scale [N], bias [N]; output y [M,N].

@@ -12,14 +12,15 @@ from .block_ops import (gated_linear, gated_linear_backward, gated_linear_dynami
 from .adapter_ops import (add_rms_norm_backward, add_rms_norm_quantize, linear_adapters, linear_adapters_backward,
                           linear_adapters_dynamic)
 from .autograd import gated_linear_ste, linear_ste
-from .module import W8A8GatedMLP, W8A8Linear, W8A8QKV
+from .module import Tokens, W8A8AdaptedLinear, W8A8GatedMLP, W8A8Linear, W8A8QKV, W8A8RMSNorm
 from .ops import (dequantize_rows, gemm_f32_fp8, gemm_i32, linear, linear_fp8, linear_splitk,
                   mfma_ceiling, num_tiles, select_splitk, splitk_workspace_bytes,
                   quantize_act, quantize_act_fp8, quantize_weight, quantize_weight_fp8,
                   select_tile, tile_info)
 from .slowpath import dequant_bf16_linear
 
-__all__ = ["LIB_PATH", "MAX_K", "W8A8Error", "W8A8GatedMLP", "W8A8Linear", "W8A8QKV", "add_rms_norm_backward",
+__all__ = ["LIB_PATH", "MAX_K", "Tokens", "W8A8AdaptedLinear", "W8A8Error", "W8A8GatedMLP", "W8A8Linear", "W8A8QKV",
+           "W8A8RMSNorm", "add_rms_norm_backward",
            "add_rms_norm_quantize", "dequant_bf16_linear",
            "dequantize_rows", "gated_linear", "gated_linear_backward", "gated_linear_dynamic", "gated_linear_ste",
            "gemm_f32_fp8", "gemm_i32",

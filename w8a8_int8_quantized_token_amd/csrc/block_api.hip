@@ -7,8 +7,43 @@
 
 #include <algorithm>
 
+namespace w8a8 {
+
+// Where the few-token kernel is the faster one.  It walks 16 channels at a time,
+// one group to a compute unit up to 4096 channels, and a group takes 0.8 us (1.2
+// beyond 16 tokens) however short K is, so many channels of a short K go to the
+// tiled kernel; beyond 16 tokens short rows do too, as the codes are a launch of
+// their own there.  Cold weights, us (quantize + tiled / few tokens):
+//   1 and 16 tokens, K = 64: 8192 channels 5.8 / 5.7 and 6.4 / 6.3, 12288 6.0 / 6.3
+//   and 6.5 / 7.1, 65536 11.7 / 16.4 and 12.2 / 17.4; K = 256: 12288 6.7 / 6.5 and
+//   7.0 / 7.2, 16384 6.7 / 7.2 and 7.1 / 8.0; K = 512: 16384 8.2 / 8.2 and 8.7 / 9.0,
+//   32768 10.4 / 11.5 and 10.8 / 12.4; K = 768: 32768 11.9 / 11.8 and 12.4 / 13.1,
+//   65536 18.7 / 18.8 and 19.4 / 20.5;
+//   12 and 16 tokens whose codes come from memory, K = 4096: 32768 37 / 31 and 37 /
+//   32, 40960 73 / 36 and 73 / 37, 65536 57 / 53 and 57 / 56; K = 5120: 50000 52 / 53
+//   and 52 / 57, 65536 62 / 64 and 62 / 70; K = 8192: 65536 114 / 92 and 115 / 98
+//   (8 tokens, K = 5120: 65536 61 / 61);
+//   17 and 32 tokens, K = 64: 512 channels 5.8 / 6.2 and 5.6 / 6.2; K = 256: 2048
+//   6.8 / 6.7 and 6.9 / 6.8, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 8192 11.3 / 9.4
+//   and 11.5 / 9.6, 16384 11.8 / 11.9 and 12.0 / 12.4 (warm 9.3 / 10.9 and 9.5 / 11.3);
+//   K = 2048: 16384 17.9 / 15.7 and 18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K =
+//   8192: 16384 54 / 34 and 54 / 38, 32768 59 / 59 and 61 / 67;
+//   gated, where long rows go on paying: 12 and 16 tokens, K = 2048: 65536 channels
+//   54 / 47 and 54 / 49, K = 4096: 65536 119 / 95 and 118 / 97; 17 and 32 tokens, K =
+//   2048: 16384 22.1 / 21.7 and 22.8 / 22.7, 65536 55 / 59 and 55 / 62, K = 4096: 24576
+//   47 / 41 and 50 / 44, 65536 118 / 104 and 120 / 112, K = 8192: 32768 111 / 94 and 112 /
+//   105.
+bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds) {
+  if (M > 16) return K >= 256 && (N <= 8 * std::min<int64_t>(K, 2048) || (gated && K >= 4096));
+  if (!gated && M > 8 && !in_lds && N > 40960 && K < 8192) return false;
+  return K >= 768 || N <= 8192 + 16 * K;
+}
+
+}  // namespace w8a8
+
 namespace {
 
+using w8a8::few_tokens_pay;
 using w8a8::GateAct;
 
 constexpr int64_t kMaxRows = int64_t(1) << 26;
@@ -45,36 +80,6 @@ struct DynamicPlan {
   int64_t xq, xs, slices;
   int64_t bytes;
 };
-// Where the few-token kernel is the faster one.  It walks 16 channels at a time,
-// one group to a compute unit up to 4096 channels, and a group takes 0.8 us (1.2
-// beyond 16 tokens) however short K is, so many channels of a short K go to the
-// tiled kernel; beyond 16 tokens short rows do too, as the codes are a launch of
-// their own there.  Cold weights, us (quantize + tiled / few tokens):
-//   1 and 16 tokens, K = 64: 8192 channels 5.8 / 5.7 and 6.4 / 6.3, 12288 6.0 / 6.3
-//   and 6.5 / 7.1, 65536 11.7 / 16.4 and 12.2 / 17.4; K = 256: 12288 6.7 / 6.5 and
-//   7.0 / 7.2, 16384 6.7 / 7.2 and 7.1 / 8.0; K = 512: 16384 8.2 / 8.2 and 8.7 / 9.0,
-//   32768 10.4 / 11.5 and 10.8 / 12.4; K = 768: 32768 11.9 / 11.8 and 12.4 / 13.1,
-//   65536 18.7 / 18.8 and 19.4 / 20.5;
-//   12 and 16 tokens whose codes come from memory, K = 4096: 32768 37 / 31 and 37 /
-//   32, 40960 73 / 36 and 73 / 37, 65536 57 / 53 and 57 / 56; K = 5120: 50000 52 / 53
-//   and 52 / 57, 65536 62 / 64 and 62 / 70; K = 8192: 65536 114 / 92 and 115 / 98
-//   (8 tokens, K = 5120: 65536 61 / 61);
-//   17 and 32 tokens, K = 64: 512 channels 5.8 / 6.2 and 5.6 / 6.2; K = 256: 2048
-//   6.8 / 6.7 and 6.9 / 6.8, 6144 6.9 / 8.0 and 7.0 / 7.9; K = 1024: 8192 11.3 / 9.4
-//   and 11.5 / 9.6, 16384 11.8 / 11.9 and 12.0 / 12.4 (warm 9.3 / 10.9 and 9.5 / 11.3);
-//   K = 2048: 16384 17.9 / 15.7 and 18.0 / 16.6, 32768 22.3 / 23.8 and 22.9 / 26.1; K =
-//   8192: 16384 54 / 34 and 54 / 38, 32768 59 / 59 and 61 / 67;
-//   gated, where long rows go on paying: 12 and 16 tokens, K = 2048: 65536 channels
-//   54 / 47 and 54 / 49, K = 4096: 65536 119 / 95 and 118 / 97; 17 and 32 tokens, K =
-//   2048: 16384 22.1 / 21.7 and 22.8 / 22.7, 65536 55 / 59 and 55 / 62, K = 4096: 24576
-//   47 / 41 and 50 / 44, 65536 118 / 104 and 120 / 112, K = 8192: 32768 111 / 94 and 112 /
-//   105.
-bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds) {
-  if (M > 16) return K >= 256 && (N <= 8 * std::min<int64_t>(K, 2048) || (gated && K >= 4096));
-  if (!gated && M > 8 && !in_lds && N > 40960 && K < 8192) return false;
-  return K >= 768 || N <= 8192 + 16 * K;
-}
-
 // More tokens: K ranges where the linear is hardly ever faster whole, be the weight
 // cold or warm (us whole / in ranges, cold; warm): 256 x 2048 x 6144 38.9 / 28.5; 27.9 /
 // 27.7, 64 x 2048 x 4096 27.8 / 20.6; 19.1 / 18.9, but 512 x 2048 x 4096 27.8 / 29.3;
@@ -483,6 +488,8 @@ w8a8_status w8a8_gated_linear_tile(const int8_t* xq, const float* x_scale, const
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, 2) ||
       !aligned(bias, 2))
     return W8A8_ERR_ALIGN;
+  if (tile < 0 && M <= w8a8::kFewTokens && few_tokens_pay(M, N, K, true, false))
+    return launched(w8a8::launch_few_tokens(nullptr, xq, x_scale, wq, w_scale, bias, y, M, N, K, act, true, stream));
   return launched(w8a8::launch_gated(tile, static_cast<GateAct>(act), xq, x_scale, wq, w_scale, bias, y, M, N, K,
                                      stream));
 }

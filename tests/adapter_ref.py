@@ -45,7 +45,7 @@ def low(x, p, ids, scaling, transposed=False):
     """x [M,C] by each row's own p[id] [R,C] (or [C,R]), times its scaling, and
     the same of magnitudes; zeros for rows without one."""
     R = p.shape[2 if transposed else 1]
-    t, size = torch.zeros(x.shape[0], R, dtype=F64), torch.zeros(x.shape[0], R, dtype=F64)
+    t, size = x.new_zeros(x.shape[0], R), x.new_zeros(x.shape[0], R)
     for i in range(p.shape[0]):
         at = (ids == i).nonzero().flatten()
         q = p[i].to(F64) if transposed else p[i].to(F64).T
@@ -56,7 +56,7 @@ def low(x, p, ids, scaling, transposed=False):
 
 def up(t, p, ids, transposed=False):
     """t [M,R] by each row's own p[id] [C,R] (or [R,C])."""
-    y = torch.zeros(t.shape[0], p.shape[2 if transposed else 1], dtype=F64)
+    y = t.new_zeros(t.shape[0], p.shape[2 if transposed else 1])
     for i in range(p.shape[0]):
         at = (ids == i).nonzero().flatten()
         y[at] = t[at] @ (p[i].to(F64) if transposed else p[i].to(F64).T)
@@ -91,8 +91,8 @@ def grads(dy, xq, xs, wq, ws, a, b, ids, scaling):
     u_off = u.abs() * HALF + u_size * (2 * N * U)
     dx = dy @ w + up(u, a, ids, transposed=True)
     dx_off = (dy.abs() @ w.abs()) * (HALF + 2 * N * U) + up(u_off + u.abs() * 2 * R * U, a.abs(), ids, transposed=True)
-    da, da_off = torch.zeros(a.shape, dtype=F64), torch.zeros(a.shape, dtype=F64)
-    db, db_off = torch.zeros(b.shape, dtype=F64), torch.zeros(b.shape, dtype=F64)
+    da, da_off = x.new_zeros(a.shape), x.new_zeros(a.shape)
+    db, db_off = x.new_zeros(b.shape), x.new_zeros(b.shape)
     for i in range(a.shape[0]):
         at = (ids == i).nonzero().flatten()
         n = len(at)

@@ -49,7 +49,7 @@ def fp8_values(q):
 
 
 # one row and few, both layouts of many rows, every number of pieces to a lane, the longest
-NORMS = [(1, 16), (1, 4096), (3, 528), (5, 4112), (2, 8192), (2, 12304), (3, 16384), (2, 16400), (2, 32768), (1023, 512),
+NORMS = [(1, 16), (1, 4096), (3, 528), (5, 4112), (2, 8192), (2, 12288), (2, 12304), (3, 16384), (2, 16400), (2, 32768), (1023, 512),
          (1024, 512), (1025, 528), (1200, 1040), (1027, 2064), (1024, 3088), (1030, 4096), (1100, 16)]
 
 
@@ -416,3 +416,25 @@ def test_the_adapters_share_alone(w8, M, K, N, R, L, kind):
     dy = torch.randn(M, N, generator=torch.Generator().manual_seed(M)).to(BF)
     dx = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, ids, scaling), da=False, db=False)[0]
     ref.check(dx, *aref.grads(dy, xq, xs, wq, ws, a, b, ids, scaling)[0], "dx", rms_steps=2.0)
+
+
+# sizes whose products take each of the larger tiles, whole and in ranges
+LARGE = [(3000, 4096, 600, 16, 3, "mixed"), (4096, 2048, 264, 64, 2, "runs"), (2000, 2976, 1024, 40, 2, "runs"),
+         (777, 2976, 8192, 16, 4, "mixed"), (1500, 2064, 1024, 8, 3, "mixed"), (1500, 1024, 8192, 64, 5, "runs"),
+         (300, 4096, 600, 24, 2, "mixed"), (520, 1024, 8192, 16, 9, "mixed"), (2000, 1024, 256, 16, 1, "one"),
+         (520, 256, 4096, 128, 3, "mixed"), (1037, 512, 8192, 16, 2, "runs"), (8192, 512, 1536, 16, 20, "mixed")]
+
+
+@pytest.mark.parametrize("M,K,N,R,L,kind", LARGE)
+def test_larger_products(w8, M, K, N, R, L, kind):
+    for scale in (1.0, 0.0):      # (0: the adapters' share alone)
+        x, wq, ws, a, b, ids, scaling, bias = dev(*adapter_inputs(M, K, N, R, L, kind, M + K + N))
+        ws = ws * scale
+        xq, xs = w8.quantize_act(x)
+        y = w8.linear_adapters(xq, xs, wq, ws, a, b, ids, scaling, bias if scale else None)
+        want, slack = aref.linear(xq, xs, wq, ws, a, b, ids, scaling, bias if scale else None)
+        ref.check(y, want, slack.cpu(), "y", rms_steps=2.0)
+        dy = torch.randn(M, N, device=DEV).to(BF)
+        got = w8.linear_adapters_backward(dy, xq, xs, wq, ws, a, b, ids, scaling)
+        for g, (want, off), name in zip(got, aref.grads(dy, xq, xs, wq, ws, a, b, ids, scaling), ("dx", "da", "db")):
+            ref.check(g, want, off.cpu(), name, rms_steps=2.0)

@@ -421,12 +421,13 @@ w8a8_status w8a8_qk_norm_rope_backward(
  * quantization in one pass, in front of a linear.  For rows of K values:
  *   h = bf16(x + residual)                     (residual NULL: h = x),
  *   v = fl32(h * weight)                       (weight NULL: ones),
- *   s = fl32(max|v| / 127), xq = rne(fl32(v / s)) in [-127, 127]
- *   (fp8 non-zero: / 448 and e4m3 codes, as w8a8_quantize_act_fp8),
+ *   s = fl32(max|v| * fl32(1 / 127)), xq = rne(fl32(v / s)) in [-127, 127]
+ *   (fp8 non-zero: 1 / 448 and e4m3 codes, nearest, ties to even),
  *   x_scale = fl32(s / sqrt(mean(h^2) + eps)),
- * so xq * x_scale is the normed row quantized as w8a8_quantize_act would the
- * fp32 values: the norm's factor is common to a row, cancels in the codes and
- * goes into the scale.  Codes are exact functions of the inputs; mean(h^2) is
+ * so xq * x_scale is the normed row on the codes' grid: the norm's factor is
+ * common to a row, cancels in the codes and goes into the scale.  (s is a
+ * product, not w8a8_quantize_act's quotient max|v| / 127: it may be a step of
+ * fp32 away from that.)  Codes are exact functions of the inputs; mean(h^2) is
  * an fp32 sum.  A row whose s is zero (all zeros) has zero codes and scale.
  * h is written where it is not NULL; it may be x or residual and overlaps
  * nothing otherwise, and no other output overlaps anything.

@@ -18,7 +18,7 @@ def norm_codes(x, residual, w, eps, fp8):
     h = x if residual is None else (x.float() + residual.float()).to(BF)
     v = h.float() if w is None else h.float() * w.float()
     top = 448.0 if fp8 else 127.0
-    s = v.abs().amax(1) / torch.tensor(top)
+    s = v.abs().amax(1) * (torch.tensor(1.0) / torch.tensor(top))
     q = (v / torch.where(s > 0, s, torch.ones_like(s))[:, None]).clamp(-top, top)
     q = q.to(torch.float8_e4m3fn).float() if fp8 else torch.round(q)
     q = torch.where(s[:, None] > 0, q, torch.zeros_like(q))

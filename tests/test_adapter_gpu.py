@@ -93,6 +93,22 @@ def test_norm_rows_of_zeros_and_small_numbers(w8):
             assert torch.isfinite(s[[0, 1]]).all()
 
 
+def test_norm_rows_of_subnormal_scales(w8):
+    # a scale of one subnormal step stands for a quotient of 1.49 (1.34): codes are clamped, not wrapped
+    K = 768
+    x, w = torch.zeros(6, K).to(BF), torch.full((K,), 2.0 ** -49).to(BF)
+    x[0, 5], x[0, 6], x[0, 700] = 190 * 2.0 ** -100, -190 * 2.0 ** -100, 31 * 2.0 ** -100
+    x[1, 5], x[1, 6], x[1, 700] = 600 * 2.0 ** -100, -600 * 2.0 ** -100, 224 * 2.0 ** -100
+    x[2, 9] = 300 * 2.0 ** -100
+    x[3, 767] = -63 * 2.0 ** -100
+    for fp8 in (False, True):
+        q, s, _ = w8.add_rms_norm_quantize(*dev(x, None, w), eps=1e-6, fp8=fp8)
+        want_q, _, _ = aref.norm_codes(x, None, w, 1e-6, fp8)
+        assert torch.equal((fp8_values(q) if fp8 else q.float()).cpu(), want_q)
+        assert want_q.abs().max() == (448 if fp8 else 127)
+        assert torch.isfinite(s).all()
+
+
 def test_norm_into_its_inputs_and_as_the_linears_input(w8):
     M, K = 40, 768
     x, r, w = norm_inputs(M, K, 5)

@@ -1,7 +1,7 @@
 // The residual's addition, the root-mean-square norm of each row and its codes
 // in one pass, and the gradient.  For rows x, residual [K] and a weight w:
-//   h = bf16(x + residual),  v = fl32(h w),  s = fl32(max|v| / 127),
-//   q = rne(fl32(v / s))  (e4m3: / 448 and the e4m3 rounding),
+//   h = bf16(x + residual),  v = fl32(h w),  s = fl32(max|v| * fl32(1 / 127)),
+//   q = rne(fl32(v / s))  (e4m3: 1 / 448 and the e4m3 rounding),
 //   scale = fl32(s / rms),  rms = sqrt(mean(h^2) + eps).
 // The normed value v / rms is never formed: its factor 1 / rms is common to the
 // row, so it cancels in v / s and goes into the scale.  h w is exact (8 + 8
@@ -68,9 +68,20 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
   q = fmaf(fmaf(-q, s, v), r, q);
   return fmaf(fmaf(-q, s, v), r, q);
 }
-// Codes of 8 values.  No clamp: |v| <= amax, so the quotient is at most a step
-// above 127 (448), which rounds to it.  The even rounding to an integer is the
-// addition of 1.5 * 2^23, whose sum has the code in its lowest byte.
+// The scale of a row, and of tiny rows (s below 2^-100) v and s times 2^100,
+// which is exact and keeps 1 / s finite.
+template <bool F8>
+__device__ __forceinline__ RowScale scale_of(float amax) {
+  RowScale rs;
+  rs.s = amax * (F8 ? 1.0f / 448.0f : 1.0f / 127.0f);
+  rs.xs = rs.s < 0x1p-100f ? 0x1p100f : 1.0f;
+  rs.ss = rs.s * rs.xs;
+  rs.r = 1.0f / rs.ss;   // correctly rounded
+  return rs;
+}
+// Codes of 8 values.  No clamp: |v| <= amax, so the quotient is at most a few
+// steps above 127 (448), which rounds to it.  The even rounding to an integer is
+// the addition of 1.5 * 2^23, whose sum has the code in its lowest byte.
 template <bool F8>
 __device__ __forceinline__ u32x2 quantize8(const float* v, const RowScale& rs) {
   float f[8];
@@ -166,7 +177,7 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
       top = fmaxf(top, p[1]);
     }
   }
-  const RowScale rs = row_scale_of<F8>(top);
+  const RowScale rs = scale_of<F8>(top);
   const bool zero = rs.s == 0.0f;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
@@ -177,9 +188,10 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
       v[2 * e] = low(h[i][e]) * low(w[i][e]);
       v[2 * e + 1] = high(h[i][e]) * high(w[i][e]);
     }
-    if (rs.xs != 1.0f) {   // a row of tiny numbers
+    if (rs.xs != 1.0f) {   // a row of tiny numbers: a subnormal s may be half of what it should be
+      const float most = (F8 ? 448.0f : 127.0f) * rs.ss;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= rs.xs;
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_fmed3f(v[e] * rs.xs, -most, most);
     }
     if (c < a.chunks) a.q[base + c] = zero ? u32x2{0, 0} : quantize8<F8>(v, rs);
   }

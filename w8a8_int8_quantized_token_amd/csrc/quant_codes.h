@@ -93,8 +93,9 @@ struct RowScale {
 };
 
 template <bool F8>
-__device__ __forceinline__ RowScale row_scale_of(float amax) {
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
   RowScale rs;
+  float amax = __uint_as_float(amax_bits << 16);
   rs.s = amax / (F8 ? 448.0f : 127.0f);  // correctly rounded (IEEE division)
   rs.xs = 1.0f;
   rs.ss = rs.s;
@@ -104,11 +105,6 @@ __device__ __forceinline__ RowScale row_scale_of(float amax) {
   }
   rs.r = 1.0f / rs.ss;   // correctly rounded
   return rs;
-}
-// From the bits of a bf16 maximum.
-template <bool F8>
-__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
-  return row_scale_of<F8>(__uint_as_float(amax_bits << 16));
 }
 
 }  // namespace

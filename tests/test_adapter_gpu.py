@@ -340,6 +340,31 @@ def test_adapter_gradients(w8, M, K, N, R, L, kind):
             assert not got[1][i].any() and not got[2][i].any()
 
 
+@pytest.mark.parametrize("R", [8, 24, 40])
+@pytest.mark.parametrize("N", [1, 2, 5, 7, 8, 9, 15, 63, 129])
+def test_gradients_of_few_channels(w8, N, R):
+    for M in (31, 70, 600):
+        inputs = grad_inputs(M, 48, N, R, 2, "mixed", M + N + R)
+        got = w8.linear_adapters_backward(*dev(*inputs))
+        for g, (want, off), name in zip(got, aref.grads(*inputs), ("dx", "da", "db")):
+            ref.check(g, want, off, name, rms_steps=2.5)   # (fewer elements than elsewhere)
+
+
+@pytest.mark.parametrize("M,R", [(1, 8), (40, 8), (289, 16), (300, 32), (700, 64)])
+def test_infinities_in_an_outputs_gradient(w8, M, R):
+    """They stay in their channel and adapter, and are no NaN."""
+    N, K = 136, 64
+    dy, xq, xs, wq, ws, a, b, ids, scaling = grad_inputs(M, K, N, R, 2, "runs", M)
+    plain = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, ids, scaling))[2]
+    bad = dy.clone()
+    bad[M - 1, 3], bad[0, 77] = float("inf"), float("-inf")   # the last of a list that fills no step, and a first one
+    got = w8.linear_adapters_backward(*dev(bad, xq, xs, wq, ws, a, b, ids, scaling))[2].cpu()
+    hit = torch.zeros(2, N, dtype=torch.bool)
+    hit[ids[M - 1], 3] = hit[ids[0], 77] = True
+    assert torch.isinf(got[hit]).all()
+    assert same(got[~hit], plain.cpu()[~hit])
+
+
 def test_tokens_without_adapters_have_the_linears_gradient(w8):
     for M, N, K in [(40, 2776, 2592), (300, 520, 256), (700, 2048, 512)]:
         inputs = dev(*grad_inputs(M, K, N, 16, 3, "none", 3))

@@ -19,6 +19,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w8a8 {
 namespace {
@@ -47,7 +48,7 @@ constexpr int kListed = 8 * kWaves * kRows;
 template <int KR, int KB>
 struct Lds {
   f32x4 part[KR * KB <= 16 ? 4 : KR * KB <= 32 ? 2 : 1][KR * KB * kWave];
-  int32_t list[kListed];
+  __attribute__((aligned(16))) int32_t list[kListed];
 };
 
 // KR ranks to a lane (16 KR of a workgroup), KB columns.
@@ -62,7 +63,11 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
   const int rb = (int)(block % (unsigned)a.rank_blocks);
   block /= (unsigned)a.rank_blocks;
   const int slice = (int)(block % (unsigned)a.parts), id = (int)(block / (unsigned)a.parts);
-  const int64_t col = (int64_t)cb * 16 * KB + l16 * KB;
+  // Where columns end inside a lane's, it takes the last KB (its neighbour has
+  // some of them too, with the same sums): no load needs a check.
+  int64_t col = (int64_t)cb * 16 * KB + l16 * KB;
+  const bool narrow = a.C < KB;
+  if (!narrow) col = min(col, a.C - KB);
   const int rank = rb * 16 * KR + l16 * KR;
   // this part's rows of the adapter's list
   const int from = a.starts[id], to = a.starts[id + 1];
@@ -79,18 +84,18 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     uint32_t x[8][kWords];
     uint32_t v[8][(KR + 1) / 2];
   };
-  // Places past the `n` listed ones: the last row again, with zeros of v.
-  auto load = [&](int p0, int n, Step& s) __attribute__((always_inline)) {
+  // The step at place p0 of the listed rows (the list goes on with its last row).
+  auto load = [&](int p0, Step& s, auto whole) __attribute__((always_inline)) {
+    int32_t rows[8];
+    __builtin_memcpy(rows, __builtin_assume_aligned(lds.list + p0 + 8 * h, 16), 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int p = p0 + 8 * h + i;
-      const int64_t m = lds.list[min(p, n - 1)];
+      const int64_t m = rows[i];
       if constexpr (kCodes) {
-        const int8_t* row = static_cast<const int8_t*>(a.x) + m * a.C;
-        __builtin_memcpy(s.x[i], __builtin_assume_aligned(row + min(col, a.C - KB), KB), KB);
+        __builtin_memcpy(s.x[i], __builtin_assume_aligned(static_cast<const int8_t*>(a.x) + m * a.C + col, KB), KB);
       } else {
         const uint16_t* row = static_cast<const uint16_t*>(a.x) + m * a.C;
-        if (col + KB <= a.C) {
+        if constexpr (decltype(whole)::value) {
           __builtin_memcpy(s.x[i], row + col, 2 * KB);
         } else {
 #pragma unroll
@@ -102,14 +107,10 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
         }
       }
       const uint16_t* v = a.v + m * a.ldt + min(rank, a.ldt - KR);
-      if constexpr (KR == 1) {
-        s.v[i][0] = *v;
-      } else {
-        __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
-      }
-#pragma unroll
-      for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = p < n ? s.v[i][w] : 0;
+      if constexpr (KR == 1) s.v[i][0] = *v;
+      else __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
     }
+    __builtin_amdgcn_sched_barrier(0);   // (moved loads would be waited for sooner)
   };
   auto multiply = [&](const Step& s) __attribute__((always_inline)) {
     u32x4 fv[KR];
@@ -132,21 +133,46 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
         acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[r]),
                                                             __builtin_bit_cast(bf16x8, fx), acc[r][j], 0, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // This wavefront's steps of the n listed rows, the next step's loads on their
+  // way (past the end the last step's again).  The rows that make no whole step
+  // are one wavefront's.
+  auto run = [&](int n) __attribute__((always_inline)) {
+    const int whole = narrow ? 0 : n / kRows, count = (whole - wave + kWaves - 1) / kWaves;
+    auto at = [&](int i) { return (wave + min(i, count - 1) * kWaves) * kRows; };
+    if (count > 0) {
+      Step even, odd;
+      load(at(0), even, std::true_type{});
+      int i = 0;
+      for (; i + 2 <= count; i += 2) {
+        load(at(i + 1), odd, std::true_type{});
+        multiply(even);
+        load(at(i + 2), even, std::true_type{});
+        multiply(odd);
+      }
+      if (i < count) multiply(even);
+    }
+    for (int p = (whole + (wave - whole % kWaves + kWaves) % kWaves) * kRows; p < n; p += kWaves * kRows) {
+      Step s;
+      load(p, s, std::false_type{});
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = p + 8 * h + i < n;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) s.x[i][w] = in ? s.x[i][w] : 0;
+#pragma unroll
+        for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = in ? s.v[i][w] : 0;
+      }
+      multiply(s);
+    }
   };
   for (int base = first; base < last; base += kListed) {
     const int n = min(kListed, last - base);
     if (base > first) __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) lds.list[i] = a.list[base + i];
+    for (int i = threadIdx.x; i < (n + kRows - 1) / kRows * kRows; i += kThreads) lds.list[i] = a.list[base + min(i, n - 1)];
     __syncthreads();
-    if (wave * kRows < n) {
-      Step now, next;
-      load(wave * kRows, n, now);
-      for (int p = wave * kRows; p < n; p += kWaves * kRows) {
-        if (p + kWaves * kRows < n) load(p + kWaves * kRows, n, next);
-        multiply(now);
-        now = next;
-      }
-    }
+    run(n);
   }
   // the other wavefronts' sums onto the first's, in order
 #pragma unroll
@@ -200,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, 
 
 // Ranks of a lane, and columns: as many sums as registers allow.
 int ranks_of(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
-int columns_of(int R, bool codes) { return R <= 32 ? (codes ? 16 : 8) : codes ? 8 : 4; }
+int columns_of(int R, bool codes) { return R <= 32 && codes ? 16 : 8; }
 
 int64_t col_blocks_of(int64_t C, int R, bool codes) { return (C + 16 * columns_of(R, codes) - 1) / (16 * columns_of(R, codes)); }
 int64_t rank_blocks_of(int R) { return (R + 16 * ranks_of(R) - 1) / (16 * ranks_of(R)); }
@@ -274,7 +300,7 @@ hipError_t launch_adapter_grads(AdapterGrad ga, AdapterGrad gb, hipStream_t s) {
   switch (ranks_of(na ? ga.R : gb.R)) {
     case 1: hipLaunchKernelGGL((adapter_grad_kernel<1, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
     case 2: hipLaunchKernelGGL((adapter_grad_kernel<2, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
-    default: hipLaunchKernelGGL((adapter_grad_kernel<4, 8, 4>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    default: hipLaunchKernelGGL((adapter_grad_kernel<4, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
   }
   return hipGetLastError();
 }

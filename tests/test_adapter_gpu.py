@@ -302,6 +302,23 @@ def test_outputs_workspaces_and_addresses(w8):
     assert w8.linear_adapters_dynamic(e, wq, ws, a, b, ids[:0], scaling, bias).shape == (0, 96)
 
 
+@pytest.mark.parametrize("M,N,K", [(4, 96, 800), (20, 512, 1024), (40, 264, 6144), (300, 264, 256), (700, 1032, 512)])
+def test_scales_and_biases_at_any_address(w8, M, N, K):
+    x, wq, ws, a, b, ids, scaling, bias = dev(*adapter_inputs(M, K, N, 24, 3, "mixed", 33))
+    xq, xs = w8.quantize_act(x)
+    want = w8.linear_adapters(xq, xs, wq, ws, a, b, ids, scaling, bias)
+
+    def moved(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        room[1:] = t
+        return room[1:]
+    for name in ("xs", "ws", "bias", "ids", "scaling"):
+        args = dict(xs=xs, ws=ws, bias=bias, ids=ids, scaling=scaling)
+        args[name] = moved(args[name])
+        got = w8.linear_adapters(xq, args["xs"], wq, args["ws"], a, b, args["ids"], args["scaling"], args["bias"])
+        assert same(got, want), name
+
+
 # ---- adapters, gradients ----
 
 # every path of dx (few tokens from the codes, tiles whole and in ranges, dy copied or not), rows and blocks of the

@@ -816,7 +816,8 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
         return buffer_load16(rt, r0 + l_r < extra.ldt ? o : kOOB);
       };
       auto frags_b = [&](int a, int r0, v4i (&f)[kLowN]) {   // channels
-        const __amdgpu_buffer_rsrc_t rb = buffer_range(extra.b + a * extra.b_stride + (int64_t)at.n0 * extra.R, chans);
+        const __amdgpu_buffer_rsrc_t rb =
+            buffer_range(extra.b + max(a, 0) * extra.b_stride + (int64_t)at.n0 * extra.R, a < 0 ? 0 : chans);
 #pragma unroll
         for (int j = 0; j < kLowN; ++j) {
           int c;
@@ -871,51 +872,67 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           }
         }
       } else {
+        // passes: each adapter with each 16 ranks; the fragments of the next
+        // kPasses - 1 are on the way (past the last one zeros, from an empty range)
+        constexpr int kPasses = T::BM * T::BN < 256 * 256 ? 3 : 2;   // (as registers allow)
         all_left();
-        int a = next_adapter();
-        v4i ft[kLowM], fn[kLowN], ahead[kLowN];
-        auto load_t = [&](int r0) {
+        int a = next_adapter(), r0 = 0, pass_a[kPasses], pass_r[kPasses], r_t = 0;
+        v4i ft[kLowM], fb[kPasses][kLowN];
+        auto load_t = [&](int r) __attribute__((always_inline)) {
 #pragma unroll
-          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r0);
+          for (int i = 0; i < kLowM; ++i) ft[i] = frag_t(i, r);
         };
-        if (a >= 0) {
-          load_t(0);
-          frags_b(a, 0, ahead);
-        }
-        before();
-        for (int r0 = 0; a >= 0;) {
-#pragma unroll
-          for (int j = 0; j < kLowN; ++j) fn[j] = ahead[j];
-          const int now = a, r_now = r0;
+        auto request = [&](int p) __attribute__((always_inline)) {
+          pass_a[p] = a;
+          pass_r[p] = r0;
+          frags_b(a, r0, fb[p]);
+          if (a < 0) return;
           a = next_adapter();
           if (a < 0 && r0 + kLowStep < extra.R) {   // the next ranks, from the first adapter on
             r0 += kLowStep;
             all_left();
             a = next_adapter();
           }
-          if (a >= 0) frags_b(a, r0, ahead);
+        };
+        load_t(0);
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) request(p);
+        before();
+        auto add = [&](int p) __attribute__((always_inline)) {
           uint32_t most = 0;   // largest magnitudes of both halves of the words
 #pragma unroll
           for (int j = 0; j < kLowN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fn[j][e] & 0x7fff7fffu);
+            for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fb[p][j][e] & 0x7fff7fffu);
           const bool drop = __builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0;
 #pragma unroll
           for (int j = 0; j < kLowN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fn[j][e] = drop ? 0 : fn[j][e];
+            for (int e = 0; e < 4; ++e) fb[p][j][e] = drop ? 0 : fb[p][j][e];
 #pragma unroll
           for (int i = 0; i < kLowM; ++i) {
             v4i t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = id[i] == now ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
+            for (int e = 0; e < 4; ++e) t[e] = id[i] == pass_a[p] ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
 #pragma unroll
             for (int j = 0; j < kLowN; ++j)
               acc[i][j] = __builtin_bit_cast(
-                  v16i, __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fn[j]), __builtin_bit_cast(bf16x8, t),
+                  v16i, __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fb[p][j]), __builtin_bit_cast(bf16x8, t),
                                                                 __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
           }
-          if (a >= 0 && r0 != r_now) load_t(r0);
+        };
+        while (pass_a[0] >= 0) {
+#pragma unroll
+          for (int p = 0; p < kPasses; ++p) {
+            if (pass_a[p] < 0) break;
+            if (pass_r[p] != r_t) {
+              r_t = pass_r[p];
+              load_t(r_t);
+              __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): waited for here, not in every pass
+            }
+            add(p);
+            request(p);
+          }
         }
       }
     }

@@ -12,9 +12,8 @@
 // Few rows: a workgroup takes one row and 16 ranks, a wavefront two of them,
 // with the lanes along k (M K R fused multiply-adds, and P read once for each
 // row, from L2 where rows share an adapter).  More rows: a workgroup takes 32
-// of them on the bf16 matrix cores (codes are exact in bf16), its wavefronts
-// a range of k each, and goes through the adapters that its rows
-// have one after another; a row takes the sums of its own adapter alone.
+// rows of one adapter at a time on the bf16 matrix cores (codes are exact in
+// bf16), its wavefronts a range of k each.
 #include "adapter_sum.h"
 #include "kernels.h"
 #include "quant_codes.h"
@@ -149,44 +148,61 @@ __global__ __launch_bounds__(kThreads) void down_row_kernel(Down a) {
   down_row<R>(a);
 }
 
-// ---- 32 rows per workgroup ----
+// ---- 32 rows of one adapter at a time ----
 
-constexpr int kBlockRows = 32;
-// LDS of a workgroup: the wavefronts' sums.
+constexpr int kTileRows = 32, kChunk = 256, kIds = kChunk / kWave;
+// A workgroup's LDS: the wavefronts' sums, and each wavefront's list of rows.
 template <int kTiles>
-using Sums = f32x4[kWaves][kTiles][2][kWave];
+struct Lds {
+  f32x4 part[kWaves][kTiles][2][kWave];
+  uint16_t list[kWaves][kChunk];
+};
 
+// The rows of a chunk are sorted by their adapters, each adapter's rows cut into
+// tiles of 32, and the tiles dealt to `slots` workgroups: so the work is that of
+// the tiles, in whatever order the ids come.  (Blocks of 32 rows in the rows'
+// own order, each going through all the adapters that it has: as fast for long
+// runs, but 38 us and not 15 for 2048 rows of 4096 codes with sixteen adapters
+// mixed, 129 and not 25 for 8192.)
+//
 // A step is 64 or 128 values of k, a quarter of them in a row in each lane
 // (both operands are dealt alike), 16 bytes for an MFMA.  Each wavefront has a
-// range of k of its own, and blocks start at different places of it: rows are
+// range of k of its own, and tiles start at different places of it: rows are
 // whole pages or parts of them apart, and wavefronts that all read the same
 // place of every row keep a few memory channels busy (8192 rows of 4096 codes: 26
 // us).  kDepth steps of loads are in flight.
-// The adapters of a workgroup's rows are shared out over `slots` workgroups.
 template <Rows R, int kTiles>
-__device__ __forceinline__ void down_block(const Down& a, int64_t block, int rank_block, int slot, int slots,
-                                           Sums<kTiles>& part) {
+__device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int rank_block, int slot, int slots,
+                                           Lds<kTiles>& lds) {
   constexpr bool kCodes = R == Rows::kCodes;
   constexpr int kMma = kCodes && kTiles < 4 ? 4 : 2;     // MFMAs of a step and tile
   constexpr int kLane = kMma * 8, kStepK = 4 * kLane;    // values of a lane and of a step
   constexpr int kDepth = kTiles == 1 ? 3 : 2;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int l16 = lane % 16, h = lane / 16;
-  const int64_t m0 = block * kBlockRows;
+  const int64_t m0 = chunk * kChunk;
   const int first = rank_block * kTiles * 16;   // rank
-  int id[2];
-  int64_t row[2];
-  bool mine[2];   // this workgroup writes the row
+  int id[kIds];
+  uint64_t left[kIds];   // lanes whose rows are still to come
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = m0 + i * 16 + l16;
-    row[i] = min(m, a.M - 1);
-    id[i] = m < a.M ? adapter_of(a, m) : -1;
-    mine[i] = id[i] < 0 && slot == 0;
+  for (int j = 0; j < kIds; ++j) {
+    const int64_t m = m0 + j * kWave + lane;
+    id[j] = m < a.M ? adapter_of(a, m) : -1;
+    left[j] = __builtin_amdgcn_ballot_w64(id[j] >= 0);
   }
-  f32x4 res[kTiles][2];
+  auto zeros = [&](int64_t m) __attribute__((always_inline)) {
+    for (int r = first; r < min(first + 16 * kTiles, a.ldt); r += 8) {
+      *reinterpret_cast<u32x4*>(a.t + m * a.ldt + r) = kZeros;
+      if (a.t2 != nullptr) *reinterpret_cast<u32x4*>(a.t2 + m * a.ldt + r) = kZeros;
+    }
+  };
+  if (slot == 0) {
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) res[t][0] = res[t][1] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < kIds; ++j) {
+      const int64_t m = m0 + j * kWave + lane;
+      if (j == wave && m < a.M && id[j] < 0) zeros(m);
+    }
+  }
 
   constexpr int kWords = kCodes ? kMma / 2 : kMma;   // 16-byte words of a lane's values of x
   struct Step {
@@ -194,7 +210,8 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t block, int ran
   };
   const int steps = (a.K + kStepK - 1) / kStepK, per = (steps + kWaves - 1) / kWaves;
   const int from = wave * per, here = max(min(per, steps - from), 0);   // this wavefront's steps
-  const int turn = here * (int)(block % 4) / 4;
+  int64_t row[2];
+  int turn = 0;
   // Step n of the wavefront's; past its end zeros.
   auto load = [&](const uint16_t* p, int n, Step& v) __attribute__((always_inline)) {
     int s = n + turn;
@@ -222,106 +239,117 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t block, int ran
       }
     }
   };
-  uint64_t left[2] = {__builtin_amdgcn_ballot_w64(id[0] >= 0), __builtin_amdgcn_ballot_w64(id[1] >= 0)};
-  for (int pass = 0; (left[0] | left[1]) != 0; ++pass) {
-    const int ad = left[0] != 0 ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
-                                : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
+  // (the control flow is the same in all wavefronts)
+  for (int tile = 0;;) {
+    int ad = -1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) left[i] &= ~__builtin_amdgcn_ballot_w64(id[i] == ad);
-    if (pass % slots != slot) continue;
-    const uint16_t* p = a.p + ad * a.p_stride;
-    f32x4 acc[kTiles][2];
+    for (int j = kIds - 1; j >= 0; --j)
+      if (left[j] != 0) ad = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
+    if (ad < 0) break;
+    uint64_t with[kIds];
+    int rows = 0;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
-    auto multiply = [&](const Step& v) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        u32x4 x[kMma];
-        if constexpr (kCodes) {
-#pragma unroll
-          for (int g = 0; g < kMma; ++g) {
-            float f[8];
-            codes4(v.x[i][g / 2][2 * (g % 2)], f);
-            codes4(v.x[i][g / 2][2 * (g % 2) + 1], f + 4);
-            x[g] = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
-          }
-        } else {
-#pragma unroll
-          for (int g = 0; g < kMma; ++g) x[g] = v.x[i][g];
-        }
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int g = 0; g < kMma; ++g)
-            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.p[t][g]),
-                                                                __builtin_bit_cast(bf16x8, x[g]), acc[t][i], 0, 0, 0);
-      }
-    };
-    Step ring[kDepth];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(p, d, ring[d]);
-    for (int n = 0; n < here; n += kDepth) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        multiply(ring[d]);
-        load(p, n + kDepth + d, ring[d]);
-      }
+    for (int j = 0; j < kIds; ++j) {
+      with[j] = __builtin_amdgcn_ballot_w64(id[j] == ad);
+      left[j] &= ~with[j];
+      rows += __popcll(with[j]);
     }
+    const int tiles = (rows + kTileRows - 1) / kTileRows;
+    int mine = slot - tile;   // the first of the adapter's tiles that is this workgroup's
+    while (mine < 0) mine += slots;
+    tile += tiles;
+    if (mine >= tiles) continue;
+    int before = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mine[i] |= id[i] == ad;
+    for (int j = 0; j < kIds; ++j) {
+      if (id[j] == ad)
+        lds.list[wave][before + __popcll(with[j] & ((uint64_t(1) << lane) - 1))] = (uint16_t)(j * kWave + lane);
+      before += __popcll(with[j]);
+    }
+    const uint16_t* p = a.p + ad * a.p_stride;
+    for (; mine < tiles; mine += slots) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) row[i] = m0 + lds.list[wave][min(mine * kTileRows + i * 16 + l16, rows - 1)];
+      // what the sums are multiplied by: on the way from here on
+      const int t = wave / 2, i = wave % 2, r = first + t * 16 + 4 * h;
+      const bool writes = t < kTiles && r < a.ldt && mine * kTileRows + i * 16 + l16 < rows;
+      const int64_t m = i ? row[1] : row[0];
+      const float f = a.scaling[ad], scale = kCodes ? a.scale[m] : 1.0f, s2 = a.t2 != nullptr ? a.scale2[m] : 0.0f;
+      turn = here * (int)((chunk * (kChunk / kTileRows) + mine) % 4) / 4;
+      f32x4 acc[kTiles][2];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
+      auto multiply = [&](const Step& v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          u32x4 x[kMma];
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int g = 0; g < kMma; ++g) {
+              float f[8];
+              codes4(v.x[i][g / 2][2 * (g % 2)], f);
+              codes4(v.x[i][g / 2][2 * (g % 2) + 1], f + 4);
+              x[g] = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < kMma; ++g) x[g] = v.x[i][g];
+          }
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int g = 0; g < kMma; ++g)
+              acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.p[t][g]),
+                                                                  __builtin_bit_cast(bf16x8, x[g]), acc[t][i], 0, 0, 0);
+        }
+      };
+      Step ring[kDepth];
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) load(p, d, ring[d]);
+      for (int n = 0; n < here; n += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+          multiply(ring[d]);
+          load(p, n + kDepth + d, ring[d]);
+        }
+      }
+      __syncthreads();   // the sums of the tile before are read
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) res[t][i][e] = id[i] == ad ? acc[t][i][e] : res[t][i][e];
+        for (int i = 0; i < 2; ++i) lds.part[wave][t][i][lane] = acc[t][i];
+      __syncthreads();
+      // a wavefront for each 16 ranks by 16 rows; lane: row l16, ranks 4h .. 4h + 3
+      if (!writes) continue;
+      f32x4 sum = lds.part[0][t][i][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += lds.part[w][t][i][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = r < a.R ? sum[e] * scale * f : 0.0f;
+      *reinterpret_cast<u32x2*>(a.t + m * a.ldt + r) = u32x2{pack2(sum[0], sum[1]), pack2(sum[2], sum[3])};
+      if (a.t2 != nullptr) {
+        const auto v = [&](int e) { return r < a.R ? sum[e] * s2 : 0.0f; };
+        *reinterpret_cast<u32x2*>(a.t2 + m * a.ldt + r) = u32x2{pack2(v(0), v(1)), pack2(v(2), v(3))};
+      }
     }
-  }
-  // (the same in all wavefronts)
-  if (__builtin_amdgcn_ballot_w64(mine[0] || mine[1]) == 0) return;
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[wave][t][i][lane] = res[t][i];
-  __syncthreads();
-  // a wavefront for each 16 ranks by 16 rows; lane: row l16, ranks 4h .. 4h + 3
-  if (wave >= 2 * kTiles) return;
-  const int t = wave / 2, i = wave % 2;
-  const int64_t m = m0 + i * 16 + l16;
-  const int r = first + t * 16 + 4 * h;
-  if (m >= a.M || r >= a.ldt || !(i ? mine[1] : mine[0])) return;
-  f32x4 sum = part[0][t][i][lane];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) sum += part[w][t][i][lane];
-  const int ad = i ? id[1] : id[0];
-  float f = 0.0f, scale = 1.0f;
-  if (ad >= 0) f = a.scaling[ad];
-  if constexpr (R == Rows::kCodes) scale = a.scale[m];
-  const bool on = ad >= 0 && r < a.R;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sum[e] = on ? sum[e] * scale * f : 0.0f;
-  *reinterpret_cast<u32x2*>(a.t + m * a.ldt + r) = u32x2{pack2(sum[0], sum[1]), pack2(sum[2], sum[3])};
-  if (a.t2 != nullptr) {
-    const float s2 = on ? a.scale2[m] : 0.0f;
-    *reinterpret_cast<u32x2*>(a.t2 + m * a.ldt + r) =
-        u32x2{pack2(sum[0] * s2, sum[1] * s2), pack2(sum[2] * s2, sum[3] * s2)};
   }
 }
 
-// grid (blocks of rows, blocks of ranks, slots); two products share a launch,
+// grid (chunks of rows, blocks of ranks, slots); two products share a launch,
 // of codes and of values (b, the last grid.z = slots ones).
 template <int kTiles>
 __global__ __launch_bounds__(kThreads) void down_block_kernel(Down a) {
-  __shared__ Sums<kTiles> part;
-  down_block<Rows::kCodes, kTiles>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, part);
+  __shared__ Lds<kTiles> lds;
+  down_block<Rows::kCodes, kTiles>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, lds);
 }
 template <int kTiles>
 __global__ __launch_bounds__(kThreads) void down_block_kernel2(Down codes, Down values, int slots) {
-  __shared__ Sums<kTiles> part;
+  __shared__ Lds<kTiles> lds;
   const int z = blockIdx.z;
   if (codes.M > 0 && z >= slots)   // (the longer rows first)
-    down_block<Rows::kCodes, kTiles>(codes, blockIdx.x, blockIdx.y, z - slots, slots, part);
+    down_block<Rows::kCodes, kTiles>(codes, blockIdx.x, blockIdx.y, z - slots, slots, lds);
   else
-    down_block<Rows::kValues, kTiles>(values, blockIdx.x, blockIdx.y, z, slots, part);
+    down_block<Rows::kValues, kTiles>(values, blockIdx.x, blockIdx.y, z, slots, lds);
 }
 template <int kUnused>
 __global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down values) {
@@ -329,14 +357,26 @@ __global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down va
   else down_row<Rows::kCodes>(codes);
 }
 
-// Workgroups that share out the adapters of a block of rows, where blocks leave
-// compute units idle (one with nothing to do still takes 2 us).
-int slots_of(const Down& a) {
-  const int64_t blocks = (a.M + kBlockRows - 1) / kBlockRows * ((a.R + 63) / 64);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.count, 256 / blocks, 16}));
+// Workgroups to a chunk of rows: one for each tile of long runs; more, for the
+// partial tiles of mixed ids, where compute units are idle otherwise (one with
+// nothing to do still takes 2 us).
+int slots_of(const Down& a, int tiles) {
+  const int64_t blocks = (a.M + kChunk - 1) / kChunk * ((a.R + 16 * tiles - 1) / (16 * tiles));
+  constexpr int kFull = kChunk / kTileRows;
+  return (int)std::max<int64_t>(kFull, std::min<int64_t>((int64_t)kFull + a.count, 256 / blocks));
 }
 dim3 block_grid(const Down& a, int tiles, int z) {
-  return dim3((unsigned)((a.M + kBlockRows - 1) / kBlockRows), (unsigned)((a.R + 16 * tiles - 1) / (16 * tiles)), (unsigned)z);
+  return dim3((unsigned)((a.M + kChunk - 1) / kChunk), (unsigned)((a.R + 16 * tiles - 1) / (16 * tiles)), (unsigned)z);
+}
+// Tiles of 16 ranks to a workgroup: as few as leave no compute unit more than
+// one workgroup, since a row of x is read from L2 faster than many ranks are by
+// one workgroup (codes, 2048 rows of 4096, 64 ranks: four tiles 21.8 us, one
+// 12.5; but 4096 rows of both products, one tile 33.7, four 26.7).
+int tiles_of(const Down& a, int products) {
+  const int64_t rows = products * ((a.M + kTileRows - 1) / kTileRows);
+  int tiles = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
+  while (tiles > 1 && rows * ((a.R + 8 * tiles - 1) / (8 * tiles)) <= 256) tiles /= 2;
+  return tiles;
 }
 
 }  // namespace
@@ -352,10 +392,11 @@ hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
   } else if (a.M <= kDownRows) {
     hipLaunchKernelGGL(down_row_kernel<Rows::kCodes>, rows, threads, 0, s, a);
   } else {
-    const int slots = slots_of(a);
-    if (a.R <= 16) hipLaunchKernelGGL(down_block_kernel<1>, block_grid(a, 1, slots), threads, 0, s, a);
-    else if (a.R <= 32) hipLaunchKernelGGL(down_block_kernel<2>, block_grid(a, 2, slots), threads, 0, s, a);
-    else hipLaunchKernelGGL(down_block_kernel<4>, block_grid(a, 4, slots), threads, 0, s, a);
+    const int tiles = tiles_of(a, 1);
+    const dim3 grid = block_grid(a, tiles, slots_of(a, tiles));
+    if (tiles == 1) hipLaunchKernelGGL(down_block_kernel<1>, grid, threads, 0, s, a);
+    else if (tiles == 2) hipLaunchKernelGGL(down_block_kernel<2>, grid, threads, 0, s, a);
+    else hipLaunchKernelGGL(down_block_kernel<4>, grid, threads, 0, s, a);
   }
   return hipGetLastError();
 }
@@ -374,10 +415,11 @@ hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s
     hipLaunchKernelGGL(down_row_kernel2<0>, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
     return hipGetLastError();
   }
-  const int slots = slots_of(v);
-  if (v.R <= 16) hipLaunchKernelGGL(down_block_kernel2<1>, block_grid(v, 1, both * slots), threads, 0, s, c, v, slots);
-  else if (v.R <= 32) hipLaunchKernelGGL(down_block_kernel2<2>, block_grid(v, 2, both * slots), threads, 0, s, c, v, slots);
-  else hipLaunchKernelGGL(down_block_kernel2<4>, block_grid(v, 4, both * slots), threads, 0, s, c, v, slots);
+  const int tiles = tiles_of(v, both), slots = slots_of(v, tiles);
+  const dim3 grid = block_grid(v, tiles, both * slots);
+  if (tiles == 1) hipLaunchKernelGGL(down_block_kernel2<1>, grid, threads, 0, s, c, v, slots);
+  else if (tiles == 2) hipLaunchKernelGGL(down_block_kernel2<2>, grid, threads, 0, s, c, v, slots);
+  else hipLaunchKernelGGL(down_block_kernel2<4>, grid, threads, 0, s, c, v, slots);
   return hipGetLastError();
 }
 

@@ -8,11 +8,17 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
                            const uint16_t* bias, const Low& low, uint16_t* y, int64_t M, int64_t N, int64_t K,
                            hipStream_t stream) {
   const LowArgs args{low.t, low.b, low.ids, N * low.R, (int)low.ldt, (int)low.R, (int)low.count};
-  if (tile < 0) tile = choose_tile(M, N, K);
+  if (tile < 0) {
+    tile = choose_tile(M, N, K);
+    // the 128x256 tiles where the linear takes 256x128 ones (2048 x 4096 x 4096,
+    // rank 16: 51.3 us and not 55.2, rank 64: 63 and not 70)
+    if (kPlans[tile].main == k256x128) --tile;
+  }
   // the plans of the 256x256 split ring are those of its whole-stage form here
   if (tile < kNumPlans && kPlans[tile].main == kSplit256) tile += 2;
   static_assert(kPlans[2].main == kWhole256 && kPlans[3].main == kWhole256 && kPlans[2].tail == kPlans[0].tail &&
-                    kPlans[3].tail == kPlans[1].tail, "the order of the plans");
+                    kPlans[3].tail == kPlans[1].tail && kPlans[5].main == kTail128x256 && kPlans[6].main == k256x128,
+                "the order of the plans");
   return launch_plan<OpI8, Epilogue::kBf16ScaleBiasLow>(tile, {xq, wq, sx, sw, bias, y, args}, M, N, K, stream);
 }
 

@@ -439,8 +439,8 @@ w8a8_status w8a8_qk_norm_rope_backward(
  *   needs the workspace; zeros without rows).
  * dx may be dn, dh or h and overlaps nothing otherwise.  Arithmetic is fp32, each bf16
  * output rounded once.  Of a row of zeros with eps = 0, r is taken as 0.
- * Contract: 16 <= K <= 32768, K % 16 == 0; M times 64 (K <= 4096), 256 (K <=
- * 16384) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; finite inputs whose
+ * Contract: 16 <= K <= 32768, K % 16 == 0; M times 64 (K <= 1024), 256 (K <
+ * 8192) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; finite inputs whose
  * squares' sum and products with the weight are finite in fp32; all bf16
  * pointers and the codes 16-byte aligned, scales and dweight 4-byte aligned.
  */

@@ -50,7 +50,8 @@ def fp8_values(q):
 
 # one row and few, both layouts of many rows, every number of pieces to a lane, the longest
 NORMS = [(1, 16), (1, 4096), (3, 528), (5, 4112), (2, 8192), (2, 12288), (2, 12304), (3, 16384), (2, 16400), (2, 32768), (1023, 512),
-         (1024, 512), (1025, 528), (1200, 1040), (1027, 2064), (1024, 3088), (1030, 4096), (1100, 16)]
+         (1024, 512), (1025, 528), (1200, 1040), (1027, 2064), (1024, 3088), (1030, 4096), (1100, 16),
+         (4097, 16), (4096, 512), (4099, 528), (4098, 1024), (4096, 1040), (512, 4096), (513, 4112), (520, 6160), (40, 8176)]
 
 
 @pytest.mark.parametrize("M,K", NORMS)
@@ -129,7 +130,7 @@ def test_norm_into_its_inputs_and_as_the_linears_input(w8):
 
 
 NORM_GRADS = [(1, 16), (2, 2048), (7, 2064), (33, 4096), (5, 4112), (3, 8192), (4, 8208), (2, 16384), (2, 16400),
-              (1, 32768), (1500, 80), (2000, 1168)]
+              (1, 32768), (1500, 80), (2000, 1168), (4100, 16), (4096, 1024), (600, 4080), (600, 4096)]
 
 
 @pytest.mark.parametrize("M,K", NORM_GRADS)
@@ -237,7 +238,9 @@ SHAPES = [(1, 16, 1, 8, 1, "one"), (1, 2048, 2048, 16, 4, "mixed"), (3, 784, 77,
           (50, 6144, 264, 8, 2, "runs"), (100, 272, 130, 16, 1, "one"), (256, 512, 300, 72, 4, "runs"),
           (257, 512, 300, 72, 4, "runs"), (300, 1168, 4603, 40, 9, "mixed"), (777, 1168, 603, 128, 70, "mixed"),
           (1000, 256, 1024, 32, 3, "runs"), (2048, 128, 2048, 16, 5, "mixed"), (513, 4096, 513, 48, 2, "none"),
-          (260, 20000, 64, 8, 3, "mixed")]
+          (260, 20000, 64, 8, 3, "mixed"), (1290, 20000, 64, 8, 3, "mixed"), (1280, 512, 264, 16, 3, "mixed"),
+          (160, 512, 300, 120, 4, "mixed"), (161, 512, 300, 120, 4, "mixed"), (4, 1024, 520, 8, 3, "mixed"),
+          (1, 1024, 8200, 16, 2, "one"), (2, 1024, 4100, 16, 2, "mixed"), (1, 2048, 300, 32, 3, "one")]
 
 
 @pytest.mark.parametrize("M,K,N,R,L,kind", SHAPES)
@@ -327,7 +330,8 @@ GRADS = [(1, 16, 1, 8, 1, "one"), (3, 784, 77, 24, 5, "mixed"), (64, 256, 512, 1
          (64, 2592, 2776, 40, 9, "mixed"), (100, 1024, 5000, 8, 2, "runs"), (257, 512, 300, 72, 4, "runs"),
          (300, 1168, 1203, 40, 9, "mixed"), (777, 528, 603, 128, 70, "mixed"), (1037, 272, 5466, 8, 3, "mixed"),
          (2048, 1024, 1024, 16, 1, "one"), (2100, 512, 2048, 64, 4, "runs"), (3000, 2064, 264, 32, 2, "mixed"),
-         (500, 64, 64, 16, 5, "none"), (1300, 1040, 1000, 24, 2, "runs"), (4500, 96, 130, 48, 3, "mixed")]
+         (500, 64, 64, 16, 5, "none"), (1300, 1040, 1000, 24, 2, "runs"), (4500, 96, 130, 48, 3, "mixed"),
+         (1280, 256, 520, 16, 3, "mixed"), (1290, 304, 523, 8, 300, "mixed")]
 
 
 def grad_inputs(M, K, N, R, L, kind, seed):

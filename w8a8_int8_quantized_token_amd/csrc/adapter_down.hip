@@ -14,6 +14,14 @@
 // row, from L2 where rows share an adapter).  More rows: a workgroup takes 32
 // rows of one adapter at a time on the bf16 matrix cores (codes are exact in
 // bf16), its wavefronts a range of k each.
+//
+// Bound by reading X where ranks are few: 8192 rows of 4096 codes, rank 16, 13 us
+// warm and 23 from cold memory (a copy of these bytes: 21); 16 rows, quantized
+// on the way, 4.6.  Where they are many, by P, which every 32 rows read from
+// L2 anew: 8192 rows, rank 64, codes of 4096 and values of 8192: 74 us warm, 570
+// MB at 7.7 TB/s, which is what the lines that a compute unit's L1 can have
+// outstanding allow (with all rows of P the same one: 36).  Tiles of 64 rows
+// halve P's share but leave half the compute units idle at that size (72).
 #include "adapter_sum.h"
 #include "kernels.h"
 #include "quant_codes.h"
@@ -379,17 +387,25 @@ int tiles_of(const Down& a, int products) {
   return tiles;
 }
 
+// Few rows: a workgroup for each row and 16 ranks.  Warm codes, us by rows / in
+// tiles, one adapter: K = 4096, rank 16: 256 rows 5.0 / 11.9, 1024 9.0 / 11.9, 1280
+// 10.4 / 12.0, 1536 11.9 / 11.8; rank 32: 512 9.1 / 11.9, 768 11.8 / 11.9, 1024 14.9 /
+// 11.9; rank 128: 128 8.7 / 11.6, 192 11.6 / 11.7, 256 14.5 / 11.8; K = 1168, rank
+// 16: 1024 5.4 / 6.7, 1280 6.2 / 6.6, 1536 6.9 / 6.7.  With sixteen adapters mixed,
+// rank 16: 1536 12.4 / 15.3, 2048 15.2 / 15.4; rank 128: 128 15.2 / 14.8.
+bool by_rows(int64_t M, int64_t R) { return M * ((R + 15) / 16 * 16) <= 20480; }
+
 }  // namespace
 
-bool down_quantizes(int64_t M, int64_t K) { return M <= kDownRows && K <= kMaxFused; }
+bool down_quantizes(int64_t M, int64_t K, int64_t R) { return by_rows(M, R) && K <= kMaxFused; }
 
 hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
   if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0) return hipErrorInvalidValue;
   const dim3 threads(kThreads), rows((unsigned)a.M, (unsigned)(a.ldt / kRanks));
   if (quantize) {
-    if (!down_quantizes(a.M, a.K)) return hipErrorInvalidValue;
+    if (!down_quantizes(a.M, a.K, a.R)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(down_row_kernel<Rows::kQuantize>, rows, threads, 0, s, a);
-  } else if (a.M <= kDownRows) {
+  } else if (by_rows(a.M, a.R)) {
     hipLaunchKernelGGL(down_row_kernel<Rows::kCodes>, rows, threads, 0, s, a);
   } else {
     const int tiles = tiles_of(a, 1);
@@ -411,7 +427,7 @@ hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s
     return hipErrorInvalidValue;
   const dim3 threads(kThreads);
   const int both = c.M > 0 ? 2 : 1;
-  if (v.M <= kDownRows) {
+  if (by_rows(v.M, v.R)) {
     hipLaunchKernelGGL(down_row_kernel2<0>, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
     return hipGetLastError();
   }

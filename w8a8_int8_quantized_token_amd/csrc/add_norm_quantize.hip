@@ -15,7 +15,12 @@
 //
 // Bound by memory: 7 bytes per value forward (3 without a residual), 8 backward
 // (6 without dh).  A row stays in registers between its reductions and its
-// codes.
+// codes, so it is read once.  Measured: 16384 x 4096 82 us (5.7 TB/s), e4m3 of
+// 1531 x 5136 without a residual 7.5 (3.1 TB/s; the launch and one chain of load,
+// maximum, codes), 1 x 4096 2.8 us on the GPU; gradient, 8192 x 4096 with dh 46.6
+// (5.8 TB/s, 4.8 us of them the weight's sums in a launch of their own: joined
+// in the first, its last workgroup would wait for the others' writes across the
+// XCDs), 777 x 1168 9.5.
 #include "kernels.h"
 #include "quant_codes.h"
 
@@ -365,8 +370,13 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(const float* __re
   }
 }
 
-// Threads of the gradient's workgroups, 16 values to a thread where K allows.
-int grad_threads(int64_t K) { return K <= 4096 ? 256 : K <= 16384 ? 512 : 1024; }
+// Threads of the gradient's workgroups (us, 512 workgroups of 256 threads / 256
+// of 512, with a residual's gradient: 4096 x 2560 21.5 / 24.4, 4096 x 4096 28.4 /
+// 27.1, 4096 x 8192 50.0 / 48.6), and their number: about one row in flight for
+// each wavefront that the compute units hold, and more where short rows leave
+// the weight's sums cheap (16384 x 1024: 512 workgroups 37.7, 1024 31.7; 1024 x
+// 1024: 8.7, 9.4).
+int grad_threads(int64_t K) { return K < 4096 ? 256 : K <= 16384 ? 512 : 1024; }
 
 template <int kThreads, int kPieces, Rows kRows>
 hipError_t backward(const NormGrad& a, int rows, hipStream_t s) {
@@ -376,34 +386,39 @@ hipError_t backward(const NormGrad& a, int rows, hipStream_t s) {
 
 }  // namespace
 
+// Wavefronts to a row of the forward pass.  Us by 1 / 4 / 16 of them, with a
+// residual: 16384 x 512 14.2 / 21.2 / 58, 4096 x 1024 8.3 / 9.0 / 17.1, 1024 x 1024
+// 4.9 / 4.5 / 6.3; 16384 x 4096 80.9 / 73.6 / 86.8, 512 x 4096 9.0 / 5.0 / 4.7, 200 x
+// 5136 12.1 / 5.5 / 4.7, 1531 x 5136 18.7 / 14.1 / 14.7; 512 x 8192 - / 8.9 / 7.9,
+// 16384 x 8192 - / 164 / 161, 8192 x 12288 - / 128 / 120.
+int norm_waves(int64_t M, int64_t K) {
+  if (K >= 8192 || (K >= 4096 && M <= 512)) return 16;
+  return K <= 1024 && M >= 4096 ? 1 : 4;
+}
+
 // A launch has under 2^32 threads.
 bool norm_fits(int64_t M, int64_t K) {
-  return K <= kMaxNorm && M * (K <= 4096 ? kWave : K <= 16384 ? 4 * kWave : 16 * kWave) < (int64_t(1) << 32) - 1024;
+  return K <= kMaxNorm && M * norm_waves(M, K) * kWave < (int64_t(1) << 32) - 1024;
 }
 
 hipError_t launch_add_norm_quantize(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint16_t* h,
                                     void* q, float* scale, int64_t M, int64_t K, float eps, bool fp8, hipStream_t s) {
   const auto in = [](const uint16_t* p) { return reinterpret_cast<const u32x4*>(p); };
   const Norm a{in(x), in(residual), in(weight), reinterpret_cast<u32x4*>(h), static_cast<u32x2*>(q), scale, M, (int)(K / 8), eps};
-  if (K > 16384) return forward<16, 4>(a, fp8, s);
-  if (K <= 4096 && M >= 1024) {
-    const int pieces = (a.chunks + kWave - 1) / kWave;
-    if (pieces <= 1) return forward<1, 1>(a, fp8, s);
-    if (pieces <= 2) return forward<1, 2>(a, fp8, s);
-    if (pieces <= 4) return forward<1, 4>(a, fp8, s);
-    if (pieces <= 6) return forward<1, 6>(a, fp8, s);
-    return forward<1, 8>(a, fp8, s);
+  const int waves = norm_waves(M, K), pieces = (a.chunks + waves * kWave - 1) / (waves * kWave);
+  if (waves == 1) return pieces == 1 ? forward<1, 1>(a, fp8, s) : forward<1, 2>(a, fp8, s);
+  if (waves == 4) {
+    if (pieces == 1) return forward<4, 1>(a, fp8, s);
+    if (pieces == 2) return forward<4, 2>(a, fp8, s);
+    return pieces == 3 ? forward<4, 3>(a, fp8, s) : forward<4, 4>(a, fp8, s);
   }
-  const int pieces = (a.chunks + 4 * kWave - 1) / (4 * kWave);
-  if (pieces <= 1) return forward<4, 1>(a, fp8, s);
-  if (pieces <= 2) return forward<4, 2>(a, fp8, s);
-  if (pieces <= 3) return forward<4, 3>(a, fp8, s);
-  if (pieces <= 4) return forward<4, 4>(a, fp8, s);
-  if (pieces <= 6) return forward<4, 6>(a, fp8, s);
-  return forward<4, 8>(a, fp8, s);
+  if (pieces == 1) return forward<16, 1>(a, fp8, s);
+  return pieces == 2 ? forward<16, 2>(a, fp8, s) : forward<16, 4>(a, fp8, s);
 }
 
-int64_t norm_grad_rows(int64_t M, int64_t K) { return std::min<int64_t>(M, 128 * 1024 / grad_threads(K)); }
+int64_t norm_grad_rows(int64_t M, int64_t K) {
+  return std::min<int64_t>(M, K <= 1024 && M >= 4096 ? 1024 : 128 * 1024 / grad_threads(K));
+}
 
 hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
                                 uint16_t* dx, float* part, float* dweight, int64_t M, int64_t K, float eps,
@@ -413,7 +428,8 @@ hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const ui
   const int rows = (int)norm_grad_rows(M, K);
   hipError_t e;
   if (K <= 2048) e = backward<256, 1, Rows::kAhead>(a, rows, s);
-  else if (K <= 4096) e = backward<256, 2, Rows::kAhead>(a, rows, s);
+  else if (K < 4096) e = backward<256, 2, Rows::kAhead>(a, rows, s);
+  else if (K == 4096) e = backward<512, 1, Rows::kAhead>(a, rows, s);
   else if (K <= 8192) e = backward<512, 2, Rows::kAhead>(a, rows, s);
   else if (K <= 16384) e = backward<512, 4, Rows::kKept>(a, rows, s);
   else e = backward<1024, 4, Rows::kReload>(a, rows, s);

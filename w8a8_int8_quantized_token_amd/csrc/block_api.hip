@@ -308,7 +308,7 @@ struct AdapterPlan {
 AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int64_t R, bool dynamic, bool y_aligned, int tile) {
   AdapterPlan p{};
   p.quantize = dynamic;
-  p.in_down = dynamic && w8a8::down_quantizes(M, K);
+  p.in_down = dynamic && w8a8::down_quantizes(M, K, R);
   p.few = tile < 0 && M <= w8a8::kFewTokens && few_tokens_pay(M, N, K, false, false) && w8a8::few_tokens_low_fit(M, N);
   p.alone = p.few && dynamic && w8a8::few_tokens_low_from_x(M, N, K, R);
   p.splits = 1;

@@ -53,7 +53,7 @@ constexpr int kRows = 16;            // output channels of a group
 constexpr int kPiece = 128;          // bytes of K of a piece
 constexpr int kPieceBytes = kRows * kPiece;
 constexpr int kCodeBytes = 22 * 1024;
-constexpr int kFewRank = 64;               // ranks of adapters whose first products are made here
+constexpr int kFewRank = 32;               // ranks of adapters whose first products are made here
 constexpr uint32_t kOOB = 0x80000000u;    // buffer offset past any range: reads as zeros
 constexpr int kRsrcWord3 = 0x00020000;
 
@@ -578,9 +578,16 @@ hipError_t launch_act(const uint16_t* x, const int8_t* xq, const float* sx, cons
 }  // namespace
 
 // Where every workgroup makes the first products for itself: the codes fit LDS,
-// and the adapters' rows that each has to read are as few as a launch costs.
+// and the adapters' rows that each has to read, two at a time by a wavefront, take
+// less than a launch.  Cold weights, us so / in two launches, 2048 channels: 1 token
+// of K = 2048, rank 16 8.5 / 10.1, rank 32 9.4 / 10.2, rank 64 12.4 / 9.8; K = 4096,
+// rank 16 10.1 / 10.7, rank 32 11.7 / 10.8; 2 tokens of 2048, rank 16 9.7 / 10.7; 4,
+// rank 8 9.2 / 10.3; 4 of 1024, rank 16 11.8 / 9.7.  8192 channels: 1 token, rank 16,
+// K = 1024 9.0 / 10.5, 2048 10.8 / 10.4, 4096 14.4 / 14.7; 2 tokens of 2048 11.4 /
+// 10.7; 4, rank 8 11.9 / 10.3.
 bool few_tokens_low_from_x(int64_t M, int64_t N, int64_t K, int64_t R) {
-  return few_tokens_in_lds(M, K) && R <= kFewRank && M * R * K <= 65536 && few_tokens_low_fit(M, N);
+  return few_tokens_in_lds(M, K) && M * R <= (N <= 4096 ? kFewRank : kFewRank / 2) && M * R * K <= 65536 &&
+         few_tokens_low_fit(M, N);
 }
 
 hipError_t launch_few_tokens_low_from_x(const uint16_t* x, const int8_t* wq, const float* sw, const uint16_t* bias,

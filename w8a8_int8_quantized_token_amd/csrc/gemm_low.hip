@@ -1,5 +1,10 @@
 // The int8 linear with low-rank adapters on the kernel of gemm_kernel.h:
 //   y = bf16(((acc*sx)*sw)+b + sum_r t[m,r] b[id(m)][n,r]).
+// The second product is an epilogue (add_low): the sums are in fp32 before the
+// only rounding, and y is written once.  Bound by the int8 product: 8192 x 12288
+// x 4096, rank 16, 355 us beside 345 for the linear; with ids mixed by its passes,
+// one for each adapter and 16 ranks: 2048 x 4096 x 4096 with sixteen adapters,
+// rank 16, 50 us beside 38, rank 64, 80.
 #include "gemm_kernel.h"
 
 namespace w8a8 {

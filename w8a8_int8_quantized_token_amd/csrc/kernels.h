@@ -219,7 +219,6 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
 // quantizing x (where down_quantizes()): codes [M,K] and code_scale [M] are
 // outputs; bf16 values: x at any 2-byte address, rows of K.  t2, where not
 // null: the same times scale2[m].
-constexpr int64_t kDownRows = 256;   // up to here a workgroup for each row
 struct Down {
   const void* x;
   const float* scale;
@@ -234,7 +233,7 @@ struct Down {
   int64_t M;
   int K, ldp, R, ldt, count;
 };
-bool down_quantizes(int64_t M, int64_t K);
+bool down_quantizes(int64_t M, int64_t K, int64_t R);
 hipError_t launch_down(const Down& a, bool quantize, hipStream_t stream);
 // Products of codes and of bf16 values (each null for none) in one launch, of
 // the same M, R and ldt.

@@ -17,7 +17,7 @@
 // (6 without dh).  A row stays in registers between its reductions and its
 // codes, so it is read once.  Measured: 16384 x 4096 82 us (5.7 TB/s), e4m3 of
 // 1531 x 5136 without a residual 7.5 (3.1 TB/s; the launch and one chain of load,
-// maximum, codes), 1 x 4096 2.8 us on the GPU; gradient, 8192 x 4096 with dh 46.6
+// maximum, codes), 1 x 4096 2.3 on the GPU, an empty launch; gradient, 8192 x 4096 with dh 46.6
 // (5.8 TB/s, 4.8 us of them the weight's sums in a launch of their own: joined
 // in the first, its last workgroup would wait for the others' writes across the
 // XCDs), 777 x 1168 9.5.

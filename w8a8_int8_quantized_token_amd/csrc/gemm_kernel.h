@@ -786,7 +786,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // The adapters' share of a tile, t b^T, added to its fp32 values, which are
   // in the accumulators: for 16 (bf16 32) ranks at a time one pass for each
   // adapter that the wavefront's tokens have, with the other tokens' rows of t
-  // taken as zeros; the next adapter's fragments are on the way meanwhile.  (A
+  // taken as zeros; the next passes' fragments are on the way meanwhile.  (A
   // zero times an infinity or a NaN would reach the other tokens, so where an
   // adapter's fragments of b hold one they are taken as zeros and its own
   // tokens' of t as NaNs.)  The bf16 tiles have no registers for that: there

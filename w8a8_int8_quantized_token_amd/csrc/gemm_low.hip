@@ -1,10 +1,11 @@
 // The int8 linear with low-rank adapters on the kernel of gemm_kernel.h:
 //   y = bf16(((acc*sx)*sw)+b + sum_r t[m,r] b[id(m)][n,r]).
 // The second product is an epilogue (add_low): the sums are in fp32 before the
-// only rounding, and y is written once.  Bound by the int8 product: 8192 x 12288
-// x 4096, rank 16, 355 us beside 345 for the linear; with ids mixed by its passes,
-// one for each adapter and 16 ranks: 2048 x 4096 x 4096 with sixteen adapters,
-// rank 16, 50 us beside 38, rank 64, 80.
+// only rounding, and y is written once.  Bound by the int8 product; its passes,
+// one for each 16 ranks of each adapter that a wavefront's tokens have, come on
+// top (us, this kernel / the linear): 8192 x 12288 x 4096 in runs of 512 tokens,
+// rank 16 409 / 382, rank 64 438 / 367; 2048 x 4096 x 4096, sixteen adapters in runs,
+// rank 16 39.5 / 39.7, rank 64 42.9 / 39.5, mixed 43.7 / 39.2 and 74.8 / 39.4.
 #include "gemm_kernel.h"
 
 namespace w8a8 {

@@ -501,8 +501,9 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t *x, const int8_t *wq,
  * bf16 [M,K], [L,R,K] and [L,N,R]; an adapter without tokens gets zeros.  Each
  * is left out where its pointer is NULL; dx needs wq, w_scale, a and b, da needs
  * b, xq and x_scale, db needs a, xq and x_scale.  Sums are fp32, on operands
- * rounded to bf16 once (of da, u times x's scale); no atomics, the same bits
- * from call to call.  Contract as for w8a8_linear_adapters and
+ * rounded to bf16 once (of da, u times x's scale); in small calls (M times R,
+ * rounded up to 16, at most 2048) da and db take what that rounding leaves, too.
+ * No atomics, the same bits from call to call.  Contract as for w8a8_linear_adapters and
  * w8a8_linear_backward; da and db 16-byte aligned.
  */
 size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R,

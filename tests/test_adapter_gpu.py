@@ -361,6 +361,16 @@ def test_adapter_gradients(w8, M, K, N, R, L, kind):
             assert not got[1][i].any() and not got[2][i].any()
 
 
+@pytest.mark.parametrize("M,K,N,R,L,kind", [(1, 512, 520, 8, 1, "one"), (3, 256, 255, 24, 2, "runs"), (22, 256, 255, 8, 7, "runs"),
+                                            (16, 512, 264, 128, 2, "mixed"), (128, 256, 264, 16, 3, "mixed")])
+def test_few_tokens_gradients_are_rounded_once(w8, M, K, N, R, L, kind):
+    """No other error of the adapters' gradients is seen beside their own rounding: fp32 sums, and operands to 2^-17."""
+    inputs = grad_inputs(M, K, N, R, L, kind, M + N)
+    for got, (want, _) in zip(w8.linear_adapters_backward(*dev(*inputs))[1:], aref.grads(*inputs)[1:]):
+        rms = lambda e: float(e.square().mean().sqrt())
+        assert rms(got.cpu().double() - want) <= 1.03 * rms(want.to(BF).double() - want)
+
+
 @pytest.mark.parametrize("R", [8, 24, 40])
 @pytest.mark.parametrize("N", [1, 2, 5, 7, 8, 9, 15, 63, 129])
 def test_gradients_of_few_channels(w8, N, R):

@@ -146,7 +146,16 @@ __device__ __forceinline__ void down_row(const Down& a) {
     *reinterpret_cast<uint32_t*>(a.t + m * a.ldt + r0) = pack2(sum[0], sum[1]);
     if (a.t2 != nullptr) {
       const float s2 = id >= 0 ? a.scale2[m] : 0.0f;
-      *reinterpret_cast<uint32_t*>(a.t2 + m * a.ldt + r0) = pack2(sum[0] * s2, sum[1] * s2);
+      sum[0] *= s2, sum[1] *= s2;
+      *reinterpret_cast<uint32_t*>(a.t2 + m * a.ldt + r0) = pack2(sum[0], sum[1]);
+    }
+    if (a.low != nullptr) {
+      const uint32_t w = pack2(sum[0], sum[1]);
+      const auto rest = [](float v, uint32_t bits) {   // (of an infinity or a NaN: nothing)
+        const float high = __uint_as_float(bits);
+        return fabsf(high) < INFINITY ? v - high : 0.0f;
+      };
+      *reinterpret_cast<uint32_t*>(a.low + m * a.ldt + r0) = pack2(rest(sum[0], w << 16), rest(sum[1], w & 0xffff0000u));
     }
   }
 }
@@ -400,7 +409,8 @@ bool by_rows(int64_t M, int64_t R) { return M * ((R + 15) / 16 * 16) <= 20480; }
 bool down_quantizes(int64_t M, int64_t K, int64_t R) { return by_rows(M, R) && K <= kMaxFused; }
 
 hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
-  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0) return hipErrorInvalidValue;
+  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0 || (a.low != nullptr && !by_rows(a.M, a.R)))
+    return hipErrorInvalidValue;
   const dim3 threads(kThreads), rows((unsigned)a.M, (unsigned)(a.ldt / kRanks));
   if (quantize) {
     if (!down_quantizes(a.M, a.K, a.R)) return hipErrorInvalidValue;
@@ -423,7 +433,7 @@ hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s
   Down c{};   // (M = 0: none)
   if (codes != nullptr) c = *codes;
   if (v.M < 1 || v.R < 8 || v.R % 8 != 0 || v.ldt < v.R || v.ldt % 16 != 0 ||
-      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)))
+      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)) || ((v.low != nullptr || c.low != nullptr) && !by_rows(v.M, v.R)))
     return hipErrorInvalidValue;
   const dim3 threads(kThreads);
   const int both = c.M > 0 ? 2 : 1;

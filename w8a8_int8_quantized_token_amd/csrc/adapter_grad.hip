@@ -17,6 +17,12 @@
 // adapters leave compute units idle; the wavefronts' sums are joined through
 // LDS and the parts' go to slices for launch_finish, each in a fixed order.
 //
+// v is rounded to bf16 once, a relative error of up to 2^-9 in each of its terms.
+// Over a thousand of them these average to about the output's own rounding; where
+// they are fewer (a.low; a token's gradient has eight in all at rank 8) they do not,
+// and v comes in two parts, which a second pass over the few rows adds (22 tokens,
+// rank 8: 4 of 31 us).
+//
 // Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 17.5
 // us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 (168 MB of x,
 // 2.5 TB/s: 384 workgroups for 256 compute units, whose registers hold one each).
@@ -89,6 +95,7 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     uint32_t v[8][(KR + 1) / 2];
   };
   // The step at place p0 of the listed rows (the list goes on with its last row).
+  const uint16_t* from_v = a.v;
   auto load = [&](int p0, Step& s, auto whole) __attribute__((always_inline)) {
     int32_t rows[8];
     __builtin_memcpy(rows, __builtin_assume_aligned(lds.list + p0 + 8 * h, 16), 32);
@@ -110,13 +117,24 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
           }
         }
       }
-      const uint16_t* v = a.v + m * a.ldt + min(rank, a.ldt - KR);
+      const uint16_t* v = from_v + m * a.ldt + min(rank, a.ldt - KR);
       if constexpr (KR == 1) s.v[i][0] = *v;
       else __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
     }
     __builtin_amdgcn_sched_barrier(0);   // (moved loads would be waited for sooner)
   };
-  auto multiply = [&](const Step& s) __attribute__((always_inline)) {
+  auto multiply = [&](Step& s) __attribute__((always_inline)) {
+    if constexpr (!kCodes) {
+      if (from_v != a.v) {   // the low parts of v: an infinity is in the sum already, and times them it would be a NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            const uint32_t x = s.x[i][w];
+            s.x[i][w] = ((x & 0x7f80u) == 0x7f80u ? 0 : x & 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0 : x & 0xffff0000u);
+          }
+      }
+    }
     u32x4 fv[KR];
 #pragma unroll
     for (int r = 0; r < KR; ++r)
@@ -176,7 +194,11 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     if (base > first) __syncthreads();
     for (int i = threadIdx.x; i < (n + kRows - 1) / kRows * kRows; i += kThreads) lds.list[i] = a.list[base + min(i, n - 1)];
     __syncthreads();
-    run(n);
+    for (;; from_v = a.low) {   // (an accumulator takes both parts)
+      run(n);
+      if (a.low == nullptr || from_v == a.low) break;
+    }
+    from_v = a.v;
   }
   // the other wavefronts' sums onto the first's, in order
 #pragma unroll

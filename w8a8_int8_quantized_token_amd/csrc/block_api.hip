@@ -389,8 +389,9 @@ w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, 
 struct AdapterBackPlan {
   BackPlan x;
   int64_t ldt, ldn;
-  int64_t bt, at, list, starts, t, u, v, slices_a, slices_b;
+  int64_t bt, at, list, starts, t, u, v, low_a, low_b, slices_a, slices_b;
   int parts_a, parts_b;
+  bool exact;   // v and t of the matrices' gradients in two parts
   int64_t bytes;
 };
 AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, bool dx, bool da, bool db,
@@ -399,6 +400,7 @@ AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, in
   p.x = back_plan(M, N, K, false, dx, false, false, copy_dy, few, true);
   p.ldt = up(R, 16);
   p.ldn = up(N, 16);
+  p.exact = M * p.ldt <= w8a8::kExactRows;
   Pieces w;
   w.bytes = p.x.bytes;
   if (dx || da) {
@@ -412,11 +414,13 @@ AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, in
   }
   if (da) {
     p.v = w.add(2 * M * p.ldt);
+    if (p.exact) p.low_a = w.add(2 * M * p.ldt);
     p.parts_a = w8a8::adapter_grad_parts(M, K, R, L, true);
     p.slices_a = w.add(4 * p.parts_a * L * R * K);
   }
   if (db) {
     p.t = w.add(2 * M * p.ldt);
+    if (p.exact) p.low_b = w.add(2 * M * p.ldt);
     p.parts_b = w8a8::adapter_grad_parts(M, N, R, L, false);
     p.slices_b = w.add(4 * p.parts_b * L * R * N);
   }
@@ -762,6 +766,7 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   dt.p_stride = R * K;
   dt.K = dt.ldp = (int)K;
   dt.t = t;
+  if (p.exact) dt.low = at<uint16_t>(ws, p.low_b);
   du.x = dy;
   du.p = bt;
   du.p_stride = R * p.ldn;
@@ -771,6 +776,7 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   if (da) {
     du.t2 = v;
     du.scale2 = x_scale;
+    if (p.exact) du.low = at<uint16_t>(ws, p.low_a);
   }
   TRY(w8a8::launch_down_pair(db ? &dt : nullptr, dx || da ? &du : nullptr, stream));
   w8a8::JoinJob join[w8a8::kMaxJobs];
@@ -789,11 +795,11 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   }
   w8a8::AdapterGrad ga{}, gb{};
   if (da) {
-    ga = {xq, v, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
+    ga = {xq, v, du.low, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
     join[joins++] = {ga.slices, da, p.parts_a, L * R * K, true, 0};
   }
   if (db) {
-    gb = {dy, t, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
+    gb = {dy, t, dt.low, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
     join[joins++] = {gb.slices, db, p.parts_b, L * R * N, true, 0};
   }
   TRY(w8a8::launch_adapter_grads(ga, gb, stream));

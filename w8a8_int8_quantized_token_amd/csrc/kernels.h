@@ -218,7 +218,9 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
 // multiple of 16 and at least K, zeros past column K).  Codes: scale [M];
 // quantizing x (where down_quantizes()): codes [M,K] and code_scale [M] are
 // outputs; bf16 values: x at any 2-byte address, rows of K.  t2, where not
-// null: the same times scale2[m].
+// null: the same times scale2[m].  low, where not null (up to kExactRows rows
+// times ldt): what the rounding of t2, or of t without one, left, in bf16.
+constexpr int64_t kExactRows = 2048;
 struct Down {
   const void* x;
   const float* scale;
@@ -228,7 +230,7 @@ struct Down {
   int64_t p_stride;
   const int32_t* ids;
   const float* scaling;
-  uint16_t *t, *t2;
+  uint16_t *t, *t2, *low;
   const float* scale2;
   int64_t M;
   int K, ldp, R, ldt, count;
@@ -260,7 +262,7 @@ hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const f
 // adapter_grad_parts(); col_blocks and rank_blocks are set by the launch.
 struct AdapterGrad {
   const void* x;
-  const uint16_t* v;
+  const uint16_t *v, *low;   // low, or null: what v's rounding left (Down::low)
   const int32_t *list, *starts;
   float* slices;
   int64_t C;

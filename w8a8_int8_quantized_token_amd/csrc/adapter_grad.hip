@@ -23,9 +23,9 @@
 // and v comes in two parts, which a second pass over the few rows adds (22 tokens,
 // rank 8: 4 of 31 us).
 //
-// Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 17.5
-// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 (168 MB of x,
-// 2.5 TB/s: 384 workgroups for 256 compute units, whose registers hold one each).
+// Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 16.4
+// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 58 (168 MB of x,
+// 2.9 TB/s: 384 workgroups for 256 compute units, whose registers hold one each).
 #include "kernels.h"
 
 #include <algorithm>
@@ -55,17 +55,15 @@ __device__ __forceinline__ uint32_t pair(uint32_t first, uint32_t second, int j)
 // wait for the loads of x that were sent before it.
 constexpr int kListed = 8 * kWaves * kRows;
 
-template <int KR, int KB>
 struct Lds {
-  f32x4 part[KR * KB <= 16 ? 4 : KR * KB <= 32 ? 2 : 1][KR * KB * kWave];
+  f32x4 part[kWaves][kWaves][kWave];   // of each wavefront, as many of its sums
   __attribute__((aligned(16))) int32_t list[kListed];
 };
 
 // KR ranks to a lane (16 KR of a workgroup), KB columns.
 template <int KR, int KB, bool kCodes>
-__device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned block, Lds<KR, KB>& lds) {
+__device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned block, Lds& lds) {
   constexpr int kWords = kCodes ? KB / 4 : KB / 2;   // of a lane's columns in a row
-  constexpr int kAtOnce = sizeof(lds.part) / sizeof(lds.part[0]);   // wavefronts' sums in LDS at once
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int l16 = lane % 16, h = lane / 16;
   const int cb = (int)(block % (unsigned)a.col_blocks);
@@ -200,40 +198,28 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     }
     from_v = a.v;
   }
-  // the other wavefronts' sums onto the first's, in order
-#pragma unroll
-  for (int w0 = 1; w0 < kWaves; w0 += kAtOnce) {
-    if (wave >= w0 && wave < w0 + kAtOnce) {
-#pragma unroll
-      for (int r = 0; r < KR; ++r)
-#pragma unroll
-        for (int j = 0; j < KB; ++j) lds.part[wave - w0][(r * KB + j) * kWave + lane] = acc[r][j];
-    }
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 0; w < kAtOnce; ++w)
-        if (w0 + w < kWaves) {
-#pragma unroll
-          for (int r = 0; r < KR; ++r)
-#pragma unroll
-            for (int j = 0; j < KB; ++j) acc[r][j] += lds.part[w][(r * KB + j) * kWave + lane];
-        }
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
-  // lane: column col + j, ranks KR (4h + e) + r of the block's
+  // The sums of the wavefronts that had rows, in order: eight at a time through
+  // LDS, one to each wavefront to add up and store.  (The first wavefront alone:
+  // 76 tokens, rank 40 20.3 us and not 12.6; 8192 tokens, rank 64 68 and not 58.)
+  const int active = min(kWaves, (last - first + kRows - 1) / kRows);
   float* out = a.slices + ((int64_t)slice * a.count + id) * a.R * a.C;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int r0 = rb * 16 * KR + KR * (4 * h + e);
+  for (int c = 0; c < KR * KB; c += kWaves) {
+    if (c > 0) __syncthreads();
+    if (wave < active) {
 #pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      if (r0 + r >= a.R) continue;
+      for (int k = 0; k < kWaves; ++k) lds.part[wave][k][lane] = acc[(c + k) / KB][(c + k) % KB];
+    }
+    __syncthreads();
+    f32x4 sum = {0, 0, 0, 0};
+    for (int w = 0; w < active; ++w) sum += lds.part[w][wave][lane];
+    // lane: column col + j, ranks KR (4h + e) + r of the block's
+    const int r = c / KB, j = c % KB + wave;
+    if (col + j >= a.C) continue;
 #pragma unroll
-      for (int j = 0; j < KB; ++j)
-        if (col + j < a.C) out[kCodes ? (r0 + r) * a.C + col + j : (col + j) * a.R + r0 + r] = acc[r][j][e];
+    for (int e = 0; e < 4; ++e) {
+      const int rank = rb * 16 * KR + KR * (4 * h + e) + r;
+      if (rank < a.R) out[kCodes ? rank * a.C + col + j : (col + j) * a.R + rank] = sum[e];
     }
   }
 }
@@ -242,12 +228,9 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
 // longer, before a's.
 template <int KR, int KA, int KB>
 __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, AdapterGrad gb, unsigned blocks_b) {
-  __shared__ union {
-    Lds<KR, KA> a;
-    Lds<KR, KB> b;
-  } lds;
-  if (blockIdx.x < blocks_b) adapter_grad<KR, KB, false>(gb, blockIdx.x, lds.b);
-  else adapter_grad<KR, KA, true>(ga, blockIdx.x - blocks_b, lds.a);
+  __shared__ Lds lds;
+  if (blockIdx.x < blocks_b) adapter_grad<KR, KB, false>(gb, blockIdx.x, lds);
+  else adapter_grad<KR, KA, true>(ga, blockIdx.x - blocks_b, lds);
 }
 
 // Ranks of a lane, and columns: as many sums as registers allow.

@@ -401,24 +401,27 @@ int tiles_of(const Down& a, int products) {
 // 10.4 / 12.0, 1536 11.9 / 11.8; rank 32: 512 9.1 / 11.9, 768 11.8 / 11.9, 1024 14.9 /
 // 11.9; rank 128: 128 8.7 / 11.6, 192 11.6 / 11.7, 256 14.5 / 11.8; K = 1168, rank
 // 16: 1024 5.4 / 6.7, 1280 6.2 / 6.6, 1536 6.9 / 6.7.  With sixteen adapters mixed,
-// rank 16: 1536 12.4 / 15.3, 2048 15.2 / 15.4; rank 128: 128 15.2 / 14.8.
-bool by_rows(int64_t M, int64_t R) { return M * ((R + 15) / 16 * 16) <= 20480; }
+// rank 16: 1536 12.4 / 15.3, 2048 15.2 / 15.4; rank 128: 128 15.2 / 14.8.  Both
+// products of codes of 4096 and values of 4096, rank 16: 768 12.7 / 14.4, 1024 16.6 /
+// 14.5, eight adapters mixed 16.4 / 16.5; of 672 and 8432: 1024 22.0 / 23.9, 1280
+// 26.6 / 24.1, mixed 26.3 / 28.1.
+bool by_rows(int64_t M, int64_t R, int products) {
+  return M * ((R + 15) / 16 * 16) <= (products == 1 ? 20480 : 17408);
+}
 
-}  // namespace
-
-bool down_quantizes(int64_t M, int64_t K, int64_t R) { return by_rows(M, R) && K <= kMaxFused; }
-
-hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
-  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0 || (a.low != nullptr && !by_rows(a.M, a.R)))
+// Codes alone, by the rules of as many products: a gradient's bits do not depend
+// on which others are asked for.
+hipError_t launch_codes(const Down& a, bool quantize, int products, hipStream_t s) {
+  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0 || (a.low != nullptr && !by_rows(a.M, a.R, products)))
     return hipErrorInvalidValue;
   const dim3 threads(kThreads), rows((unsigned)a.M, (unsigned)(a.ldt / kRanks));
   if (quantize) {
     if (!down_quantizes(a.M, a.K, a.R)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(down_row_kernel<Rows::kQuantize>, rows, threads, 0, s, a);
-  } else if (by_rows(a.M, a.R)) {
+  } else if (by_rows(a.M, a.R, products)) {
     hipLaunchKernelGGL(down_row_kernel<Rows::kCodes>, rows, threads, 0, s, a);
   } else {
-    const int tiles = tiles_of(a, 1);
+    const int tiles = tiles_of(a, products);
     const dim3 grid = block_grid(a, tiles, slots_of(a, tiles));
     if (tiles == 1) hipLaunchKernelGGL(down_block_kernel<1>, grid, threads, 0, s, a);
     else if (tiles == 2) hipLaunchKernelGGL(down_block_kernel<2>, grid, threads, 0, s, a);
@@ -427,21 +430,27 @@ hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) {
   return hipGetLastError();
 }
 
+}  // namespace
+
+bool down_quantizes(int64_t M, int64_t K, int64_t R) { return by_rows(M, R, 1) && K <= kMaxFused; }
+
+hipError_t launch_down(const Down& a, bool quantize, hipStream_t s) { return launch_codes(a, quantize, 1, s); }
+
 hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s) {
-  if (values == nullptr) return codes != nullptr ? launch_down(*codes, false, s) : hipSuccess;
+  if (values == nullptr) return codes != nullptr ? launch_codes(*codes, false, 2, s) : hipSuccess;
   const Down& v = *values;
   Down c{};   // (M = 0: none)
   if (codes != nullptr) c = *codes;
   if (v.M < 1 || v.R < 8 || v.R % 8 != 0 || v.ldt < v.R || v.ldt % 16 != 0 ||
-      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)) || ((v.low != nullptr || c.low != nullptr) && !by_rows(v.M, v.R)))
+      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)) || ((v.low != nullptr || c.low != nullptr) && !by_rows(v.M, v.R, 2)))
     return hipErrorInvalidValue;
   const dim3 threads(kThreads);
   const int both = c.M > 0 ? 2 : 1;
-  if (by_rows(v.M, v.R)) {
+  if (by_rows(v.M, v.R, 2)) {
     hipLaunchKernelGGL(down_row_kernel2<0>, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
     return hipGetLastError();
   }
-  const int tiles = tiles_of(v, both), slots = slots_of(v, tiles);
+  const int tiles = tiles_of(v, 2), slots = slots_of(v, tiles);
   const dim3 grid = block_grid(v, tiles, both * slots);
   if (tiles == 1) hipLaunchKernelGGL(down_block_kernel2<1>, grid, threads, 0, s, c, v, slots);
   else if (tiles == 2) hipLaunchKernelGGL(down_block_kernel2<2>, grid, threads, 0, s, c, v, slots);

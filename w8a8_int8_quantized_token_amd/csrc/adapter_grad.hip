@@ -15,7 +15,8 @@
 // v_mfma_f32_16x16x32_bf16; v's ranks are dealt to the lanes the same way.  No
 // transposition goes through LDS.  The list is cut into parts where columns and
 // adapters leave compute units idle; the wavefronts' sums are joined through
-// LDS and the parts' go to slices for launch_finish, each in a fixed order.
+// LDS and the parts' go to slices for launch_finish, each in a fixed order; of one
+// part the result is written at once.
 //
 // v is rounded to bf16 once, a relative error of up to 2^-9 in each of its terms.
 // Over a thousand of them these average to about the output's own rounding; where
@@ -202,7 +203,8 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
   // LDS, one to each wavefront to add up and store.  (The first wavefront alone:
   // 76 tokens, rank 40 20.3 us and not 12.6; 8192 tokens, rank 64 68 and not 58.)
   const int active = min(kWaves, (last - first + kRows - 1) / kRows);
-  float* out = a.slices + ((int64_t)slice * a.count + id) * a.R * a.C;
+  const int64_t matrix = (int64_t)a.R * a.C;
+  float* const part = a.slices + ((int64_t)slice * a.count + id) * matrix;
 #pragma unroll
   for (int c = 0; c < KR * KB; c += kWaves) {
     if (c > 0) __syncthreads();
@@ -219,7 +221,10 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int rank = rb * 16 * KR + KR * (4 * h + e) + r;
-      if (rank < a.R) out[kCodes ? rank * a.C + col + j : (col + j) * a.R + rank] = sum[e];
+      if (rank >= a.R) continue;
+      const int64_t at = kCodes ? rank * a.C + col + j : (col + j) * a.R + rank;
+      if (a.parts > 1) part[at] = sum[e];
+      else a.out[id * matrix + at] = __builtin_bit_cast(uint16_t, (__bf16)sum[e]);
     }
   }
 }
@@ -249,7 +254,7 @@ int parts_of(int64_t M, int64_t C, int R, int count, bool codes) {
 
 // Workgroups of one of the gradients (none: 0).
 int64_t set_blocks(AdapterGrad& g, bool codes) {
-  if (g.slices == nullptr) return 0;
+  if (g.out == nullptr) return 0;
   g.col_blocks = (int)col_blocks_of(g.C, g.R, codes);
   g.rank_blocks = (int)rank_blocks_of(g.R);
   return (int64_t)g.col_blocks * g.rank_blocks * g.parts * g.count;

@@ -416,13 +416,13 @@ AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, in
     p.v = w.add(2 * M * p.ldt);
     if (p.exact) p.low_a = w.add(2 * M * p.ldt);
     p.parts_a = w8a8::adapter_grad_parts(M, K, R, L, true);
-    p.slices_a = w.add(4 * p.parts_a * L * R * K);
+    if (p.parts_a > 1) p.slices_a = w.add(4 * p.parts_a * L * R * K);
   }
   if (db) {
     p.t = w.add(2 * M * p.ldt);
     if (p.exact) p.low_b = w.add(2 * M * p.ldt);
     p.parts_b = w8a8::adapter_grad_parts(M, N, R, L, false);
-    p.slices_b = w.add(4 * p.parts_b * L * R * N);
+    if (p.parts_b > 1) p.slices_b = w.add(4 * p.parts_b * L * R * N);
   }
   p.bytes = w.bytes;
   return p;
@@ -795,12 +795,12 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   }
   w8a8::AdapterGrad ga{}, gb{};
   if (da) {
-    ga = {xq, v, du.low, list, starts, at<float>(ws, p.slices_a), K, (int)p.ldt, (int)R, (int)L, p.parts_a};
-    join[joins++] = {ga.slices, da, p.parts_a, L * R * K, true, 0};
+    ga = {xq, v, du.low, list, starts, at<float>(ws, p.slices_a), da, K, (int)p.ldt, (int)R, (int)L, p.parts_a};
+    if (p.parts_a > 1) join[joins++] = {ga.slices, da, p.parts_a, L * R * K, true, 0};
   }
   if (db) {
-    gb = {dy, t, dt.low, list, starts, at<float>(ws, p.slices_b), N, (int)p.ldt, (int)R, (int)L, p.parts_b};
-    join[joins++] = {gb.slices, db, p.parts_b, L * R * N, true, 0};
+    gb = {dy, t, dt.low, list, starts, at<float>(ws, p.slices_b), db, N, (int)p.ldt, (int)R, (int)L, p.parts_b};
+    if (p.parts_b > 1) join[joins++] = {gb.slices, db, p.parts_b, L * R * N, true, 0};
   }
   TRY(w8a8::launch_adapter_grads(ga, gb, stream));
   return joins > 0 ? launched(w8a8::launch_finish(join, joins, stream)) : W8A8_OK;

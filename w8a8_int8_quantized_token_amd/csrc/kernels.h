@@ -259,18 +259,20 @@ hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const f
 // [R][C] from codes x [M,C] (rows 16-byte aligned), or [parts][count][C][R] from
 // bf16 x (any 2-byte address), for a JoinJob.  v bf16 [M,ldt]; list [M] and
 // starts [count + 1]: the rows of each adapter (LayoutJob::kLists).  parts =
-// adapter_grad_parts(); col_blocks and rank_blocks are set by the launch.
+// adapter_grad_parts(); of one part the result goes to out in bf16, and slices are
+// not used.  col_blocks and rank_blocks are set by the launch.
 struct AdapterGrad {
   const void* x;
   const uint16_t *v, *low;   // low, or null: what v's rounding left (Down::low)
   const int32_t *list, *starts;
   float* slices;
+  uint16_t* out;
   int64_t C;
   int ldt, R, count, parts, col_blocks, rank_blocks;
 };
 int adapter_grad_parts(int64_t M, int64_t C, int64_t R, int64_t count, bool codes);
 bool adapter_grads_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t count);
-// Both gradients, each left out where its slices are null.
+// Both gradients, each left out where its out is null.
 hipError_t launch_adapter_grads(AdapterGrad codes, AdapterGrad values, hipStream_t stream);
 // out fp32 [M,C] = sum_r u[m,r] p[ids[m]][r,c] (p bf16 [count,R,C], C % 16 == 0), for few rows.
 hipError_t launch_adapter_up(const uint16_t* u, int64_t ldt, const uint16_t* p, const int32_t* ids, int64_t count,

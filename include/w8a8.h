@@ -428,7 +428,9 @@ w8a8_status w8a8_qk_norm_rope_backward(
  * common to a row, cancels in the codes and goes into the scale.  (s is a
  * product, not w8a8_quantize_act's quotient max|v| / 127: it may be a step of
  * fp32 away from that.)  Codes are exact functions of the inputs; mean(h^2) is
- * an fp32 sum.  A row whose s is zero (all zeros) has zero codes and scale.
+ * an fp32 sum.  A row whose s is zero (all zeros) has zero codes and scale; one
+ * with a NaN or an infinity in h or in h * weight has a scale that is not finite,
+ * and so has every output that is made of its codes.
  * h is written where it is not NULL; it may be x or residual and overlaps
  * nothing otherwise, and no other output overlaps anything.
  * The gradient, the rounding to codes passed straight through, for dn (of the

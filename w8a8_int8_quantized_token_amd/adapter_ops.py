@@ -16,7 +16,8 @@ def add_rms_norm_quantize(x, residual=None, weight=None, eps: float = 1e-6, fp8:
     codes: (xq int8 [M,K] or, ``fp8``, uint8 e4m3 bits; x_scale fp32 [M]; h =
     bf16(x + residual)).  x, residual bf16 [M,K], weight bf16 [K] or None.
     xq * x_scale is the normed row on the codes' grid (127 or 448 steps of the
-    row's largest magnitude).
+    row's largest magnitude).  A row with a NaN or an infinity has a scale that
+    is not finite.
     Without a residual h is x itself; a given h (it may be x or residual)
     receives the sum."""
     if h is None:

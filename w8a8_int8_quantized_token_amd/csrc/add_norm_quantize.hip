@@ -60,8 +60,10 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
 __device__ __forceinline__ float wave_sum(float v) {
   return over_lanes(v, [](float a, float b) { return a + b; });
 }
+// (a NaN stays: fmaxf would drop it, and a row of NaNs would have finite codes)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_maxf(float v) {
-  return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
+  return over_lanes(v, [](float a, float b) { return larger(a, b); });
 }
 
 // fl32(v / s) for any fp32 |v| <= 448 s, from the correctly rounded r = 1 / s:
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
       const float lo = low(h[i][e]), hi = high(h[i][e]);
       sq = fmaf(lo, lo, sq);
       sq = fmaf(hi, hi, sq);
-      top = fmaxf(top, fmaxf(fabsf(lo * low(w[i][e])), fabsf(hi * high(w[i][e]))));
+      top = larger(top, larger(fabsf(lo * low(w[i][e])), fabsf(hi * high(w[i][e]))));
     }
   }
   if (a.h != nullptr) {
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
     for (int k = 0; k < kWaves; ++k) {
       const f32x2 p = part[k];
       sq += p[0];
-      top = fmaxf(top, p[1]);
+      top = larger(top, p[1]);
     }
   }
   const RowScale rs = scale_of<F8>(top);
@@ -304,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGrad a) {
     for (int k = 0; k < kWaves; ++k) sq += part[parity][k][0], along += part[parity][k][1];
     parity ^= 1;
     const float power = sq / n + a.eps;
-    const float r = power > 0.0f ? 1.0f / sqrtf(power) : 0.0f;
+    const float r = power == 0.0f ? 0.0f : 1.0f / sqrtf(power);
     const float t = along * r / n;   // mean(dn w hh)
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {

@@ -428,7 +428,7 @@ w8a8_status w8a8_qk_norm_rope_backward(
  * common to a row, cancels in the codes and goes into the scale.  (s is a
  * product, not w8a8_quantize_act's quotient max|v| / 127: it may be a step of
  * fp32 away from that.)  Codes are exact functions of the inputs; mean(h^2) is
- * an fp32 sum.  A row whose s is zero (all zeros) has zero codes and scale; one
+ * a sum in fp32.  A row whose s is zero (all zeros) has zero codes and scale; one
  * with a NaN or an infinity in h or in h * weight has a scale that is not finite,
  * and so has every output that is made of its codes.
  * h is written where it is not NULL; it may be x or residual and overlaps
@@ -442,8 +442,8 @@ w8a8_status w8a8_qk_norm_rope_backward(
  * dx may be dn, dh or h and overlaps nothing otherwise.  Arithmetic is fp32, each bf16
  * output rounded once.  Of a row of zeros with eps = 0, r is taken as 0.
  * Contract: 16 <= K <= 32768, K % 16 == 0; M times 64 (K <= 1024), 256 (K <
- * 8192) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; finite inputs whose
- * squares' sum and products with the weight are finite in fp32; all bf16
+ * 8192) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; inputs of any magnitude
+ * (squares that vanish or overflow in fp32 are summed again in range); all bf16
  * pointers and the codes 16-byte aligned, scales and dweight 4-byte aligned.
  */
 w8a8_status w8a8_add_rms_norm_quantize(const uint16_t *x, const uint16_t *residual,

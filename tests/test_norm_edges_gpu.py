@@ -1,10 +1,10 @@
 """The norm that leaves codes, and its gradient, at values where it can go
-wrong: NaNs and infinities among the inputs, which no finite result may hide."""
+wrong: NaNs and infinities among the inputs, which no finite result may hide,
+and rows whose squares fp32 does not hold."""
 import pytest
 import torch
 
 import adapter_ref as aref
-import block_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,65 @@ def test_gradient_of_rows_that_are_not_finite(w8, M, K):
     bad = w.clone()
     bad[5] = NAN
     assert torch.isnan(w8.add_rms_norm_backward(*dev(dn, h, bad))[0]).all()
+
+
+# squares that vanish or overflow in fp32: rows of these magnitudes
+FAR = [2.0 ** e for e in (-132, -126, -110, -90, -74, -70, -64, -52, -48, 0, 50, 62, 66, 90, 120)]
+
+
+def far_rows(K, seed):
+    x = torch.randn(len(FAR), K, generator=torch.Generator().manual_seed(seed)).clamp(-4, 4)
+    x[x.abs() < 2.0 ** -6] = 2.0 ** -6
+    return (x * torch.tensor(FAR)[:, None]).to(BF)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-33, 1e-30, 1e-12, 1e-6])
+@pytest.mark.parametrize("copies,K", [(1, 64), (300, 512), (1, 2064), (1, 4096), (1, 8192), (1, 16400)])
+def test_rows_whose_squares_leave_the_range(w8, copies, K, eps, fp8):
+    x = far_rows(K, K).repeat(copies, 1)
+    w = (1 + 0.3 * torch.randn(K, generator=torch.Generator().manual_seed(1))).clamp(0.25, 2).to(BF)
+    q, s, _ = w8.add_rms_norm_quantize(*dev(x, None, w), eps=eps, fp8=fp8)
+    eps = float(torch.tensor(eps))              # as the kernel has it
+    want_q, want_s, _ = aref.norm_codes(x, None, w, eps, fp8)
+    assert torch.equal((fp8_values(q) if fp8 else q.float()).cpu(), want_q)
+    # the bound of the ordinary rows' test, and half a step of the smallest fp32 number
+    assert ((s.cpu().double() - want_s).abs() <= ((64 + 6 + 16 + 2) / 2 + 4) * U * want_s + 2.0 ** -150).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-33, 1e-6])
+@pytest.mark.parametrize("copies,K", [(1, 64), (280, 512), (1, 2064), (1, 4096), (1, 8192), (1, 16384), (1, 16400)])
+def test_gradient_of_rows_whose_squares_leave_the_range(w8, copies, K, eps):
+    h = far_rows(K, K + 1).repeat(copies, 1)
+    M = h.shape[0]
+    g = torch.Generator().manual_seed(2)
+    w = (1 + 0.3 * torch.randn(K, generator=g)).clamp(0.25, 2).to(BF)
+    dn = (torch.randn(M, K, generator=g) * 2.0 ** -20).to(BF)
+    dh = torch.randn(M, K, generator=g).to(BF)
+    for other in (None, dh):
+        dx, dw = w8.add_rms_norm_backward(*dev(dn, h, w), eps=eps, dh=None if other is None else other.to(DEV))
+        want, size, want_dw, dw_size = aref.norm_grad(dn, other, h, w, float(torch.tensor(eps)))
+        # (the ordinary rows' bounds; row by row, since magnitudes differ)
+        off = (dx.cpu().double() - want).abs()
+        assert (off <= 2 * (64 + 22 + 8) * U * size + 2.0 ** -8 * want.abs() + 2.0 ** -134).all()
+        assert ((dw.cpu().double() - want_dw).abs() <= (M + 64 + 60) * U * dw_size + 1e-30).all()
+
+
+@pytest.mark.parametrize("K", [512, 2064, 4096, 8192, 12288, 20480])
+def test_gradient_of_such_rows_in_place(w8, K):
+    h = far_rows(K, 5).repeat(90, 1)
+    dn, dh = (torch.randn_like(h.float()).mul(2.0 ** -20).to(BF) for _ in range(2))
+    want = w8.add_rms_norm_backward(*dev(dn, h), eps=0.0, dh=dh.to(DEV))
+    for into in range(3):
+        t = list(dev(dn, h, dh))
+        got = w8.add_rms_norm_backward(t[0], t[1], eps=0.0, dh=t[2], dx=t[into])
+        assert got[0].data_ptr() == t[into].data_ptr()
+        assert torch.equal(bits(got[0]), bits(want[0])) and torch.equal(bits(got[1]), bits(want[1]))
+
+
+def test_zero_rows_pass_the_residuals_gradient_alone(w8):
+    z = torch.zeros(3, 2064, dtype=BF, device=DEV)
+    dx, dw = w8.add_rms_norm_backward(z + 1, z, None, eps=0.0, dh=z + 2)
+    assert (dx == 2).all() and not dw.any()
+    q, s, _ = w8.add_rms_norm_quantize(z, eps=0.0)
+    assert not q.any() and not s.any()

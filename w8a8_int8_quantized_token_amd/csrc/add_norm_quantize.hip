@@ -6,7 +6,8 @@
 // The normed value v / rms is never formed: its factor 1 / rms is common to the
 // row, so it cancels in v / s and goes into the scale.  h w is exact (8 + 8
 // bits), so the codes depend on no order of summation; the sum of squares
-// enters the scale alone.
+// enters the scale alone.  Squares of bf16 values may vanish or overflow in fp32
+// (below 2^-75, above 2^64): such a row, found by its sum, is summed again.
 //
 // Gradient with the rounding to codes passed straight through, for dn (of the
 // normed row) and dh (of h, from what else reads it), r = 1 / rms, hh = h r:
@@ -64,6 +65,18 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_maxf(float v) {
   return over_lanes(v, [](float a, float b) { return larger(a, b); });
+}
+
+// Whether fp32 has the sum of squares: 24 bits of it, or eps is so much larger
+// that what vanished does not matter.  (The same in all lanes: a scalar branch.)
+__device__ __forceinline__ bool in_range(float sq, float eps) {
+  return __builtin_amdgcn_ballot_w64(sq < INFINITY && (sq >= 0x1p-100f || eps >= 0x1p-100f)) != 0;
+}
+// Where it has not, the sum is made again in 64 bits, from the row in registers.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll 1
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
 }
 
 // fl32(v / s) for any fp32 |v| <= 448 s, from the correctly rounded r = 1 / s:
@@ -131,6 +144,7 @@ template <int kWaves, int kPieces, bool F8>
 __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel(Norm a) {
   constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves, kStride = kWaves * kWave;
   __shared__ f32x2 part[kRows > 1 ? 1 : kWaves];
+  __shared__ double far_part[kRows > 1 ? 1 : kWaves];
   const int tid = threadIdx.x % kStride;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kStride;
   if (kRows > 1 && row >= a.M) return;   // whole wavefronts, and no barriers with several rows
@@ -186,6 +200,27 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
   }
   const RowScale rs = scale_of<F8>(top);
   const bool zero = rs.s == 0.0f;
+  const float n = (float)(a.chunks * 8);
+  float far_scale = -1.0f;   // (below 0: not used)
+  if (!in_range(sq, a.eps)) {
+    double far = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        far = fma((double)low(h[i][e]), (double)low(h[i][e]), far);
+        far = fma((double)high(h[i][e]), (double)high(h[i][e]), far);
+      }
+    far = wave_sum(far);
+    if constexpr (kWaves > 1) {
+      if (threadIdx.x % kWave == 0) far_part[threadIdx.x / kWave] = far;
+      __syncthreads();
+      far = 0.0;
+#pragma unroll 1
+      for (int k = 0; k < kWaves; ++k) far += far_part[k];
+    }
+    far_scale = (float)(rs.s / sqrt(far / n + a.eps));
+  }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = tid + i * kStride;
@@ -202,7 +237,7 @@ __global__ __launch_bounds__(kWave * (kWaves > 4 ? kWaves : 4)) void norm_kernel
     }
     if (c < a.chunks) a.q[base + c] = zero ? u32x2{0, 0} : quantize8<F8>(v, rs);
   }
-  if (tid == 0) a.scale[row] = zero ? 0.0f : rs.s / sqrtf(sq / (float)(a.chunks * 8) + a.eps);
+  if (tid == 0) a.scale[row] = zero ? 0.0f : far_scale < 0.0f ? rs.s / sqrtf(sq / n + a.eps) : far_scale;
 }
 
 template <int kWaves, int kPieces>
@@ -268,34 +303,19 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGrad a) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) load(row, i, p[i]);
   };
-  if constexpr (kRows == Rows::kAhead) load_row(blockIdx.x, now);
-  int parity = 0;
-  const float n = (float)(a.chunks * 8);
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    if constexpr (kRows == Rows::kAhead) load_row(row + gridDim.x, next);
-    else if constexpr (kRows == Rows::kKept) load_row(row, now);
-    float sq = 0.0f, along = 0.0f;
-    auto reduce = [&](const Piece& p, u32x4 wt) __attribute__((always_inline)) {
+  float sq, along;   // of a row: h^2 and dn w h
+  auto reduce = [&](const Piece& p, u32x4 wt, auto f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float h0 = low(p.h[e]), h1 = high(p.h[e]);
-        sq = fmaf(h0, h0, sq);
-        sq = fmaf(h1, h1, sq);
-        along = fmaf(low(p.dn[e]) * low(wt[e]), h0, along);
-        along = fmaf(high(p.dn[e]) * high(wt[e]), h1, along);
-      }
-    };
-    if constexpr (kRows == Rows::kReload) {
-#pragma unroll 1
-      for (int i = 0; i < kPieces; ++i) {
-        Piece p;
-        load(row, i, p);
-        reduce(p, weight(i));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) reduce(now[i], w[i]);
+    for (int e = 0; e < 4; ++e) {
+      const float h0 = f(low(p.h[e])), h1 = f(high(p.h[e]));
+      sq = fmaf(h0, h0, sq);
+      sq = fmaf(h1, h1, sq);
+      along = fmaf(low(p.dn[e]) * low(wt[e]), h0, along);
+      along = fmaf(high(p.dn[e]) * high(wt[e]), h1, along);
     }
+  };
+  int parity = 0;
+  auto join = [&]() __attribute__((always_inline)) {
     sq = wave_sum(sq);
     along = wave_sum(along);
     // (two buffers: a wavefront is at most one barrier ahead of another)
@@ -305,33 +325,75 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGrad a) {
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) sq += part[parity][k][0], along += part[parity][k][1];
     parity ^= 1;
-    const float power = sq / n + a.eps;
-    const float r = power == 0.0f ? 0.0f : 1.0f / sqrtf(power);
-    const float t = along * r / n;   // mean(dn w hh)
-#pragma unroll
+  };
+  auto sums_of_reloaded = [&](int64_t row, auto f) __attribute__((always_inline)) {
+    sq = along = 0.0f;
+#pragma unroll 1
     for (int i = 0; i < kPieces; ++i) {
-      const int c = tid + i * kThreads;
       Piece p;
-      u32x4 wt;
-      if constexpr (kRows == Rows::kReload) {
-        load(row, i, p);
-        wt = weight(i);
-      } else {
-        p = now[i];
-        wt = w[i];
-      }
-      u32x4 o;
+      load(row, i, p);
+      reduce(p, weight(i), f);
+    }
+    join();
+  };
+  const float n = (float)(a.chunks * 8);
+  // Piece i of dx, and its share of the weight's gradient; t: mean(dn w hh).
+  auto put = [&](int64_t row, int i, const Piece& p, u32x4 wt, float r, float t, auto f) __attribute__((always_inline)) {
+    const int c = tid + i * kThreads;
+    u32x4 o;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float h0 = low(p.h[e]) * r, h1 = high(p.h[e]) * r;
-        const float d0 = low(p.dn[e]), d1 = high(p.dn[e]);
-        sum[i][2 * e] = fmaf(d0, h0, sum[i][2 * e]);
-        sum[i][2 * e + 1] = fmaf(d1, h1, sum[i][2 * e + 1]);
-        const float g0 = fmaf(d0, low(wt[e]), -(h0 * t)), g1 = fmaf(d1, high(wt[e]), -(h1 * t));
-        o[e] = pack2(fmaf(r, g0, low(p.dh[e])), fmaf(r, g1, high(p.dh[e])));
+    for (int e = 0; e < 4; ++e) {
+      const float h0 = f(low(p.h[e])) * r, h1 = f(high(p.h[e])) * r;
+      const float d0 = low(p.dn[e]), d1 = high(p.dn[e]);
+      sum[i][2 * e] = fmaf(d0, h0, sum[i][2 * e]);
+      sum[i][2 * e + 1] = fmaf(d1, h1, sum[i][2 * e + 1]);
+      const float g0 = f(fmaf(d0, low(wt[e]), -(h0 * t))), g1 = f(fmaf(d1, high(wt[e]), -(h1 * t)));
+      o[e] = pack2(fmaf(r, g0, low(p.dh[e])), fmaf(r, g1, high(p.dh[e])));
+    }
+    if (c < a.chunks) a.dx[row * a.chunks + c] = o;
+  };
+  auto plain = [](float v) __attribute__((always_inline)) { return v; };
+
+  if constexpr (kRows == Rows::kAhead) load_row(blockIdx.x, now);
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+    if constexpr (kRows == Rows::kAhead) load_row(row + gridDim.x, next);
+    else if constexpr (kRows == Rows::kKept) load_row(row, now);
+    if constexpr (kRows == Rows::kReload) {
+      sums_of_reloaded(row, plain);
+    } else {
+      sq = along = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) reduce(now[i], w[i], plain);
+      join();
+    }
+    // A row whose squares leave fp32's range (or, with eps = 0, one of zeros): h
+    // times a power of two, half of it here and half in r: hh = (h half) (r half),
+    // dx = dh + (r half) (half (dn w - hh t)).  Such a row is loaded again, which
+    // leaves the others their registers (4096 x 2560 21.8 us; 22.3 with half in every
+    // row's products, 21.1 without any of this; in the loop of reloaded rows half costs
+    // nothing).
+    float half = 1.0f;
+    if (kRows != Rows::kReload && in_range(sq, a.eps)) {
+      const float r = 1.0f / sqrtf(sq / n + a.eps), t = along * r / n;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) put(row, i, now[i], w[i], r, t, plain);
+    } else {
+      if (kRows != Rows::kReload || !in_range(sq, a.eps)) {
+        half = sq < 1.0f ? 0x1p50f : 0x1p-50f;
+        sums_of_reloaded(row, [&](float v) __attribute__((always_inline)) { return v * (half * half); });
       }
-      if (c < a.chunks) a.dx[row * a.chunks + c] = o;
-      if constexpr (kRows == Rows::kAhead) now[i] = next[i];
+      const float power = sq / n + a.eps * half * half * half * half;
+      const float r = power == 0.0f ? 0.0f : 1.0f / sqrtf(power), t = along * r / n;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        Piece p;
+        load(row, i, p);
+        put(row, i, p, weight(i), r * half, t, [&](float v) __attribute__((always_inline)) { return v * half; });
+      }
+    }
+    if constexpr (kRows == Rows::kAhead) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) now[i] = next[i];
     }
   }
   if (a.part == nullptr) return;

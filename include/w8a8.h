@@ -466,7 +466,8 @@ w8a8_status w8a8_add_rms_norm_backward(const uint16_t *dn, const uint16_t *dh, c
  * Sums are fp32; t is rounded because it is an operand of the bf16 matrix
  * cores.  A token without an adapter has the bits of w8a8_linear, and no
  * token's result depends on another adapter's values (be they NaN) or on its
- * neighbours.  Adapters of different ranks are padded with zeros.  Any order
+ * neighbours; a value of b that is not finite reaches its channel of its
+ * adapter's tokens alone, whichever kernel runs.  Adapters of different ranks are padded with zeros.  Any order
  * of ids is right; long runs of tokens with the same adapter are the fast one.
  * The dynamic form takes bf16 activations, with the same bits as
  * w8a8_quantize_act and w8a8_linear_adapters: two launches for a few tokens.

@@ -1,0 +1,78 @@
+"""The linear with low-rank adapters where it can go wrong: values of an
+adapter that are not finite."""
+import pytest
+import torch
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF = torch.bfloat16
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def w8():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible GPU")
+    import w8a8_int8_quantized_token_amd as pkg
+    return pkg
+
+
+def dev(*ts):
+    return tuple(None if t is None else t.to(DEV) for t in ts)
+
+
+def same(a, b):
+    a, b = a.detach().contiguous(), b.detach().contiguous()
+    return a.shape == b.shape and torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def inputs(M, K, N, R, L, seed):
+    g = torch.Generator().manual_seed(seed + M + N)
+    xq, xs = ref.codes_of(torch.randn(M, K, generator=g).to(BF))
+    wq, ws = ref.codes_of((torch.randn(N, K, generator=g) * 0.05).to(BF))
+    a = (torch.randn(L, R, K, generator=g) / K ** 0.5).to(BF)
+    b = (torch.randn(L, N, R, generator=g) * 0.3).to(BF)
+    scaling = torch.rand(L, generator=g) + 0.5
+    ids = torch.randint(-1, L, (M,), generator=g).to(torch.int32)
+    return xq, xs, wq, ws, a, b, ids, scaling
+
+
+@pytest.mark.parametrize("M,N,K,R", [(1, 300, 256, 16), (5, 300, 1024, 24), (16, 5000, 800, 16), (32, 520, 512, 40), (48, 256, 6144, 16),
+                                     (300, 520, 256, 24), (777, 603, 400, 40), (700, 1032, 512, 128), (4608, 4104, 256, 16)])
+def test_a_channel_that_is_not_finite_is_alone(w8, M, N, K, R):
+    """A NaN or an infinity in an adapter's b reaches its own tokens in its own channel, in every tile alike."""
+    xq, xs, wq, ws, a, b, ids, scaling = inputs(M, K, N, R, 4, 1)
+    ids[0] = 1
+    bad = b.clone()
+    bad[1, 5, 2], bad[1, N - 1, R - 1], bad[2, 70, :], bad[3, 200, 0] = INF, NAN, -INF, -INF
+    hit = torch.zeros(M, N, dtype=torch.bool)
+    for i, n in [(1, 5), (1, N - 1), (2, 70), (3, 200)]:
+        hit[ids == i, n] = True
+    hit = hit.to(DEV)
+    first = dev(xq, xs, wq, ws, a)
+    last = dev(ids, scaling)
+    for tile in (-1, *range(w8.num_tiles())):
+        clean = w8.linear_adapters(*first, b.to(DEV), *last, tile=tile)
+        y = w8.linear_adapters(*first, bad.to(DEV), *last, tile=tile)
+        assert not torch.isfinite(y[hit]).any(), tile
+        assert same(y[~hit], clean[~hit]), tile
+        assert torch.isinf(y[(ids == 1).to(DEV), 5]).all() and torch.isinf(y[(ids == 3).to(DEV), 200]).all(), tile
+
+
+@pytest.mark.parametrize("M,N,K,R", [(5, 64, 300 * 16, 16), (40, 2776, 2592, 16), (300, 520, 272, 24), (700, 2048, 512, 40)])
+def test_a_column_that_is_not_finite_is_alone_in_gradients(w8, M, N, K, R):
+    """The same of a and the input's gradient."""
+    xq, xs, wq, ws, a, b, ids, scaling = inputs(M, K, N, R, 4, 2)
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(M)).to(BF)
+    bad = a.clone()
+    bad[1, 2, 5], bad[2, R - 1, K - 1] = INF, NAN
+    hit = torch.zeros(M, K, dtype=torch.bool)
+    hit[ids == 1, 5] = hit[ids == 2, K - 1] = True
+    hit = hit.to(DEV)
+    args = dev(dy, xq, xs, wq, ws)
+    clean = w8.linear_adapters_backward(*args, *dev(a, b, ids, scaling), da=False, db=False)[0]
+    dx = w8.linear_adapters_backward(*args, *dev(bad, b, ids, scaling), da=False, db=False)[0]
+    assert not torch.isfinite(dx[hit]).any() and same(dx[~hit], clean[~hit])

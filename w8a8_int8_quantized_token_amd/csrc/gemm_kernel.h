@@ -206,6 +206,11 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
+// The two 16-bit halves of a word as bf16 values, with zeros for infinities and NaNs.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0 : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0 : w & 0xffff0000u);
+}
+
 // Buffer accesses (kept out of the kernel's lambdas like dma16): a range of
 // `n` bf16 values, 16-byte loads and stores at byte offsets in it; loads past
 // its end give zeros, stores past it are dropped.
@@ -787,13 +792,14 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
   // in the accumulators: for 16 (bf16 32) ranks at a time one pass for each
   // adapter that the wavefront's tokens have, with the other tokens' rows of t
   // taken as zeros; the next passes' fragments are on the way meanwhile.  (A
-  // zero times an infinity or a NaN would reach the other tokens, so where an
-  // adapter's fragments of b hold one they are taken as zeros and its own
-  // tokens' of t as NaNs.)  The bf16 tiles have no registers for that: there
+  // zero times an infinity or a NaN would reach the other tokens, so such values
+  // of b are taken as zeros here and `put_low_left` adds them to the outputs of
+  // the adapter's own tokens.)  The bf16 tiles have no registers for that: there
   // each product is made by itself and taken by the adapter's tokens alone.
   constexpr int kLowRows = Op::kBf16 ? 16 : 32, kLowM = T::TM / kLowRows;   // row tiles of a wavefront
   constexpr int kLowN = Op::kBf16 ? 2 * T::FN : T::FN;                      // fragments of its channels
   constexpr int kLowStep = Op::kBf16 ? 32 : 16;                            // ranks of an MFMA
+  [[maybe_unused]] bool low_left = false;   // values of b that are not finite were met
   // `before`: called once the first pass's loads are on the way.
   auto add_low = [&](const TileAddr& at, auto before) __attribute__((always_inline)) {
     if constexpr (kLow<EPI>) {
@@ -904,16 +910,18 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           for (int j = 0; j < kLowN; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) most = max_halves(most, (uint32_t)fb[p][j][e] & 0x7fff7fffu);
-          const bool drop = __builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0;
+          if (__builtin_amdgcn_ballot_w64((most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u) != 0) {
+            low_left = true;
 #pragma unroll
-          for (int j = 0; j < kLowN; ++j)
+            for (int j = 0; j < kLowN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fb[p][j][e] = drop ? 0 : fb[p][j][e];
+              for (int e = 0; e < 4; ++e) fb[p][j][e] = finite_halves(fb[p][j][e]);
+          }
 #pragma unroll
           for (int i = 0; i < kLowM; ++i) {
             v4i t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = id[i] == pass_a[p] ? (drop ? 0x7fc07fc0 : ft[i][e]) : 0;
+            for (int e = 0; e < 4; ++e) t[e] = id[i] == pass_a[p] ? ft[i][e] : 0;
 #pragma unroll
             for (int j = 0; j < kLowN; ++j)
               acc[i][j] = __builtin_bit_cast(
@@ -933,6 +941,40 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
             add(p);
             request(p);
           }
+        }
+      }
+    }
+  };
+
+  // What add_low left out of a tile that begins at (m0, n0), once the wavefront's
+  // outputs are stored: t b of the values of b that are not finite, added to the
+  // outputs of their channels.  Rare, so a plain loop without registers to speak
+  // of (a choice between two results in add_low's passes spills).
+  auto put_low_left = [&](int m0, int n0) __attribute__((always_inline)) {
+    if constexpr (kLow<EPI> && !Op::kBf16) {
+      if (!low_left) return;
+      low_left = false;
+      wait_vmcnt<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      int e_lane = lane;
+      asm volatile("" : "+v"(e_lane) : : "memory");
+#pragma unroll 1
+      for (int i = 0; i < T::FM; ++i) {
+        const int m = m0 + wm * T::TM + i * 32 + e_lane % 32, id = m < M ? extra.ids[m] : -1;
+        if (id < 0 || id >= extra.count) continue;
+        const uint16_t* const t = extra.t + (int64_t)m * extra.ldt;
+#pragma unroll 1
+        for (int c = e_lane / 32; c < T::TN; c += 2) {
+          const int n = n0 + wn * T::TN + c;
+          if (n >= N) break;
+          const uint16_t* const b = extra.b + id * extra.b_stride + (int64_t)n * extra.R;
+          float left = 0.0f;
+#pragma unroll 1
+          for (int r = 0; r < extra.R; ++r)
+            if ((b[r] & 0x7f80u) == 0x7f80u) left += bf16_to_float(t[r]) * bf16_to_float(b[r]);
+          if (left == 0.0f) continue;
+          uint16_t* const y = reinterpret_cast<uint16_t*>(out) + (int64_t)m * ldy + n;
+          *y = __builtin_bit_cast(uint16_t, (__bf16)(bf16_to_float(*y) + left));
         }
       }
     }
@@ -1573,6 +1615,7 @@ __global__ __launch_bounds__(T::kThreads, (kResident<T, EPI, Op>)) void gemm_i8_
           }
         }
       }
+      put_low_left(m0, n0);
       if (has_next) cur = nxt;
     } else {
       TileAddr nxt;

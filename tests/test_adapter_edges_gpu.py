@@ -1,5 +1,5 @@
 """The linear with low-rank adapters where it can go wrong: values of an
-adapter that are not finite."""
+adapter that are not finite, and what the other tokens are."""
 import pytest
 import torch
 
@@ -76,3 +76,30 @@ def test_a_column_that_is_not_finite_is_alone_in_gradients(w8, M, N, K, R):
     clean = w8.linear_adapters_backward(*args, *dev(a, b, ids, scaling), da=False, db=False)[0]
     dx = w8.linear_adapters_backward(*args, *dev(bad, b, ids, scaling), da=False, db=False)[0]
     assert not torch.isfinite(dx[hit]).any() and same(dx[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("M,K,R", [(4096, 4096, 16), (8192, 4096, 16), (3000, 2576, 32), (2048, 4096, 64)])
+def test_a_token_does_not_depend_on_its_neighbours_adapters(w8, M, K, R):
+    """t as it is: the weight adds nothing and b is the identity.  Of the gradients, u likewise."""
+    L = 16
+    xq, xs, _, _, a, _, ids, scaling = inputs(M, K, R, R, L, 3)
+    other = torch.where(torch.rand(M, generator=torch.Generator().manual_seed(4)) < 0.5, ids, (ids + 5) % L).to(torch.int32)
+    keep = (other == ids).to(DEV)
+    runs = torch.arange(M, dtype=torch.int32) * L // M
+    no_weight = dev(torch.zeros(R, K, dtype=torch.int8), torch.zeros(R))
+    eye = torch.eye(R).to(BF).expand(L, R, R).contiguous()
+
+    def t(ids):
+        return w8.linear_adapters(*dev(xq, xs), *no_weight, *dev(a, eye, ids, scaling))
+
+    assert same(t(ids)[keep], t(other)[keep])
+    own = (runs == ids).to(DEV)
+    assert own.any() and same(t(ids)[own], t(runs)[own])
+    dy = torch.randn(M, K, generator=torch.Generator().manual_seed(5)).to(BF)
+    b = (a.transpose(1, 2) * 0.3).contiguous()
+    no_weight = dev(torch.zeros(K, R, dtype=torch.int8), torch.zeros(K))
+
+    def u(ids):
+        return w8.linear_adapters_backward(dy.to(DEV), None, None, *no_weight, *dev(eye, b, ids, scaling), da=False, db=False)[0]
+
+    assert same(u(ids)[keep], u(other)[keep]) and same(u(ids)[own], u(runs)[own])

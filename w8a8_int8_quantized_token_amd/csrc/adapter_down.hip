@@ -184,10 +184,11 @@ struct Lds {
 //
 // A step is 64 or 128 values of k, a quarter of them in a row in each lane
 // (both operands are dealt alike), 16 bytes for an MFMA.  Each wavefront has a
-// range of k of its own, and tiles start at different places of it: rows are
-// whole pages or parts of them apart, and wavefronts that all read the same
-// place of every row keep a few memory channels busy (8192 rows of 4096 codes: 26
-// us).  kDepth steps of loads are in flight.
+// range of k of its own and walks it in order, so that a row's sum is the same
+// whatever rows share its tile.  (Starts that differ from tile to tile, so that
+// not all wavefronts read the same place of rows that are pages apart: no faster
+// on codes, 8192 rows of 4096 values 36 us and not 37.)  kDepth steps of loads are
+// in flight.
 template <Rows R, int kTiles>
 __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int rank_block, int slot, int slots,
                                            Lds<kTiles>& lds) {
@@ -228,12 +229,9 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int ran
   const int steps = (a.K + kStepK - 1) / kStepK, per = (steps + kWaves - 1) / kWaves;
   const int from = wave * per, here = max(min(per, steps - from), 0);   // this wavefront's steps
   int64_t row[2];
-  int turn = 0;
   // Step n of the wavefront's; past its end zeros.
   auto load = [&](const uint16_t* p, int n, Step& v) __attribute__((always_inline)) {
-    int s = n + turn;
-    s = from + (s < here ? s : s - here);
-    const int k = n < here ? s * kStepK + kLane * h : a.ldp;
+    const int k = n < here ? (from + n) * kStepK + kLane * h : a.ldp;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -292,7 +290,6 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int ran
       const bool writes = t < kTiles && r < a.ldt && mine * kTileRows + i * 16 + l16 < rows;
       const int64_t m = i ? row[1] : row[0];
       const float f = a.scaling[ad], scale = kCodes ? a.scale[m] : 1.0f, s2 = a.t2 != nullptr ? a.scale2[m] : 0.0f;
-      turn = here * (int)((chunk * (kChunk / kTileRows) + mine) % 4) / 4;
       f32x4 acc[kTiles][2];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};

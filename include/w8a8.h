@@ -497,16 +497,16 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t *x, const int8_t *wq,
  * Gradients of w8a8_linear_adapters for dy bf16 [M,N], on frozen codes of the
  * weight, the rounding of the activations to codes passed straight through.
  * With i = ids[m], x and t as above and
- *   u[m,r] = bf16( scaling[i] * sum_n dy[m,n] * b[i][n,r] ):
+ *   u[m,r] = scaling[i] * sum_n dy[m,n] * b[i][n,r]:
  *   dx[m,k]    = bf16( sum_n dy[m,n] * w[n,k] + sum_r u[m,r] * a[i][r,k] ),
  *   da[i][r,k] = bf16( sum over the adapter's tokens of u[m,r] * x[m,k] ),
  *   db[i][n,r] = bf16( sum over the adapter's tokens of dy[m,n] * t[m,r] ),
  * bf16 [M,K], [L,R,K] and [L,N,R]; an adapter without tokens gets zeros.  Each
  * is left out where its pointer is NULL; dx needs wq, w_scale, a and b, da needs
- * b, xq and x_scale, db needs a, xq and x_scale.  Sums are fp32, on operands
- * rounded to bf16 once (of da, u times x's scale); in small calls (M times R,
- * rounded up to 16, at most 2048) da and db take what that rounding leaves, too.
- * No atomics, the same bits from call to call.  Contract as for w8a8_linear_adapters and
+ * b, xq and x_scale, db needs a, xq and x_scale.  Sums are fp32.  Of dx, u and
+ * w are rounded to bf16 once; da and db take u (times x's scale) and t to 2^-16, so
+ * that their own rounding is the only one that is seen.  No atomics, the same bits
+ * from call to call.  Contract as for w8a8_linear_adapters and
  * w8a8_linear_backward; da and db 16-byte aligned.
  */
 size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R,

@@ -1,8 +1,10 @@
 """The linear with low-rank adapters where it can go wrong: values of an
-adapter that are not finite, and what the other tokens are."""
+adapter that are not finite, what the other tokens are, and the roundings of
+gradients whatever the number of tokens."""
 import pytest
 import torch
 
+import adapter_ref as aref
 import block_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +105,64 @@ def test_a_token_does_not_depend_on_its_neighbours_adapters(w8, M, K, R):
         return w8.linear_adapters_backward(dy.to(DEV), None, None, *no_weight, *dev(eye, b, ids, scaling), da=False, db=False)[0]
 
     assert same(u(ids)[keep], u(other)[keep]) and same(u(ids)[own], u(runs)[own])
+
+
+def rms(e):
+    return float(e.square().mean().sqrt())
+
+
+def once(got, want, rows=None):
+    """Beside its own rounding to bf16 no other error of a gradient is seen (fp32 sums, operands to 2^-17)."""
+    got, want = got.cpu().double(), want.cpu()
+    if rows is not None:
+        got, want = got[rows], want[rows]
+    return rms(got - want) <= 1.03 * rms(want.to(BF).double() - want)
+
+
+# few tokens of each adapter in a batch of some, of few assigned tokens among many, of long lists; rows and blocks
+# of the first products
+ONCE = [(150, 256, 264, 8, 8, "mixed"), (33, 512, 264, 64, 5, "mixed"), (300, 256, 255, 16, 40, "mixed"), (1500, 512, 520, 24, 200, "mixed"),
+        (600, 512, 520, 16, 3, "rare"), (2500, 512, 520, 16, 3, "rare"), (2100, 512, 264, 128, 2, "rare"),
+        (1000, 512, 520, 16, 1, "mixed"), (4096, 512, 520, 16, 1, "mixed"), (4096, 256, 264, 64, 4, "mixed"), (9000, 256, 136, 32, 2, "mixed"),
+        (700, 256, 5, 40, 2, "mixed")]
+
+
+@pytest.mark.parametrize("M,K,N,R,L,kind", ONCE)
+def test_adapters_gradients_are_rounded_once(w8, M, K, N, R, L, kind):
+    xq, xs, wq, ws, a, b, ids, scaling = inputs(M, K, N, R, L, 6)
+    g = torch.Generator().manual_seed(M)
+    dy = torch.randn(M, N, generator=g).to(BF)
+    if kind == "rare":
+        ids = torch.where(torch.rand(M, generator=g) < 12 / M, ids, torch.full_like(ids, -1))
+    inp = (dy, xq, xs, wq, ws, a, b, ids, scaling)
+    got = w8.linear_adapters_backward(*dev(*inp))
+    want = aref.grads(*inp)
+    for i in (1, 2):
+        assert once(got[i], want[i][0]), ("da", "db")[i - 1]
+    # each asked for alone has the same bits
+    assert same(w8.linear_adapters_backward(*dev(*inp), False, True, False)[1], got[1])
+    assert same(w8.linear_adapters_backward(*dev(*inp), False, False, True)[2], got[2])
+
+
+@pytest.mark.parametrize("M", [40, 3000])
+def test_infinities_beside_the_roundings_rest(w8, M):
+    """An infinity in dy, x's scale or the scaling is no NaN in the gradients that the definition leaves infinite."""
+    K, N, R = 64, 136, 16
+    xq, xs, wq, ws, a, b, ids, scaling = inputs(M, K, N, R, 2, 7)
+    ids = torch.arange(M, dtype=torch.int32) * 2 // M
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(M)).to(BF)
+    plain = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, ids, scaling))
+    bad = dy.clone()
+    bad[0, 3], bad[M - 1, 77] = INF, -INF
+    got = w8.linear_adapters_backward(*dev(bad, xq, xs, wq, ws, a, b, ids, scaling))[2]
+    hit = torch.zeros(2, N, dtype=torch.bool, device=DEV)
+    hit[0, 3] = hit[1, 77] = True
+    assert torch.isinf(got[hit]).all() and same(got[~hit], plain[2][~hit])
+    # an infinite scaling: t is infinite, and db where dy is not zero (a sum of infinities of either sign is a NaN)
+    big = scaling.clone()
+    big[0] = INF
+    one = ids.clone()
+    one[1:] = 1                                       # the first adapter has one token
+    got = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, one, big))
+    assert torch.isinf(got[2][0]).all() and torch.isfinite(got[2][1].float()).all() and torch.isfinite(got[1][1].float()).all()
+    assert torch.isinf(got[1][0][:, (xq[0] != 0).to(DEV)]).all()

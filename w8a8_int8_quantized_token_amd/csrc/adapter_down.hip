@@ -6,8 +6,9 @@
 // are quantized on the way (codes and scales are outputs too, the same as
 // quantize_rows'), or bf16 values.  t is rounded to bf16 once, from fp32 sums:
 // it is the operand of the next product, on the bf16 matrix cores, whose result
-// is rounded to bf16 with the linear's; t's rounding is 2^-9 of each of its
-// terms, of either sign.
+// is rounded to bf16 with the linear's; t's rounding is up to 2^-8 of each of its
+// terms, of either sign.  For the matrices' gradients, whose sums are long, the
+// values come out in two bf16 parts instead (`two_parts`).
 //
 // Few rows: a workgroup takes one row and 16 ranks, a wavefront two of them,
 // with the lanes along k (M K R fused multiply-adds, and P read once for each
@@ -41,6 +42,14 @@ constexpr u32x4 kZeros = {0, 0, 0, 0};
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+// v in two bf16 parts, the high half its leading bits, the low half the rest.
+// Both have v's sign and neither is a zero unless v is, so that the products with
+// an infinity are the same infinity: a rest of nothing is taken as 2^-17 of v.
+__device__ __forceinline__ uint32_t two_parts(float v) {
+  const uint32_t bits = __float_as_uint(v) | (__float_as_uint(v) % 65536 != 0 || v == 0.0f ? 0u : 0x40u);
+  const float high = __uint_as_float(bits & 0xffff0000u), rest = __uint_as_float(bits) - high;
+  return (bits & 0xffff0000u) | (fabsf(v) < INFINITY ? pack2(rest, 0.0f) : bits >> 16);
 }
 // Eight bf16 values of a row of K from column k on, zeros past its end, from
 // any 2-byte address.
@@ -143,19 +152,10 @@ __device__ __forceinline__ void down_row(const Down& a) {
     for (int k = 0; k < 2; ++k) sum[k] = sum_lanes(sum[k]) * scale * f;
   }
   if (lane == 0) {
-    *reinterpret_cast<uint32_t*>(a.t + m * a.ldt + r0) = pack2(sum[0], sum[1]);
-    if (a.t2 != nullptr) {
-      const float s2 = id >= 0 ? a.scale2[m] : 0.0f;
-      sum[0] *= s2, sum[1] *= s2;
-      *reinterpret_cast<uint32_t*>(a.t2 + m * a.ldt + r0) = pack2(sum[0], sum[1]);
-    }
-    if (a.low != nullptr) {
-      const uint32_t w = pack2(sum[0], sum[1]);
-      const auto rest = [](float v, uint32_t bits) {   // (of an infinity or a NaN: nothing)
-        const float high = __uint_as_float(bits);
-        return fabsf(high) < INFINITY ? v - high : 0.0f;
-      };
-      *reinterpret_cast<uint32_t*>(a.low + m * a.ldt + r0) = pack2(rest(sum[0], w << 16), rest(sum[1], w & 0xffff0000u));
+    if (a.t != nullptr) *reinterpret_cast<uint32_t*>(a.t + m * a.ldt + r0) = pack2(sum[0], sum[1]);
+    if (a.parts != nullptr) {
+      const float f = a.parts_scale == nullptr ? 1.0f : id >= 0 ? a.parts_scale[m] : 0.0f;
+      *reinterpret_cast<u32x2*>(a.parts + m * a.ldt + r0) = u32x2{two_parts(sum[0] * f), two_parts(sum[1] * f)};
     }
   }
 }
@@ -210,8 +210,7 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int ran
   }
   auto zeros = [&](int64_t m) __attribute__((always_inline)) {
     for (int r = first; r < min(first + 16 * kTiles, a.ldt); r += 8) {
-      *reinterpret_cast<u32x4*>(a.t + m * a.ldt + r) = kZeros;
-      if (a.t2 != nullptr) *reinterpret_cast<u32x4*>(a.t2 + m * a.ldt + r) = kZeros;
+      if (a.t != nullptr) *reinterpret_cast<u32x4*>(a.t + m * a.ldt + r) = kZeros;
     }
   };
   if (slot == 0) {
@@ -289,7 +288,7 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int ran
       const int t = wave / 2, i = wave % 2, r = first + t * 16 + 4 * h;
       const bool writes = t < kTiles && r < a.ldt && mine * kTileRows + i * 16 + l16 < rows;
       const int64_t m = i ? row[1] : row[0];
-      const float f = a.scaling[ad], scale = kCodes ? a.scale[m] : 1.0f, s2 = a.t2 != nullptr ? a.scale2[m] : 0.0f;
+      const float f = a.scaling[ad], scale = kCodes ? a.scale[m] : 1.0f, s2 = a.parts_scale != nullptr ? a.parts_scale[m] : 1.0f;
       f32x4 acc[kTiles][2];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
@@ -340,10 +339,12 @@ __device__ __forceinline__ void down_block(const Down& a, int64_t chunk, int ran
       for (int w = 1; w < kWaves; ++w) sum += lds.part[w][t][i][lane];
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = r < a.R ? sum[e] * scale * f : 0.0f;
-      *reinterpret_cast<u32x2*>(a.t + m * a.ldt + r) = u32x2{pack2(sum[0], sum[1]), pack2(sum[2], sum[3])};
-      if (a.t2 != nullptr) {
-        const auto v = [&](int e) { return r < a.R ? sum[e] * s2 : 0.0f; };
-        *reinterpret_cast<u32x2*>(a.t2 + m * a.ldt + r) = u32x2{pack2(v(0), v(1)), pack2(v(2), v(3))};
+      if (a.t != nullptr) *reinterpret_cast<u32x2*>(a.t + m * a.ldt + r) = u32x2{pack2(sum[0], sum[1]), pack2(sum[2], sum[3])};
+      if (a.parts != nullptr) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = r < a.R ? two_parts(sum[e] * s2) : 0u;
+        *reinterpret_cast<u32x4*>(a.parts + m * a.ldt + r) = w;
       }
     }
   }
@@ -409,7 +410,7 @@ bool by_rows(int64_t M, int64_t R, int products) {
 // Codes alone, by the rules of as many products: a gradient's bits do not depend
 // on which others are asked for.
 hipError_t launch_codes(const Down& a, bool quantize, int products, hipStream_t s) {
-  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0 || (a.low != nullptr && !by_rows(a.M, a.R, products)))
+  if (a.M < 1 || a.R < 8 || a.R % 8 != 0 || a.ldt < a.R || a.ldt % 16 != 0)
     return hipErrorInvalidValue;
   const dim3 threads(kThreads), rows((unsigned)a.M, (unsigned)(a.ldt / kRanks));
   if (quantize) {
@@ -439,7 +440,7 @@ hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s
   Down c{};   // (M = 0: none)
   if (codes != nullptr) c = *codes;
   if (v.M < 1 || v.R < 8 || v.R % 8 != 0 || v.ldt < v.R || v.ldt % 16 != 0 ||
-      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)) || ((v.low != nullptr || c.low != nullptr) && !by_rows(v.M, v.R, 2)))
+      (c.M > 0 && (c.M != v.M || c.R != v.R || c.ldt != v.ldt)))
     return hipErrorInvalidValue;
   const dim3 threads(kThreads);
   const int both = c.M > 0 ? 2 : 1;

@@ -1,9 +1,16 @@
 // Gradients of the low-rank adapters' two matrices: for each adapter i, over its
 // rows m (tokens),
 //   out[i][r, c] = sum_m v[m, r] x[m, c],
-// v bf16 [M, ldt] (t or u, which have the scalings), x the activations' codes
-// (v then has their scales too) or the output's gradient in bf16.  fp32 sums on
-// the bf16 matrix cores, both operands exact.
+// v [M, ldt] (t or u, which have the scalings), x the activations' codes (v then
+// has their scales too) or the output's gradient in bf16.  fp32 sums on the bf16
+// matrix cores.
+//
+// x is exact in bf16; v comes in two bf16 parts, each multiplied by the same
+// fragment of x.  Rounded to one part, v would be off by up to 2^-8 in each term,
+// and that error grows with the sum as the sum itself does, so that a gradient
+// of any number of rows had 1.4 times the error of its own rounding (relative
+// error 2.4e-3 and not 1.7e-3).  The second part costs nothing up to rank 32
+// and 10 us of 130 at 8192 rows of 4096 and 8192, rank 64.
 //
 // The rows of an adapter come as a list (`lists`, made beside the operands'
 // layout), so ids may be in any order; a row's values lie together, and only
@@ -18,15 +25,9 @@
 // LDS and the parts' go to slices for launch_finish, each in a fixed order; of one
 // part the result is written at once.
 //
-// v is rounded to bf16 once, a relative error of up to 2^-9 in each of its terms.
-// Over a thousand of them these average to about the output's own rounding; where
-// they are fewer (a.low; a token's gradient has eight in all at rank 8) they do not,
-// and v comes in two parts, which a second pass over the few rows adds (22 tokens,
-// rank 8: 4 of 31 us).
-//
 // Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 16.4
-// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 58 (168 MB of x,
-// 2.9 TB/s: 384 workgroups for 256 compute units, whose registers hold one each).
+// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 (168 MB of x,
+// read again for the second 32 ranks).
 #include "kernels.h"
 
 #include <algorithm>
@@ -91,10 +92,9 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
 
   struct Step {
     uint32_t x[8][kWords];
-    uint32_t v[8][(KR + 1) / 2];
+    uint32_t v[8][KR];
   };
   // The step at place p0 of the listed rows (the list goes on with its last row).
-  const uint16_t* from_v = a.v;
   auto load = [&](int p0, Step& s, auto whole) __attribute__((always_inline)) {
     int32_t rows[8];
     __builtin_memcpy(rows, __builtin_assume_aligned(lds.list + p0 + 8 * h, 16), 32);
@@ -116,29 +116,18 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
           }
         }
       }
-      const uint16_t* v = from_v + m * a.ldt + min(rank, a.ldt - KR);
-      if constexpr (KR == 1) s.v[i][0] = *v;
-      else __builtin_memcpy(s.v[i], __builtin_assume_aligned(v, 2 * KR), 2 * KR);
+      __builtin_memcpy(s.v[i], __builtin_assume_aligned(a.v + m * a.ldt + min(rank, a.ldt - KR), KR == 3 ? 4 : 4 * KR), 4 * KR);
     }
     __builtin_amdgcn_sched_barrier(0);   // (moved loads would be waited for sooner)
   };
   auto multiply = [&](Step& s) __attribute__((always_inline)) {
-    if constexpr (!kCodes) {
-      if (from_v != a.v) {   // the low parts of v: an infinity is in the sum already, and times them it would be a NaN
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t x = s.x[i][w];
-            s.x[i][w] = ((x & 0x7f80u) == 0x7f80u ? 0 : x & 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0 : x & 0xffff0000u);
-          }
-      }
-    }
-    u32x4 fv[KR];
+    u32x4 fv[2][KR];   // both parts
 #pragma unroll
     for (int r = 0; r < KR; ++r)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) fv[r][q] = pair(s.v[2 * q][r / 2], s.v[2 * q + 1][r / 2], r);
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) fv[half][r][q] = pair(s.v[2 * q][r], s.v[2 * q + 1][r], half);
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       u32x4 fx;
@@ -150,9 +139,11 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
         else fx[q] = pair(s.x[2 * q][j / 2], s.x[2 * q + 1][j / 2], j);
       }
 #pragma unroll
-      for (int r = 0; r < KR; ++r)
-        acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[r]),
-                                                            __builtin_bit_cast(bf16x8, fx), acc[r][j], 0, 0, 0);
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fv[half][r]),
+                                                              __builtin_bit_cast(bf16x8, fx), acc[r][j], 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -183,7 +174,7 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
 #pragma unroll
         for (int w = 0; w < kWords; ++w) s.x[i][w] = in ? s.x[i][w] : 0;
 #pragma unroll
-        for (int w = 0; w < (KR + 1) / 2; ++w) s.v[i][w] = in ? s.v[i][w] : 0;
+        for (int w = 0; w < KR; ++w) s.v[i][w] = in ? s.v[i][w] : 0;
       }
       multiply(s);
     }
@@ -193,11 +184,7 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     if (base > first) __syncthreads();
     for (int i = threadIdx.x; i < (n + kRows - 1) / kRows * kRows; i += kThreads) lds.list[i] = a.list[base + min(i, n - 1)];
     __syncthreads();
-    for (;; from_v = a.low) {   // (an accumulator takes both parts)
-      run(n);
-      if (a.low == nullptr || from_v == a.low) break;
-    }
-    from_v = a.v;
+    run(n);
   }
   // The sums of the wavefronts that had rows, in order: eight at a time through
   // LDS, one to each wavefront to add up and store.  (The first wavefront alone:
@@ -238,9 +225,15 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, 
   else adapter_grad<KR, KA, true>(ga, blockIdx.x - blocks_b, lds);
 }
 
-// Ranks of a lane, and columns: as many sums as registers allow.
-int ranks_of(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
-int columns_of(int R, bool codes) { return R <= 32 && codes ? 16 : 8; }
+// Ranks of a lane, and columns: as many sums as registers allow.  Us of both
+// gradients without the input's, by ranks and columns (codes, values) of a lane:
+// 4096 rows of 4096 and 4096, rank 32: 2 16 8 46.4, 2 8 8 44.6, 3 8 8 46.8, 4 4 4 42.9;
+// 217 of 2048: 22.0, 21.8, 22.2, 19.8; rank 40, 2048 of 4096: 62, 58.3, 55.1, 56.8; 64
+// of 2592 and 2776: 34.6, 32.8, 27.0, 29.4; rank 48, 4096 of 2048 and 5136: 72, 67, 61,
+// 62; rank 64, 8192 of 4096 and 8192: 146, 142, 161, 142; 2048 of 4096: 44.4, 42.5,
+// 46.1, 43.3; rank 128, 1024 of 4096: 45, 40.8, 44.5, 40.4.
+int ranks_of(int R) { return R <= 16 ? 1 : R > 32 && R <= 48 ? 3 : 2; }
+int columns_of(int R, bool codes) { return R <= 16 && codes ? 16 : 8; }
 
 int64_t col_blocks_of(int64_t C, int R, bool codes) { return (C + 16 * columns_of(R, codes) - 1) / (16 * columns_of(R, codes)); }
 int64_t rank_blocks_of(int R) { return (R + 16 * ranks_of(R) - 1) / (16 * ranks_of(R)); }
@@ -313,8 +306,8 @@ hipError_t launch_adapter_grads(AdapterGrad ga, AdapterGrad gb, hipStream_t s) {
   const dim3 grid((unsigned)(na + nb)), block(kThreads);
   switch (ranks_of(na ? ga.R : gb.R)) {
     case 1: hipLaunchKernelGGL((adapter_grad_kernel<1, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
-    case 2: hipLaunchKernelGGL((adapter_grad_kernel<2, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
-    default: hipLaunchKernelGGL((adapter_grad_kernel<4, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    case 2: hipLaunchKernelGGL((adapter_grad_kernel<2, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    default: hipLaunchKernelGGL((adapter_grad_kernel<3, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
   }
   return hipGetLastError();
 }

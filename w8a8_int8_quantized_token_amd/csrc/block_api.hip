@@ -384,14 +384,13 @@ w8a8_status adapters(const uint16_t* x, const int8_t* xq, const float* x_scale, 
 
 // Workspace of the adapters' gradients: that of dx by itself, the adapters'
 // matrices turned (b: the first operand's rows contiguous along the channels;
-// a: along the ranks), the rows of each adapter, t, u, and u with the codes'
-// scales, and the slices of the matrices' gradients.
+// a: along the ranks), the rows of each adapter, u, t and u with the codes'
+// scales (v), both in two parts, and the slices of the matrices' gradients.
 struct AdapterBackPlan {
   BackPlan x;
   int64_t ldt, ldn;
-  int64_t bt, at, list, starts, t, u, v, low_a, low_b, slices_a, slices_b;
+  int64_t bt, at, list, starts, t, u, v, slices_a, slices_b;
   int parts_a, parts_b;
-  bool exact;   // v and t of the matrices' gradients in two parts
   int64_t bytes;
 };
 AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, bool dx, bool da, bool db,
@@ -400,27 +399,22 @@ AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, in
   p.x = back_plan(M, N, K, false, dx, false, false, copy_dy, few, true);
   p.ldt = up(R, 16);
   p.ldn = up(N, 16);
-  p.exact = M * p.ldt <= w8a8::kExactRows;
   Pieces w;
   w.bytes = p.x.bytes;
-  if (dx || da) {
-    p.bt = w.add(2 * L * R * p.ldn);
-    p.u = w.add(2 * M * p.ldt);
-  }
+  if (dx || da) p.bt = w.add(2 * L * R * p.ldn);
+  if (dx) p.u = w.add(2 * M * p.ldt);
   if (dx && !few) p.at = w.add(2 * L * K * R);
   if (da || db) {
     p.list = w.add(4 * M);
     p.starts = w.add(4 * (L + 1));
   }
   if (da) {
-    p.v = w.add(2 * M * p.ldt);
-    if (p.exact) p.low_a = w.add(2 * M * p.ldt);
+    p.v = w.add(4 * M * p.ldt);
     p.parts_a = w8a8::adapter_grad_parts(M, K, R, L, true);
     if (p.parts_a > 1) p.slices_a = w.add(4 * p.parts_a * L * R * K);
   }
   if (db) {
-    p.t = w.add(2 * M * p.ldt);
-    if (p.exact) p.low_b = w.add(2 * M * p.ldt);
+    p.t = w.add(4 * M * p.ldt);
     p.parts_b = w8a8::adapter_grad_parts(M, N, R, L, false);
     if (p.parts_b > 1) p.slices_b = w.add(4 * p.parts_b * L * R * N);
   }
@@ -735,8 +729,8 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   if (st != W8A8_OK) return st;
   using Job = w8a8::LayoutJob;
   void* const ws = workspace;
-  uint16_t *bt = at<uint16_t>(ws, p.bt), *a_turned = at<uint16_t>(ws, p.at), *t = at<uint16_t>(ws, p.t),
-           *u = at<uint16_t>(ws, p.u), *v = at<uint16_t>(ws, p.v);
+  uint16_t *bt = at<uint16_t>(ws, p.bt), *a_turned = at<uint16_t>(ws, p.at), *u = at<uint16_t>(ws, p.u);
+  uint32_t *t = at<uint32_t>(ws, p.t), *v = at<uint32_t>(ws, p.v);
   int32_t *list = at<int32_t>(ws, p.list), *starts = at<int32_t>(ws, p.starts);
   Job jobs[w8a8::kMaxJobs];
   int n = 0;
@@ -765,18 +759,16 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   dt.p = a;
   dt.p_stride = R * K;
   dt.K = dt.ldp = (int)K;
-  dt.t = t;
-  if (p.exact) dt.low = at<uint16_t>(ws, p.low_b);
+  dt.parts = t;
   du.x = dy;
   du.p = bt;
   du.p_stride = R * p.ldn;
   du.K = (int)N;
   du.ldp = (int)p.ldn;
-  du.t = u;
+  if (dx) du.t = u;
   if (da) {
-    du.t2 = v;
-    du.scale2 = x_scale;
-    if (p.exact) du.low = at<uint16_t>(ws, p.low_a);
+    du.parts = v;
+    du.parts_scale = x_scale;
   }
   TRY(w8a8::launch_down_pair(db ? &dt : nullptr, dx || da ? &du : nullptr, stream));
   w8a8::JoinJob join[w8a8::kMaxJobs];
@@ -795,11 +787,11 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   }
   w8a8::AdapterGrad ga{}, gb{};
   if (da) {
-    ga = {xq, v, du.low, list, starts, at<float>(ws, p.slices_a), da, K, (int)p.ldt, (int)R, (int)L, p.parts_a};
+    ga = {xq, v, list, starts, at<float>(ws, p.slices_a), da, K, (int)p.ldt, (int)R, (int)L, p.parts_a};
     if (p.parts_a > 1) join[joins++] = {ga.slices, da, p.parts_a, L * R * K, true, 0};
   }
   if (db) {
-    gb = {dy, t, dt.low, list, starts, at<float>(ws, p.slices_b), db, N, (int)p.ldt, (int)R, (int)L, p.parts_b};
+    gb = {dy, t, list, starts, at<float>(ws, p.slices_b), db, N, (int)p.ldt, (int)R, (int)L, p.parts_b};
     if (p.parts_b > 1) join[joins++] = {gb.slices, db, p.parts_b, L * R * N, true, 0};
   }
   TRY(w8a8::launch_adapter_grads(ga, gb, stream));

@@ -217,10 +217,10 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
 // and p [count][R][ldp] (adapters p_stride apart; rows 16-byte aligned, ldp a
 // multiple of 16 and at least K, zeros past column K).  Codes: scale [M];
 // quantizing x (where down_quantizes()): codes [M,K] and code_scale [M] are
-// outputs; bf16 values: x at any 2-byte address, rows of K.  t2, where not
-// null: the same times scale2[m].  low, where not null (up to kExactRows rows
-// times ldt): what the rounding of t2, or of t without one, left, in bf16.
-constexpr int64_t kExactRows = 2048;
+// outputs; bf16 values: x at any 2-byte address, rows of K.  t and parts may be
+// null.  parts [M,ldt] has the values (times parts_scale[m], where not null) in 32
+// bits: two bf16 numbers whose sum is the value to 2^-16, the larger one in the
+// upper half (rows without an adapter are not written where rows are many).
 struct Down {
   const void* x;
   const float* scale;
@@ -230,8 +230,9 @@ struct Down {
   int64_t p_stride;
   const int32_t* ids;
   const float* scaling;
-  uint16_t *t, *t2, *low;
-  const float* scale2;
+  uint16_t* t;
+  uint32_t* parts;
+  const float* parts_scale;
   int64_t M;
   int K, ldp, R, ldt, count;
 };
@@ -257,13 +258,13 @@ hipError_t launch_splitk_reduce_low(const int32_t* partials, int chunks, const f
 
 // Gradients of an adapter's matrix (adapter_grad.hip): slices fp32 [parts][count]
 // [R][C] from codes x [M,C] (rows 16-byte aligned), or [parts][count][C][R] from
-// bf16 x (any 2-byte address), for a JoinJob.  v bf16 [M,ldt]; list [M] and
-// starts [count + 1]: the rows of each adapter (LayoutJob::kLists).  parts =
-// adapter_grad_parts(); of one part the result goes to out in bf16, and slices are
-// not used.  col_blocks and rank_blocks are set by the launch.
+// bf16 x (any 2-byte address), for a JoinJob.  v [M,ldt] in two parts (Down::parts);
+// list [M] and starts [count + 1]: the rows of each adapter (LayoutJob::kLists).
+// parts = adapter_grad_parts(); of one part the result goes to out in bf16, and
+// slices are not used.  col_blocks and rank_blocks are set by the launch.
 struct AdapterGrad {
   const void* x;
-  const uint16_t *v, *low;   // low, or null: what v's rounding left (Down::low)
+  const uint32_t* v;
   const int32_t *list, *starts;
   float* slices;
   uint16_t* out;

@@ -507,7 +507,9 @@ w8a8_status w8a8_linear_adapters_dynamic(const uint16_t *x, const int8_t *wq,
  * w are rounded to bf16 once; da and db take u (times x's scale) and t to 2^-16, so
  * that their own rounding is the only one that is seen.  No atomics, the same bits
  * from call to call.  Contract as for w8a8_linear_adapters and
- * w8a8_linear_backward; da and db 16-byte aligned.
+ * w8a8_linear_backward; da and db 16-byte aligned; those of w, a and b that are
+ * needed in another order (for dx all, for da b) have under 2^24 tiles of 64 by 64
+ * values, each adapter's counted by themselves (else W8A8_ERR_SHAPE, workspace 0).
  */
 size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t R,
                                                int64_t L, int dx, int da, int db);

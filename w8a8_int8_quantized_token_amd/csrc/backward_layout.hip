@@ -365,22 +365,32 @@ int64_t transpose_sum_span(int64_t R, int64_t C) {
   return span;
 }
 
+namespace {
+// Workgroups of a job.
+int64_t blocks_of(const LayoutJob& j) {
+  const auto tiles = [](int64_t v, int64_t t) { return (v + t - 1) / t; };
+  return j.kind == LayoutJob::kPadRows      ? tiles(j.R * (j.ld / 8), kPadBlock)
+         : j.kind == LayoutJob::kTurnValues ? tiles(j.C, kT) * tiles(j.R, j.span)
+         : j.kind == LayoutJob::kTurnEach   ? tiles(j.C, kT) * tiles(j.ld, j.span) * j.batch
+         : j.kind == LayoutJob::kLists      ? j.C
+                                            : tiles(j.C, kCodeCols) * tiles(j.ld, kCodeRows);
+}
+}  // namespace
+
+bool prepare_fits(const LayoutJob* jobs, int n) {
+  int64_t blocks = 0;
+  for (int k = 0; k < n; ++k) blocks += blocks_of(jobs[k]);
+  return blocks <= kMaxBlocks;
+}
+
 hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream) {
+  if (!prepare_fits(jobs, n)) return hipErrorInvalidValue;
   Prepare p;
   int64_t end = 0;
   for (int k = 0; k < kMaxJobs; ++k) {
-    if (k < n) {
-      const LayoutJob& j = p.job[k] = jobs[k];
-      const auto tiles = [](int64_t v, int64_t t) { return (v + t - 1) / t; };
-      end += j.kind == LayoutJob::kPadRows      ? tiles(j.R * (j.ld / 8), kPadBlock)
-             : j.kind == LayoutJob::kTurnValues ? tiles(j.C, kT) * tiles(j.R, j.span)
-             : j.kind == LayoutJob::kTurnEach   ? tiles(j.C, kT) * tiles(j.ld, j.span) * j.batch
-             : j.kind == LayoutJob::kLists      ? j.C
-                                                : tiles(j.C, kCodeCols) * tiles(j.ld, kCodeRows);
-    }
+    if (k < n) end += blocks_of(p.job[k] = jobs[k]);
     p.end[k] = end;
   }
-  if (end > kMaxBlocks) return hipErrorInvalidValue;
   hipLaunchKernelGGL(prepare_kernel, dim3((unsigned)end), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }

@@ -422,6 +422,33 @@ AdapterBackPlan adapter_back_plan(int64_t M, int64_t N, int64_t K, int64_t R, in
   return p;
 }
 
+// The layout in front of the adapters' gradients: its jobs without their
+// addresses, and each of them, or null where there is none.
+struct AdapterLayout {
+  w8a8::LayoutJob jobs[w8a8::kMaxJobs] = {};
+  int n = 0;
+  w8a8::LayoutJob *copy = nullptr, *w = nullptr, *a = nullptr, *b = nullptr, *lists = nullptr;
+
+  AdapterLayout(const AdapterBackPlan& p, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, bool dx, bool da, bool db,
+                bool copy_dy, bool few) {
+    using Job = w8a8::LayoutJob;
+    auto add = [&](Job::Kind kind, int64_t rows, int64_t cols, int64_t ld, int64_t span = 0, int64_t batch = 0) {
+      Job& j = jobs[n++];
+      j.kind = kind;
+      j.R = rows, j.C = cols, j.ld = ld, j.span = span, j.batch = batch;
+      return &j;
+    };
+    if (dx && !few) {
+      if (copy_dy) copy = add(Job::kPadRows, M, N, p.x.ldy);
+      w = add(Job::kTurnCodes, N, K, p.x.ld);
+      a = add(Job::kTurnEach, R, K, R, 64, L);
+    }
+    if (dx || da) b = add(Job::kTurnEach, N, R, p.ldn, 64, L);
+    if (da || db) lists = add(Job::kLists, M, L, 0);
+  }
+  AdapterLayout(const AdapterLayout&) = delete;
+};
+
 // ---- norm with codes ----
 
 w8a8_status check_norm(int64_t M, int64_t K, float eps) {
@@ -697,8 +724,11 @@ size_t w8a8_linear_adapters_backward_workspace(int64_t M, int64_t N, int64_t K, 
   int64_t most = 0;   // the largest of the plans that calls of these sizes may take, as their addresses are
   for (const bool copy : {true, false})
     for (const bool few : {false, true})
-      if ((copy || (N % 8 == 0 && N % kLine != 0)) && (!few || few_rows(M, N, K)))
-        most = std::max(most, adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few).bytes);
+      if ((copy || (N % 8 == 0 && N % kLine != 0)) && (!few || few_rows(M, N, K))) {
+        const AdapterBackPlan p = adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few);
+        const AdapterLayout layout(p, M, N, K, R, L, dx, da, db, copy, few);
+        if (w8a8::prepare_fits(layout.jobs, layout.n)) most = std::max(most, p.bytes);
+      }
   return (size_t)most;
 }
 
@@ -715,6 +745,11 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
     return W8A8_OK;
   }
   if (!dx && !da && !db) return W8A8_OK;
+  const bool few = dx && few_rows(M, N, K) && aligned(dx, 16);
+  const bool copy = N % 8 != 0 || !aligned(dy, 16) || (dx && copy_lines(M, N, K));
+  const AdapterBackPlan p = adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few);
+  AdapterLayout layout(p, M, N, K, R, L, dx, da, db, copy, few);
+  if (!w8a8::prepare_fits(layout.jobs, layout.n)) return W8A8_ERR_SHAPE;
   const bool codes = da || db;   // the activations
   if (!dy || !scaling || !ids || (codes && (!xq || !x_scale)) || (dx && (!wq || !w_scale)) || ((dx || db) && !a) ||
       ((dx || da) && !b))
@@ -722,30 +757,24 @@ w8a8_status w8a8_linear_adapters_backward(const uint16_t* dy, const int8_t* xq, 
   if (!aligned(scaling, 4) || !aligned(ids, 4) || !aligned(a, 16) || !aligned(b, 16) ||
       (codes && (!aligned(xq, 16) || !aligned(x_scale, 4))) || (dx && (!aligned(wq, 16) || !aligned(w_scale, 4))))
     return W8A8_ERR_ALIGN;
-  const bool few = dx && few_rows(M, N, K) && aligned(dx, 16);
-  const bool copy = N % 8 != 0 || !aligned(dy, 16) || (dx && copy_lines(M, N, K));
-  const AdapterBackPlan p = adapter_back_plan(M, N, K, R, L, dx, da, db, copy, few);
   const w8a8_status st = check_workspace(workspace, workspace_bytes, p.bytes);
   if (st != W8A8_OK) return st;
-  using Job = w8a8::LayoutJob;
   void* const ws = workspace;
   uint16_t *bt = at<uint16_t>(ws, p.bt), *a_turned = at<uint16_t>(ws, p.at), *u = at<uint16_t>(ws, p.u);
   uint32_t *t = at<uint32_t>(ws, p.t), *v = at<uint32_t>(ws, p.v);
   int32_t *list = at<int32_t>(ws, p.list), *starts = at<int32_t>(ws, p.starts);
-  Job jobs[w8a8::kMaxJobs];
-  int n = 0;
-  const uint16_t* first = dy;
-  if (dx && !few) {
-    if (copy) {
-      jobs[n++] = {Job::kPadRows, dy, nullptr, at<uint16_t>(ws, p.x.copy), nullptr, M, N, p.x.ldy, 0};
-      first = at<uint16_t>(ws, p.x.copy);
-    }
-    jobs[n++] = {Job::kTurnCodes, wq, w_scale, at<uint16_t>(ws, p.x.wt), nullptr, N, K, p.x.ld, 0};
-    jobs[n++] = {Job::kTurnEach, a, nullptr, a_turned, nullptr, R, K, R, 64, L};
-  }
-  if (dx || da) jobs[n++] = {Job::kTurnEach, b, nullptr, bt, nullptr, N, R, p.ldn, 64, L};
-  if (codes) jobs[n++] = {Job::kLists, ids, nullptr, nullptr, nullptr, M, L, 0, 0, 0, list, starts};
-  if (n > 0) TRY(w8a8::launch_prepare(jobs, n, stream));
+  const auto set = [](w8a8::LayoutJob* j, const void* in, uint16_t* out) {
+    if (j) j->in = in, j->out = out;
+  };
+  set(layout.copy, dy, at<uint16_t>(ws, p.x.copy));
+  set(layout.w, wq, at<uint16_t>(ws, p.x.wt));
+  if (layout.w) layout.w->scale = w_scale;
+  set(layout.a, a, a_turned);
+  set(layout.b, b, bt);
+  set(layout.lists, ids, nullptr);
+  if (layout.lists) layout.lists->list = list, layout.lists->starts = starts;
+  const uint16_t* first = layout.copy ? layout.copy->out : dy;
+  if (layout.n > 0) TRY(w8a8::launch_prepare(layout.jobs, layout.n, stream));
   w8a8::Down d{};
   d.ids = ids;
   d.scaling = scaling;

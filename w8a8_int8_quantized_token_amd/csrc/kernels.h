@@ -159,6 +159,7 @@ int few_grad_slices(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_few_grad(const uint16_t* d, int64_t ldd, const int8_t* q, const float* scale, float* slices,
                            int64_t M, int64_t N, int64_t K, bool gated, hipStream_t stream);
 int64_t transpose_sum_span(int64_t R, int64_t C);   // kTurnValues' rows of one block of sums
+bool prepare_fits(const LayoutJob* jobs, int n);   // (by their kinds and sizes)
 hipError_t launch_prepare(const LayoutJob* jobs, int n, hipStream_t stream);
 hipError_t launch_finish(const JoinJob* jobs, int n, hipStream_t stream);
 hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream);   // 16-bit zeros

@@ -39,6 +39,25 @@ bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds) {
   return K >= 768 || N <= 8192 + 16 * K;
 }
 
+// The same where the codes are there already, so that no launch is saved.  Cold
+// weights, us (tiled / few tokens):
+//   1 and 16 tokens, K = 64: 256 channels 2.8 / 3.3 and 2.9 / 3.7, 8192 3.6 / 4.7 and 3.6 /
+//   4.8; K = 256: 2048 3.9 / 3.8 and 4.0 / 3.9, 8192 4.3 / 4.8 and 4.3 / 5.0; K = 384: 4096
+//   4.6 / 4.0, 8192 4.7 / 4.9 and 4.7 / 5.1; K = 512: 8192 5.5 / 5.0 and 5.5 / 5.3, 10240
+//   5.6 / 5.9 and 5.7 / 6.1, 16384 5.8 / 6.8 and 5.9 / 7.2; K = 640: 12288 6.4 / 6.0 and 6.5 /
+//   6.4, 16384 6.6 / 6.8 and 6.7 / 7.2; K = 768: 16384 7.0 / 6.9 and 7.1 / 7.2, 32768 9.0 / 9.8
+//   and 9.2 / 10.2; K = 832: 16384 7.7 / 7.0 and 7.8 / 7.7, 32768 13.3 / 9.9 and 13.3 / 10.9;
+//   32 tokens, K = 256: 256 channels 3.8 / 4.0, 2048 4.0 / 4.1; K = 320: 1000 4.2 / 4.1;
+//   gated, K = 256: 256 channels 3.9 / 4.0 and 4.0 / 4.1, 4096 4.3 / 4.3 and 4.4 / 4.4; K =
+//   320: 1000 4.2 / 4.1 and 4.3 / 4.2, 6144 5.0 / 5.7 and 5.1 / 6.0; K = 512: 4096 5.6 / 4.5
+//   and 5.6 / 4.6, 8192 5.8 / 6.2 and 5.9 / 6.4; K = 704: 14336 8.4 / 8.9 and 8.5 / 9.5; K =
+//   896: 14336 9.1 / 8.6 and 9.5 / 9.4, 24576 12.4 / 11.1 and 13.1 / 12.4 (at the worst of
+//   it, K = 960, 14336, 9.3 / 9.5 and 9.5 / 10.4).
+bool few_tokens_pay_from_codes(int64_t M, int64_t N, int64_t K, bool gated) {
+  return few_tokens_pay(M, N, K, gated, false) && K >= (M > 16 || gated ? 320 : 256) &&
+         ((gated ? 2 : 1) * N <= 16 * K || K >= 832);
+}
+
 }  // namespace w8a8
 
 namespace {
@@ -513,7 +532,7 @@ w8a8_status w8a8_gated_linear_tile(const int8_t* xq, const float* x_scale, const
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, 2) ||
       !aligned(bias, 2))
     return W8A8_ERR_ALIGN;
-  if (tile < 0 && M <= w8a8::kFewTokens && few_tokens_pay(M, N, K, true, false))
+  if (tile < 0 && M <= w8a8::kFewTokens && w8a8::few_tokens_pay_from_codes(M, N, K, true))
     return launched(w8a8::launch_few_tokens(nullptr, xq, x_scale, wq, w_scale, bias, y, M, N, K, act, true, stream));
   return launched(w8a8::launch_gated(tile, static_cast<GateAct>(act), xq, x_scale, wq, w_scale, bias, y, M, N, K,
                                      stream));

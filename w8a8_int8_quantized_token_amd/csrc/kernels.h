@@ -169,7 +169,9 @@ hipError_t launch_zero(void* p, int64_t halves, hipStream_t stream);   // 16-bit
 // given (xq not null; needed where few_tokens_in_lds() says no).
 constexpr int64_t kFewTokens = 32;
 bool few_tokens_in_lds(int64_t M, int64_t K);
-bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds);   // against the tiled kernel
+// Against the tiled kernel, which needs the codes made first, and of codes that are there.
+bool few_tokens_pay(int64_t M, int64_t N, int64_t K, bool gated, bool in_lds);
+bool few_tokens_pay_from_codes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_few_tokens(const uint16_t* x, const int8_t* xq, const float* sx, const int8_t* wq,
                              const float* sw, const uint16_t* bias, uint16_t* y, int64_t M, int64_t N,
                              int64_t K, int act, bool gated, hipStream_t stream);

@@ -144,7 +144,7 @@ w8a8_status linear_epi(w8a8::Epilogue epi, const int8_t* xq, const float* x_scal
   if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(y, 2) ||
       (bias && !aligned(bias, 2)))
     return W8A8_ERR_ALIGN;
-  if (tile < 0 && !fp8 && M <= w8a8::kFewTokens && w8a8::few_tokens_pay(M, N, K, false, false))
+  if (tile < 0 && !fp8 && M <= w8a8::kFewTokens && w8a8::few_tokens_pay_from_codes(M, N, K, false))
     return w8a8::launch_few_tokens(nullptr, xq, x_scale, wq, w_scale, bias, y, M, N, K,
                                    epi == w8a8::Epilogue::kBf16GeluScaleBias, false, stream) == hipSuccess
                ? W8A8_OK

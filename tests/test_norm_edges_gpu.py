@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import adapter_ref as aref
+import block_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +181,18 @@ def test_zero_rows_pass_the_residuals_gradient_alone(w8):
     assert (dx == 2).all() and not dw.any()
     q, s, _ = w8.add_rms_norm_quantize(z, eps=0.0)
     assert not q.any() and not s.any()
+
+
+# both sides of the sizes at which the gradient's workgroups change
+@pytest.mark.parametrize("M,K", [(1024, 2048), (1024, 2064), (1025, 2064), (1500, 3568), (1500, 3584), (100, 3568), (1030, 4080), (1030, 4112)])
+def test_gradient_on_both_sides_of_its_rules(w8, M, K):
+    h, dh, w = inputs(M, K, 3)
+    dn = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).to(BF)
+    dx, dw = w8.add_rms_norm_backward(*dev(dn, h, w), eps=1e-5, dh=dh.to(DEV))
+    want, size, want_dw, dw_size = aref.norm_grad(dn, dh, h, w, 1e-5)
+    ref.check(dx, want, 2 * (64 + 22 + 8) * U * size, "dx")
+    assert ((dw.cpu().double() - want_dw).abs() <= (M + 64 + 60) * U * dw_size + 1e-30).all()
+    need = w8.lib.w8a8_add_rms_norm_backward_workspace(M, K)
+    space = torch.full((need + 32,), 255, dtype=torch.uint8, device=DEV)
+    got = w8.add_rms_norm_backward(*dev(dn, h, w), eps=1e-5, dh=dh.to(DEV), workspace=space[:need])
+    assert torch.equal(bits(got[0]), bits(dx)) and torch.equal(bits(got[1]), bits(dw)) and (space[need:] == 255).all()

@@ -434,13 +434,18 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(const float* __re
   }
 }
 
-// Threads of the gradient's workgroups (us, 512 workgroups of 256 threads / 256
-// of 512, with a residual's gradient: 4096 x 2560 21.5 / 24.4, 4096 x 4096 28.4 /
-// 27.1, 4096 x 8192 50.0 / 48.6), and their number: about one row in flight for
-// each wavefront that the compute units hold, and more where short rows leave
-// the weight's sums cheap (16384 x 1024: 512 workgroups 37.7, 1024 31.7; 1024 x
-// 1024: 8.7, 9.4).
-int grad_threads(int64_t K) { return K < 4096 ? 256 : K <= 16384 ? 512 : 1024; }
+// Threads of the gradient's workgroups, and their number: about one row in flight
+// for each wavefront that the compute units hold (512 workgroups of 256 threads,
+// 256 of 512), and more where short rows leave the weight's sums cheap (16384 x
+// 1024: 512 workgroups 37.7 us, 1024 31.7; 1024 x 1024: 8.7, 9.4).  Us by 256 / 512
+// threads, with a residual's gradient: 100 rows of 2064 6.4 / 6.1, of 3840 7.2 / 6.8;
+// 777 of 2064 11.8 / 10.5, of 3840 13.7 / 11.8; 4096 of 2064 22.5 / 23.6, of 2816 23.7 /
+// 24.9, of 3584 26.7 / 26.7, of 4096 29.0 / 28.2; 16384 of 2064 60 / 69, of 2816 67 / 72,
+// of 3584 80.2 / 81.6, of 4096 88.3 / 87.2.
+int grad_threads(int64_t M, int64_t K) {
+  if (K > 16384) return 1024;
+  return K >= 3584 || (K > 2048 && M <= 1024) ? 512 : 256;
+}
 
 template <int kThreads, int kPieces, Rows kRows>
 hipError_t backward(const NormGrad& a, int rows, hipStream_t s) {
@@ -481,7 +486,7 @@ hipError_t launch_add_norm_quantize(const uint16_t* x, const uint16_t* residual,
 }
 
 int64_t norm_grad_rows(int64_t M, int64_t K) {
-  return std::min<int64_t>(M, K <= 1024 && M >= 4096 ? 1024 : 128 * 1024 / grad_threads(K));
+  return std::min<int64_t>(M, K <= 1024 && M >= 4096 ? 1024 : 128 * 1024 / grad_threads(M, K));
 }
 
 hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
@@ -492,8 +497,8 @@ hipError_t launch_add_norm_grad(const uint16_t* dn, const uint16_t* dh, const ui
   const int rows = (int)norm_grad_rows(M, K);
   hipError_t e;
   if (K <= 2048) e = backward<256, 1, Rows::kAhead>(a, rows, s);
-  else if (K < 4096) e = backward<256, 2, Rows::kAhead>(a, rows, s);
-  else if (K == 4096) e = backward<512, 1, Rows::kAhead>(a, rows, s);
+  else if (grad_threads(M, K) == 256) e = backward<256, 2, Rows::kAhead>(a, rows, s);
+  else if (K <= 4096) e = backward<512, 1, Rows::kAhead>(a, rows, s);
   else if (K <= 8192) e = backward<512, 2, Rows::kAhead>(a, rows, s);
   else if (K <= 16384) e = backward<512, 4, Rows::kKept>(a, rows, s);
   else e = backward<1024, 4, Rows::kReload>(a, rows, s);

@@ -166,3 +166,12 @@ def test_infinities_beside_the_roundings_rest(w8, M):
     got = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws, a, b, one, big))
     assert torch.isinf(got[2][0]).all() and torch.isfinite(got[2][1].float()).all() and torch.isfinite(got[1][1].float()).all()
     assert torch.isinf(got[1][0][:, (xq[0] != 0).to(DEV)]).all()
+
+
+@pytest.mark.parametrize("M,R", [(1280, 8), (1281, 8), (1280, 16), (1281, 16), (512, 32), (513, 32), (341, 48), (342, 48), (128, 128), (129, 128)])
+def test_gradients_on_both_sides_of_the_first_products_rule(w8, M, R):
+    xq, xs, wq, ws, a, b, ids, scaling = inputs(M, 272, 264, R, 3, 8)
+    dy = torch.randn(M, 264, generator=torch.Generator().manual_seed(M)).to(BF)
+    inp = (dy, xq, xs, wq, ws, a, b, ids, scaling)
+    for g, (want, off), name in zip(w8.linear_adapters_backward(*dev(*inp)), aref.grads(*inp), ("dx", "da", "db")):
+        ref.check(g, want, off, name, rms_steps=2.0)

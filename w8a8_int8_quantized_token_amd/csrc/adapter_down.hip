@@ -400,11 +400,18 @@ int tiles_of(const Down& a, int products) {
 // 11.9; rank 128: 128 8.7 / 11.6, 192 11.6 / 11.7, 256 14.5 / 11.8; K = 1168, rank
 // 16: 1024 5.4 / 6.7, 1280 6.2 / 6.6, 1536 6.9 / 6.7.  With sixteen adapters mixed,
 // rank 16: 1536 12.4 / 15.3, 2048 15.2 / 15.4; rank 128: 128 15.2 / 14.8.  Both
-// products of codes of 4096 and values of 4096, rank 16: 768 12.7 / 14.4, 1024 16.6 /
-// 14.5, eight adapters mixed 16.4 / 16.5; of 672 and 8432: 1024 22.0 / 23.9, 1280
-// 26.6 / 24.1, mixed 26.3 / 28.1.
+// products, with da and db, by rows times ranks, one adapter and eight mixed: rank 8
+// of 4096 and 4096: 16384 27.8 / 29.4 and 32.5 / 35.9, 20480 31.3 / 30.6 and 35.4 / 36.1,
+// 24576 36.5 / 33.8 and 38.0 / 36.3; of 1024 and 8192: 20480 32.3 / 39.4 and 46.7 / 53.7,
+// 32768 43.1 / 41.2 and 57.2 / 55.8; of 1168 and 1168: 12288 19.4 / 19.8 and 21.7 /
+// 24.2, 20480 23.7 / 21.4 and 26.1 / 25.7; rank 32 of 4096 and 4096: 12288 28.4 / 30.0
+// and 35.2 / 38.2, 16384 32.9 / 30.4 and 38.8 / 38.7, 20480 41.3 / 35.3 and 42.6 / 38.9; of
+// 1024 and 8192: 16384 36.6 / 41.4 and 50.4 / 57.6, 20480 41.5 / 42.1 and 54.9 / 56.8;
+// rank 64 of 2064 and 5466: 16384 33.4 / 30.4 and 59.6 / 59.0, 20480 41.2 / 34.0 and 62.6 /
+// 57.8; of 4096 and 12288: 16384 44.7 / 48.9 and 97.7 / 101.9, 20480 51.0 / 49.2 and
+// 103.4 / 99.4.
 bool by_rows(int64_t M, int64_t R, int products) {
-  return M * ((R + 15) / 16 * 16) <= (products == 1 ? 20480 : 17408);
+  return M * ((R + 15) / 16 * 16) <= (products == 1 || R <= 16 ? 20480 : 16384);
 }
 
 // Codes alone, by the rules of as many products: a gradient's bits do not depend

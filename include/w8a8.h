@@ -466,11 +466,14 @@ w8a8_status w8a8_add_rms_norm_backward(const uint16_t *dn, const uint16_t *dh, c
  * Sums are fp32; t is rounded because it is an operand of the bf16 matrix
  * cores.  A token without an adapter has the bits of w8a8_linear, and no
  * token's result depends on another adapter's values (be they NaN) or on its
- * neighbours; a value of b that is not finite reaches its channel of its
- * adapter's tokens alone, whichever kernel runs.  Adapters of different ranks are padded with zeros.  Any order
- * of ids is right; long runs of tokens with the same adapter are the fast one.
+ * neighbours (on their number alone, which may choose another kernel); a value of
+ * b that is not finite reaches its channel of its adapter's tokens alone, whichever
+ * kernel runs.  Adapters of different ranks are padded with zeros.  Any order of ids
+ * is right; long runs of tokens with the same adapter are the fast one.
  * The dynamic form takes bf16 activations, with the same bits as
- * w8a8_quantize_act and w8a8_linear_adapters: two launches for a few tokens.
+ * w8a8_quantize_act and w8a8_linear_adapters: one launch for up to four short
+ * tokens, two for a few tokens, three or four beyond and for rows of over 16384
+ * values.
  * Contract as for w8a8_linear, and 8 <= R <= 128, R % 8 == 0, 1 <= L <= 65536;
  * a and b 16-byte aligned, scaling and ids 4-byte aligned.  Workspace as for
  * w8a8_linear_dynamic (always needed).  `tile` as for w8a8_linear_tile, for

@@ -104,7 +104,7 @@ def linear_adapters(xq, x_scale, wq, w_scale, a, b, ids, scaling, bias=None, y=N
 
 def linear_adapters_dynamic(x, wq, w_scale, a, b, ids, scaling, bias=None, y=None, workspace=None):
     """bf16 x [M,K] -> bf16 y [M,N]: ``quantize_act`` and ``linear_adapters`` in
-    one call, the same bits; two launches for a few tokens."""
+    one call, the same bits; one or two launches for a few tokens."""
     if y is None and workspace is None:
         out = _calls.linear_adapters(x, None, wq, w_scale, bias, a, b, ids, scaling)
         if out is not None:

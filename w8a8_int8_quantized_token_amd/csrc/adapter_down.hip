@@ -366,7 +366,6 @@ __global__ __launch_bounds__(kThreads) void down_block_kernel2(Down codes, Down 
   else
     down_block<Rows::kValues, kTiles>(values, blockIdx.x, blockIdx.y, z, slots, lds);
 }
-template <int kUnused>
 __global__ __launch_bounds__(kThreads) void down_row_kernel2(Down codes, Down values) {
   if (blockIdx.z == 0) down_row<Rows::kValues>(values);
   else down_row<Rows::kCodes>(codes);
@@ -452,7 +451,7 @@ hipError_t launch_down_pair(const Down* codes, const Down* values, hipStream_t s
   const dim3 threads(kThreads);
   const int both = c.M > 0 ? 2 : 1;
   if (by_rows(v.M, v.R, 2)) {
-    hipLaunchKernelGGL(down_row_kernel2<0>, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
+    hipLaunchKernelGGL(down_row_kernel2, dim3((unsigned)v.M, (unsigned)(v.ldt / kRanks), both), threads, 0, s, c, v);
     return hipGetLastError();
   }
   const int tiles = tiles_of(v, 2), slots = slots_of(v, tiles);

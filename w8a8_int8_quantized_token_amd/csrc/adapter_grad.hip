@@ -10,7 +10,7 @@
 // and that error grows with the sum as the sum itself does, so that a gradient
 // of any number of rows had 1.4 times the error of its own rounding (relative
 // error 2.4e-3 and not 1.7e-3).  The second part costs nothing up to rank 32
-// and 10 us of 130 at 8192 rows of 4096 and 8192, rank 64.
+// and 10 to 20 us of 130 at 8192 rows of 4096 and 8192, rank 64.
 //
 // The rows of an adapter come as a list (`lists`, made beside the operands'
 // layout), so ids may be in any order; a row's values lie together, and only
@@ -26,8 +26,8 @@
 // part the result is written at once.
 //
 // Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 16.4
-// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 (168 MB of x,
-// read again for the second 32 ranks).
+// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 to 79 (168 MB of
+// x, read again for the second 32 ranks).
 #include "kernels.h"
 
 #include <algorithm>

@@ -16,8 +16,10 @@ hipError_t launch_gemm_low(int tile, const int8_t* xq, const float* sx, const in
   const LowArgs args{low.t, low.b, low.ids, N * low.R, (int)low.ldt, (int)low.R, (int)low.count};
   if (tile < 0) {
     tile = choose_tile(M, N, K);
-    // the 128x256 tiles where the linear takes 256x128 ones (2048 x 4096 x 4096,
-    // rank 16: 51.3 us and not 55.2, rank 64: 63 and not 70)
+    // the 128x256 tiles where the linear takes 256x128 ones (us, 256x128 / 128x256, of
+    // adapters in runs and mixed: 2048 x 4096 x 4096, rank 16 55.8 / 51.6 and 65.8 / 59.9,
+    // rank 64 58.9 / 54.8 and 97 / 100; 1024 x 8192 x 4096 52.8 / 48.6 and 54.0 / 49.8; 4096
+    // x 2048 x 2048 38.2 / 34.7 and 40.3 / 36.4; 1536 x 5120 x 5120 65.6 / 59.3 and 69.9 / 63.2)
     if (kPlans[tile].main == k256x128) --tile;
   }
   // the plans of the 256x256 split ring are those of its whole-stage form here

@@ -113,9 +113,9 @@ class W8A8AdaptedLinear(W8A8Linear):
                    torch.full((adapters,), float(scaling), device=dev))
 
     def forward(self, x: torch.Tensor | Tokens, adapters: torch.Tensor | int = 0) -> torch.Tensor:
-        """adapters: one index for all tokens, or int32 of x's leading shape or
-        of its first dimensions (one for each sequence of a batch); outside
-        [0, L): none."""
+        """adapters: one index for all tokens (the first adapter unless given), or
+        integers of x's leading shape or of its first dimensions (one for each
+        sequence of a batch); outside [0, L): none."""
         lead = x.shape[:-1]
         x2 = _tokens(x, self.in_features, "W8A8AdaptedLinear")
         codes = isinstance(x2, Tokens)
@@ -194,7 +194,8 @@ class W8A8GatedMLP(torch.nn.Module):
         return cls(*_codes(gate, up), W8A8Linear.from_linear(down), act)
 
     def forward(self, x: torch.Tensor | Tokens, adapters: torch.Tensor | int | None = None) -> torch.Tensor:
-        """adapters: those of a W8A8AdaptedLinear as the down projection."""
+        """adapters: those of a W8A8AdaptedLinear as the down projection; without
+        them its own default, the first adapter for every token."""
         x2 = _tokens(x, self.in_features, "W8A8GatedMLP")
         if isinstance(x2, Tokens):
             args = (self.wq, self.w_scale, self.bias)
@@ -250,7 +251,8 @@ class W8A8QKV(torch.nn.Module):
         fp32 [P, rot/2], positions int32, one per token.  Without positions a
         token is at its index in its sequence (the last dimension before the
         features), in sequences longer than the tables at that index mod P.
-        adapters: those of a W8A8AdaptedLinear as the projection."""
+        adapters: those of a W8A8AdaptedLinear as the projection; without them its
+        own default, the first adapter for every token."""
         if positions is None and x.dim() > 2:
             cos, sin = self._tables(x.shape[-2], x.shape[:-2].numel(), cos, sin)
         qkv = self.proj(x) if adapters is None else self.proj(x, adapters)

@@ -33,3 +33,10 @@ def test_what_needs_no_layout_is_taken(w8):
     M, N, K, R, L = 4, 8192, 8192, 8, 65536
     assert call(w8, M, N, K, R, L, dx=None, da=None, n=16) == ARG and size(M, N, K, R, L, 0, 0, 1) > 0
     assert call(w8, M, N, K, R, L, dx=None, n=16) == ARG and size(M, N, K, R, L, 0, 1, 1) > 0
+
+
+def test_larger_ranks_of_as_many_adapters(w8):
+    """Ranks above 48 take more workgroups, and more than one dimension of a grid has threads for."""
+    size = w8.lib.w8a8_linear_adapters_backward_workspace
+    for R in (8, 48, 64, 128):
+        assert call(w8, 4, 8192, 1024, R, 65536, dx=None, da=None, n=16) == ARG and size(4, 8192, 1024, R, 65536, 0, 0, 1) > 0, R

@@ -175,3 +175,26 @@ def test_gradients_on_both_sides_of_the_first_products_rule(w8, M, R):
     inp = (dy, xq, xs, wq, ws, a, b, ids, scaling)
     for g, (want, off), name in zip(w8.linear_adapters_backward(*dev(*inp)), aref.grads(*inp), ("dx", "da", "db")):
         ref.check(g, want, off, name, rms_steps=2.0)
+
+
+def test_more_workgroups_than_a_row_of_the_grid(w8):
+    """65536 adapters beside 2184 channels, a few of them with tokens."""
+    M, K, N, R, L = 70, 64, 2184, 8, 65536
+    g = torch.Generator().manual_seed(9)
+    xq, xs = ref.codes_of(torch.randn(M, K, generator=g).to(BF))
+    dy = torch.randn(M, N, generator=g).to(BF)
+    used = torch.tensor([0, 1, 60000, 65534, 65535])
+    ids = used[torch.randint(0, 5, (M,), generator=g)].to(torch.int32)
+    a = (torch.randn(5, R, K, generator=g) / K ** 0.5).to(BF)
+    scaling = torch.rand(L, generator=g) + 0.5
+    all_a = torch.zeros(L, R, K, dtype=BF, device=DEV)
+    all_a[used.to(DEV)] = a.to(DEV)
+    all_b = torch.zeros(L, N, R, dtype=BF, device=DEV)
+    wq, ws = torch.zeros(N, K, dtype=torch.int8), torch.zeros(N)
+    db = w8.linear_adapters_backward(*dev(dy, xq, xs, wq, ws), all_a, all_b, *dev(ids, scaling), dx=False, da=False)[2]
+    which = torch.stack([(used == int(i)).nonzero()[0, 0] for i in ids]).to(torch.int32)
+    want, off = aref.grads(dy, xq, xs, wq, ws, a, torch.zeros(5, N, R, dtype=BF), which, scaling[used])[2]
+    ref.check(db[used.to(DEV)], want, off, "db", rms_steps=2.0)
+    rest = torch.ones(L, dtype=torch.bool, device=DEV)
+    rest[used.to(DEV)] = False
+    assert not db[rest].any()

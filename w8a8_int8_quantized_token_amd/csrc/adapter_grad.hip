@@ -10,7 +10,7 @@
 // and that error grows with the sum as the sum itself does, so that a gradient
 // of any number of rows had 1.4 times the error of its own rounding (relative
 // error 2.4e-3 and not 1.7e-3).  The second part costs nothing up to rank 32
-// and 10 to 20 us of 130 at 8192 rows of 4096 and 8192, rank 64.
+// and 13 us of 131 at 8192 rows of 4096 and 8192, rank 64.
 //
 // The rows of an adapter come as a list (`lists`, made beside the operands'
 // layout), so ids may be in any order; a row's values lie together, and only
@@ -26,8 +26,8 @@
 // part the result is written at once.
 //
 // Measured, both matrices: 4096 rows of 4096 codes and 4096 values, rank 16, 16.4
-// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 68 to 79 (168 MB of
-// x, read again for the second 32 ranks).
+// us (50 MB); 8192 rows of 4096 and 8192, four adapters of rank 64, 79 (168 MB of x;
+// 58 with v in one part, whose registers allowed a lane twice the columns).
 #include "kernels.h"
 
 #include <algorithm>
@@ -203,7 +203,8 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
     f32x4 sum = {0, 0, 0, 0};
     for (int w = 0; w < active; ++w) sum += lds.part[w][wave][lane];
     // lane: column col + j, ranks KR (4h + e) + r of the block's
-    const int r = c / KB, j = c % KB + wave;
+    constexpr bool kOneRank = KB % kWaves == 0;   // of the eight sums
+    const int r = kOneRank ? c / KB : (c + wave) / KB, j = kOneRank ? c % KB + wave : (c + wave) % KB;
     if (col + j >= a.C) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -217,12 +218,15 @@ __device__ __forceinline__ void adapter_grad(const AdapterGrad& a, unsigned bloc
 }
 
 // The gradients of both matrices in one launch: b's workgroups, whose rows are
-// longer, before a's.
+// longer, before a's.  (The grid's rows are for more workgroups than one dimension
+// of it may have threads.)
 template <int KR, int KA, int KB>
-__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, AdapterGrad gb, unsigned blocks_b) {
+__global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, AdapterGrad gb, unsigned blocks_b,
+                                                                unsigned blocks) {
   __shared__ Lds lds;
-  if (blockIdx.x < blocks_b) adapter_grad<KR, KB, false>(gb, blockIdx.x, lds);
-  else adapter_grad<KR, KA, true>(ga, blockIdx.x - blocks_b, lds);
+  const unsigned block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block < blocks_b) adapter_grad<KR, KB, false>(gb, block, lds);
+  else if (block < blocks) adapter_grad<KR, KA, true>(ga, block - blocks_b, lds);
 }
 
 // Ranks of a lane, and columns: as many sums as registers allow.  Us of both
@@ -231,9 +235,10 @@ __global__ __launch_bounds__(kThreads) void adapter_grad_kernel(AdapterGrad ga, 
 // 217 of 2048: 22.0, 21.8, 22.2, 19.8; rank 40, 2048 of 4096: 62, 58.3, 55.1, 56.8; 64
 // of 2592 and 2776: 34.6, 32.8, 27.0, 29.4; rank 48, 4096 of 2048 and 5136: 72, 67, 61,
 // 62; rank 64, 8192 of 4096 and 8192: 146, 142, 161, 142; 2048 of 4096: 44.4, 42.5,
-// 46.1, 43.3; rank 128, 1024 of 4096: 45, 40.8, 44.5, 40.4.
-int ranks_of(int R) { return R <= 16 ? 1 : R > 32 && R <= 48 ? 3 : 2; }
-int columns_of(int R, bool codes) { return R <= 16 && codes ? 16 : 8; }
+// 46.1, 43.3; 300 of 1024: 27.5, 26.4, 27.4, 25.8; rank 128, 1024 of 4096: 45, 40.8,
+// 44.5, 40.4.
+int ranks_of(int R) { return R <= 16 ? 1 : R > 32 && R <= 48 ? 3 : 4; }
+int columns_of(int R, bool codes) { return ranks_of(R) == 4 ? 4 : ranks_of(R) == 1 && codes ? 16 : 8; }
 
 int64_t col_blocks_of(int64_t C, int R, bool codes) { return (C + 16 * columns_of(R, codes) - 1) / (16 * columns_of(R, codes)); }
 int64_t rank_blocks_of(int R) { return (R + 16 * ranks_of(R) - 1) / (16 * ranks_of(R)); }
@@ -244,6 +249,9 @@ int parts_of(int64_t M, int64_t C, int R, int count, bool codes) {
   const int64_t blocks = col_blocks_of(C, R, codes) * rank_blocks_of(R) * count, want = codes ? 96 : 160;
   return (int)std::max<int64_t>(1, std::min(want / blocks, (M + kWaves * kRows - 1) / (kWaves * kRows)));
 }
+
+// A row of the grid, and all of it.
+constexpr int64_t kGridRow = int64_t(1) << 20, kMaxBlocks = int64_t(1) << 31;
 
 // Workgroups of one of the gradients (none: 0).
 int64_t set_blocks(AdapterGrad& g, bool codes) {
@@ -297,17 +305,19 @@ bool adapter_grads_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t count
     const int64_t C = codes ? K : N;
     blocks += col_blocks_of(C, (int)R, codes) * rank_blocks_of((int)R) * count * parts_of(M, C, (int)R, (int)count, codes);
   }
-  return blocks * kThreads < (int64_t(1) << 32);   // threads of a launch
+  return blocks <= kMaxBlocks;
 }
 
 hipError_t launch_adapter_grads(AdapterGrad ga, AdapterGrad gb, hipStream_t s) {
   const int64_t na = set_blocks(ga, true), nb = set_blocks(gb, false);
   if (na + nb == 0) return hipSuccess;
-  const dim3 grid((unsigned)(na + nb)), block(kThreads);
+  if (na + nb > kMaxBlocks) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)std::min(na + nb, kGridRow), (unsigned)((na + nb + kGridRow - 1) / kGridRow)), block(kThreads);
+  const unsigned first = (unsigned)nb, all = (unsigned)(na + nb);
   switch (ranks_of(na ? ga.R : gb.R)) {
-    case 1: hipLaunchKernelGGL((adapter_grad_kernel<1, 16, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
-    case 2: hipLaunchKernelGGL((adapter_grad_kernel<2, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
-    default: hipLaunchKernelGGL((adapter_grad_kernel<3, 8, 8>), grid, block, 0, s, ga, gb, (unsigned)nb); break;
+    case 1: hipLaunchKernelGGL((adapter_grad_kernel<1, 16, 8>), grid, block, 0, s, ga, gb, first, all); break;
+    case 3: hipLaunchKernelGGL((adapter_grad_kernel<3, 8, 8>), grid, block, 0, s, ga, gb, first, all); break;
+    default: hipLaunchKernelGGL((adapter_grad_kernel<4, 4, 4>), grid, block, 0, s, ga, gb, first, all); break;
   }
   return hipGetLastError();
 }

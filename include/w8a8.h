@@ -442,9 +442,11 @@ w8a8_status w8a8_qk_norm_rope_backward(
  * dx may be dn, dh or h and overlaps nothing otherwise.  Arithmetic is fp32, each bf16
  * output rounded once.  Of a row of zeros with eps = 0, r is taken as 0.
  * Contract: 16 <= K <= 32768, K % 16 == 0; M times 64 (K <= 1024), 256 (K <
- * 8192) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; inputs of any magnitude
- * (squares that vanish or overflow in fp32 are summed again in range); all bf16
- * pointers and the codes 16-byte aligned, scales and dweight 4-byte aligned.
+ * 8192) or 1024 below 2^32 - 1024, M <= 2^26; eps >= 0; h of any magnitude
+ * (squares that vanish or overflow in fp32 are summed again in range) whose
+ * products with the weight, and of the gradient dn * weight * h, are finite in
+ * fp32; all bf16 pointers and the codes 16-byte aligned, scales and dweight 4-byte
+ * aligned.
  */
 w8a8_status w8a8_add_rms_norm_quantize(const uint16_t *x, const uint16_t *residual,
                                        const uint16_t *weight, uint16_t *h, void *xq,
